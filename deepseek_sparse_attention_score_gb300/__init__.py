@@ -6,6 +6,15 @@ in ``include/dsa.h``); :mod:`.abi` is its thin Python binding and
 """
 from .abi import (  # noqa: F401
     DSAError,
+    PageTables,
+    RopeTarget,
+    dsa_build_page_tables,
+    dsa_q4_read_rows,
+    dsa_q4_write_back,
+    dsa_rope,
+    dsa_rope_freqs,
+    dsa_sparse_mla_decode_q4,
+    dsa_window_mla,
     dsa_build_block_union,
     dsa_device_sm_count,
     dsa_launch_count,

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -31,6 +32,7 @@ STATUS_BAD_METADATA = 0x2
 STATUS_BAD_INDEX = 0x4
 STATUS_TIMEOUT = 0x8
 STATUS_INTERNAL = 0x10
+STATUS_NO_PAGES = 0x20
 
 EXPORTS = (
     "dsa_index_build_share_map",
@@ -52,7 +54,15 @@ EXPORTS = (
     "dsa_device_sm_count",
     "dsa_launch_count",
     "dsa_sparse_mla_decode_noalloc",
+    "dsa_build_page_tables",
+    "dsa_rope",
+    "dsa_rope_freqs",
+    "dsa_q4_write_back",
+    "dsa_q4_read_rows",
+    "dsa_sparse_mla_decode_q4",
+    "dsa_window_mla",
 )
+Q4_ROW_BYTES = 416  # one row of the 4-bit latent cache
 
 
 class DSAError(RuntimeError):
@@ -66,6 +76,14 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
+_L = ctypes.c_int64
+
+
+class _RopeTargetC(ctypes.Structure):
+    _fields_ = [("x", _P), ("y", _P), ("x_stride_t", _L), ("x_stride_h", _L), ("y_stride_t", _L),
+                ("y_stride_h", _L), ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("rot_off", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", _F)]
 
 
 def lib() -> ctypes.CDLL:
@@ -107,6 +125,15 @@ def lib() -> ctypes.CDLL:
     L.dsa_indexer_topk_approx.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                           _P, _P, _Z, _P]
     L.dsa_selftest_wait_timeout.argtypes = [_P, ctypes.c_longlong, _P]
+    L.dsa_build_page_tables.argtypes = [_P, _P, _P, _P, _L, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]
+    L.dsa_rope.argtypes = [_P, _P, _I, _I, _I, _P, _P, _I]
+    L.dsa_rope_freqs.argtypes = [_I, _D, _I, _D, _I, _D, _D, _P, _P]
+    L.dsa_q4_write_back.argtypes = [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]
+    L.dsa_q4_read_rows.argtypes = [_P, _P, _I, _I, _P, _I, _P, _I, _P]
+    L.dsa_sparse_mla_decode_q4.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F,
+                                           _P, _P, _P, _Z, _P]
+    L.dsa_window_mla.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _F,
+                                 _P, _P, _P, _Z, _P]
     L.dsa_device_sm_count.argtypes = []
     L.dsa_launch_count.argtypes = []
     L.dsa_launch_count.restype = ctypes.c_longlong
@@ -479,3 +506,273 @@ def dsa_selftest_wait_timeout(dev_status, limit_clocks=2_000_000):
     _need(dev_status, "dev_status", torch.int32, dev_status.device, 1)
     rc = lib().dsa_selftest_wait_timeout(_stream(dev_status.device), int(limit_clocks), _ptr(dev_status))
     _check("dsa_selftest_wait_timeout", rc)
+
+
+# ------------------------------------------- the steps around the attention
+def _launch(dev, name, *args):
+    """Call a device entry point on ``dev``'s current stream (whatever device
+    is current) and raise on an error code."""
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device, got {dev}")
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(torch.cuda.current_stream(dev).cuda_stream, *args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(torch.cuda.current_stream(dev).cuda_stream, *args)
+    _check(name, rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status):
+    S, PTW = _meta(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
+    if cu_q_lens.numel() != S + 1 or cu_kv_lens.numel() != S + 1:
+        raise ValueError(f"cu_q_lens and cu_kv_lens need {S + 1} entries for {S} requests")
+    _status(dev_status, dev)
+    return S, PTW, (_addr(seq_lens), _addr(cu_q_lens), _addr(cu_kv_lens), _addr(page_indices))
+
+
+def _status(dev_status, dev):
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, dev, 1)
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status must hold one word")
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+class PageTables(NamedTuple):
+    """What :func:`dsa_build_page_tables` writes (int32)."""
+
+    cu_q_lens: torch.Tensor     # [S + 1]
+    cu_kv_lens: torch.Tensor    # [S + 1]
+    page_indices: torch.Tensor  # [PTW], -1 behind the last page
+    token_seq: torch.Tensor     # [T], -1 behind the last token
+    positions: torch.Tensor     # [T]
+    slots: torch.Tensor         # [T], page * ps + row
+    n_taken: torch.Tensor       # [1], pages taken from the free list
+
+
+def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, PTW, ps=64, out=None,
+                          dev_status=None):
+    """A step's ragged metadata and slot map from its requests' lengths.
+
+    ``q_lens`` [S] new tokens and ``seq_lens`` [S] positions with them;
+    ``block_table`` [S, W] holds each request's pages and is extended in place
+    by the pages that the new tokens are the first to need, taken in order
+    from ``free_pages`` [F]. ``T`` and ``PTW`` may be upper bounds of the
+    tokens and page-table entries (the rest is -1); with ``T`` the number of
+    tokens, ``(seq_lens, out.cu_q_lens, out.cu_kv_lens, out.page_indices)`` is
+    the metadata of every other call. ``out``: a :class:`PageTables` to write
+    into."""
+    dev = q_lens.device
+    _need(q_lens, "q_lens", torch.int32, dev, 1)
+    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
+    S = q_lens.numel()
+    _shape(seq_lens, "seq_lens", (S,))
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise TypeError("block_table must be an int32 tensor [S, W]")
+    if block_table.device != dev or block_table.shape[0] != S:
+        raise ValueError(f"block_table must be on {dev} with {S} rows")
+    W = block_table.shape[1]
+    if block_table.numel() and (W > 1 and block_table.stride(1) != 1 or S > 1 and block_table.stride(0) < W):
+        raise ValueError("block_table rows must be contiguous and must not overlap")
+    F = 0
+    if free_pages is not None:
+        _need(free_pages, "free_pages", torch.int32, dev, 1)
+        F = free_pages.numel()
+    _status(dev_status, dev)
+    T, PTW = int(T), int(PTW)
+    if T < 0 or PTW < 0:
+        raise ValueError("T and PTW must not be negative")
+    if out is None:
+        # one allocation; the page table first, on a 16-byte boundary
+        buf = torch.empty(PTW + 2 * (S + 1) + 3 * T + 1, dtype=torch.int32, device=dev)
+        pages, cu_q, cu_kv, seq, pos, slots, taken = buf.split((PTW, S + 1, S + 1, T, T, T, 1))
+        out = PageTables(cu_q, cu_kv, pages, seq, pos, slots, taken)
+    else:
+        for name, n in (("cu_q_lens", S + 1), ("cu_kv_lens", S + 1), ("page_indices", PTW), ("token_seq", T),
+                        ("positions", T), ("slots", T), ("n_taken", 1)):
+            _need(getattr(out, name), f"out.{name}", torch.int32, dev, 1)
+            _shape(getattr(out, name), f"out.{name}", (n,))
+    _launch(dev, "dsa_build_page_tables", _addr(q_lens), _addr(seq_lens), _addr(block_table),
+            max(W, block_table.stride(0)) if S > 1 else W, W, _addr(free_pages), F, S, T, PTW, int(ps),
+            _addr(out.cu_q_lens), _addr(out.cu_kv_lens), _addr(out.page_indices), _addr(out.token_seq),
+            _addr(out.positions), _addr(out.slots), _addr(out.n_taken), _addr(dev_status))
+    return out
+
+
+_ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
+
+
+class RopeTarget:
+    """Rows to rotate in one :func:`dsa_rope` call: ``x`` [T, H, D] (bf16 or
+    fp32, any strides with contiguous columns), turned in columns ``rot_off``
+    .. ``rot_off + rot_dim - 1`` (all after ``rot_off`` by default) into ``y``
+    of the same shape, or in place without one. ``layout``: "interleaved"
+    pairs (2i, 2i+1) or "half" pairs (i, i + rot_dim/2). ``scale`` multiplies
+    the rotated columns. Holds its tensors; may be kept and used again."""
+
+    __slots__ = ("x", "y", "rot_dim", "c")
+
+    def __init__(self, x, y=None, *, rot_off=0, rot_dim=None, layout="half", scale=1.0):
+        if y is None:
+            y = x
+        for name, t in (("x", x), ("y", y)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype not in _ROPE_DTYPES:
+                raise TypeError(f"{name} must be a bf16 or fp32 tensor [T, H, D]")
+            if t.shape[2] > 1 and t.stride(2) != 1:
+                raise ValueError(f"the columns of {name} must be contiguous")
+        if y.dtype != x.dtype or y.device != x.device or y.shape != x.shape:
+            raise ValueError("y must have the type, device and shape of x")
+        if layout not in _ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
+        T, H, D = x.shape
+        self.x, self.y = x, y
+        self.rot_dim = D - rot_off if rot_dim is None else int(rot_dim)
+        self.c = _RopeTargetC(x.data_ptr(), y.data_ptr(), x.stride(0), x.stride(1), y.stride(0), y.stride(1), H, D,
+                              rot_off, _ROPE_LAYOUTS[layout], _ROPE_DTYPES[x.dtype], scale)
+
+
+def dsa_rope(targets, positions, freqs, *, inverse=False):
+    """Rotate the rows of one or several :class:`RopeTarget` in one launch.
+    ``positions`` int32 [T] (rows with a negative one are left alone),
+    ``freqs`` fp64 [rot_dim / 2] as :func:`dsa_rope_freqs` makes them.
+    ``inverse`` turns back, which is also the gradient. Returns the rotated
+    tensors, one or a list as ``targets`` came."""
+    one = isinstance(targets, RopeTarget)
+    ts = [targets] if one else list(targets)
+    dev = positions.device
+    _need(positions, "positions", torch.int32, dev, 1)
+    _need(freqs, "freqs", torch.float64, dev, 1)
+    T, rot = positions.numel(), 2 * freqs.numel()
+    for g in ts:
+        if g.x.device != dev or g.x.shape[0] != T:
+            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(g.x.shape)} on {g.x.device}")
+        if g.rot_dim != rot:
+            raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
+    arr = (_RopeTargetC * len(ts))(*[g.c for g in ts])
+    _launch(dev, "dsa_rope", arr, len(ts), T, rot, _addr(positions), _addr(freqs), 1 if inverse else 0)
+    return ts[0].y if one else [g.y for g in ts]
+
+
+def dsa_rope_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, orig_max_pos=4096, beta_fast=32.0,
+                   beta_slow=1.0, device=None):
+    """Frequencies (fp64 [rot_dim / 2], radians per position) of the rotary
+    pairs and the factor that goes with them, scaled for long contexts:
+    "none", "linear" (all divided by ``factor``) or "yarn" (by parts)."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
+    freqs = torch.empty(max(0, int(rot_dim) // 2), dtype=torch.float64)
+    ms = ctypes.c_double(1.0)
+    rc = lib().dsa_rope_freqs(int(rot_dim), float(base), _ROPE_SCALINGS[scaling], float(factor), int(orig_max_pos),
+                              float(beta_fast), float(beta_slow), _addr(freqs), ctypes.byref(ms))
+    _check("dsa_rope_freqs", rc)
+    return (freqs if device is None else freqs.to(device)), ms.value
+
+
+def _rows576(t, name, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise TypeError(f"{name} must be a bf16 tensor [N, W]")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.shape[1] < 576 or t.stride(1) != 1:
+        raise ValueError(f"{name} needs at least 576 contiguous columns")
+    return t.stride(0) if t.shape[0] > 1 else max(576, t.shape[1] // 8 * 8)
+
+
+def _cache4(cache, dev):
+    _need(cache, "cache", torch.uint8, dev, 3)
+    if cache.shape[2] != Q4_ROW_BYTES:
+        raise ValueError(f"a 4-bit cache is [P, ps, {Q4_ROW_BYTES}], got {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1]
+
+
+def dsa_q4_write_back(rows, cache, seq_lens, cu_q_lens, cu_kv_lens, page_indices, *, dev_status=None):
+    """Quantise each query token's latent row (``rows`` [T, >= 576]) into its
+    slot of the 4-bit ``cache`` [P, ps, 416] (uint8), in place."""
+    dev = cache.device
+    P, ps = _cache4(cache, dev)
+    stride = _rows576(rows, "rows", dev)
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status)
+    _launch(dev, "dsa_q4_write_back", _addr(rows), stride, _addr(cache), *meta, rows.shape[0], S, P, PTW, ps,
+            _addr(dev_status))
+    return cache
+
+
+def dsa_q4_read_rows(cache, slots, *, out=None, dev_status=None):
+    """The bf16 values [N, 576] of the rows in ``slots`` (page * ps + row) of a
+    4-bit cache; a negative slot gives zeros."""
+    dev = cache.device
+    P, ps = _cache4(cache, dev)
+    _need(slots, "slots", torch.int32, dev, 1)
+    _status(dev_status, dev)
+    N = slots.numel()
+    if out is None:
+        out = torch.empty((N, 576), dtype=torch.bfloat16, device=dev)
+    stride = _rows576(out, "out", dev)
+    if out.shape[0] != N:
+        raise ValueError(f"out needs {N} rows")
+    _launch(dev, "dsa_q4_read_rows", _addr(cache), P, ps, _addr(slots), N, _addr(out), stride, _addr(dev_status))
+    return out
+
+
+def _attend_out(dev, T, H, Dv, o, lse, want_lse, ws):
+    if o is None:
+        o = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(o, "o", torch.bfloat16, dev, 3)
+        _shape(o, "o", (T, H, Dv))
+    if want_lse and lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _need(lse, "lse", torch.float32, dev, 2)
+        _shape(lse, "lse", (T, H))
+    if ws is None:
+        ws = torch.empty(max(1, dsa_sparse_mla_decode_workspace_size(T, H, Dv)), dtype=torch.uint8, device=dev)
+    else:
+        _need(ws, "ws", torch.uint8, dev, 1)
+    return o, lse, ws
+
+
+def dsa_sparse_mla_decode_q4(q, cache, seq_lens, cu_q_lens, cu_kv_lens, page_indices, sel, *, unit, sm_scale, o=None,
+                             lse=None, want_lse=False, ws=None, dev_status=None, Dv=512):
+    """:func:`dsa_sparse_mla_decode` over the 4-bit latent ``cache``
+    [P, ps, 416] that :func:`dsa_q4_write_back` fills."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev, 3)
+    P, ps = _cache4(cache, dev)
+    _need(sel, "sel", torch.int32, dev, 2)
+    T, H, Dk = q.shape
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status)
+    K = sel.shape[1]
+    _shape(sel, "sel", (T, K))
+    o, lse, ws = _attend_out(dev, T, H, Dv, o, lse, want_lse, ws)
+    _launch(dev, "dsa_sparse_mla_decode_q4", _addr(q), _addr(cache), *meta, _addr(sel), K, int(unit), T, S, P, PTW, ps,
+            H, Dk, Dv, float(sm_scale), _addr(o), _addr(lse), _addr(ws), ws.numel(), _addr(dev_status))
+    return (o, lse) if lse is not None else o
+
+
+def dsa_window_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, *, max_kv, sm_scale, sliding_window,
+                   num_sinks=0, soft_cap=0.0, o=None, lse=None, want_lse=False, ws=None, dev_status=None, Dv=512):
+    """Causal absorbed-MLA over the ``sliding_window`` most recent positions
+    and the first ``num_sinks`` ones (:func:`dsa_dense_mla` with sinks)."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev, 3)
+    _need(kv, "kv", torch.bfloat16, dev, 3)
+    T, H, Dk = q.shape
+    P, ps, row_stride = kv.shape
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status)
+    o, lse, ws = _attend_out(dev, T, H, Dv, o, lse, want_lse, ws)
+    _launch(dev, "dsa_window_mla", _addr(q), _addr(kv), row_stride, *meta, int(max_kv), T, S, P, PTW, ps, H, Dk, Dv,
+            float(sm_scale), int(sliding_window), int(num_sinks), float(soft_cap), _addr(o), _addr(lse), _addr(ws),
+            ws.numel(), _addr(dev_status))
+    return (o, lse) if lse is not None else o

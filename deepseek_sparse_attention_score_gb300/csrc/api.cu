@@ -11,6 +11,7 @@
 #include "attend.cuh"
 #include "common.cuh"
 #include "indexer.cuh"
+#include "steps.cuh"
 
 namespace dsa {
 
@@ -384,16 +385,16 @@ int dsa_sparse_mla_decode(dsa_stream_t stream, const uint16_t* q, const uint16_t
   return run_attend(static_cast<cudaStream_t>(stream), prm, ws, ws_bytes);
 }
 
-int dsa_dense_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
-                  const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices, int max_kv,
-                  int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, int sliding_window,
-                  float soft_cap, uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status) {
-  NvtxRange nvtx_range("dsa_dense_mla");
+static int dense_common(cudaStream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
+                        const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
+                        const int32_t* page_indices, int max_kv, int T, int S, int P, int PTW, int ps, int H, int Dk,
+                        int Dv, float sm_scale, int sliding_window, int num_sinks, float soft_cap, uint16_t* o,
+                        float* lse, void* ws, size_t ws_bytes, int32_t* dev_status) {
   int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
   if (rc) return rc;
   rc = attend_check(q, kv, row_stride, T, H, Dk, Dv, o);
   if (rc) return rc;
-  if (max_kv < 1 || sliding_window < 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (max_kv < 1 || sliding_window < 0 || num_sinks < 0) return DSA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(sm_scale) || !std::isfinite(soft_cap) || soft_cap < 0.f) return DSA_ERR_INVALID_ARGUMENT;
   if (T == 0 || H == 0) return DSA_OK;
   AttendParams prm{};
@@ -419,13 +420,175 @@ int dsa_dense_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, in
     prm.cap_log2 = soft_cap * 1.4426950408889634f;
   }
   prm.K = (max_kv + ps - 1) / ps;  // pages of the longest request: the split unit
+  if (sliding_window > 0 && num_sinks > 0) {
+    // at most the sinks' pages and the window's, which may start inside one
+    prm.sinks = num_sinks;
+    const long long most = ((long long)num_sinks + ps - 1) / ps + ((long long)sliding_window + ps - 1) / ps + 1;
+    prm.K = (int)std::min<long long>(prm.K, most);
+  }
   prm.o = o;
   prm.lse = lse;
   prm.dev_status = dev_status;
   int z = attend_num_splits(T, H, prm.K, prm.mode);
   if (z > 1 && (!ws || ws_bytes < attend_workspace_bytes(T, H, z) || !aligned16(ws))) z = 1;
   prm.nsplit = z;
+  return run_attend(stream, prm, ws, ws_bytes);
+}
+
+int dsa_dense_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
+                  const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices, int max_kv,
+                  int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, int sliding_window,
+                  float soft_cap, uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_dense_mla");
+  return dense_common(static_cast<cudaStream_t>(stream), q, kv, row_stride, seq_lens, cu_q_lens, cu_kv_lens,
+                      page_indices, max_kv, T, S, P, PTW, ps, H, Dk, Dv, sm_scale, sliding_window, 0, soft_cap, o, lse,
+                      ws, ws_bytes, dev_status);
+}
+
+int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
+                   const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices, int max_kv,
+                   int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, int sliding_window,
+                   int num_sinks, float soft_cap, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                   int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_window_mla");
+  return dense_common(static_cast<cudaStream_t>(stream), q, kv, row_stride, seq_lens, cu_q_lens, cu_kv_lens,
+                      page_indices, max_kv, T, S, P, PTW, ps, H, Dk, Dv, sm_scale, sliding_window, num_sinks, soft_cap,
+                      o, lse, ws, ws_bytes, dev_status);
+}
+
+int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8_t* cache, const int32_t* seq_lens,
+                             const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices,
+                             const int32_t* sel, int K, int unit, int T, int S, int P, int PTW, int ps, int H, int Dk,
+                             int Dv, float sm_scale, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
+                             int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_sparse_mla_decode_q4");
+  int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
+  if (rc) return rc;
+  rc = attend_check(q, reinterpret_cast<const uint16_t*>(cache), 576, T, H, Dk, Dv, o);
+  if (rc) return rc;
+  if (K < 1 || (T > 0 && !sel)) return DSA_ERR_INVALID_ARGUMENT;
+  if (unit != 1 && unit != ps) return DSA_ERR_INVALID_ARGUMENT;
+  AttendParams prm{};
+  prm.scale_log2 = sm_scale * 1.4426950408889634f;
+  if (!std::isfinite(prm.scale_log2 * 128.f)) return DSA_ERR_INVALID_ARGUMENT;  // the kernel's logit factor
+  if (T == 0 || H == 0) return DSA_OK;
+  prm.q = q;
+  prm.kv4 = cache;
+  prm.seq_lens = seq_lens;
+  prm.cu_q_lens = cu_q_lens;
+  prm.cu_kv_lens = cu_kv_lens;
+  prm.page_indices = page_indices;
+  prm.T = T;
+  prm.S = S;
+  prm.P = P;
+  prm.PTW = PTW;
+  prm.ps = ps;
+  prm.H = H;
+  prm.mode = unit == 1 ? kModeToken : kModePage;
+  prm.sel = sel;
+  prm.K = K;
+  prm.o = o;
+  prm.lse = lse;
+  prm.dev_status = dev_status;
+  int z = attend_num_splits(T, H, K, prm.mode);
+  if (z > 1 && (!ws || ws_bytes < attend_workspace_bytes(T, H, z) || !aligned16(ws))) z = 1;
+  prm.nsplit = z;
   return run_attend(static_cast<cudaStream_t>(stream), prm, ws, ws_bytes);
+}
+
+int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int32_t* seq_lens, int32_t* block_table,
+                          int64_t bt_stride, int width, const int32_t* free_pages, int F, int S, int T, int PTW,
+                          int ps, int32_t* cu_q_lens, int32_t* cu_kv_lens, int32_t* page_indices, int32_t* token_seq,
+                          int32_t* positions, int32_t* slots, int32_t* n_taken, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_build_page_tables");
+  if (S < 0 || T < 0 || PTW < 0 || F < 0 || width < 0 || bt_stride < width) return DSA_ERR_INVALID_ARGUMENT;
+  if (!ps_supported(ps) || S > kTablesMaxRequests || (long long)width * ps >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  if (!cu_q_lens || !cu_kv_lens || !n_taken) return DSA_ERR_INVALID_ARGUMENT;
+  if ((S > 0 && (!q_lens || !seq_lens)) || (S > 0 && width > 0 && !block_table) || (F > 0 && !free_pages) ||
+      (PTW > 0 && !page_indices) || (T > 0 && (!token_seq || !positions || !slots)))
+    return DSA_ERR_INVALID_ARGUMENT;
+  TablesParams p{q_lens, seq_lens, block_table, bt_stride, width, free_pages, F, S, T, PTW, ps, cu_q_lens, cu_kv_lens,
+                 page_indices, token_seq, positions, slots, n_taken, dev_status, false};
+  return run_page_tables(static_cast<cudaStream_t>(stream), p);
+}
+
+int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets, int T, int rot_dim,
+             const int32_t* positions, const double* freqs, int inverse) {
+  NvtxRange nvtx_range("dsa_rope");
+  if (T < 0 || !targets || n_targets < 1) return DSA_ERR_INVALID_ARGUMENT;
+  if (n_targets > kRopeMaxTargets) return DSA_ERR_UNSUPPORTED;
+  if (rot_dim < 2 || rot_dim % 2) return DSA_ERR_INVALID_ARGUMENT;
+  if (rot_dim > kRopeMaxDim) return DSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_targets; ++i) {
+    const dsa_rope_target& g = targets[i];
+    if (g.H < 0 || g.D < 0 || g.rot_off < 0 || (long long)g.rot_off + rot_dim > g.D) return DSA_ERR_INVALID_ARGUMENT;
+    if ((g.layout != DSA_ROPE_INTERLEAVED && g.layout != DSA_ROPE_HALF) || !std::isfinite(g.scale))
+      return DSA_ERR_INVALID_ARGUMENT;
+    if (g.dtype != DSA_DTYPE_BF16 && g.dtype != DSA_DTYPE_F32) return DSA_ERR_UNSUPPORTED;
+    if ((long long)g.H * g.D >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+    if (T == 0 || g.H == 0) continue;
+    if (!g.x || !g.y) return DSA_ERR_INVALID_ARGUMENT;
+    if (g.x == g.y && (g.x_stride_t != g.y_stride_t || g.x_stride_h != g.y_stride_h)) return DSA_ERR_INVALID_ARGUMENT;
+    const uintptr_t es = g.dtype == DSA_DTYPE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(g.x) % es || reinterpret_cast<uintptr_t>(g.y) % es) return DSA_ERR_ALIGNMENT;
+  }
+  if (T == 0) return DSA_OK;
+  if (!positions || !freqs) return DSA_ERR_INVALID_ARGUMENT;
+  return run_rope(static_cast<cudaStream_t>(stream), targets, n_targets, T, rot_dim, positions, freqs, inverse != 0);
+}
+
+int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor, int orig_max_pos, double beta_fast,
+                   double beta_slow, double* freqs, double* mscale) {
+  if (rot_dim < 2 || rot_dim % 2 || !freqs || !std::isfinite(base) || base <= 1.0) return DSA_ERR_INVALID_ARGUMENT;
+  if (scaling < DSA_ROPE_SCALE_NONE || scaling > DSA_ROPE_SCALE_YARN) return DSA_ERR_UNSUPPORTED;
+  const bool yarn = scaling == DSA_ROPE_SCALE_YARN;
+  if (scaling != DSA_ROPE_SCALE_NONE && (!std::isfinite(factor) || factor < 1.0)) return DSA_ERR_INVALID_ARGUMENT;
+  if (yarn && (orig_max_pos < 1 || !std::isfinite(beta_fast) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow)))
+    return DSA_ERR_INVALID_ARGUMENT;
+  double lo = 0, hi = 0;
+  if (yarn) {
+    // pair index at which a frequency makes `turns` turns over orig_max_pos
+    auto at = [&](double turns) {
+      return rot_dim * std::log(orig_max_pos / (turns * 2.0 * 3.14159265358979323846)) / (2.0 * std::log(base));
+    };
+    lo = std::max(std::floor(at(beta_fast)), 0.0);
+    hi = std::min(std::ceil(at(beta_slow)), (double)rot_dim - 1);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot_dim);
+    double keep = scaling == DSA_ROPE_SCALE_NONE ? 1.0 : 0.0;
+    if (yarn) keep = 1.0 - std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+    freqs[i] = keep == 1.0 ? f : f * keep + f / factor * (1.0 - keep);
+  }
+  if (mscale) *mscale = yarn ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return DSA_OK;
+}
+
+int dsa_q4_write_back(dsa_stream_t stream, const uint16_t* rows, int src_stride, uint8_t* cache,
+                      const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
+                      const int32_t* page_indices, int T, int S, int P, int PTW, int ps, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_q4_write_back");
+  int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
+  if (rc) return rc;
+  if (src_stride < 576 || src_stride % 8) return DSA_ERR_UNSUPPORTED;
+  if (T == 0) return DSA_OK;
+  if (!rows || !cache) return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(rows) || !aligned16(cache)) return DSA_ERR_ALIGNMENT;
+  return run_q4_write_back(static_cast<cudaStream_t>(stream), rows, src_stride, cache, seq_lens, cu_q_lens, cu_kv_lens,
+                           page_indices, T, S, P, PTW, ps, dev_status);
+}
+
+int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, int ps, const int32_t* slots, int N,
+                     uint16_t* rows, int dst_stride, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_q4_read_rows");
+  if (P < 0 || N < 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (!ps_supported(ps) || (long long)P * ps >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  if (dst_stride < 576 || dst_stride % 8) return DSA_ERR_UNSUPPORTED;
+  if (N == 0) return DSA_OK;
+  if ((P > 0 && !cache) || !slots || !rows) return DSA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(cache) || !aligned16(rows)) return DSA_ERR_ALIGNMENT;
+  return run_q4_read_rows(static_cast<cudaStream_t>(stream), cache, (long long)P * ps, slots, N, rows, dst_stride,
+                          dev_status);
 }
 
 // No-allocation variant of dsa_sparse_mla_decode: the same checks and split

@@ -11,6 +11,7 @@ enum : int { kModeToken = 0, kModePage = 1, kModeQblock = 2, kModeDense = 3 };
 struct AttendParams {
   const uint16_t* q;   // bf16 [T, H, 576]
   const uint16_t* kv;  // bf16 [P, ps, row_stride]
+  const uint8_t* kv4;  // or the 4-bit cache [P, ps, kRow4Bytes] (token and page modes), else null
   int row_stride;
   const int32_t* seq_lens;
   const int32_t* cu_q_lens;
@@ -26,6 +27,7 @@ struct AttendParams {
   const int32_t* counts;
   int QB, u_max;
   int window;           // dense mode: keep the `window` most recent positions (0 = all)
+  int sinks;            // dense mode with a window: and the first `sinks` ones
   int soft_cap_on;      // logits l -> cap * tanh(l / cap) before the softmax
   float inv_cap_scale;  // sm_scale / cap
   float cap_log2;       // cap * log2(e)

@@ -1,0 +1,204 @@
+// A serving step's metadata from its requests' lengths: cumulative offsets,
+// the packed page table, block-table growth from a free list, and per query
+// token its request, position and cache slot.
+//
+// With q = q_lens[s], n = seq_lens[s], had = ceil((n - q) / ps) and
+// need = ceil(n / ps):
+//   cu_q_lens[s] = sum_{r<s} q_r        cu_kv_lens[s] = ps * sum_{r<s} need_r
+//   block_table[s][had + i] = free_pages[sum_{r<s} (need_r - had_r) + i]
+//   page_indices[cu_kv_lens[s] / ps + j] = block_table[s][j],  j < need
+//   token t = cu_q_lens[s] + i:  pos = n - q + i,
+//   slot = block_table[s][pos / ps] * ps + pos % ps
+//
+// One launch. Every CTA scans all S lengths by itself (three sums at once,
+// 64-bit, into shared memory), so no CTA waits for another; then the CTAs
+// share the tokens and the page entries, each found by a binary search of
+// the sums. A page taken from the free list is read from there, never from
+// the block table, whose new entries other CTAs may still be writing. What
+// bounds it is latency: the launch, one round trip for the lengths, the scan,
+// one for the pages.
+#include <climits>
+
+#include "common.cuh"
+#include "steps.cuh"
+
+namespace dsa {
+
+namespace {
+constexpr int kTbThreads = 512;
+constexpr int kTbWarps = kTbThreads / 32;
+constexpr int kEntriesPerThread = 4;  // page entries a thread resolves with one search
+
+struct Sums {
+  long long q, need, grow;
+};
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.q + b.q, a.need + b.need, a.grow + b.grow}; }
+__device__ __forceinline__ Sums shfl_up(Sums a, int d) {
+  return {__shfl_up_sync(0xffffffffu, a.q, d), __shfl_up_sync(0xffffffffu, a.need, d),
+          __shfl_up_sync(0xffffffffu, a.grow, d)};
+}
+__device__ __forceinline__ int sat(long long x, int top) { return x < top ? (int)x : top; }
+
+// Lengths of request s; one that cannot be right counts as empty.
+__device__ __forceinline__ bool lens_of(const TablesParams& p, int s, int& q, int& n) {
+  q = __ldg(p.q_lens + s);
+  n = __ldg(p.seq_lens + s);
+  const bool ok = q >= 0 && n >= q && n <= p.width * (long long)p.ps;
+  if (!ok) q = n = 0;
+  return ok;
+}
+
+// largest s with a[s] <= x, a[0] == 0 and x < a[S] (skips empty requests)
+__device__ __forceinline__ int find(const int* a, int S, int x) {
+  int lo = 0, hi = S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  extern __shared__ int sums[];  // cumulative tokens, pages and taken pages, S + 1 each
+  __shared__ Sums s_warp[kTbWarps];
+  int* cq = sums;
+  int* cp = cq + p.S + 1;
+  int* cg = cp + p.S + 1;
+  const int tid = threadIdx.x, lane = lane_id(), w = warp_id();
+  const int lg = 31 - __clz(p.ps), top_pages = INT_MAX >> lg;
+  // each thread sums a contiguous run of requests
+  const int per = (p.S + kTbThreads - 1) / kTbThreads;
+  const int s0 = min(p.S, tid * per), s1 = min(p.S, s0 + per);
+  Sums mine = {0, 0, 0};
+  bool bad = false;
+  for (int s = s0; s < s1; ++s) {
+    int q, n;
+    bad |= !lens_of(p, s, q, n);
+    const int need = (int)(((long long)n + p.ps - 1) >> lg), had = (int)(((long long)n - q + p.ps - 1) >> lg);
+    mine = mine + Sums{q, need, need - had};
+  }
+  Sums x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Sums y = shfl_up(x, d);
+    if (lane >= d) x = x + y;
+  }
+  if (lane == 31) s_warp[w] = x;
+  __syncthreads();
+  Sums run = {x.q - mine.q, x.need - mine.need, x.grow - mine.grow}, all = {0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kTbWarps; ++i) {
+    if (i < w) run = run + s_warp[i];
+    all = all + s_warp[i];
+  }
+  for (int s = s0; s < s1; ++s) {
+    int q, n;
+    lens_of(p, s, q, n);
+    const int need = (int)(((long long)n + p.ps - 1) >> lg), had = (int)(((long long)n - q + p.ps - 1) >> lg);
+    cq[s] = sat(run.q, INT_MAX);
+    cp[s] = sat(run.need, top_pages);
+    cg[s] = sat(run.grow, INT_MAX);
+    run = run + Sums{q, need, need - had};
+  }
+  if (tid == 0) {
+    cq[p.S] = sat(all.q, INT_MAX);
+    cp[p.S] = sat(all.need, top_pages);
+    cg[p.S] = sat(all.grow, INT_MAX);
+  }
+  __syncthreads();
+  const int total_q = cq[p.S], total_p = cp[p.S];
+  if (blockIdx.x == 0) {
+    for (int s = tid; s <= p.S; s += kTbThreads) {
+      p.cu_q_lens[s] = cq[s];
+      p.cu_kv_lens[s] = cp[s] << lg;
+    }
+    if (tid == 0) {
+      *p.n_taken = cg[p.S];
+      if (all.q > p.T || all.need > p.PTW) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
+      if (all.grow > p.F) set_status(p.dev_status, DSA_STATUS_NO_PAGES);
+    }
+    if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
+  }
+  auto taken = [&](int s, int i) {  // page i of those that request s takes
+    const long long k = (long long)cg[s] + i;
+    return k < p.F ? __ldg(p.free_pages + k) : -1;
+  };
+
+  const int step = gridDim.x * kTbThreads, first = blockIdx.x * kTbThreads + tid;
+  // tokens
+  for (int t = first; t < p.T; t += step) {
+    int s = -1, pos = -1, slot = -1;
+    if (t < total_q) {
+      s = find(cq, p.S, t);
+      int q, n;
+      lens_of(p, s, q, n);
+      pos = n - q + (t - cq[s]);
+      const int j = pos >> lg, had = (int)(((long long)n - q + p.ps - 1) >> lg);
+      const int pg = j < had ? p.block_table[(size_t)s * p.bt_stride + j] : taken(s, j - had);
+      if (pg >= 0 && pg <= (INT_MAX >> lg) - 1) slot = (pg << lg) + (pos & (p.ps - 1));
+    }
+    p.token_seq[t] = s;
+    p.positions[t] = pos;
+    p.slots[t] = slot;
+  }
+  // page-table entries, a few consecutive ones per thread
+  const int groups = (p.PTW + kEntriesPerThread - 1) / kEntriesPerThread;
+  for (int g = first; g < groups; g += step) {
+    const int e0 = g * kEntriesPerThread;
+    int out[kEntriesPerThread];
+    int s = 0, had = 0, end = 0;
+    if (e0 < total_p) {
+      s = find(cp, p.S, e0);
+      end = cp[s + 1];
+      int q, n;
+      lens_of(p, s, q, n);
+      had = (int)(((long long)n - q + p.ps - 1) >> lg);
+    }
+#pragma unroll
+    for (int i = 0; i < kEntriesPerThread; ++i) {
+      const int e = e0 + i;
+      out[i] = -1;
+      if (e < total_p && e < p.PTW) {
+        if (e >= end) {
+          do ++s; while (cp[s + 1] <= e);
+          end = cp[s + 1];
+          int q, n;
+          lens_of(p, s, q, n);
+          had = (int)(((long long)n - q + p.ps - 1) >> lg);
+        }
+        const int j = e - cp[s];
+        int32_t* bt = p.block_table + (size_t)s * p.bt_stride + j;
+        if (j < had) {
+          out[i] = *bt;
+        } else {
+          out[i] = taken(s, j - had);
+          *bt = out[i];
+        }
+      }
+    }
+    if (e0 + kEntriesPerThread <= p.PTW && p.vec_out) {
+      *reinterpret_cast<int4*>(p.page_indices + e0) = make_int4(out[0], out[1], out[2], out[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEntriesPerThread; ++i)
+        if (e0 + i < p.PTW) p.page_indices[e0 + i] = out[i];
+    }
+  }
+}
+}  // namespace
+
+static size_t tables_smem(int S) { return 3 * ((size_t)S + 1) * sizeof(int); }
+
+int run_page_tables(cudaStream_t stream, TablesParams p) {
+  p.vec_out = (reinterpret_cast<uintptr_t>(p.page_indices) & 15u) == 0;
+  const long long items = std::max<long long>(p.T, ((long long)p.PTW + kEntriesPerThread - 1) / kEntriesPerThread);
+  const int grid = (int)std::max<long long>(1, std::min<long long>(2LL * sm_count(),
+                                                                   (items + kTbThreads - 1) / kTbThreads));
+  set_smem_attr_once(reinterpret_cast<const void*>(page_tables_kernel), (int)tables_smem(kTablesMaxRequests));
+  DSA_LAUNCH_PDL(page_tables_kernel, dim3(grid), dim3(kTbThreads), tables_smem(p.S), stream, p);
+  return DSA_OK;
+}
+
+}  // namespace dsa

@@ -73,6 +73,7 @@ enum dsa_error {
 #define DSA_STATUS_BAD_INDEX 0x4       /* a selected unit or page id out of range */
 #define DSA_STATUS_TIMEOUT 0x8         /* a pipeline wait gave up (about 2 s) */
 #define DSA_STATUS_INTERNAL 0x10       /* a launch-time invariant failed on the device */
+#define DSA_STATUS_NO_PAGES 0x20       /* the free list holds fewer pages than a step takes */
 
 /* ------------------------------------------------------------------------
  * IndexShare layer -> slot map (host only).
@@ -357,6 +358,158 @@ DSA_API int dsa_paged_write_back_pair(dsa_stream_t stream, const uint16_t* rows0
 DSA_API int dsa_topk_pages_from_tokens(dsa_stream_t stream, const int32_t* topk, int T, int K, int ps,
                                        int max_pages, int cap, int32_t* pages, int32_t* counts,
                                        int32_t* dev_status);
+
+/* ------------------------------------------------------------------------
+ * A step's page tables from its requests' lengths (the ragged metadata that
+ * every other call reads, which the pages' backend assembles on the host;
+ * dsa_sparse_backend.py, _scatter_paged and _fixed_stride_pages).
+ * Request s has q_lens[s] new tokens and seq_lens[s] positions with them. It
+ * holds its pages in a row of `block_table`; the pages that its new tokens
+ * are the first to need are taken from `free_pages` in order, request by
+ * request, and written into the row. With had = ceil((seq - q) / ps) and
+ * need = ceil(seq / ps):
+ *   q_lens, seq_lens  int32 [S]
+ *   block_table  int32 [S, bt_stride] in/out: entries [0, had) are read,
+ *                [had, need) written, no others touched; the first `width`
+ *                entries of a row may be used
+ *   free_pages   int32 [F] (may be NULL with F == 0: rows already hold every
+ *                page that a call needs when seq - q is a page multiple's end)
+ *   cu_q_lens    int32 [S+1] out   cu_kv_lens  int32 [S+1] out
+ *   page_indices int32 [PTW] out   packed rows, -1 behind the last
+ *   token_seq, positions, slots  int32 [T] out: request, absolute position
+ *                and cache slot (page * ps + row) of every token, -1 behind
+ *                the last token, so T and PTW may be upper bounds
+ *   n_taken      int32 [1] out     pages this step takes from the list
+ * cu_q_lens, cu_kv_lens and page_indices are the metadata of the other calls
+ * when T is the number of tokens. The call reads no state of its own: run
+ * again on the same inputs it writes the same values.
+ * Device conditions: a request with q < 0, seq < q or seq > width * ps counts
+ * as empty and sets DSA_STATUS_BAD_METADATA, as do more tokens than T or more
+ * pages than PTW (those past the end, and block-table entries behind them,
+ * are not written); a list that runs out sets DSA_STATUS_NO_PAGES, its
+ * missing pages and their slots are -1 and n_taken says how many it takes.
+ * Supported: ps in {32, 64, 128}, S <= 16384, width * ps < 2^31. Outputs
+ * overlap no input. Needs no workspace.
+ * ------------------------------------------------------------------------ */
+DSA_API int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int32_t* seq_lens,
+                                  int32_t* block_table, int64_t bt_stride, int width, const int32_t* free_pages,
+                                  int F, int S, int T, int PTW, int ps, int32_t* cu_q_lens, int32_t* cu_kv_lens,
+                                  int32_t* page_indices, int32_t* token_seq, int32_t* positions, int32_t* slots,
+                                  int32_t* n_taken, int32_t* dev_status);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions (no counterpart on the pages, whose queries and rows
+ * arrive rotated). Pair i of a row at position p turns by p * freqs[i]:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ * with (a, b) the elements (2i, 2i+1) (DSA_ROPE_INTERLEAVED) or
+ * (i, i + rot_dim/2) (DSA_ROPE_HALF) of columns [rot_off, rot_off + rot_dim).
+ * `inverse` != 0 turns by the negative angle: that call maps an output's
+ * gradient to the input's. Every target of a call is rotated in one launch:
+ * a layer's queries, latent rows, indexer queries and indexer keys.
+ *   x, y       [T, H, D] of `dtype` with element strides (*_stride_t,
+ *              *_stride_h, 1). y == x (same strides) works in place and
+ *              touches the rotated columns only; otherwise y receives the
+ *              other columns too and must not overlap x
+ *   positions  int32 [T]; a row with a negative position is left as it is
+ *   freqs      fp64 [rot_dim / 2], radians per position (dsa_rope_freqs)
+ * Angles are reduced in fp64; products are fp32, rounded once to `dtype`.
+ * Supported: 1 to 8 targets, even rot_dim <= 512. Any strides and alignment
+ * of whole elements; 16-byte aligned rows and columns move 16 bytes at a time.
+ * ------------------------------------------------------------------------ */
+enum dsa_dtype { DSA_DTYPE_BF16 = 0, DSA_DTYPE_F32 = 1 };
+enum dsa_rope_layout { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
+typedef struct dsa_rope_target {
+  const void* x;
+  void* y;
+  int64_t x_stride_t, x_stride_h, y_stride_t, y_stride_h;
+  int32_t H, D, rot_off;
+  int32_t layout; /* dsa_rope_layout */
+  int32_t dtype;  /* dsa_dtype */
+  float scale;
+} dsa_rope_target;
+DSA_API int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets /* host */, int n_targets, int T,
+                     int rot_dim, const int32_t* positions, const double* freqs, int inverse);
+
+/* Frequencies of the rotary pairs (host only): base^(-2i / rot_dim) radians
+ * per position, scaled for contexts beyond the trained `orig_max_pos`:
+ *   DSA_ROPE_SCALE_NONE    as they are (factor is ignored)
+ *   DSA_ROPE_SCALE_LINEAR  divided by factor (positions interpolated)
+ *   DSA_ROPE_SCALE_YARN    by parts: pairs that turn more than beta_fast
+ *       times within orig_max_pos keep their frequency, those below beta_slow
+ *       turns are divided by factor, a linear ramp over the pair index between
+ *   freqs   host fp64 [rot_dim / 2] out
+ *   mscale  host out or NULL: the factor that goes with it for the rotated
+ *           columns of queries and keys, 0.1 ln(factor) + 1 (YaRN, factor > 1)
+ *           or 1 */
+enum dsa_rope_scaling { DSA_ROPE_SCALE_NONE = 0, DSA_ROPE_SCALE_LINEAR = 1, DSA_ROPE_SCALE_YARN = 2 };
+DSA_API int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor, int orig_max_pos, double beta_fast,
+                           double beta_slow, double* freqs, double* mscale);
+
+/* ------------------------------------------------------------------------
+ * 4-bit latent cache: the rows [c_kv(512) | k_rope(64)] in 416 bytes instead
+ * of 1152 (no counterpart on the pages). A row:
+ *   bytes   0..255  512 codes e2m1. 32-bit word w holds dims 8w .. 8w+7: the
+ *                   even dims in nibbles 0..3, the odd ones in nibbles 4..7
+ *   bytes 256..287  32 scales e4m3, one per 16 dims
+ *   bytes 288..415  the 64 rotary dims as bf16, as they came
+ * Writing: scale = max|x| / 6 rounded to e4m3, code = x / scale rounded to
+ * e2m1 (both to the nearest, ties to even, saturating); the value is code *
+ * scale, exact in bf16. A group with an infinity or a NaN gets the scale NaN
+ * and zero codes and reads back as NaN,
+ * one with max|x| <= 6 * 2^-10 as zeros.
+ *
+ * dsa_q4_write_back is dsa_paged_write_back into such a cache: token t's row
+ * goes to the slot of its position, every other row is left untouched, and a
+ * token without a slot sets DSA_STATUS_BAD_METADATA and is skipped.
+ *   rows   bf16 [T, src_stride], the first 576 columns
+ *   cache  [P, ps, 416] bytes
+ * dsa_q4_read_rows writes the values of N slots (page * ps + row, as
+ * dsa_build_page_tables numbers them) as bf16 rows of 576 columns; a
+ * negative slot gives zeros, one past the cache too and sets
+ * DSA_STATUS_BAD_INDEX.
+ * Supported: strides that are multiples of 8 and at least 576, 16-byte
+ * aligned rows and cache, P * ps < 2^31. Need no workspace.
+ * ------------------------------------------------------------------------ */
+#define DSA_Q4_ROW_BYTES 416
+DSA_API int dsa_q4_write_back(dsa_stream_t stream, const uint16_t* rows, int src_stride, uint8_t* cache,
+                              const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
+                              const int32_t* page_indices, int T, int S, int P, int PTW, int ps,
+                              int32_t* dev_status);
+DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, int ps, const int32_t* slots, int N,
+                             uint16_t* rows, int dst_stride, int32_t* dev_status);
+
+/* ------------------------------------------------------------------------
+ * Sparse absorbed-MLA attention over the 4-bit latent cache: as
+ * dsa_sparse_mla_decode (token or page units, workspace, lse, empty rows,
+ * reproducibility) with `cache` [P, ps, 416] bytes in the place of kv and
+ * row_stride. Only rows of visible selected positions are read, in page units
+ * too, so unwritten rows may hold anything. Prefill tokens go through it with
+ * page units, one selection per token.
+ * Supported: as dsa_sparse_mla_decode; |sm_scale| * 185 finite in fp32.
+ * ------------------------------------------------------------------------ */
+DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8_t* cache,
+                                     const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
+                                     const int32_t* page_indices, const int32_t* sel, int K, int unit, int T, int S,
+                                     int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, uint16_t* o,
+                                     float* lse, void* ws, size_t ws_bytes, int32_t* dev_status);
+
+/* ------------------------------------------------------------------------
+ * Absorbed-MLA attention with a sliding window and sinks: dsa_dense_mla where
+ * token t sees, of the positions j < seq_len with j <= pos(t), those with
+ * j > pos(t) - sliding_window and the first num_sinks, j < num_sinks (a
+ * position that is both counts once). num_sinks == 0 is dsa_dense_mla; with
+ * sliding_window == 0 every position is visible and num_sinks changes nothing.
+ * Only pages that hold a visible position are read, in runs of 32 rows (see
+ * the finite-rows rule of dsa_sparse_mla_decode): a cache may drop the pages
+ * between the sinks and the window.
+ *   max_kv, ws  as dsa_dense_mla
+ * Supported: as dsa_dense_mla; num_sinks >= 0.
+ * ------------------------------------------------------------------------ */
+DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
+                           const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
+                           const int32_t* page_indices, int max_kv, int T, int S, int P, int PTW, int ps, int H,
+                           int Dk, int Dv, float sm_scale, int sliding_window, int num_sinks, float soft_cap,
+                           uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status);
 
 /* Self-test of failure detection; the source pages have no counterpart.
  * Every pipeline wait in these kernels is bounded: when it runs out, the CTA
