@@ -509,37 +509,56 @@ def dsa_selftest_wait_timeout(dev_status, limit_clocks=2_000_000):
 
 
 # ------------------------------------------- the steps around the attention
+# These calls are short, so what their checks cost counts: each check reads
+# every property of a tensor once, and the raw stream handle is taken without
+# building a torch.cuda.Stream (2 us of a call's 10, measured).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _launch(dev, name, *args):
     """Call a device entry point on ``dev``'s current stream (whatever device
     is current) and raise on an error code."""
     if dev.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a CUDA device, got {dev}")
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(torch.cuda.current_stream(dev).cuda_stream, *args)
+    fn = getattr(_lib or lib(), name)
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        rc = fn(_raw_stream(i) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream, *args)
     else:
         with torch.cuda.device(dev):
             rc = fn(torch.cuda.current_stream(dev).cuda_stream, *args)
-    _check(name, rc)
+    if rc:
+        raise DSAError(name, rc)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status):
-    S, PTW = _meta(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
+def _i32(t, name, dev):
+    """The address of a contiguous 1-D int32 tensor."""
+    if type(t) is torch.Tensor and t.dtype is torch.int32 and t.dim() == 1 and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, torch.int32, dev, 1)
+    return t.data_ptr()
+
+
+def _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices):
+    meta = (_i32(seq_lens, "seq_lens", dev), _i32(cu_q_lens, "cu_q_lens", dev), _i32(cu_kv_lens, "cu_kv_lens", dev),
+            _i32(page_indices, "page_indices", dev))
+    S = seq_lens.numel()
     if cu_q_lens.numel() != S + 1 or cu_kv_lens.numel() != S + 1:
         raise ValueError(f"cu_q_lens and cu_kv_lens need {S + 1} entries for {S} requests")
-    _status(dev_status, dev)
-    return S, PTW, (_addr(seq_lens), _addr(cu_q_lens), _addr(cu_kv_lens), _addr(page_indices))
+    return S, page_indices.numel(), meta
 
 
 def _status(dev_status, dev):
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32, dev, 1)
-        if dev_status.numel() < 1:
-            raise ValueError("dev_status must hold one word")
+    if dev_status is None:
+        return None
+    p = _i32(dev_status, "dev_status", dev)
+    if dev_status.numel() < 1:
+        raise ValueError("dev_status must hold one word")
+    return p
 
 
 def _shape(t, name, shape):
@@ -572,22 +591,21 @@ def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, 
     the metadata of every other call. ``out``: a :class:`PageTables` to write
     into."""
     dev = q_lens.device
-    _need(q_lens, "q_lens", torch.int32, dev, 1)
-    _need(seq_lens, "seq_lens", torch.int32, dev, 1)
+    a_q, a_seq = _i32(q_lens, "q_lens", dev), _i32(seq_lens, "seq_lens", dev)
     S = q_lens.numel()
-    _shape(seq_lens, "seq_lens", (S,))
+    if seq_lens.numel() != S:
+        raise ValueError(f"seq_lens must have {S} entries like q_lens, got {seq_lens.numel()}")
     if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise TypeError("block_table must be an int32 tensor [S, W]")
-    if block_table.device != dev or block_table.shape[0] != S:
+    rows, W = block_table.shape
+    bt_stride, one = block_table.stride()
+    if block_table.device != dev or rows != S:
         raise ValueError(f"block_table must be on {dev} with {S} rows")
-    W = block_table.shape[1]
-    if block_table.numel() and (W > 1 and block_table.stride(1) != 1 or S > 1 and block_table.stride(0) < W):
+    if S and W and (W > 1 and one != 1 or S > 1 and bt_stride < W):
         raise ValueError("block_table rows must be contiguous and must not overlap")
-    F = 0
+    F, a_free = 0, None
     if free_pages is not None:
-        _need(free_pages, "free_pages", torch.int32, dev, 1)
-        F = free_pages.numel()
-    _status(dev_status, dev)
+        F, a_free = free_pages.numel(), _i32(free_pages, "free_pages", dev)
     T, PTW = int(T), int(PTW)
     if T < 0 or PTW < 0:
         raise ValueError("T and PTW must not be negative")
@@ -601,10 +619,10 @@ def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, 
                         ("positions", T), ("slots", T), ("n_taken", 1)):
             _need(getattr(out, name), f"out.{name}", torch.int32, dev, 1)
             _shape(getattr(out, name), f"out.{name}", (n,))
-    _launch(dev, "dsa_build_page_tables", _addr(q_lens), _addr(seq_lens), _addr(block_table),
-            max(W, block_table.stride(0)) if S > 1 else W, W, _addr(free_pages), F, S, T, PTW, int(ps),
-            _addr(out.cu_q_lens), _addr(out.cu_kv_lens), _addr(out.page_indices), _addr(out.token_seq),
-            _addr(out.positions), _addr(out.slots), _addr(out.n_taken), _addr(dev_status))
+    cu_q, cu_kv, pages, seq, pos, slots, taken = out
+    _launch(dev, "dsa_build_page_tables", a_q, a_seq, block_table.data_ptr(), max(W, bt_stride) if S > 1 else W, W,
+            a_free, F, S, T, PTW, int(ps), cu_q.data_ptr(), cu_kv.data_ptr(), pages.data_ptr(), seq.data_ptr(),
+            pos.data_ptr(), slots.data_ptr(), taken.data_ptr(), _status(dev_status, dev))
     return out
 
 
@@ -626,20 +644,23 @@ class RopeTarget:
     def __init__(self, x, y=None, *, rot_off=0, rot_dim=None, layout="half", scale=1.0):
         if y is None:
             y = x
-        for name, t in (("x", x), ("y", y)):
-            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype not in _ROPE_DTYPES:
-                raise TypeError(f"{name} must be a bf16 or fp32 tensor [T, H, D]")
-            if t.shape[2] > 1 and t.stride(2) != 1:
-                raise ValueError(f"the columns of {name} must be contiguous")
-        if y.dtype != x.dtype or y.device != x.device or y.shape != x.shape:
+        if not isinstance(x, torch.Tensor) or not isinstance(y, torch.Tensor) or x.dim() != 3:
+            raise TypeError("x and y must be tensors [T, H, D]")
+        dtype, shape, lay = _ROPE_DTYPES.get(x.dtype), x.shape, _ROPE_LAYOUTS.get(layout)
+        if dtype is None:
+            raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
+        if y is not x and (y.dtype is not x.dtype or y.shape != shape or y.device != x.device):
             raise ValueError("y must have the type, device and shape of x")
-        if layout not in _ROPE_LAYOUTS:
+        if lay is None:
             raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
-        T, H, D = x.shape
+        _, H, D = shape
+        xt, xh, xd = x.stride()
+        yt, yh, yd = y.stride()
+        if D > 1 and (xd != 1 or yd != 1):
+            raise ValueError("the columns of x and y must be contiguous")
         self.x, self.y = x, y
-        self.rot_dim = D - rot_off if rot_dim is None else int(rot_dim)
-        self.c = _RopeTargetC(x.data_ptr(), y.data_ptr(), x.stride(0), x.stride(1), y.stride(0), y.stride(1), H, D,
-                              rot_off, _ROPE_LAYOUTS[layout], _ROPE_DTYPES[x.dtype], scale)
+        self.rot_dim = D - rot_off if rot_dim is None else rot_dim
+        self.c = _RopeTargetC(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, H, D, rot_off, lay, dtype, scale)
 
 
 def dsa_rope(targets, positions, freqs, *, inverse=False):
@@ -651,7 +672,7 @@ def dsa_rope(targets, positions, freqs, *, inverse=False):
     one = isinstance(targets, RopeTarget)
     ts = [targets] if one else list(targets)
     dev = positions.device
-    _need(positions, "positions", torch.int32, dev, 1)
+    a_pos = _i32(positions, "positions", dev)
     _need(freqs, "freqs", torch.float64, dev, 1)
     T, rot = positions.numel(), 2 * freqs.numel()
     for g in ts:
@@ -660,7 +681,7 @@ def dsa_rope(targets, positions, freqs, *, inverse=False):
         if g.rot_dim != rot:
             raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
     arr = (_RopeTargetC * len(ts))(*[g.c for g in ts])
-    _launch(dev, "dsa_rope", arr, len(ts), T, rot, _addr(positions), _addr(freqs), 1 if inverse else 0)
+    _launch(dev, "dsa_rope", arr, len(ts), T, rot, a_pos, freqs.data_ptr(), 1 if inverse else 0)
     return ts[0].y if one else [g.y for g in ts]
 
 
@@ -684,16 +705,19 @@ def _rows576(t, name, dev):
         raise TypeError(f"{name} must be a bf16 tensor [N, W]")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.shape[1] < 576 or t.stride(1) != 1:
+    n, w = t.shape
+    stride, one = t.stride()
+    if w < 576 or one != 1:
         raise ValueError(f"{name} needs at least 576 contiguous columns")
-    return t.stride(0) if t.shape[0] > 1 else max(576, t.shape[1] // 8 * 8)
+    return n, stride if n > 1 else 576
 
 
 def _cache4(cache, dev):
     _need(cache, "cache", torch.uint8, dev, 3)
-    if cache.shape[2] != Q4_ROW_BYTES:
+    P, ps, row = cache.shape
+    if row != Q4_ROW_BYTES:
         raise ValueError(f"a 4-bit cache is [P, ps, {Q4_ROW_BYTES}], got {tuple(cache.shape)}")
-    return cache.shape[0], cache.shape[1]
+    return P, ps
 
 
 def dsa_q4_write_back(rows, cache, seq_lens, cu_q_lens, cu_kv_lens, page_indices, *, dev_status=None):
@@ -701,10 +725,10 @@ def dsa_q4_write_back(rows, cache, seq_lens, cu_q_lens, cu_kv_lens, page_indices
     slot of the 4-bit ``cache`` [P, ps, 416] (uint8), in place."""
     dev = cache.device
     P, ps = _cache4(cache, dev)
-    stride = _rows576(rows, "rows", dev)
-    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status)
-    _launch(dev, "dsa_q4_write_back", _addr(rows), stride, _addr(cache), *meta, rows.shape[0], S, P, PTW, ps,
-            _addr(dev_status))
+    T, stride = _rows576(rows, "rows", dev)
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
+    _launch(dev, "dsa_q4_write_back", rows.data_ptr(), stride, cache.data_ptr(), *meta, T, S, P, PTW, ps,
+            _status(dev_status, dev))
     return cache
 
 
@@ -713,15 +737,15 @@ def dsa_q4_read_rows(cache, slots, *, out=None, dev_status=None):
     4-bit cache; a negative slot gives zeros."""
     dev = cache.device
     P, ps = _cache4(cache, dev)
-    _need(slots, "slots", torch.int32, dev, 1)
-    _status(dev_status, dev)
+    a_slots = _i32(slots, "slots", dev)
     N = slots.numel()
     if out is None:
         out = torch.empty((N, 576), dtype=torch.bfloat16, device=dev)
-    stride = _rows576(out, "out", dev)
-    if out.shape[0] != N:
+    rows, stride = _rows576(out, "out", dev)
+    if rows != N:
         raise ValueError(f"out needs {N} rows")
-    _launch(dev, "dsa_q4_read_rows", _addr(cache), P, ps, _addr(slots), N, _addr(out), stride, _addr(dev_status))
+    _launch(dev, "dsa_q4_read_rows", cache.data_ptr(), P, ps, a_slots, N, out.data_ptr(), stride,
+            _status(dev_status, dev))
     return out
 
 
@@ -752,12 +776,12 @@ def dsa_sparse_mla_decode_q4(q, cache, seq_lens, cu_q_lens, cu_kv_lens, page_ind
     P, ps = _cache4(cache, dev)
     _need(sel, "sel", torch.int32, dev, 2)
     T, H, Dk = q.shape
-    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status)
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
     K = sel.shape[1]
     _shape(sel, "sel", (T, K))
     o, lse, ws = _attend_out(dev, T, H, Dv, o, lse, want_lse, ws)
     _launch(dev, "dsa_sparse_mla_decode_q4", _addr(q), _addr(cache), *meta, _addr(sel), K, int(unit), T, S, P, PTW, ps,
-            H, Dk, Dv, float(sm_scale), _addr(o), _addr(lse), _addr(ws), ws.numel(), _addr(dev_status))
+            H, Dk, Dv, float(sm_scale), _addr(o), _addr(lse), _addr(ws), ws.numel(), _status(dev_status, dev))
     return (o, lse) if lse is not None else o
 
 
@@ -770,9 +794,9 @@ def dsa_window_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, *, max_
     _need(kv, "kv", torch.bfloat16, dev, 3)
     T, H, Dk = q.shape
     P, ps, row_stride = kv.shape
-    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices, dev_status)
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
     o, lse, ws = _attend_out(dev, T, H, Dv, o, lse, want_lse, ws)
     _launch(dev, "dsa_window_mla", _addr(q), _addr(kv), row_stride, *meta, int(max_kv), T, S, P, PTW, ps, H, Dk, Dv,
             float(sm_scale), int(sliding_window), int(num_sinks), float(soft_cap), _addr(o), _addr(lse), _addr(ws),
-            ws.numel(), _addr(dev_status))
+            ws.numel(), _status(dev_status, dev))
     return (o, lse) if lse is not None else o
