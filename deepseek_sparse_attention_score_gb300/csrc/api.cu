@@ -429,6 +429,7 @@ static int dense_common(cudaStream_t stream, const uint16_t* q, const uint16_t* 
   prm.o = o;
   prm.lse = lse;
   prm.dev_status = dev_status;
+  if (prm.sinks) return run_attend_cache(stream, prm);
   int z = attend_num_splits(T, H, prm.K, prm.mode);
   if (z > 1 && (!ws || ws_bytes < attend_workspace_bytes(T, H, z) || !aligned16(ws))) z = 1;
   prm.nsplit = z;
@@ -490,10 +491,7 @@ int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8
   prm.o = o;
   prm.lse = lse;
   prm.dev_status = dev_status;
-  int z = attend_num_splits(T, H, K, prm.mode);
-  if (z > 1 && (!ws || ws_bytes < attend_workspace_bytes(T, H, z) || !aligned16(ws))) z = 1;
-  prm.nsplit = z;
-  return run_attend(static_cast<cudaStream_t>(stream), prm, ws, ws_bytes);
+  return run_attend_cache(static_cast<cudaStream_t>(stream), prm);
 }
 
 int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int32_t* seq_lens, int32_t* block_table,

@@ -32,8 +32,7 @@
 
 #include "common.cuh"
 #include "attend.cuh"
-#include "q4.cuh"
-#include "steps.cuh"
+#include "tilegen.cuh"
 
 namespace dsa {
 
@@ -46,15 +45,6 @@ namespace {
 // 8: query-block prefill 6.50 ms with six, 6.35 with four).
 constexpr int kCopyWarpsToken = 10;
 constexpr int kCopyWarpsRuns = 4;
-// The 4-bit cache's rows pass through registers: eight warps, each with eight
-// keys of a tile.
-constexpr int kCopyWarps4 = 8;
-constexpr int kKeysPerWarp4 = 8;
-static_assert(kCopyWarps4 * kKeysPerWarp4 == 64, "a tile's keys");
-// What a kernel instantiation reads: the bf16 cache, the same with a window
-// and sinks (dense mode), or the 4-bit cache (token and page modes).
-enum : int { kCacheBf16 = 0, kCacheBf16Window = 1, kCache4Bit = 2 };
-constexpr int kSubKeys = 32;   // keys resolved / copied per generator step
 constexpr int kTileKeys = 64;  // keys per MMA tile (two generator steps)
 // generator steps buffered ahead of the gather: token mode keeps 32 physical
 // rows per step, the page-run modes only a step's first row, so their ring
@@ -89,9 +79,7 @@ struct RingLayout {
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 template <int kCopyW>
-constexpr bool kRowsInRing = kCopyW != kCopyWarpsRuns;
-template <int kCopyW>
-using LayoutOf = RingLayout<kRowsInRing<kCopyW> ? kRingToken : kRingRuns, kRowsInRing<kCopyW>>;
+using LayoutOf = RingLayout<kCopyW == kCopyWarpsToken ? kRingToken : kRingRuns, kCopyW == kCopyWarpsToken>;
 static_assert(OFF_KST % 1024 == 0 && OFF_VST % 1024 == 0, "swizzle atoms need 1 KB alignment");
 constexpr uint32_t kIdescQK = make_idesc_bf16(128, kTileKeys, false, false);
 constexpr uint32_t kIdescPV = make_idesc_bf16(128, kDvHalf, false, true);
@@ -112,205 +100,6 @@ static_assert(OFF_WTS + kMaxSplits * 128 * 4 <= OFF_VST, "the stage must stay cl
 __device__ __forceinline__ uint32_t full_arrivals(int copy_threads) { return 2u * (uint32_t)(copy_threads + 1); }
 
 }  // namespace
-
-// Warp-wide generator of 32-key tiles. Every lane gets the flat physical row
-// of "its" key (or -1) and the ballot of valid keys; returns false when the
-// CTA's key list is exhausted. Runs on one full warp. Loads are batched so a
-// whole window of selections (8 x 32 token entries, or 32 pages / union
-// slots) resolves to physical rows in two or three dependent global loads.
-template <int kCache>
-struct TileGen {
-  static constexpr int GB = 8;  // token windows resolved per refill
-  const AttendParams* p;
-  int mode, t, seq, pos, kv_len, n_vis, page_base;
-  int e, e1;          // token / page modes: next entry, end of this CTA's range
-  int win;            // page / qblock: start of the next 32-window
-  // token mode: buffered tiles
-  int buf_row[GB];
-  uint32_t buf_mask[GB];
-  uint32_t buf_pend;  // windows of the buffer with keys, not returned yet
-  // page / qblock modes: current window
-  uint32_t pend;      // units of the window still to visit
-  int w_key0;         // this lane's unit: first key position (page) or kp base (qblock)
-  int w_phys;         // this lane's unit: physical page, -1 if none
-  int cur_key0, cur_phys, sub, cur_valid;
-  int b, qq, cnt;     // qblock
-  int ps_log2;        // the page size is a power of two
-  int key_lo;         // dense: first key position inside the window
-  int n_sink, p_skip; // dense with sinks: pages listed before the window's, pages skipped after them
-
-  __device__ void init(const AttendParams& prm, int tok, int split) {
-    p = &prm;
-    mode = prm.mode;
-    ps_log2 = 31 - __clz(prm.ps);
-    t = tok;
-    const int sq = seq_of_token_warp(prm.cu_q_lens, prm.S, tok);
-    TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, 0x3fffffff, tok,
-                             prm.dev_status, sq);
-    seq = g.seq;
-    pos = g.pos;
-    kv_len = g.kv_len;
-    n_vis = g.n_vis;
-    page_base = g.page_base;
-    buf_pend = 0;
-    pend = 0;
-    sub = 0;
-    cur_valid = 0;
-    key_lo = 0;
-    if (mode == kModeDense) {
-      // every page that holds a visible position inside the window, split
-      // evenly across the CTAs of this token
-      key_lo = prm.window > 0 ? max(0, pos - prm.window + 1) : 0;
-      int p_lo = key_lo / prm.ps, p_hi = (n_vis + prm.ps - 1) / prm.ps;
-      if constexpr (kCache == kCacheBf16Window) {
-        // the list is the sinks' pages below the window, then the window's
-        n_sink = (int)min((long long)p_lo, ((long long)prm.sinks + prm.ps - 1) / prm.ps);
-        p_skip = p_lo - n_sink;
-        p_lo = 0;
-        p_hi -= p_skip;
-      }
-      const int per = (max(0, p_hi - p_lo) + prm.nsplit - 1) / prm.nsplit;
-      e = min(p_hi, p_lo + split * per);
-      e1 = min(p_hi, e + per);
-      win = e;
-    } else if (mode == kModeQblock) {
-      b = tok / prm.QB;
-      qq = tok % prm.QB;
-      cnt = min(__ldg(prm.counts + b), prm.u_max);
-      win = 0;
-    } else {
-      int per = ((prm.K + prm.nsplit - 1) / prm.nsplit + 31) & ~31;
-      // pages are 32 keys at least: a share need not be a whole window of 32
-      if constexpr (kCache == kCache4Bit)
-        if (mode == kModePage) per = (prm.K + prm.nsplit - 1) / prm.nsplit;
-      e = split * per;
-      e1 = min(prm.K, e + per);
-      win = e;
-    }
-  }
-
-  // physical page of packed page-table entry `ent` (checked), or -1
-  __device__ __forceinline__ int page_of(int ent) const {
-    if (ent < 0 || ent >= p->PTW) {
-      set_status(p->dev_status, DSA_STATUS_BAD_INDEX);
-      return -1;
-    }
-    const int pg = __ldg(p->page_indices + ent);
-    if (pg < 0 || pg >= p->P) {
-      set_status(p->dev_status, DSA_STATUS_BAD_METADATA);
-      return -1;
-    }
-    return pg;
-  }
-
-  // base: first physical row of the tile when its 32 keys are 32 consecutive
-  // rows of one page (page and qblock modes), else -1
-  __device__ bool next(long long& row, uint32_t& mask, long long& base) {
-    const int lane = lane_id();
-    const int ps = p->ps;
-    base = -1;
-    if (mode == kModeToken) {
-      while (!buf_pend) {
-        if (e >= e1) return false;
-        int j[GB];
-#pragma unroll
-        for (int g = 0; g < GB; ++g) {
-          const int ee = e + 32 * g + lane;
-          j[g] = ee < e1 ? __ldg(p->sel + (size_t)t * p->K + ee) : -1;
-        }
-        int pg[GB];
-#pragma unroll
-        for (int g = 0; g < GB; ++g) pg[g] = (j[g] >= 0 && j[g] < n_vis) ? page_of(page_base + (j[g] >> ps_log2)) : -1;
-        // every array index below is a compile-time constant, so the buffer
-        // stays in registers
-#pragma unroll
-        for (int g = 0; g < GB; ++g) {
-          const bool v = pg[g] >= 0;
-          const uint32_t m = __ballot_sync(0xffffffffu, v);
-          buf_row[g] = v ? pg[g] * ps + (j[g] & (ps - 1)) : -1;
-          buf_mask[g] = m;
-          buf_pend |= (m ? 1u : 0u) << g;
-        }
-        e += 32 * GB;
-      }
-      const int gsel = __ffs(buf_pend) - 1;
-      buf_pend &= buf_pend - 1u;
-      int r = -1;
-      uint32_t m = 0;
-#pragma unroll
-      for (int g = 0; g < GB; ++g)
-        if (g == gsel) {
-          r = buf_row[g];
-          m = buf_mask[g];
-        }
-      row = r;
-      mask = m;
-      return true;
-    }
-    const int tiles_per_unit = ps / kSubKeys;
-    while (true) {
-      if (cur_valid && sub < tiles_per_unit) {
-        const int k0 = sub * kSubKeys + lane;
-        bool v;
-        if (mode == kModePage) {
-          v = cur_key0 + k0 < n_vis;
-        } else if (mode == kModeDense) {
-          v = cur_key0 + k0 < n_vis && cur_key0 + k0 >= key_lo;
-          if constexpr (kCache == kCacheBf16Window) v = v || (cur_key0 + k0 < n_vis && cur_key0 + k0 < p->sinks);
-        } else {
-          const int kp = cur_key0 + k0;  // kp = g*ps + r - base_tok
-          v = kp <= pos && kp < kv_len;
-        }
-        base = (long long)cur_phys * ps + sub * kSubKeys;
-        ++sub;
-        row = v ? (long long)cur_phys * ps + k0 : -1;
-        mask = __ballot_sync(0xffffffffu, v);
-        if (mask) return true;
-        continue;
-      }
-      cur_valid = 0;
-      sub = 0;
-      if (!pend) {
-        // resolve a window of 32 candidate units to physical pages
-        if (mode == kModeDense) {
-          if (win >= e1) return false;
-          int pgl = win + lane;
-          const bool in = pgl < e1;
-          if constexpr (kCache == kCacheBf16Window) pgl += pgl < n_sink ? 0 : p_skip;
-          w_phys = in ? page_of(page_base + pgl) : -1;
-          w_key0 = pgl * ps;
-        } else if (mode == kModePage) {
-          if (win >= e1) return false;
-          const int ee = win + lane;
-          const int pgl = ee < e1 ? __ldg(p->sel + (size_t)t * p->K + ee) : -1;
-          const bool v = pgl >= 0 && (long long)pgl * ps < n_vis;
-          w_phys = v ? page_of(page_base + pgl) : -1;
-          w_key0 = pgl * ps;
-        } else {
-          if (win >= cnt) return false;
-          const int u = win + lane;
-          bool has = false;
-          int g = -1;
-          if (u < cnt) {
-            const uint32_t wd = __ldg(p->member + ((size_t)b * p->u_max + u) * (p->QB / 32) + (qq >> 5));
-            g = __ldg(p->units + (size_t)b * p->u_max + u);
-            has = (wd >> (qq & 31)) & 1u;
-          }
-          w_phys = has ? page_of(g) : -1;
-          w_key0 = (g - page_base) * ps;
-        }
-        pend = __ballot_sync(0xffffffffu, w_phys >= 0);
-        win += 32;
-        continue;
-      }
-      const int bit = __ffs(pend) - 1;
-      pend &= pend - 1u;
-      cur_phys = __shfl_sync(0xffffffffu, w_phys, bit);
-      cur_key0 = __shfl_sync(0xffffffffu, w_key0, bit);
-      cur_valid = 1;
-    }
-  }
-};
 
 // The MMA issuer (one thread). Every operand descriptor is a base register
 // plus a compile-time offset, so issuing an MMA costs a couple of
@@ -398,163 +187,11 @@ __device__ __forceinline__ void mma_issuer(uint32_t tmem, uint32_t qs_addr, uint
   }
 }
 
-// Whether a softmax sum holds any weight. A sum is never negative; over the
-// 4-bit cache and with sinks a NaN sum counts, so that a NaN key shows in the
-// log-sum too (the other forms report such a row as one without keys).
-template <int kCache>
-__device__ __forceinline__ bool some_weight(float sum) {
-  return kCache == kCacheBf16 ? sum > 0.f : sum != 0.f;
-}
-
-// The copier of the 4-bit cache: warp cw brings keys 8 cw .. 8 cw + 7 of every
-// tile from global memory through registers into the swizzled bf16 column
-// blocks that the MMAs read. A lane holds word `lane` (8 dims) of the K part
-// and of the V part of each of its keys, so a key's 128 bytes are one
-// contiguous load and its eight 16-byte chunks one conflict-free 128-byte row
-// of a column block per quarter warp.
-//
-// A word's bits are shifted into place as bf16 bit patterns worth 2^-126 of
-// the codes' values, and one packed multiply by the scale times 2^119 finishes
-// them: the product with 2^126 would overflow at scales above 2 (the largest
-// is 448 < 2^9), so a tile holds the keys times 2^-7. The rotary dims are
-// multiplied to match, the softmax scales the logits back and the epilogue
-// the output; powers of two, so all exact.
-//
-// The loads of the next tile's K words are in flight while this tile's V words
-// are unpacked, and the V words' while its successor's K words are.
-template <int kRing>
-__device__ __forceinline__ void gather4(const uint8_t* __restrict__ cache, int half, int cw, const int* ring_rows,
-                                        volatile uint32_t* ring_mask, volatile uint32_t* ring_end, uint8_t* kst_s,
-                                        uint8_t* vst_s, volatile uint32_t* kst_end, volatile uint32_t* vst_mask,
-                                        volatile uint32_t* vst_end, uint64_t* kfull, uint64_t* kempty,
-                                        uint64_t* vfull, uint64_t* vempty, uint64_t* rfull, uint64_t* rempty,
-                                        volatile int* abort_flag) {
-  constexpr int N = kKeysPerWarp4;
-  const int lane = lane_id(), ctid = cw * 32 + lane;
-  const int sb = cw >> 2;                 // this warp's step of the tile
-  const int key0 = (cw & 3) * N;          // its first key in that step
-  const int kh = half ^ 1;                // the K part holds the other value half and the rotary dims
-  uint32_t kw[N], vw[N], kb[N], vb[N];    // words and scale bytes
-  uint4 rp[N / 4];                        // rotary: 16 bytes of key key0 + 4 i + lane / 8
-  int row[N];
-  // K and V words of the tile's keys; a masked key (row < 0) has zero codes
-  // and a zero scale
-  auto load_k = [&](int slot) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      row[i] = ring_rows[slot * 32 + key0 + i];
-      const uint8_t* p = cache + (size_t)max(row[i], 0) * kRow4Bytes;
-      kw[i] = row[i] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + kh * 128) + lane) : 0u;
-      kb[i] = row[i] >= 0 ? __ldg(p + kRow4Codes + kh * 16 + (lane >> 1)) : 0u;
-    }
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const int r = ring_rows[slot * 32 + key0 + 4 * i + (lane >> 3)];
-      const uint8_t* p = cache + (size_t)max(r, 0) * kRow4Bytes + kRow4Codes + kRow4Scales;
-      rp[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(p) + (lane & 7)) : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  auto load_v = [&]() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint8_t* p = cache + (size_t)max(row[i], 0) * kRow4Bytes;
-      vw[i] = row[i] >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + half * 128) + lane) : 0u;
-      vb[i] = row[i] >= 0 ? __ldg(p + kRow4Codes + half * 16 + (lane >> 1)) : 0u;
-    }
-  };
-  auto unpack = [&](uint32_t dst, uint32_t w, uint32_t sbyte, int key) {
-    const uint4 v = q4_scaled8(w, bf16x2_of(e4m3_value(sbyte) * 0x1p119f));
-    st_shared_v4(dst + (lane >> 3) * kBlk + sw128_offset(key, lane & 7), v.x, v.y, v.z, v.w);
-  };
-  // waits for both steps of tile ti; 0: gave up, 1: a tile, 2: the end
-  auto acquire = [&](int ti) -> int {
-    const int j0 = 2 * ti;
-    if (!mbar_wait(rfull + j0 % kRing, (j0 / kRing) & 1, abort_flag)) return 0;
-    if (ring_end[j0 % kRing]) return 2;
-    if (!mbar_wait(rfull + (j0 + 1) % kRing, ((j0 + 1) / kRing) & 1, abort_flag)) return 0;
-    return 1;
-  };
-  uint32_t m0 = 0, m1 = 0;
-  auto release = [&](int ti) {
-    m0 = ring_mask[2 * ti % kRing];
-    m1 = ring_mask[(2 * ti + 1) % kRing];
-    mbar_arrive(rempty + 2 * ti % kRing);
-    mbar_arrive(rempty + (2 * ti + 1) % kRing);
-  };
-  int have = acquire(0);
-  if (have == 1) {
-    load_k((sb) % kRing);
-    load_v();
-    release(0);
-  }
-  for (int ti = 0; have; ++ti) {
-    const int ks = ti % kKStages, vs = ti % kVStages;
-    if (!mbar_wait(kempty + ks, ((ti / kKStages) & 1) ^ 1, abort_flag)) break;
-    if (have == 2) {
-      // the end marker stands for a whole tile: all of its arrivals
-      if (!mbar_wait(vempty + vs, ((ti / kVStages) & 1) ^ 1, abort_flag)) break;
-      if (ctid == 0) {
-        kst_end[ks] = 1u;
-        vst_end[vs] = 1u;
-        mbar_arrive(kfull + ks);
-        mbar_arrive(vfull + vs);
-        mbar_arrive(kfull + ks);
-        mbar_arrive(vfull + vs);
-      }
-      mbar_arrive(kfull + ks);
-      mbar_arrive(vfull + vs);
-      mbar_arrive(kfull + ks);
-      mbar_arrive(vfull + vs);
-      break;
-    }
-    // ---- K part: four blocks of codes, one of rotary dims
-    const uint32_t kd = smem_u32(kst_s + ks * kKStageBytes) + sb * (kSubKeys * 128);
-#pragma unroll
-    for (int i = 0; i < N; ++i) unpack(kd, kw[i], kb[i], key0 + i);
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      constexpr uint32_t k2m7 = 0x3c003c00u;  // 2^-7 in both halves
-      st_shared_v4(kd + 4 * kBlk + sw128_offset(key0 + 4 * i + (lane >> 3), lane & 7), mul_bf16x2(rp[i].x, k2m7),
-                   mul_bf16x2(rp[i].y, k2m7), mul_bf16x2(rp[i].z, k2m7), mul_bf16x2(rp[i].w, k2m7));
-    }
-    fence_proxy_async_smem();
-    if (ctid == 0) {
-      kst_end[ks] = 0u;
-      mbar_arrive(kfull + ks);
-      mbar_arrive(kfull + ks);
-    }
-    mbar_arrive(kfull + ks);
-    mbar_arrive(kfull + ks);
-    const uint32_t cur0 = m0, cur1 = m1;
-    have = acquire(ti + 1);
-    if (have == 1) load_k((2 * (ti + 1) + sb) % kRing);
-    // ---- V part
-    if (!mbar_wait(vempty + vs, ((ti / kVStages) & 1) ^ 1, abort_flag)) break;
-    const uint32_t vd = smem_u32(vst_s + vs * kVStageBytes) + sb * (kSubKeys * 128);
-#pragma unroll
-    for (int i = 0; i < N; ++i) unpack(vd, vw[i], vb[i], key0 + i);
-    fence_proxy_async_smem();
-    if (ctid == 0) {
-      vst_mask[2 * vs] = cur0;
-      vst_mask[2 * vs + 1] = cur1;
-      vst_end[vs] = 0u;
-      mbar_arrive(vfull + vs);
-      mbar_arrive(vfull + vs);
-    }
-    mbar_arrive(vfull + vs);
-    mbar_arrive(vfull + vs);
-    if (have == 1) {
-      load_v();
-      release(ti + 1);
-    }
-  }
-}
-
 // kSoftCap: the logit cap of the dense fallback, a separate instantiation
 // so that the common path carries none of its code
-// kCopyW: copier warps (kCopyWarpsToken, kCopyWarpsRuns or kCopyWarps4); the
-// block has (6 + kCopyW) warps
-template <bool kSoftCap, int kCopyW, int kCache>
+// kCopyW: copier warps (kCopyWarpsToken or kCopyWarpsRuns); the block has
+// (6 + kCopyW) warps
+template <bool kSoftCap, int kCopyW>
 __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
     sparse_mla_kernel(const AttendParams prm, const __grid_constant__ CUtensorMap kvmap,
                       const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
@@ -574,9 +211,8 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
   uint8_t* kst_s = smem + OFF_KST;
   uint8_t* vst_s = smem + OFF_VST;
   using L = LayoutOf<kCopyW>;
-  constexpr bool kRows = kRowsInRing<kCopyW>;  // page-run steps carry only their first row
-  constexpr int kRing = kRows ? kRingToken : kRingRuns;
-  constexpr bool k4 = kCache == kCache4Bit;
+  constexpr int kRing = kCopyW == kCopyWarpsToken ? kRingToken : kRingRuns;
+  constexpr bool kRows = kCopyW == kCopyWarpsToken;  // page-run steps carry only their first row
   int* ring_rows = reinterpret_cast<int*>(smem + L::OFF_RING);
   volatile uint32_t* ring_mask = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_RINFO);
   volatile uint32_t* ring_end = ring_mask + kRing;
@@ -650,7 +286,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
   // calling TileGen::next from the generator loop alone, which halves its
   // inlined code, made the query-block prefill 60% slower; the time of this
   // kernel follows its code layout as much as its instruction count.)
-  TileGen<kCache> gen;
+  TileGen<kCacheBf16> gen;
   bool gen_more = false;
   long long gen_row = -1, gen_base = -1;
   uint32_t gen_mask = 0;
@@ -726,14 +362,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
       // decode rows come from all over HBM: start pulling this step's rows
       // into L2 now, a whole ring ahead of the gather (union pages of a query
       // block are shared by its queries and are L2-resident anyway)
-      if constexpr (k4) {
-        if (more && row >= 0) {
-          const uint8_t* rp = prm.kv4 + (size_t)row * kRow4Bytes;
-#pragma unroll
-          for (int l = 0; l < kRow4Bytes; l += 128) prefetch_l2(rp + l);
-          prefetch_l2(rp + kRow4Bytes - 1);  // a row may end in a fifth line
-        }
-      } else if (more && row >= 0 && (prm.mode == kModeToken || prm.mode == kModePage)) {
+      if (more && row >= 0 && (prm.mode == kModeToken || prm.mode == kModePage)) {
         const char* rp = reinterpret_cast<const char*>(prm.kv + (size_t)row * prm.row_stride);
 #pragma unroll
         for (int l = 0; l < kDk * 2 / 128; ++l) prefetch_l2_line(rp + l * 128);
@@ -746,11 +375,6 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
       if (!publish(row, mask, base, !more)) break;
       if (!more) break;
     }
-  } else if (k4 && (warp < 4 || warp >= 8)) {
-    // ------------------------------------------------------------ 4-bit gather
-    if constexpr (k4)
-      gather4<kRing>(prm.kv4, half, warp < 4 ? warp - 2 : warp - 6, ring_rows, ring_mask, ring_end, kst_s, vst_s,
-                     kst_end, vst_mask, vst_end, kfull, kempty, vfull, vempty, rfull, rempty, abort_flag);
   } else if (warp < 4 || warp >= 8) {
     // ------------------------------------------------------------ gather
     // Tile by tile (two generator steps): the K parts of both steps as soon
@@ -875,8 +499,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
     // ------------------------------------------------------------ softmax
     const int r = (warp & 3) * 32 + lane;  // head row == TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    // the 4-bit cache's tiles hold the keys times 2^-7 (gather4)
-    const float sl2 = k4 ? prm.scale_log2 * 128.f : prm.scale_log2;
+    const float sl2 = prm.scale_log2;
     float m_run = -INFINITY, l_run = 0.f;
     int n = 0;
     bool ok = true;
@@ -972,9 +595,8 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
     tc_fence_after();
     const int h = h0 + r;
     const bool hv = h < prm.H;
-    const bool some = some_weight<kCache>(l_run);
-    const float inv_l = some ? (k4 ? 128.f : 1.f) / l_run : 0.f;
-    const float lse_v = some ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+    const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+    const float lse_v = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
     const bool have_o = n > 0 && ok;
     // O is read back from TMEM 64 columns at a time (one wait per two loads)
     auto load_o64 = [&](int c0, uint32_t (&oa)[32], uint32_t (&ob)[32]) {
@@ -1108,19 +730,15 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
 #pragma unroll 1
         for (int z = 0; z < prm.nsplit; ++z) {
           const float lz = lse_of(z);
-          // (all splits empty: mx and every lz are -inf; a NaN lz stays one)
-          const float w = ((kCache == kCacheBf16 && mx == -INFINITY) || lz == -INFINITY)
-                              ? 0.f
-                              : exp2f((lz - mx) * 1.4426950408889634f);
+          const float w = (mx == -INFINITY || lz == -INFINITY) ? 0.f : exp2f((lz - mx) * 1.4426950408889634f);
           wts[z * 128 + tid] = w;
           tot += w;
         }
-        const bool some = some_weight<kCache>(tot);
-        const float inv = some ? 1.f / tot : 0.f;
+        const float inv = tot > 0.f ? 1.f / tot : 0.f;
 #pragma unroll 1
         for (int z = 0; z < prm.nsplit; ++z) wts[z * 128 + tid] *= inv;
         if (tid < nrows && half == 0 && prm.lse)
-          prm.lse[(size_t)t * prm.H + h0 + tid] = some ? mx + logf(tot) : -INFINITY;
+          prm.lse[(size_t)t * prm.H + h0 + tid] = tot > 0.f ? mx + logf(tot) : -INFINITY;
       }
       __syncthreads();
       // every warp merges groups of four rows; this CTA's own split is read
@@ -1223,8 +841,8 @@ int run_attend(cudaStream_t stream, AttendParams prm, void* ws, size_t ws_bytes)
                                           lse_bytes(prm.T, prm.H, prm.nsplit));
     if (cudaMemsetAsync(prm.counters, 0, (size_t)prm.T * cols * 4, stream) != cudaSuccess) return DSA_ERR_CUDA;
   }
-  CUtensorMap kvmap{}, qmap;  // kvmap: the bf16 cache; the 4-bit rows are read without one
-  if (!prm.kv4 && !encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, 32, kDk))
+  CUtensorMap kvmap, qmap;
+  if (!encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, 32, kDk))
     return DSA_ERR_CUDA;
   if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, 128, kDk)) return DSA_ERR_CUDA;
   CUtensorMap omap;  // the output [T][H][512] in boxes of 64 columns x 32 head rows
@@ -1232,19 +850,16 @@ int run_attend(cudaStream_t stream, AttendParams prm, void* ws, size_t ws_bytes)
   dim3 grid(cols, prm.tn > 0 ? prm.tn : prm.T, prm.nsplit);
   void (*kern)(AttendParams, CUtensorMap, CUtensorMap, CUtensorMap);
   int threads, smem_bytes;
-  if (prm.kv4) {  // token and page modes
-    kern = sparse_mla_kernel<false, kCopyWarps4, kCache4Bit>;
-    threads = (6 + kCopyWarps4) * 32;
-    smem_bytes = LayoutOf<kCopyWarps4>::SMEM;
+  if (prm.soft_cap_on) {  // dense mode only: page runs
+    kern = sparse_mla_kernel<true, kCopyWarpsRuns>;
+    threads = (6 + kCopyWarpsRuns) * 32;
+    smem_bytes = LayoutOf<kCopyWarpsRuns>::SMEM;
   } else if (prm.mode == kModeToken) {
-    kern = sparse_mla_kernel<false, kCopyWarpsToken, kCacheBf16>;
+    kern = sparse_mla_kernel<false, kCopyWarpsToken>;
     threads = (6 + kCopyWarpsToken) * 32;
     smem_bytes = LayoutOf<kCopyWarpsToken>::SMEM;
-  } else {  // page runs; the logit cap and the sinks: dense mode only
-    kern = prm.sinks > 0 ? (prm.soft_cap_on ? sparse_mla_kernel<true, kCopyWarpsRuns, kCacheBf16Window>
-                                            : sparse_mla_kernel<false, kCopyWarpsRuns, kCacheBf16Window>)
-                         : (prm.soft_cap_on ? sparse_mla_kernel<true, kCopyWarpsRuns, kCacheBf16>
-                                            : sparse_mla_kernel<false, kCopyWarpsRuns, kCacheBf16>);
+  } else {
+    kern = sparse_mla_kernel<false, kCopyWarpsRuns>;
     threads = (6 + kCopyWarpsRuns) * 32;
     smem_bytes = LayoutOf<kCopyWarpsRuns>::SMEM;
   }

@@ -11,7 +11,6 @@ enum : int { kModeToken = 0, kModePage = 1, kModeQblock = 2, kModeDense = 3 };
 struct AttendParams {
   const uint16_t* q;   // bf16 [T, H, 576]
   const uint16_t* kv;  // bf16 [P, ps, row_stride]
-  const uint8_t* kv4;  // or the 4-bit cache [P, ps, kRow4Bytes] (token and page modes), else null
   int row_stride;
   const int32_t* seq_lens;
   const int32_t* cu_q_lens;
@@ -27,7 +26,6 @@ struct AttendParams {
   const int32_t* counts;
   int QB, u_max;
   int window;           // dense mode: keep the `window` most recent positions (0 = all)
-  int sinks;            // dense mode with a window: and the first `sinks` ones
   int soft_cap_on;      // logits l -> cap * tanh(l / cap) before the softmax
   float inv_cap_scale;  // sm_scale / cap
   float cap_log2;       // cap * log2(e)
@@ -40,11 +38,16 @@ struct AttendParams {
   float* lse_part;  // per-CTA lse copies (set by run_attend)
   int* counters;    // split arrival counters (set by run_attend)
   int32_t* dev_status;
+  const uint8_t* kv4;  // run_attend_cache: the 4-bit cache [P, ps, kRow4Bytes], in the place of kv
+  int sinks;           // dense mode with a window: the first `sinks` positions stay visible
 };
 
 int attend_num_splits(int T, int H, int K, int mode);
 size_t attend_workspace_bytes(int T, int H, int nsplit);
 int run_attend(cudaStream_t stream, AttendParams prm, void* ws, size_t ws_bytes);
+// Over the 4-bit cache, or with a window and sinks (attend_cache.cu); chooses
+// the splits itself and needs no workspace.
+int run_attend_cache(cudaStream_t stream, AttendParams prm);
 // Same as run_attend with the split scratch in a built-in device array.
 int run_attend_static_scratch(cudaStream_t stream, AttendParams prm);
 
