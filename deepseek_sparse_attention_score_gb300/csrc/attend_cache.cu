@@ -16,6 +16,8 @@
 // The loops are rolled. Five roles share the SM's instruction cache; with
 // attend.cu's unrolled loops it hit 60% of the time here and warps waited for
 // instructions more than for anything else, rolled it hits 96%.
+#include <type_traits>
+
 #include "attend.cuh"
 #include "common.cuh"
 #include "q4.cuh"
@@ -85,74 +87,82 @@ struct Bars {
   __device__ __forceinline__ uint64_t* fin() const { return b + 2 * kRing + 14; }            // commit while unwinding
 };
 
-// The MMA issuer (one thread). Per tile i: QK^T(i) over the K part, then over
+// The MMA issuer (one converged warp). Per tile i: QK^T(i) over the K part, then over
 // the V part, then PV(i - 1), so that the softmax of a tile runs beside the
 // next tile's QK^T.
 __device__ __forceinline__ void issue_mmas(int half, uint32_t tmem, uint32_t smem0, const Bars& br,
                                            volatile const uint32_t* ring_end, volatile int* abort_flag) {
+  const uint32_t lead = elect_one();
   const uint64_t dq = make_sdesc(smem0 + OFF_Q, 16, 1024, kSwizzle128B);
   const uint64_t dk = make_sdesc(smem0 + OFF_K, 16, 1024, kSwizzle128B);
   const uint64_t dv = make_sdesc(smem0 + OFF_V, 16, 1024, kSwizzle128B);
   const uint64_t dvn = make_sdesc(smem0 + OFF_V, kBlk, 1024, kSwizzle128B);  // MN-major: blocks kBlk apart
-  // n column blocks of keys from b against query blocks in TMEM or from a
+  // N column blocks of keys from b against the query blocks in TMEM (0-3), or
+  // in shared memory from a
   auto blocks_ts = [&](uint32_t tS, uint64_t b, uint32_t acc) {
-    uint32_t a = tmem + kColQ;
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c, a += 32, b += kBlk >> 4) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk, acc = 1u) umma_bf16_ts(tS, a + kk * 8, b + kk * 2, kIdescQK, acc);
-    }
+    for (int k = 0; k < 16; ++k, acc = 1u)
+      umma_bf16_ts_lead(lead, tS, tmem + kColQ + k * 8, b + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, kIdescQK, acc);
   };
-  auto blocks_ss = [&](uint32_t tS, uint64_t a, uint64_t b, int n, uint32_t acc) {
-#pragma unroll 1
-    for (int c = 0; c < n; ++c, a += kQBlk >> 4, b += kBlk >> 4) {
+  auto blocks_ss = [&](uint32_t tS, uint64_t a, uint64_t b, uint32_t acc, auto N) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk, acc = 1u) umma_bf16_ss(tS, a + kk * 2, b + kk * 2, kIdescQK, acc);
-    }
+    for (int k = 0; k < 4 * decltype(N)::value; ++k, acc = 1u)
+      umma_bf16_ss_lead(lead, tS, a + (k >> 2) * (kQBlk >> 4) + (k & 3) * 2, b + (k >> 2) * (kBlk >> 4) + (k & 3) * 2,
+                        kIdescQK, acc);
   };
-  bool ok = mbar_wait(br.qbar(), 0, abort_flag), issued = false;
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // the same answer in every lane
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (lead) umma_commit(bar);
+    __syncwarp();
+  };
+  bool ok = wait(br.qbar(), 0), issued = false;
 #pragma unroll 1
   for (int i = 0; ok; ++i) {
     const int slot = i % kRing, st = i & 1, ph = (i >> 1) & 1;
-    if (!(ok = mbar_wait(br.rfull(slot), (i / kRing) & 1, abort_flag))) break;
-    const bool end = ring_end[slot] != 0;
-    mbar_arrive(br.rempty(slot));
+    if (!(ok = wait(br.rfull(slot), (i / kRing) & 1))) break;
+    const bool end = __any_sync(0xffffffffu, ring_end[slot] != 0);
+    if (lead) mbar_arrive(br.rempty(slot));
+    __syncwarp();
     if (!end) {
       const uint32_t tS = tmem + kColS + (uint32_t)st * kTile;
       const uint64_t kb = dk + (uint64_t)(st * (kKStage >> 4)), vb = dv + (uint64_t)(st * (kVStage >> 4));
-      if (!(ok = mbar_wait(br.full(0, st), ph, abort_flag))) break;
+      if (!(ok = wait(br.full(0, st), ph))) break;
       fence_proxy_async_smem();
       tc_fence_after();
       // value half 0: dims 256-575 are the K part, dims 0-255 the V part;
       // half 1: dims 0-255 and the rotary block, then dims 256-511
       if (half) blocks_ts(tS, kb, 0u);
-      blocks_ss(tS, dq + (uint64_t)(half ? 4 * (kQBlk >> 4) : 0), kb + (uint64_t)(half ? 4 * (kBlk >> 4) : 0),
-                half ? 1 : 5, half ? 1u : 0u);
-      umma_commit(br.empty(0, st));
+      else blocks_ss(tS, dq, kb, 0u, Four{});
+      blocks_ss(tS, dq + 4 * (kQBlk >> 4), kb + 4 * (kBlk >> 4), 1u, One{});
+      commit(br.empty(0, st));
       issued = true;
-      if (!(ok = mbar_wait(br.full(1, st), ph, abort_flag))) break;
+      if (!(ok = wait(br.full(1, st), ph))) break;
       fence_proxy_async_smem();
       tc_fence_after();
-      if (half) blocks_ss(tS, dq, vb, 4, 1u);
+      if (half) blocks_ss(tS, dq, vb, 1u, Four{});
       else blocks_ts(tS, vb, 1u);
-      umma_commit(br.sfull(st));
+      commit(br.sfull(st));
     }
     if (i > 0) {
       const int j = i - 1, sj = j & 1;
-      if (!(ok = mbar_wait(br.pfull(sj), (j >> 1) & 1, abort_flag))) break;
+      if (!(ok = wait(br.pfull(sj), (j >> 1) & 1))) break;
       tc_fence_after();
       const uint32_t tP = tmem + kColS + (uint32_t)sj * kTile;
       const uint64_t vb = dvn + (uint64_t)(sj * (kVStage >> 4));
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        umma_bf16_ts(tmem + kColO, tP + k * 8, vb + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-      umma_commit(br.empty(1, sj));
-      umma_commit(br.pvdone());
+        umma_bf16_ts_lead(lead, tmem + kColO, tP + k * 8, vb + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+      commit(br.empty(1, sj));
+      commit(br.pvdone());
     }
     if (end) break;
   }
   if (!ok && issued) {  // unwinding: no MMA may be left reading shared memory
-    umma_commit(br.fin());
+    commit(br.fin());
     mbar_wait_drain(br.fin(), 0);
   }
 }
@@ -361,7 +371,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   tc_fence_after();
 
   if (warp == 0) {
-    if (lane == 0) issue_mmas(half, tmem, smem_u32(smem), br, ring_end, abort_flag);
+    issue_mmas(half, __shfl_sync(0xffffffffu, tmem, 0), smem_u32(smem), br, ring_end, abort_flag);
   } else if (warp == 1) {
     // ---------------------------------------------------------- key generator
     bool more = true;
