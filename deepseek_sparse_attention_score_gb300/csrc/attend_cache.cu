@@ -16,6 +16,7 @@
 // The loops are rolled. Five roles share the SM's instruction cache; with
 // attend.cu's unrolled loops it hit 60% of the time here and warps waited for
 // instructions more than for anything else, rolled it hits 96%.
+#include <atomic>
 #include <type_traits>
 
 #include "attend.cuh"
@@ -653,14 +654,44 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   }
 }
 
-// Splits of a key list: a power of two, at most one CTA per SM, and not below
-// kMinSplitKeys keys each.
-constexpr int kMinSplitKeys = 32;
-int num_splits(int T, int H, long long keys) {
-  const long long ctas = 2LL * T * ((H + kHeads - 1) / kHeads);
-  int z = 1;
-  while (2 * z <= kMaxSplits && ctas * 2 * z <= sm_count() && keys / (2 * z) >= kMinSplitKeys) z *= 2;
-  return z;
+using Kernel = void (*)(AttendParams, CUtensorMap, CUtensorMap, CUtensorMap);
+
+// How many clusters of 2^lz CTAs the current device runs at once (a cluster
+// lies in one GPC, so this is less than SMs / 2^lz); asked once per device.
+int clusters_at_once(Kernel kern, bool k4, int lz) {
+  static std::atomic<int> cached[64][2][4];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cached[dev][k4][lz].load(std::memory_order_relaxed);
+  if (n) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1 << lz);
+  cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16Window>);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1 << lz;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  cached[dev][k4][lz].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+// Splits of a key list: a power of two up to eight, as long as all clusters
+// run at once and a split keeps 64 keys (128 among eight). Measured, one
+// request, z = 1 / 2 / 4 / 8: 128 keys 10.9 / 11.3 / 12.3 / 14.5 us, 256 keys
+// 15.0 / 13.1 / 12.5 / 14.7, 1024 keys 35 / 23.7 / 18.0 / 16.5; 8 requests of
+// 2048 keys 64 / 39 / 27.9 / 46.9 (16 clusters of eight are more than fit).
+int num_splits(Kernel kern, bool k4, int T, int H, long long keys) {
+  const long long clusters = 2LL * T * ((H + kHeads - 1) / kHeads);
+  int lz = 0;
+  while (lz < 3 && (keys >> (lz + 1)) >= (lz == 2 ? 128 : 64) && clusters <= clusters_at_once(kern, k4, lz + 1)) ++lz;
+  return 1 << lz;
 }
 }  // namespace
 
@@ -668,14 +699,14 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
   if (prm.T == 0 || prm.H == 0) return DSA_OK;
   if (prm.ps < kSubKeys || (prm.ps & (prm.ps - 1))) return DSA_ERR_UNSUPPORTED;  // pages: 2^n rows, n >= 5
   const bool k4 = prm.kv4 != nullptr;
-  prm.nsplit = num_splits(prm.T, prm.H, (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps));
   CUtensorMap kvmap{}, qmap, omap;  // kvmap: the bf16 cache; 4-bit rows are read without one
   if (!k4 && !encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, kSubKeys, kDk))
     return DSA_ERR_CUDA;
   if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kHeads, kDk)) return DSA_ERR_CUDA;
   if (!encode_bf16_3d(&omap, prm.o, kDv, (uint64_t)prm.H, (uint64_t)prm.T, 32)) return DSA_ERR_CUDA;
-  auto kern = k4 ? cache_mla_kernel<kCache4Bit> : cache_mla_kernel<kCacheBf16Window>;
+  const Kernel kern = k4 ? cache_mla_kernel<kCache4Bit> : cache_mla_kernel<kCacheBf16Window>;
   set_smem_attr_once(reinterpret_cast<const void*>(kern), kSmem);
+  prm.nsplit = num_splits(kern, k4, prm.T, prm.H, (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * ((prm.H + kHeads - 1) / kHeads), prm.T, prm.nsplit);
   cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16Window>);
