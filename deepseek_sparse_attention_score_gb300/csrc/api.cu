@@ -523,7 +523,7 @@ int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets,
     if ((g.layout != DSA_ROPE_INTERLEAVED && g.layout != DSA_ROPE_HALF) || !std::isfinite(g.scale))
       return DSA_ERR_INVALID_ARGUMENT;
     if (g.dtype != DSA_DTYPE_BF16 && g.dtype != DSA_DTYPE_F32) return DSA_ERR_UNSUPPORTED;
-    if ((long long)g.H * g.D >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+    if (g.H > kRopeMaxHeads || g.D > kRopeMaxColumns) return DSA_ERR_UNSUPPORTED;
     if (T == 0 || g.H == 0) continue;
     if (!g.x || !g.y) return DSA_ERR_INVALID_ARGUMENT;
     if (g.x == g.y && (g.x_stride_t != g.y_stride_t || g.x_stride_h != g.y_stride_h)) return DSA_ERR_INVALID_ARGUMENT;

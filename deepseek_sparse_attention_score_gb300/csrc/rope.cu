@@ -10,10 +10,14 @@
 // sincospi. That is a few fp64 operations per (token, pair), shared by all
 // heads of all targets through shared memory.
 //
-// What bounds it is memory: each rotated element is read and written once.
-// A CTA takes one token (of all targets) or, when there are few tokens, a
-// part of its heads, and a thread moves 16 bytes from each half of a pair
-// run; columns that only pass through (out of place) move as 16-byte copies.
+// What bounds it is memory: each rotated element is read and written once. A
+// warp takes a run of one token's units: it forms the token's cosines and
+// sines (one pair per lane and step), then moves units of two 16-byte runs,
+// the two halves of a run of pairs or two runs that only pass through, two
+// units in flight per lane. Warps share nothing, so the trigonometry of some
+// hides behind the copies of others (with one block per token and a barrier
+// between the two, 8192 tokens of the four tensors of a layer took 100 us).
+// Rows that do not lie on 16 bytes go element by element.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -22,108 +26,200 @@
 namespace dsa {
 
 namespace {
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 4;
+constexpr int kUnitsPerLane = 8;  // units a lane moves when tokens abound
 
 struct RopeTarget {
   const void* x;
   void* y;
   long long xt, xh, yt, yh;  // strides in elements
-  int H, rot_off;
+  int H, D, rot_off;
   int rot_units, units;  // per head: units that rotate, all units
-  int half, fp32, vec;   // layout, type, 16-byte path
-  int copy;              // y is not x: the other columns are copied
+  int half, fp32;        // layout, type
+  int first;             // units of the targets before
+  unsigned long long inv_units;  // ceil(2^40 / units): v * inv_units >> 40 is v / units
   float scale;
 };
 struct RopeParams {
   RopeTarget tg[kRopeMaxTargets];
-  int n, rot_dim;
+  int n, rot_dim, T;
+  int parts, chunk;  // warps per token, units per warp
   const int32_t* positions;
   const double* freqs;
   float sign;  // -1: turn back
 };
 
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T v[V];
-};
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float& d, float x) { d = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void turn1(float& a, float& b, float2 c, float scale) {
+  const float co = c.x * scale, si = c.y * scale, x = a;
+  a = x * co - b * si;
+  b = b * co + x * si;
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
-// Units u = part * threads + tid, ... of one token's row of target g. A unit
-// that rotates covers V pairs (two runs of V elements), one that copies V
-// elements.
-template <typename T, int V>
-__device__ __forceinline__ void rope_rows(const RopeTarget& g, int t, int rot_dim, const float2* cs) {
-  using P = Pack<T, V>;
-  const T* x = static_cast<const T*>(g.x) + t * g.xt;
-  T* y = static_cast<T*>(g.y) + t * g.yt;
-  const int total = g.H * g.units, step = gridDim.y * kRopeThreads;
-  for (int u = blockIdx.y * kRopeThreads + threadIdx.x; u < total; u += step) {
-    const int h = u / g.units, r = u - h * g.units;
-    const T* xr = x + h * g.xh;
-    T* yr = y + h * g.yh;
-    if (r < g.rot_units) {
-      const int i0 = r * V;  // first pair
-      const int ca = g.rot_off + (g.half ? i0 : 2 * i0), cb = ca + (g.half ? rot_dim / 2 : V);
-      const P a = *reinterpret_cast<const P*>(xr + ca), b = *reinterpret_cast<const P*>(xr + cb);
-      P oa, ob;
-      if (g.half) {
+// The pairs of two 16-byte runs, from pair 0 of cs (16-byte aligned) on:
+// halves hold a[k], b[k]; interleaved elements run on from a to b.
+__device__ __forceinline__ void rotate_bf16(uint32_t (&a)[4], uint32_t (&b)[4], bool half, float scale,
+                                            const float2* cs) {
+  const float4* c4 = reinterpret_cast<const float4*>(cs);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float2 c = cs[i0 + k];
-          const float fa = to_f(a.v[k]), fb = to_f(b.v[k]), co = c.x * g.scale, si = c.y * g.scale;
-          from_f(oa.v[k], fa * co - fb * si);
-          from_f(ob.v[k], fb * co + fa * si);
-        }
-      } else {
-        T in[2 * V], out[2 * V];
+  for (int j = 0; j < 4; ++j) {
+    if (half) {  // pairs 2j, 2j + 1
+      const float4 c = c4[j];
+      float a0 = lo_f(a[j]), a1 = hi_f(a[j]), b0 = lo_f(b[j]), b1 = hi_f(b[j]);
+      turn1(a0, b0, make_float2(c.x, c.y), scale);
+      turn1(a1, b1, make_float2(c.z, c.w), scale);
+      a[j] = pack_bf16(a0, a1);
+      b[j] = pack_bf16(b0, b1);
+    } else {  // pairs 2j, 2j + 1 of the eight: words 2j, 2j + 1 of a then b
+      const float4 c = c4[j];
+      uint32_t& w0 = j < 2 ? a[2 * j % 4] : b[2 * j % 4];
+      uint32_t& w1 = j < 2 ? a[(2 * j + 1) % 4] : b[(2 * j + 1) % 4];
+      float x0 = lo_f(w0), y0 = hi_f(w0), x1 = lo_f(w1), y1 = hi_f(w1);
+      turn1(x0, y0, make_float2(c.x, c.y), scale);
+      turn1(x1, y1, make_float2(c.z, c.w), scale);
+      w0 = pack_bf16(x0, y0);
+      w1 = pack_bf16(x1, y1);
+    }
+  }
+}
+__device__ __forceinline__ void rotate_f32(uint32_t (&a)[4], uint32_t (&b)[4], bool half, float scale,
+                                           const float2* cs) {
+  const float4* c4 = reinterpret_cast<const float4*>(cs);
 #pragma unroll
-        for (int k = 0; k < V; ++k) in[k] = a.v[k], in[V + k] = b.v[k];
+  for (int j = 0; j < 2; ++j) {  // pairs 2j, 2j + 1 of the four
+    const float4 c = c4[j];
+    uint32_t* x[4] = {&a[2 * j], &b[2 * j], &a[2 * j + 1], &b[2 * j + 1]};
+    uint32_t(&v)[4] = j ? b : a;
+    float f[4];
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float2 c = cs[i0 + k];
-          const float fa = to_f(in[2 * k]), fb = to_f(in[2 * k + 1]), co = c.x * g.scale, si = c.y * g.scale;
-          from_f(out[2 * k], fa * co - fb * si);
-          from_f(out[2 * k + 1], fb * co + fa * si);
-        }
+    for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(half ? *x[k] : v[k]);
+    turn1(f[0], f[1], make_float2(c.x, c.y), scale);
+    turn1(f[2], f[3], make_float2(c.z, c.w), scale);
 #pragma unroll
-        for (int k = 0; k < V; ++k) oa.v[k] = out[k], ob.v[k] = out[V + k];
-      }
-      *reinterpret_cast<P*>(yr + ca) = oa;
-      *reinterpret_cast<P*>(yr + cb) = ob;
-    } else {
-      int c = (r - g.rot_units) * V;  // columns before the rotated ones, then those after
-      if (c >= g.rot_off) c += rot_dim;
-      *reinterpret_cast<P*>(yr + c) = *reinterpret_cast<const P*>(xr + c);
+    for (int k = 0; k < 4; ++k) {
+      if (half) *x[k] = __float_as_uint(f[k]);
+      else v[k] = __float_as_uint(f[k]);
     }
   }
 }
 
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+// One unit of a token: where its two runs of V elements are read and written.
+// kBytes: 16, or 0 for single elements (V = 1).
+struct Unit {
+  const uint8_t* xa;
+  const uint8_t* xb;
+  uint8_t* ya;
+  uint8_t* yb;  // null: the unit has one run only
+  int target;   // -1: no unit
+  int pair0;    // first pair, -1: passes through
+};
+template <int kBytes>
+__device__ __forceinline__ Unit unit_of(const RopeParams& p, int t, int u, int end) {
+  Unit m;
+  m.target = -1;
+  if (u >= end) return m;
+  int k = 0;
+  while (k + 1 < p.n && u >= p.tg[k + 1].first) ++k;
+  const RopeTarget& g = p.tg[k];
+  const int es = g.fp32 ? 4 : 2, V = kBytes ? kBytes / es : 1;
+  const int v = u - g.first, h = (int)((unsigned)v * g.inv_units >> 40), r = v - h * g.units;
+  int ca, cb;
+  bool two = true;
+  if (r < g.rot_units) {
+    m.pair0 = r * V;
+    ca = g.rot_off + (g.half ? r * V : 2 * r * V);
+    cb = ca + (g.half ? p.rot_dim / 2 : V);
+  } else {  // runs before the rotated columns, then those after
+    m.pair0 = -1;
+    const int run = 2 * (r - g.rot_units);
+    ca = run * V;
+    cb = ca + V;
+    two = (run + 1) * V < g.D - p.rot_dim;
+    if (ca >= g.rot_off) ca += p.rot_dim;
+    if (cb >= g.rot_off) cb += p.rot_dim;
+  }
+  m.target = k;
+  const uint8_t* x = static_cast<const uint8_t*>(g.x) + (t * g.xt + h * g.xh) * es;
+  uint8_t* y = static_cast<uint8_t*>(g.y) + (t * g.yt + h * g.yh) * es;
+  m.xa = x + ca * es;
+  m.xb = two ? x + cb * es : m.xa;
+  m.ya = y + ca * es;
+  m.yb = two ? y + cb * es : nullptr;
+  return m;
+}
+
+// One pair, or two elements that pass through.
+__device__ __forceinline__ void move_elements(const Unit& m, const RopeTarget& g, const float2* cs) {
+  if (g.fp32) {
+    float a = *reinterpret_cast<const float*>(m.xa), b = *reinterpret_cast<const float*>(m.xb);
+    if (m.pair0 >= 0) turn1(a, b, cs[m.pair0], g.scale);
+    *reinterpret_cast<float*>(m.ya) = a;
+    if (m.yb) *reinterpret_cast<float*>(m.yb) = b;
+  } else {
+    __nv_bfloat16 a = *reinterpret_cast<const __nv_bfloat16*>(m.xa), b = *reinterpret_cast<const __nv_bfloat16*>(m.xb);
+    if (m.pair0 >= 0) {
+      float fa = __bfloat162float(a), fb = __bfloat162float(b);
+      turn1(fa, fb, cs[m.pair0], g.scale);
+      a = __float2bfloat16_rn(fa);
+      b = __float2bfloat16_rn(fb);
+    }
+    *reinterpret_cast<__nv_bfloat16*>(m.ya) = a;
+    if (m.yb) *reinterpret_cast<__nv_bfloat16*>(m.yb) = b;
+  }
+}
+
+template <int kBytes>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ float2 cs[kRopeMaxDim / 2];
-  const int t = blockIdx.x;
+  extern __shared__ __align__(16) float2 cs_all[];
+  const int lane = lane_id();
+  float2* cs = cs_all + warp_id() * kRopeMaxDim / 2;
+  const long long w = (long long)blockIdx.x * kRopeWarps + warp_id();
+  const int t = (int)(w / p.parts);
+  if (t >= p.T) return;
   const int pos = __ldg(p.positions + t);
   if (pos < 0) return;  // a padding row: left as it is
-  for (int i = threadIdx.x; i < p.rot_dim / 2; i += kRopeThreads) {
+  const RopeTarget& last = p.tg[p.n - 1];
+  const int begin = (int)(w % p.parts) * p.chunk, end = min(begin + p.chunk, last.first + last.H * last.units);
+  for (int i = lane; i < p.rot_dim / 2; i += 32) {
     const double turns = (double)pos * (__ldg(p.freqs + i) * 0.15915494309189533577);  // 1 / (2 pi)
     float s, c;
     sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
     cs[i] = make_float2(c, s * p.sign);
   }
-  __syncthreads();
+  __syncwarp();
 #pragma unroll 1
-  for (int k = 0; k < p.n; ++k) {
-    const RopeTarget& g = p.tg[k];
-    if (g.fp32) {
-      if (g.vec) rope_rows<float, 4>(g, t, p.rot_dim, cs);
-      else rope_rows<float, 1>(g, t, p.rot_dim, cs);
+  for (int u = begin + lane; u < end; u += 64) {
+    const Unit m[2] = {unit_of<kBytes>(p, t, u, end), unit_of<kBytes>(p, t, u + 32, end)};
+    if constexpr (kBytes == 16) {
+      uint32_t a[2][4], b[2][4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (m[k].target >= 0) {
+          *reinterpret_cast<uint4*>(a[k]) = *reinterpret_cast<const uint4*>(m[k].xa);
+          *reinterpret_cast<uint4*>(b[k]) = *reinterpret_cast<const uint4*>(m[k].xb);
+        }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (m[k].target >= 0) {
+          const RopeTarget& g = p.tg[m[k].target];
+          if (m[k].pair0 >= 0) {
+            if (g.fp32) rotate_f32(a[k], b[k], g.half, g.scale, cs + m[k].pair0);
+            else rotate_bf16(a[k], b[k], g.half, g.scale, cs + m[k].pair0);
+          }
+          *reinterpret_cast<uint4*>(m[k].ya) = *reinterpret_cast<const uint4*>(a[k]);
+          if (m[k].yb) *reinterpret_cast<uint4*>(m[k].yb) = *reinterpret_cast<const uint4*>(b[k]);
+        }
     } else {
-      if (g.vec) rope_rows<__nv_bfloat16, 8>(g, t, p.rot_dim, cs);
-      else rope_rows<__nv_bfloat16, 1>(g, t, p.rot_dim, cs);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (m[k].target >= 0) move_elements(m[k], p.tg[m[k].target], cs);
     }
   }
 }
@@ -131,35 +227,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
 int run_rope(cudaStream_t stream, const dsa_rope_target* targets, int n, int T, int rot_dim, const int32_t* positions,
              const double* freqs, bool inverse) {
+  // 16 bytes at a time where every run of every target starts and ends on 16
+  // bytes, else element by element
+  bool vec = true;
+  for (int i = 0; i < n; ++i) {
+    const dsa_rope_target& a = targets[i];
+    const int v = a.dtype == DSA_DTYPE_F32 ? 4 : 8;
+    auto mult = [&](long long k) { return k % v == 0; };
+    vec &= a.H == 0 || (mult(a.x_stride_t) && mult(a.x_stride_h) && mult(a.y_stride_t) && mult(a.y_stride_h) &&
+                        mult(a.rot_off) && mult(rot_dim / 2) && mult(a.D) &&
+                        ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y)) & 15u) == 0);
+  }
   RopeParams p{};
   long long units = 0;
   for (int i = 0; i < n; ++i) {
     const dsa_rope_target& a = targets[i];
     if (a.H == 0) continue;
-    RopeTarget& g = p.tg[p.n++];
-    g = {a.x, a.y, a.x_stride_t, a.x_stride_h, a.y_stride_t, a.y_stride_h, a.H, a.rot_off, 0, 0,
-         a.layout == DSA_ROPE_HALF, a.dtype == DSA_DTYPE_F32, 0, a.x != a.y, a.scale};
-    // 16 bytes at a time where every run of a pair and every copied run
-    // starts and ends on 16 bytes
-    const int es = g.fp32 ? 4 : 2, v = 16 / es;
-    auto mult = [&](long long k) { return k % v == 0; };
-    g.vec = mult(g.xt) && mult(g.xh) && mult(g.yt) && mult(g.yh) && mult(a.rot_off) && mult(rot_dim / 2) &&
-            mult(a.D) && ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y)) & 15u) == 0;
-    const int run = g.vec ? v : 1;
-    g.rot_units = rot_dim / 2 / run;
-    g.units = g.rot_units + (g.copy ? (a.D - rot_dim) / run : 0);
-    units += (long long)g.H * g.units;
+    const int run = !vec ? 1 : a.dtype == DSA_DTYPE_F32 ? 4 : 8;
+    const int rot_units = rot_dim / 2 / run;
+    const int copied = a.x != a.y ? ((a.D - rot_dim) / run + 1) / 2 : 0;  // in place the other columns stay
+    p.tg[p.n++] = {a.x, a.y, a.x_stride_t, a.x_stride_h, a.y_stride_t, a.y_stride_h, a.H, a.D, a.rot_off, rot_units,
+                   rot_units + copied, a.layout == DSA_ROPE_HALF, a.dtype == DSA_DTYPE_F32, (int)units,
+                   ((1ULL << 40) + rot_units + copied - 1) / (rot_units + copied), a.scale};
+    units += (long long)a.H * (rot_units + copied);
+    if (units >= (1LL << 30)) return DSA_ERR_UNSUPPORTED;
   }
   if (p.n == 0) return DSA_OK;
   p.rot_dim = rot_dim;
+  p.T = T;
   p.positions = positions;
   p.freqs = freqs;
   p.sign = inverse ? -1.f : 1.f;
-  // few tokens: several CTAs share a token's heads, until the GPU is full
-  const long long full = 4LL * sm_count();
-  const long long parts = std::min<long long>((units + kRopeThreads - 1) / kRopeThreads, (full + T - 1) / T);
-  DSA_LAUNCH_PDL(rope_kernel, dim3(T, (unsigned)std::min<long long>(std::max<long long>(parts, 1), 65535)),
-                 dim3(kRopeThreads), 0, stream, p);
+  // units per warp: eight per lane, fewer while there are fewer warps than
+  // the GPU holds (64 per SM)
+  int per_lane = kUnitsPerLane;
+  while (per_lane > 1 && (long long)T * ((units + 32 * per_lane - 1) / (32 * per_lane)) < 64LL * sm_count())
+    per_lane /= 2;
+  p.chunk = 32 * per_lane;
+  p.parts = (int)((units + p.chunk - 1) / p.chunk);
+  const long long grid = ((long long)T * p.parts + kRopeWarps - 1) / kRopeWarps;
+  if (grid >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  const size_t smem = kRopeWarps * (kRopeMaxDim / 2) * sizeof(float2);
+  if (vec)
+    DSA_LAUNCH_PDL(rope_kernel<16>, dim3((unsigned)grid), dim3(kRopeWarps * 32), smem, stream, p);
+  else
+    DSA_LAUNCH_PDL(rope_kernel<0>, dim3((unsigned)grid), dim3(kRopeWarps * 32), smem, stream, p);
   return DSA_OK;
 }
 

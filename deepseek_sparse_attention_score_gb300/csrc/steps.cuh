@@ -34,6 +34,10 @@ int run_page_tables(cudaStream_t stream, TablesParams p);
 
 constexpr int kRopeMaxTargets = 8;
 constexpr int kRopeMaxDim = 512;
+// a target's heads and columns: the kernel's division by reciprocal is exact
+// while H * (units of a head)^2 < 2^40, and a head of 4096 columns has at most
+// 2049 units
+constexpr int kRopeMaxHeads = 65536, kRopeMaxColumns = 4096;
 // Rotates every target's rows; the targets are checked by the entry point.
 int run_rope(cudaStream_t stream, const dsa_rope_target* targets, int n, int T, int rot_dim, const int32_t* positions,
              const double* freqs, bool inverse);

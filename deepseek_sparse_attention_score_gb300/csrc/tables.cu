@@ -11,7 +11,7 @@
 //   slot = block_table[s][pos / ps] * ps + pos % ps
 //
 // One launch. Every CTA scans all S lengths by itself (three sums at once,
-// 64-bit, into shared memory), so no CTA waits for another; then the CTAs
+// into shared memory), so no CTA waits for another; then the CTAs
 // share the tokens and the page entries, each found by a binary search of
 // the sums. A page taken from the free list is read from there, never from
 // the block table, whose new entries other CTAs may still be writing. What
@@ -25,19 +25,24 @@
 namespace dsa {
 
 namespace {
-constexpr int kTbThreads = 512;
+constexpr int kTbThreads = 1024;
 constexpr int kTbWarps = kTbThreads / 32;
+static_assert(kTbWarps == 32, "one warp scans the warps' sums");
 constexpr int kEntriesPerThread = 4;  // page entries a thread resolves with one search
 
+// Sums of the requests before, each stopping at INT_MAX (a sum that stops is
+// past every size that a call may have; adding that way is associative).
 struct Sums {
-  long long q, need, grow;
+  int q, need, grow;
 };
-__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.q + b.q, a.need + b.need, a.grow + b.grow}; }
+__device__ __forceinline__ int add_sat(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)INT_MAX); }
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+  return {add_sat(a.q, b.q), add_sat(a.need, b.need), add_sat(a.grow, b.grow)};
+}
 __device__ __forceinline__ Sums shfl_up(Sums a, int d) {
   return {__shfl_up_sync(0xffffffffu, a.q, d), __shfl_up_sync(0xffffffffu, a.need, d),
           __shfl_up_sync(0xffffffffu, a.grow, d)};
 }
-__device__ __forceinline__ int sat(long long x, int top) { return x < top ? (int)x : top; }
 
 // Lengths of request s; one that cannot be right counts as empty.
 __device__ __forceinline__ bool lens_of(const TablesParams& p, int s, int& q, int& n) {
@@ -47,6 +52,8 @@ __device__ __forceinline__ bool lens_of(const TablesParams& p, int s, int& q, in
   if (!ok) q = n = 0;
   return ok;
 }
+
+__device__ __forceinline__ int pages_of(int n, int ps, int lg) { return (int)(((uint32_t)n + (uint32_t)ps - 1u) >> lg); }
 
 // largest s with a[s] <= x, a[0] == 0 and x < a[S] (skips empty requests)
 __device__ __forceinline__ int find(const int* a, int S, int x) {
@@ -76,8 +83,8 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
   for (int s = s0; s < s1; ++s) {
     int q, n;
     bad |= !lens_of(p, s, q, n);
-    const int need = (int)(((long long)n + p.ps - 1) >> lg), had = (int)(((long long)n - q + p.ps - 1) >> lg);
-    mine = mine + Sums{q, need, need - had};
+    const int need = pages_of(n, p.ps, lg);
+    mine = mine + Sums{q, need, need - pages_of(n - q, p.ps, lg)};
   }
   Sums x = mine;
 #pragma unroll
@@ -86,26 +93,34 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
     if (lane >= d) x = x + y;
   }
   if (lane == 31) s_warp[w] = x;
+  Sums run = shfl_up(x, 1);
+  if (lane == 0) run = {0, 0, 0};
   __syncthreads();
-  Sums run = {x.q - mine.q, x.need - mine.need, x.grow - mine.grow}, all = {0, 0, 0};
+  if (w == 0) {  // the sums of the warps before each warp
+    Sums v = s_warp[lane];
 #pragma unroll
-  for (int i = 0; i < kTbWarps; ++i) {
-    if (i < w) run = run + s_warp[i];
-    all = all + s_warp[i];
+    for (int d = 1; d < 32; d <<= 1) {
+      const Sums y = shfl_up(v, d);
+      if (lane >= d) v = v + y;
+    }
+    s_warp[lane] = v;
   }
+  __syncthreads();
+  if (w > 0) run = s_warp[w - 1] + run;
   for (int s = s0; s < s1; ++s) {
     int q, n;
     lens_of(p, s, q, n);
-    const int need = (int)(((long long)n + p.ps - 1) >> lg), had = (int)(((long long)n - q + p.ps - 1) >> lg);
-    cq[s] = sat(run.q, INT_MAX);
-    cp[s] = sat(run.need, top_pages);
-    cg[s] = sat(run.grow, INT_MAX);
-    run = run + Sums{q, need, need - had};
+    const int need = pages_of(n, p.ps, lg);
+    cq[s] = run.q;
+    cp[s] = min(run.need, top_pages);
+    cg[s] = run.grow;
+    run = run + Sums{q, need, need - pages_of(n - q, p.ps, lg)};
   }
+  const Sums all = s_warp[kTbWarps - 1];
   if (tid == 0) {
-    cq[p.S] = sat(all.q, INT_MAX);
-    cp[p.S] = sat(all.need, top_pages);
-    cg[p.S] = sat(all.grow, INT_MAX);
+    cq[p.S] = all.q;
+    cp[p.S] = min(all.need, top_pages);
+    cg[p.S] = all.grow;
   }
   __syncthreads();
   const int total_q = cq[p.S], total_p = cp[p.S];
@@ -135,7 +150,7 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
       int q, n;
       lens_of(p, s, q, n);
       pos = n - q + (t - cq[s]);
-      const int j = pos >> lg, had = (int)(((long long)n - q + p.ps - 1) >> lg);
+      const int j = pos >> lg, had = pages_of(n - q, p.ps, lg);
       const int pg = j < had ? p.block_table[(size_t)s * p.bt_stride + j] : taken(s, j - had);
       if (pg >= 0 && pg <= (INT_MAX >> lg) - 1) slot = (pg << lg) + (pos & (p.ps - 1));
     }
@@ -154,7 +169,7 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
       end = cp[s + 1];
       int q, n;
       lens_of(p, s, q, n);
-      had = (int)(((long long)n - q + p.ps - 1) >> lg);
+      had = pages_of(n - q, p.ps, lg);
     }
 #pragma unroll
     for (int i = 0; i < kEntriesPerThread; ++i) {
@@ -166,7 +181,7 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
           end = cp[s + 1];
           int q, n;
           lens_of(p, s, q, n);
-          had = (int)(((long long)n - q + p.ps - 1) >> lg);
+          had = pages_of(n - q, p.ps, lg);
         }
         const int j = e - cp[s];
         int32_t* bt = p.block_table + (size_t)s * p.bt_stride + j;

@@ -413,7 +413,7 @@ DSA_API int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, co
  *   positions  int32 [T]; a row with a negative position is left as it is
  *   freqs      fp64 [rot_dim / 2], radians per position (dsa_rope_freqs)
  * Angles are reduced in fp64; products are fp32, rounded once to `dtype`.
- * Supported: 1 to 8 targets, even rot_dim <= 512. Any strides and alignment
+ * Supported: 1 to 8 targets, even rot_dim <= 512, H <= 65536, D <= 4096. Any strides and alignment
  * of whole elements; 16-byte aligned rows and columns move 16 bytes at a time.
  * ------------------------------------------------------------------------ */
 enum dsa_dtype { DSA_DTYPE_BF16 = 0, DSA_DTYPE_F32 = 1 };
