@@ -19,7 +19,7 @@
 namespace dsa {
 
 namespace {
-constexpr int kRowThreads = 256;  // 8 rows per CTA
+constexpr int kRowThreads = 128;  // 4 rows per CTA
 constexpr int kRowsPerCta = kRowThreads / 32;
 
 // code pair e2m1(hi) << 4 | e2m1(lo), to the nearest even, saturating

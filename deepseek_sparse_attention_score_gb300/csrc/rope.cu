@@ -27,7 +27,7 @@ namespace dsa {
 
 namespace {
 constexpr int kRopeWarps = 4;
-constexpr int kUnitsPerLane = 8;  // units a lane moves when tokens abound
+constexpr int kUnitsPerLane = 16;  // units a lane moves when tokens abound
 
 struct RopeTarget {
   const void* x;
@@ -258,7 +258,7 @@ int run_rope(cudaStream_t stream, const dsa_rope_target* targets, int n, int T, 
   p.positions = positions;
   p.freqs = freqs;
   p.sign = inverse ? -1.f : 1.f;
-  // units per warp: eight per lane, fewer while there are fewer warps than
+  // units per warp: sixteen per lane, fewer while there are fewer warps than
   // the GPU holds (64 per SM)
   int per_lane = kUnitsPerLane;
   while (per_lane > 1 && (long long)T * ((units + 32 * per_lane - 1) / (32 * per_lane)) < 64LL * sm_count())

@@ -10,6 +10,11 @@ top-k, then the block union and the query-block sparse MLA; shared layers
 (IndexShare, ref.py build_index_share_map) reuse the top-k and union tables of
 their source slot and run the attention only.
 
+A step may also start from less than finished inputs: with ``tables`` it
+builds its metadata on the GPU from the requests' lengths, with ``rope`` it
+rotates queries and keys for the positions found there, and with
+``cache_bits=4`` it keeps the latent cache in 4 bits.
+
 All buffers are allocated once up front, so a step only enqueues kernels and
 can be captured in a CUDA graph.
 """
@@ -21,11 +26,24 @@ from . import abi
 
 
 class LayerRunner:
-    def __init__(self, wl, device, page_budget=None, prefill=None):
+    def __init__(self, wl, device, page_budget=None, prefill=None, cache_bits=16, tables=False, rope=None):
         """``wl``: a dsa_inputs.Workload whose tensors already live on ``device``
         (or on the CPU; they are moved). ``page_budget``: decode page-budget
         mode with that many pages. ``prefill``: force the prefill path
-        (default: any request with more than one new token)."""
+        (default: any request with more than one new token).
+        ``cache_bits``: 16, or 4 for a 4-bit latent cache (quantised from the
+        workload's; prefill tokens then attend to their own page selections
+        through the 4-bit decode call, one by one instead of by query blocks).
+        ``tables``: build the metadata every step with dsa_build_page_tables,
+        from ``lens`` (q_lens, seq_lens), ``block_table`` and ``free_pages``.
+        ``rope``: (freqs, scale, layout), with ``tables``: the workload's
+        rotary columns (the last 64 of latent rows and queries, the first 64
+        of indexer queries and keys) are taken as not rotated yet, and every
+        step rotates its tokens'; indexer columns pair by halves."""
+        if cache_bits not in (4, 16):
+            raise ValueError(f"cache_bits must be 4 or 16, got {cache_bits}")
+        if rope is not None and not tables:
+            raise ValueError("rope needs the positions that tables=True finds")
         rg = wl.rg
         self.wl = wl
         self.dev = torch.device(device)
@@ -56,6 +74,28 @@ class LayerRunner:
         self.new_k = [c.view(-1, c.shape[-1]).index_select(0, rows).contiguous() for c in self.kcache]
         T, H = self.T, wl.H
         self.H = H
+        self.cache_bits = cache_bits
+        if cache_bits == 4:
+            self.kv4 = [self._quantised(c) for c in self.kv]
+            self.kv = None
+        self.tables = self._make_tables(rg) if tables else None
+        self.rope = None
+        if rope is not None:
+            freqs, scale, layout = rope
+            self.rope = torch.as_tensor(freqs, dtype=torch.float64).to(dev)
+            raw = lambda x, cols: x.view(T, -1, x.shape[-1])[:, :, cols].clone()
+            qk, ki = slice(512, 576), slice(0, 64)
+            turn = lambda x, cols, s, lay: abi.RopeTarget(raw(x, cols), x.view(T, -1, x.shape[-1])[:, :, cols],
+                                                          layout=lay, scale=s)
+            # layer -> what it rotates; the indexer's queries with the first layer
+            self.rope_targets = []
+            for layer in range(len(self.types)):
+                g = [turn(self.q[layer], qk, scale, layout), turn(self.new_kv[layer], qk, scale, layout)]
+                if self.full_slot[layer] >= 0:
+                    g.append(turn(self.new_k[self.full_slot[layer]], ki, 1.0, "half"))
+                if layer == 0:
+                    g.append(turn(self.q_idx, ki, 1.0, "half"))
+                self.rope_targets.append(g)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws_idx = torch.empty(max(1, abi.dsa_indexer_workspace_size(T, self.S, self.max_kv, self.ps)),
                                   dtype=torch.uint8, device=dev)
@@ -75,11 +115,61 @@ class LayerRunner:
                            for _ in range(self.num_full)]
             self.counts = [torch.empty((nqb,), dtype=torch.int32, device=dev) for _ in range(self.num_full)]
 
+    def _quantised(self, cache):
+        """The 4-bit form of a bf16 cache [P, ps, W]: every row written back
+        to where it is (one request that owns the whole pool)."""
+        P, ps = cache.shape[:2]
+        out = torch.zeros((P, ps, abi.Q4_ROW_BYTES), dtype=torch.uint8, device=self.dev)
+        i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=self.dev)
+        abi.dsa_q4_write_back(cache.view(P * ps, -1), out, i32(P * ps), i32(0, P * ps), i32(0, P * ps),
+                              torch.arange(P, dtype=torch.int32, device=self.dev))
+        return out
+
+    def _make_tables(self, rg):
+        """Inputs and outputs of dsa_build_page_tables for the workload's
+        batch: the pages that its new tokens are the first to need wait in
+        ``free_pages``, the others in ``block_table``. ``meta`` becomes the
+        outputs."""
+        had = -(-(rg.seq_lens - rg.q_lens) // self.ps)
+        need = -(-rg.seq_lens // self.ps)
+        bt = torch.full((self.S, max(1, int(need.max(initial=0)))), -1, dtype=torch.int32)
+        free = []
+        for s in range(self.S):
+            pages = rg.page_indices[rg.cu_kv_lens[s] // self.ps:][: need[s]]
+            bt[s, : had[s]] = torch.from_numpy(pages[: had[s]])
+            free.extend(pages[had[s]:].tolist())
+        self.lens = [torch.from_numpy(rg.q_lens.astype("int32")).to(self.dev), self.meta[0]]
+        self.block_table = bt.to(self.dev)
+        self.free_pages = torch.tensor(free, dtype=torch.int32, device=self.dev)
+        i32 = lambda n: torch.empty(n, dtype=torch.int32, device=self.dev)
+        out = abi.PageTables(i32(self.S + 1), i32(self.S + 1), i32(self.PTW), i32(self.T), i32(self.T), i32(self.T),
+                             i32(1))
+        self.meta = [self.meta[0], out.cu_q_lens, out.cu_kv_lens, out.page_indices]
+        return out
+
     # -- stages ---------------------------------------------------------------
+    def begin_step(self):
+        """The step's metadata from its lengths (with ``tables``)."""
+        if self.tables is not None:
+            abi.dsa_build_page_tables(*self.lens, self.block_table, self.free_pages, T=self.T, PTW=self.PTW,
+                                      ps=self.ps, out=self.tables, dev_status=self.status)
+
+    def rotate(self, layer):
+        """The layer's queries, latent rows and indexer keys at their
+        positions (with ``rope``)."""
+        if self.rope is not None:
+            abi.dsa_rope(self.rope_targets[layer], self.tables.positions, self.rope)
+
     def write_back(self, layer):
         """The layer's new latent rows, and on a full layer its new indexer
         keys, into their slots of the paged caches."""
-        if self.full_slot[layer] >= 0:  # both caches share the page table: one launch
+        if self.cache_bits == 4:
+            abi.dsa_q4_write_back(self.new_kv[layer], self.kv4[layer], *self.meta, dev_status=self.status)
+            if self.full_slot[layer] >= 0:
+                slot = self.full_slot[layer]
+                abi.dsa_paged_write_back(self.new_k[slot], self.kcache[slot], *self.meta, D=128,
+                                         dev_status=self.status)
+        elif self.full_slot[layer] >= 0:  # both caches share the page table: one launch
             slot = self.full_slot[layer]
             abi.dsa_paged_write_back_pair(self.new_kv[layer], self.kv[layer], self.new_k[slot], self.kcache[slot],
                                           *self.meta, D0=576, D1=128, dev_status=self.status)
@@ -105,7 +195,13 @@ class LayerRunner:
         """The layer's attention; ``t_range=(b, e)`` (prefill batches) writes
         only the output rows of tokens b .. e-1."""
         slot = self.src_slot[layer]
-        if self.prefill:
+        if self.cache_bits == 4:
+            paged = self.prefill or self.page_budget is not None
+            abi.dsa_sparse_mla_decode_q4(self.q[layer], self.kv4[layer], *self.meta,
+                                         (self.topk_pages if paged else self.topk)[slot],
+                                         unit=self.ps if paged else 1, sm_scale=self.wl.sm_scale, o=self.o[layer],
+                                         ws=self.ws_att, dev_status=self.status)
+        elif self.prefill:
             abi.dsa_sparse_mla_prefill_qblock(self.q[layer], self.kv[layer], *self.meta, self.units[slot],
                                               self.member[slot], self.counts[slot], QB=self.QB,
                                               sm_scale=self.wl.sm_scale, o=self.o[layer], dev_status=self.status,
@@ -120,16 +216,18 @@ class LayerRunner:
                                       dev_status=self.status)
 
     def layer_step(self, layer):
+        self.rotate(layer)
         self.write_back(layer)
         if self.full_slot[layer] >= 0:
             slot = self.full_slot[layer]
             self.index(slot)
-            if self.prefill:
+            if self.prefill and self.cache_bits == 16:
                 self.union(slot)
         self.attend(layer)
 
     def step(self):
         """Every layer of the workload once (IndexShare across layers)."""
+        self.begin_step()
         for layer in range(len(self.types)):
             self.layer_step(layer)
 
@@ -152,7 +250,11 @@ class LayerRunner:
         is written, so little of the final read-back is left after the last
         kernel. The current stream joins both side streams before it returns,
         so the step ends when every copy has landed. Can be captured in a CUDA
-        graph."""
+        graph. With ``tables``, ``h_meta`` is (q_lens, seq_lens). Queries and
+        rows arrive rotated: not with ``rope``. A 4-bit cache's attention runs
+        in one range."""
+        if self.rope is not None:
+            raise ValueError("step_host takes rotated queries and rows: use it without rope")
         cur = torch.cuda.current_stream(self.dev)
         if out_side is None:
             if getattr(self, "_out_side", None) is None:
@@ -163,7 +265,8 @@ class LayerRunner:
         def ranges(layer):
             # token ranges on query-block boundaries (first and last layer of a
             # prefill batch), else the whole batch
-            nch = max(1, min(last_chunks, self.T // self.QB)) if (self.prefill and layer in (0, nl - 1)) else 1
+            split = self.prefill and self.cache_bits == 16 and layer in (0, nl - 1)
+            nch = max(1, min(last_chunks, self.T // self.QB)) if split else 1
             if nch == 1:
                 return [(0, self.T)]
             nqb = -(-self.T // self.QB)
@@ -172,7 +275,7 @@ class LayerRunner:
 
         self.q_idx.copy_(h_q_idx, non_blocking=True)
         self.w.copy_(h_w, non_blocking=True)
-        for d, h in zip(self.meta, h_meta):
+        for d, h in zip(self.meta if self.tables is None else self.lens, h_meta):
             d.copy_(h, non_blocking=True)
         for d, h in zip(self.new_kv, h_new_kv or []):
             d.copy_(h, non_blocking=True)
@@ -192,12 +295,13 @@ class LayerRunner:
                     evs.append(ev)
                 q_ready.append(evs)
         topk_read = False
+        self.begin_step()
         for layer in range(nl):
             self.write_back(layer)
             if self.full_slot[layer] >= 0:
                 slot = self.full_slot[layer]
                 self.index(slot)
-                if self.prefill:
+                if self.prefill and self.cache_bits == 16:
                     self.union(slot)
                 if not topk_read:
                     out_side.wait_stream(cur)

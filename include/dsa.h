@@ -372,8 +372,7 @@ DSA_API int dsa_topk_pages_from_tokens(dsa_stream_t stream, const int32_t* topk,
  *   block_table  int32 [S, bt_stride] in/out: entries [0, had) are read,
  *                [had, need) written, no others touched; the first `width`
  *                entries of a row may be used
- *   free_pages   int32 [F] (may be NULL with F == 0: rows already hold every
- *                page that a call needs when seq - q is a page multiple's end)
+ *   free_pages   int32 [F], NULL with F == 0 (a step that takes no page)
  *   cu_q_lens    int32 [S+1] out   cu_kv_lens  int32 [S+1] out
  *   page_indices int32 [PTW] out   packed rows, -1 behind the last
  *   token_seq, positions, slots  int32 [T] out: request, absolute position
