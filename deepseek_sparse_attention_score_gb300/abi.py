@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -79,11 +80,10 @@ _F = ctypes.c_float
 _D = ctypes.c_double
 _L = ctypes.c_int64
 
-
-class _RopeTargetC(ctypes.Structure):
-    _fields_ = [("x", _P), ("y", _P), ("x_stride_t", _L), ("x_stride_h", _L), ("y_stride_t", _L),
-                ("y_stride_h", _L), ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("rot_off", ctypes.c_int32),
-                ("layout", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", _F)]
+# dsa_rope_target: x, y, x_stride_t, x_stride_h, y_stride_t, y_stride_h, H, D,
+# rot_off, layout, dtype, scale (72 bytes without padding). Packed bytes: a
+# ctypes.Structure takes four times as long to fill.
+_rope_target = struct.Struct("=QQqqqqiiiiif").pack
 
 
 def lib() -> ctypes.CDLL:
@@ -612,7 +612,7 @@ def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, 
     if out is None:
         # one allocation; the page table first, on a 16-byte boundary
         buf = torch.empty(PTW + 2 * (S + 1) + 3 * T + 1, dtype=torch.int32, device=dev)
-        pages, cu_q, cu_kv, seq, pos, slots, taken = buf.split((PTW, S + 1, S + 1, T, T, T, 1))
+        pages, cu_q, cu_kv, seq, pos, slots, taken = buf.split_with_sizes((PTW, S + 1, S + 1, T, T, T, 1))
         out = PageTables(cu_q, cu_kv, pages, seq, pos, slots, taken)
     else:
         for name, n in (("cu_q_lens", S + 1), ("cu_kv_lens", S + 1), ("page_indices", PTW), ("token_seq", T),
@@ -660,7 +660,7 @@ class RopeTarget:
             raise ValueError("the columns of x and y must be contiguous")
         self.x, self.y = x, y
         self.rot_dim = D - rot_off if rot_dim is None else rot_dim
-        self.c = _RopeTargetC(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, H, D, rot_off, lay, dtype, scale)
+        self.c = _rope_target(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, H, D, rot_off, lay, dtype, scale)
 
 
 def dsa_rope(targets, positions, freqs, *, inverse=False):
@@ -680,8 +680,7 @@ def dsa_rope(targets, positions, freqs, *, inverse=False):
             raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(g.x.shape)} on {g.x.device}")
         if g.rot_dim != rot:
             raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
-    arr = (_RopeTargetC * len(ts))(*[g.c for g in ts])
-    _launch(dev, "dsa_rope", arr, len(ts), T, rot, a_pos, freqs.data_ptr(), 1 if inverse else 0)
+    _launch(dev, "dsa_rope", b"".join([g.c for g in ts]), len(ts), T, rot, a_pos, freqs.data_ptr(), 1 if inverse else 0)
     return ts[0].y if one else [g.y for g in ts]
 
 

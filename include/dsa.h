@@ -479,9 +479,10 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
 
 /* ------------------------------------------------------------------------
  * Sparse absorbed-MLA attention over the 4-bit latent cache: as
- * dsa_sparse_mla_decode (token or page units, workspace, lse, empty rows,
+ * dsa_sparse_mla_decode (token or page units, lse, empty rows,
  * reproducibility) with `cache` [P, ps, 416] bytes in the place of kv and
- * row_stride. Only rows of visible selected positions are read, in page units
+ * row_stride. Split key lists are merged inside clusters: ws may be NULL (it
+ * is taken for symmetry with dsa_sparse_mla_decode and not used). Only rows of visible selected positions are read, in page units
  * too, so unwritten rows may hold anything. Prefill tokens go through it with
  * page units, one selection per token.
  * Supported: as dsa_sparse_mla_decode; |sm_scale| * 185 finite in fp32.
@@ -501,7 +502,7 @@ DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, con
  * Only pages that hold a visible position are read, in runs of 32 rows (see
  * the finite-rows rule of dsa_sparse_mla_decode): a cache may drop the pages
  * between the sinks and the window.
- *   max_kv, ws  as dsa_dense_mla
+ *   max_kv  as dsa_dense_mla;  ws  as there, not used with sinks
  * Supported: as dsa_dense_mla; num_sinks >= 0.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,

@@ -50,11 +50,11 @@ def test_page_tables_host_checks(dsa, kw, code):
 
 
 def _rope(n=1, T=4, rot=64, pos=_p(), freqs=_p(), **kw):
-    from deepseek_sparse_attention_score_gb300.abi import _RopeTargetC
+    from deepseek_sparse_attention_score_gb300.abi import _rope_target
     f = dict(x=4096, y=8192, x_stride_t=64, x_stride_h=64, y_stride_t=64, y_stride_h=64, H=1, D=64, rot_off=0,
              layout=0, dtype=0, scale=1.0)
     f.update(kw)
-    return [None, (_RopeTargetC * max(1, n))(*[_RopeTargetC(*f.values())] * max(1, n)), n, T, rot, pos, freqs, 0]
+    return [None, _rope_target(*[v or 0 for v in f.values()]) * max(1, n), n, T, rot, pos, freqs, 0]
 
 
 @pytest.mark.parametrize("kw,code", [
