@@ -469,6 +469,7 @@ int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8
   if (rc) return rc;
   if (K < 1 || (T > 0 && !sel)) return DSA_ERR_INVALID_ARGUMENT;
   if (unit != 1 && unit != ps) return DSA_ERR_INVALID_ARGUMENT;
+  if (K > (1 << 30)) return DSA_ERR_UNSUPPORTED;
   AttendParams prm{};
   prm.scale_log2 = sm_scale * 1.4426950408889634f;
   if (!std::isfinite(prm.scale_log2 * 128.f)) return DSA_ERR_INVALID_ARGUMENT;  // the kernel's logit factor

@@ -7,7 +7,7 @@
 // bf16 column blocks on their way to shared memory; bf16 keys are runs of 32
 // rows of a page, fetched by one thread as TMA boxes.
 //
-// Roles: warp 0 issues the MMAs, warp 1 resolves the keys (tilegen.cuh), warps
+// Roles: warp 0 issues the MMAs, warp 1 resolves the keys (KeyList), warps
 // 4-7 move the queries' first 256 dims into TMEM and run the softmax, warps 8
 // and up copy. Key lists are split over a cluster of up to eight CTAs, whose
 // partial outputs are merged through distributed shared memory: no workspace,
@@ -23,12 +23,15 @@
 #include "common.cuh"
 #include "q4.cuh"
 #include "steps.cuh"
-#include "tilegen.cuh"
 
 namespace dsa {
 
 namespace {
+// what an instantiation reads
+enum : int { kCacheBf16 = 0, kCache4Bit = 1 };
+
 constexpr int kDk = 576, kDv = 512;
+constexpr int kSubKeys = 32;  // keys resolved per step
 constexpr int kTile = 64, kSteps = kTile / kSubKeys;
 constexpr int kRing = 8;       // tiles resolved ahead (their rows are pulled into L2 meanwhile)
 constexpr int kMaxSplits = 8;  // CTAs of a portable cluster
@@ -74,6 +77,134 @@ template <int kCache>
 constexpr int kCopyWarps = kCache == kCache4Bit ? 16 : 1;
 template <int kCache>
 constexpr int kThreads = (8 + kCopyWarps<kCache>) * 32;
+
+// The keys a CTA visits, 32 at a time, resolved by one whole warp. 4-bit cache:
+// windows of 32 selected tokens, or runs of 32 rows of selected pages; bf16
+// cache: runs of 32 rows of the pages that hold sinks, then of those that hold
+// the window. The CTAs of a cluster take equal shares of the list.
+template <int kCache>
+struct KeyList {
+  static constexpr int kBatch = 8;  // token windows resolved at a time
+  const AttendParams* p;
+  int t, n_vis, page_base, lg;  // lg: the page size is 2^lg
+  int key_lo, n_sink, p_skip;   // window: its first position, pages of sinks before its pages, pages skipped between
+  int e, e1;                    // next entry of the list, end of this CTA's share
+  // tokens: the batch's rows, one key per lane, and its windows with keys
+  int row_of[kBatch];
+  uint32_t mask_of[kBatch], left;
+  // pages: a window of 32 entries, one per lane, and those still to visit
+  uint32_t pend;
+  int phys, first_key;          // this lane's page (-1: none) and its first position
+  int cur_phys, cur_key, sub;   // the page being walked and its next run
+
+  __device__ void init(const AttendParams& prm, int tok, int split) {
+    p = &prm;
+    t = tok;
+    lg = 31 - __clz(prm.ps);
+    const int s = seq_of_token_warp(prm.cu_q_lens, prm.S, tok);
+    const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, 0x3fffffff, tok,
+                                   prm.dev_status, s);
+    n_vis = g.n_vis;
+    page_base = g.page_base;
+    left = pend = 0;
+    sub = prm.ps / kSubKeys;
+    int n = prm.K, share;
+    if constexpr (kCache == kCacheBf16) {
+      key_lo = max(0, g.pos - prm.window + 1);
+      const int p_lo = key_lo >> lg;
+      n_sink = (int)min((long long)p_lo, ((long long)prm.sinks + prm.ps - 1) >> lg);
+      p_skip = p_lo - n_sink;
+      n = ((n_vis + prm.ps - 1) >> lg) - p_skip;
+    }
+    share = (max(n, 0) + prm.nsplit - 1) / prm.nsplit;
+    if (kCache == kCache4Bit && prm.mode == kModeToken) share = (share + 31) & ~31;
+    e = min(max(n, 0), split * share);
+    e1 = min(max(n, 0), e + share);
+  }
+
+  // physical page of packed page-table entry `ent`, or -1
+  __device__ __forceinline__ int page_of(int ent) const {
+    if (ent < 0 || ent >= p->PTW) {
+      set_status(p->dev_status, DSA_STATUS_BAD_INDEX);
+      return -1;
+    }
+    const int pg = __ldg(p->page_indices + ent);
+    if (pg < 0 || pg >= p->P) {
+      set_status(p->dev_status, DSA_STATUS_BAD_METADATA);
+      return -1;
+    }
+    return pg;
+  }
+
+  // The next 32 keys: this lane's row (-1: masked) and the mask of the rows;
+  // base: the first row of a run. False: the share is exhausted.
+  __device__ bool next(int& row, uint32_t& mask, int& base) {
+    if (kCache == kCache4Bit && p->mode == kModeToken) return next_tokens(row, mask);
+    while (true) {
+      if (sub < (p->ps >> 5)) {
+        const int k0 = sub * kSubKeys + lane_id(), key = cur_key + k0;
+        bool v = key < n_vis;
+        if constexpr (kCache == kCacheBf16) v = v && (key >= key_lo || key < p->sinks);
+        base = (cur_phys << lg) + sub * kSubKeys;
+        ++sub;
+        row = v ? (cur_phys << lg) + k0 : -1;
+        mask = __ballot_sync(0xffffffffu, v);
+        if (mask) return true;
+        continue;
+      }
+      if (!pend) {
+        if (e >= e1) return false;
+        int pg = e + lane_id();
+        bool v = pg < e1;
+        if constexpr (kCache == kCacheBf16) {
+          pg += pg < n_sink ? 0 : p_skip;
+        } else {
+          pg = v ? __ldg(p->sel + (size_t)t * p->K + pg) : -1;
+          v = pg >= 0 && ((long long)pg << lg) < n_vis;
+        }
+        phys = v ? page_of(page_base + pg) : -1;
+        first_key = v ? pg << lg : 0;
+        pend = __ballot_sync(0xffffffffu, phys >= 0);
+        e += 32;
+        continue;
+      }
+      const int bit = __ffs(pend) - 1;
+      pend &= pend - 1u;
+      cur_phys = __shfl_sync(0xffffffffu, phys, bit);
+      cur_key = __shfl_sync(0xffffffffu, first_key, bit);
+      sub = 0;
+    }
+  }
+
+  __device__ __forceinline__ bool next_tokens(int& row, uint32_t& mask) {
+    while (!left) {
+      if (e >= e1) return false;
+      // two dependent rounds of loads (entries, pages) for a whole batch;
+      // array indexes are constants, so the batch stays in registers
+      int j[kBatch], pg[kBatch];
+#pragma unroll
+      for (int g = 0; g < kBatch; ++g) {
+        const int ee = e + 32 * g + lane_id();
+        j[g] = ee < e1 ? __ldg(p->sel + (size_t)t * p->K + ee) : -1;
+      }
+#pragma unroll
+      for (int g = 0; g < kBatch; ++g) pg[g] = j[g] >= 0 && j[g] < n_vis ? page_of(page_base + (j[g] >> lg)) : -1;
+#pragma unroll
+      for (int g = 0; g < kBatch; ++g) {
+        row_of[g] = pg[g] >= 0 ? (pg[g] << lg) + (j[g] & (p->ps - 1)) : -1;
+        mask_of[g] = __ballot_sync(0xffffffffu, pg[g] >= 0);
+        left |= (mask_of[g] ? 1u : 0u) << g;
+      }
+      e += 32 * kBatch;
+    }
+    const int w = __ffs(left) - 1;
+    left &= left - 1u;
+#pragma unroll
+    for (int g = 0; g < kBatch; ++g)
+      if (g == w) row = row_of[g], mask = mask_of[g];
+    return true;
+  }
+};
 
 struct Bars {
   uint64_t* b;
@@ -346,7 +477,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
                   t * prm.H + h0);
   }
   // the generator resolves its first keys while the queries arrive
-  TileGen<kCache> gen;
+  KeyList<kCache> gen;
   if (warp == 1) gen.init(prm, t, split);
   if (warp >= 4 && warp < 8) {
     if (mbar_wait(br.qbar(), 0, abort_flag)) {
@@ -385,12 +516,12 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       bool any = false;
 #pragma unroll 1
       for (int s = 0; s < kSteps; ++s) {
-        long long row = -1, base = -kSubKeys;
+        int row = -1, base = -kSubKeys;
         uint32_t mask = 0;
         if (more && !(more = gen.next(row, mask, base))) row = -1, mask = 0, base = -kSubKeys;
         any |= mask != 0;
         if constexpr (k4) {
-          ring_rows[slot * kTile + s * kSubKeys + lane] = (int)row;
+          ring_rows[slot * kTile + s * kSubKeys + lane] = row;
           if (row >= 0) {
             // rows come from all over HBM: start pulling them into L2 now
             const uint8_t* rp = prm.kv4 + (size_t)row * kRow4Bytes;
@@ -399,7 +530,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
             prefetch_l2(rp + kRow4Bytes - 1);  // a row may end in a fifth line
           }
         } else if (lane == 0) {
-          ring_rows[slot * kTile + s] = (int)base;  // the step's first row
+          ring_rows[slot * kTile + s] = base;  // the step's first row
         }
         if (lane == 0) ring_mask[slot * kSteps + s] = mask;
       }
@@ -666,7 +797,7 @@ int clusters_at_once(Kernel kern, bool k4, int lz) {
   if (n) return n - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1 << lz);
-  cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16Window>);
+  cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16>);
   cfg.dynamicSmemBytes = kSmem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -704,12 +835,12 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
     return DSA_ERR_CUDA;
   if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kHeads, kDk)) return DSA_ERR_CUDA;
   if (!encode_bf16_3d(&omap, prm.o, kDv, (uint64_t)prm.H, (uint64_t)prm.T, 32)) return DSA_ERR_CUDA;
-  const Kernel kern = k4 ? cache_mla_kernel<kCache4Bit> : cache_mla_kernel<kCacheBf16Window>;
+  const Kernel kern = k4 ? cache_mla_kernel<kCache4Bit> : cache_mla_kernel<kCacheBf16>;
   set_smem_attr_once(reinterpret_cast<const void*>(kern), kSmem);
   prm.nsplit = num_splits(kern, k4, prm.T, prm.H, (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * ((prm.H + kHeads - 1) / kHeads), prm.T, prm.nsplit);
-  cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16Window>);
+  cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16>);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

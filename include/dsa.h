@@ -485,7 +485,9 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
  * is taken for symmetry with dsa_sparse_mla_decode and not used). Only rows of visible selected positions are read, in page units
  * too, so unwritten rows may hold anything. Prefill tokens go through it with
  * page units, one selection per token.
- * Supported: as dsa_sparse_mla_decode; |sm_scale| * 185 finite in fp32.
+ * An entry listed twice counts twice.
+ * Supported: as dsa_sparse_mla_decode, K <= 2^30, |sm_scale| * 185 finite in
+ * fp32.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8_t* cache,
                                      const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,

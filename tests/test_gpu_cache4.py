@@ -209,6 +209,24 @@ def test_rows_that_select_nothing(dsa, unit):
 
 
 @pytest.mark.parametrize("unit", [1, 64])
+def test_entries_listed_twice_count_twice(dsa, unit):
+    rg, cache, q = _batch([1, 2], [300, 200], 64, 16, seed=15)
+    sel = _select(rg, 60 if unit == 1 else 3, unit, np.random.default_rng(5))
+    sel[:, 1], sel[0, 2] = sel[:, 0], sel[0, 0]
+    _check(dsa, rg, cache, q, sel, unit, "twice")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+def test_scales_of_zero_and_below(dsa, scale):
+    rg, cache, q = _batch([1], [300], 64, 16, seed=16)
+    sel = _select(rg, 130, 1, np.random.default_rng(6))
+    o, lse = dsa.dsa_sparse_mla_decode_q4(q.to(DEV), cache.to(DEV), *meta_to(rg, DEV), torch.from_numpy(sel).to(DEV),
+                                          unit=1, sm_scale=scale, want_lse=True)
+    flat = R.q4_values(cache.numpy().reshape(-1, 416))
+    R.check_attend(o, lse, R.attend(R.f64(q), R.token_keys(rg, flat, _positions(sel, 1)), scale), f"scale {scale}")
+
+
+@pytest.mark.parametrize("unit", [1, 64])
 def test_unselected_and_unwritten_rows_may_hold_anything(dsa, unit):
     rg, cache, q = _batch([1, 3], [300, 200], 64, 16, seed=6)
     sel = _select(rg, 100 if unit == 1 else 3, unit, np.random.default_rng(3))

@@ -105,7 +105,8 @@ def _attend(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(ps=48), UNSUPPORTED), (dict(Dv=256), UNSUPPORTED), (dict(Dk=512), UNSUPPORTED), (dict(unit=32), INVALID),
-    (dict(K=0), INVALID), (dict(sel=None), INVALID), (dict(sm_scale=math.inf), INVALID),
+    (dict(K=0), INVALID), (dict(K=(1 << 30) + 1), UNSUPPORTED), (dict(sel=None), INVALID),
+    (dict(sm_scale=math.inf), INVALID),
     (dict(sm_scale=3e36), INVALID), (dict(cache=_p(4104)), ALIGNMENT), (dict(cache=None), INVALID),
     (dict(o=None), INVALID), (dict(T=65536, S=65536), UNSUPPORTED), (dict(H=-1), INVALID), (dict(H=0), OK),
     (dict(T=0, S=0, P=0, PTW=0), OK),
