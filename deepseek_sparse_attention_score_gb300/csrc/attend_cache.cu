@@ -735,22 +735,22 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
     const uint32_t smem0 = smem_u32(smem);
     float* wts = reinterpret_cast<float*>(smem + OFF_WTS);
     if (tid < nrows) {
-      auto lse_of = [&](int z) { return ld_cluster_f32(cluster_addr(smem0 + OFF_LSE + (row0 + tid) * 4, z)); };
-      float mx = -INFINITY;
-#pragma unroll 1
-      for (int z = 0; z < Z; ++z) mx = fmaxf(mx, lse_of(z));
-      float tot = 0.f;
-#pragma unroll 1
-      for (int z = 0; z < Z; ++z) {
-        const float lz = lse_of(z);  // a split without keys weighs nothing; NaN stays NaN
-        const float w = lz == -INFINITY ? 0.f : exp2f((lz - mx) * 1.4426950408889634f);
-        wts[z * kHeads + tid] = w;
-        tot += w;
+      float lz[kMaxSplits], mx = -INFINITY, tot = 0.f;  // all loads in flight at once
+#pragma unroll
+      for (int z = 0; z < kMaxSplits; ++z)
+        lz[z] = z < Z ? ld_cluster_f32(cluster_addr(smem0 + OFF_LSE + (row0 + tid) * 4, z)) : -INFINITY;
+#pragma unroll
+      for (int z = 0; z < kMaxSplits; ++z) mx = fmaxf(mx, lz[z]);
+#pragma unroll
+      for (int z = 0; z < kMaxSplits; ++z) {
+        // a split without keys weighs nothing; NaN stays NaN
+        lz[z] = lz[z] == -INFINITY ? 0.f : exp2f((lz[z] - mx) * 1.4426950408889634f);
+        tot += lz[z];
       }
       const bool some = tot != 0.f;
       const float inv = some ? 1.f / tot : 0.f;
-#pragma unroll 1
-      for (int z = 0; z < Z; ++z) wts[z * kHeads + tid] *= inv;
+#pragma unroll
+      for (int z = 0; z < kMaxSplits; ++z) wts[z * kHeads + tid] = lz[z] * inv;
       if (half == 0 && prm.lse)
         prm.lse[(size_t)t * prm.H + h0 + row0 + tid] = some ? mx + logf(tot) : -INFINITY;
     }
