@@ -8,8 +8,8 @@
 // rows of a page, fetched by one thread as TMA boxes.
 //
 // Roles: warp 0 issues the MMAs, warp 1 resolves the keys (KeyList), warps
-// 4-7 move the queries' first 256 dims into TMEM and run the softmax, warps 8
-// and up copy. Key lists are split over a cluster of up to eight CTAs, whose
+// 4-7 move the queries' first 256 dims into TMEM and run the softmax, others
+// copy. Key lists are split over a cluster of up to eight CTAs, whose
 // partial outputs are merged through distributed shared memory: no workspace,
 // no counters, and every CTA of the cluster merges a share of the head rows.
 //
@@ -75,8 +75,15 @@ constexpr uint32_t kColO = 256;
 // waited for their loads a quarter of the time)
 template <int kCache>
 constexpr int kCopyWarps = kCache == kCache4Bit ? 16 : 1;
+// the 4-bit copiers are warps 8-23; the TMA issuer is warp 2, away from the MMA
+// issuer's quarter of the SM (as warp 8 it cost 4%: 928 against 895 us for 2049
+// tokens; for the 4-bit copiers it made no difference where they were)
 template <int kCache>
-constexpr int kThreads = (8 + kCopyWarps<kCache>) * 32;
+constexpr int kThreads = (kCache == kCache4Bit ? 8 + kCopyWarps<kCache> : 8) * 32;
+template <int kCache>
+__device__ __forceinline__ int copier_of(int warp) {  // its number, or -1
+  return kCache == kCache4Bit ? max(warp - 8, -1) : warp == 2 ? 0 : -1;
+}
 
 // The keys a CTA visits, 32 at a time, resolved by one whole warp. 4-bit cache:
 // windows of 32 selected tokens, or runs of 32 rows of selected pages; bf16
@@ -539,11 +546,12 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       if (lane == 0) mbar_arrive(br.rfull(slot));
       if (!any) break;
     }
-  } else if (warp >= 8) {
+  } else if (warp < 4 || warp >= 8) {
     // ---------------------------------------------------------------- copier
-    if constexpr (k4)
-      copy_keys(prm.kv4, half, warp - 8, smem, ring_rows, ring_end, br, abort_flag);
-    else if (lane == 0)
+    const int cw = copier_of<kCache>(warp);
+    if constexpr (k4) {
+      if (cw >= 0) copy_keys(prm.kv4, half, cw, smem, ring_rows, ring_end, br, abort_flag);
+    } else if (cw >= 0 && lane == 0)
       copy_boxes(&kvmap, half, smem, ring_rows, ring_end, br, abort_flag);
   } else if (warp >= 4) {
     // --------------------------------------------------------------- softmax
