@@ -748,7 +748,7 @@ def dsa_q4_read_rows(cache, slots, *, out=None, dev_status=None):
     return out
 
 
-def _attend_out(dev, T, H, Dv, o, lse, want_lse, ws):
+def _attend_out(dev, T, H, Dv, o, lse, want_lse):
     if o is None:
         o = torch.empty((T, H, Dv), dtype=torch.bfloat16, device=dev)
     else:
@@ -759,17 +759,15 @@ def _attend_out(dev, T, H, Dv, o, lse, want_lse, ws):
     elif lse is not None:
         _need(lse, "lse", torch.float32, dev, 2)
         _shape(lse, "lse", (T, H))
-    if ws is None:
-        ws = torch.empty(max(1, dsa_sparse_mla_decode_workspace_size(T, H, Dv)), dtype=torch.uint8, device=dev)
-    else:
-        _need(ws, "ws", torch.uint8, dev, 1)
-    return o, lse, ws
+    return o, lse
 
 
 def dsa_sparse_mla_decode_q4(q, cache, seq_lens, cu_q_lens, cu_kv_lens, page_indices, sel, *, unit, sm_scale, o=None,
                              lse=None, want_lse=False, ws=None, dev_status=None, Dv=512):
     """:func:`dsa_sparse_mla_decode` over the 4-bit latent ``cache``
-    [P, ps, 416] that :func:`dsa_q4_write_back` fills."""
+    [P, ps, 416] that :func:`dsa_q4_write_back` fills. Needs no workspace
+    (``ws`` is taken as there and not used); ``q`` may have padding rows behind
+    the last token, whose outputs are left as they are."""
     dev = q.device
     _need(q, "q", torch.bfloat16, dev, 3)
     P, ps = _cache4(cache, dev)
@@ -778,24 +776,26 @@ def dsa_sparse_mla_decode_q4(q, cache, seq_lens, cu_q_lens, cu_kv_lens, page_ind
     S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
     K = sel.shape[1]
     _shape(sel, "sel", (T, K))
-    o, lse, ws = _attend_out(dev, T, H, Dv, o, lse, want_lse, ws)
+    o, lse = _attend_out(dev, T, H, Dv, o, lse, want_lse)
     _launch(dev, "dsa_sparse_mla_decode_q4", _addr(q), _addr(cache), *meta, _addr(sel), K, int(unit), T, S, P, PTW, ps,
-            H, Dk, Dv, float(sm_scale), _addr(o), _addr(lse), _addr(ws), ws.numel(), _status(dev_status, dev))
+            H, Dk, Dv, float(sm_scale), _addr(o), _addr(lse), None, 0, _status(dev_status, dev))
     return (o, lse) if lse is not None else o
 
 
 def dsa_window_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, *, max_kv, sm_scale, sliding_window,
                    num_sinks=0, soft_cap=0.0, o=None, lse=None, want_lse=False, ws=None, dev_status=None, Dv=512):
     """Causal absorbed-MLA over the ``sliding_window`` most recent positions
-    and the first ``num_sinks`` ones (:func:`dsa_dense_mla` with sinks)."""
+    and the first ``num_sinks`` ones. Needs no workspace (``ws`` is taken as in
+    :func:`dsa_dense_mla` and not used); ``q`` may have padding rows behind the
+    last token, whose outputs are left as they are."""
     dev = q.device
     _need(q, "q", torch.bfloat16, dev, 3)
     _need(kv, "kv", torch.bfloat16, dev, 3)
     T, H, Dk = q.shape
     P, ps, row_stride = kv.shape
     S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
-    o, lse, ws = _attend_out(dev, T, H, Dv, o, lse, want_lse, ws)
+    o, lse = _attend_out(dev, T, H, Dv, o, lse, want_lse)
     _launch(dev, "dsa_window_mla", _addr(q), _addr(kv), row_stride, *meta, int(max_kv), T, S, P, PTW, ps, H, Dk, Dv,
-            float(sm_scale), int(sliding_window), int(num_sinks), float(soft_cap), _addr(o), _addr(lse), _addr(ws),
-            ws.numel(), _status(dev_status, dev))
+            float(sm_scale), int(sliding_window), int(num_sinks), float(soft_cap), _addr(o), _addr(lse), None, 0,
+            _status(dev_status, dev))
     return (o, lse) if lse is not None else o

@@ -2,7 +2,9 @@
 // workspace carving, and the kernel launches of each operation.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -385,16 +387,16 @@ int dsa_sparse_mla_decode(dsa_stream_t stream, const uint16_t* q, const uint16_t
   return run_attend(static_cast<cudaStream_t>(stream), prm, ws, ws_bytes);
 }
 
-static int dense_common(cudaStream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
-                        const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
-                        const int32_t* page_indices, int max_kv, int T, int S, int P, int PTW, int ps, int H, int Dk,
-                        int Dv, float sm_scale, int sliding_window, int num_sinks, float soft_cap, uint16_t* o,
-                        float* lse, void* ws, size_t ws_bytes, int32_t* dev_status) {
+int dsa_dense_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
+                  const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices, int max_kv,
+                  int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, int sliding_window,
+                  float soft_cap, uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_dense_mla");
   int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
   if (rc) return rc;
   rc = attend_check(q, kv, row_stride, T, H, Dk, Dv, o);
   if (rc) return rc;
-  if (max_kv < 1 || sliding_window < 0 || num_sinks < 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (max_kv < 1 || sliding_window < 0) return DSA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(sm_scale) || !std::isfinite(soft_cap) || soft_cap < 0.f) return DSA_ERR_INVALID_ARGUMENT;
   if (T == 0 || H == 0) return DSA_OK;
   AttendParams prm{};
@@ -420,30 +422,13 @@ static int dense_common(cudaStream_t stream, const uint16_t* q, const uint16_t* 
     prm.cap_log2 = soft_cap * 1.4426950408889634f;
   }
   prm.K = (max_kv + ps - 1) / ps;  // pages of the longest request: the split unit
-  if (sliding_window > 0 && num_sinks > 0) {
-    // at most the sinks' pages and the window's, which may start inside one
-    prm.sinks = num_sinks;
-    const long long most = ((long long)num_sinks + ps - 1) / ps + ((long long)sliding_window + ps - 1) / ps + 1;
-    prm.K = (int)std::min<long long>(prm.K, most);
-  }
   prm.o = o;
   prm.lse = lse;
   prm.dev_status = dev_status;
-  if (prm.sinks) return run_attend_cache(stream, prm);
   int z = attend_num_splits(T, H, prm.K, prm.mode);
   if (z > 1 && (!ws || ws_bytes < attend_workspace_bytes(T, H, z) || !aligned16(ws))) z = 1;
   prm.nsplit = z;
-  return run_attend(stream, prm, ws, ws_bytes);
-}
-
-int dsa_dense_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
-                  const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices, int max_kv,
-                  int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, int sliding_window,
-                  float soft_cap, uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status) {
-  NvtxRange nvtx_range("dsa_dense_mla");
-  return dense_common(static_cast<cudaStream_t>(stream), q, kv, row_stride, seq_lens, cu_q_lens, cu_kv_lens,
-                      page_indices, max_kv, T, S, P, PTW, ps, H, Dk, Dv, sm_scale, sliding_window, 0, soft_cap, o, lse,
-                      ws, ws_bytes, dev_status);
+  return run_attend(static_cast<cudaStream_t>(stream), prm, ws, ws_bytes);
 }
 
 int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
@@ -451,10 +436,47 @@ int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, i
                    int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale, int sliding_window,
                    int num_sinks, float soft_cap, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                    int32_t* dev_status) {
+  (void)ws, (void)ws_bytes;  // taken as dsa_dense_mla takes them; this form needs none
   NvtxRange nvtx_range("dsa_window_mla");
-  return dense_common(static_cast<cudaStream_t>(stream), q, kv, row_stride, seq_lens, cu_q_lens, cu_kv_lens,
-                      page_indices, max_kv, T, S, P, PTW, ps, H, Dk, Dv, sm_scale, sliding_window, num_sinks, soft_cap,
-                      o, lse, ws, ws_bytes, dev_status);
+  int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
+  if (rc) return rc;
+  rc = attend_check(q, kv, row_stride, T, H, Dk, Dv, o);
+  if (rc) return rc;
+  if (max_kv < 1 || sliding_window < 0 || num_sinks < 0) return DSA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(sm_scale) || !std::isfinite(soft_cap) || soft_cap < 0.f) return DSA_ERR_INVALID_ARGUMENT;
+  if (T == 0 || H == 0) return DSA_OK;
+  AttendParams prm{};
+  prm.q = q;
+  prm.kv = kv;
+  prm.row_stride = row_stride;
+  prm.seq_lens = seq_lens;
+  prm.cu_q_lens = cu_q_lens;
+  prm.cu_kv_lens = cu_kv_lens;
+  prm.page_indices = page_indices;
+  prm.T = T;
+  prm.S = S;
+  prm.P = P;
+  prm.PTW = PTW;
+  prm.ps = ps;
+  prm.H = H;
+  prm.scale_log2 = sm_scale * 1.4426950408889634f;
+  prm.mode = kModeDense;
+  prm.window = sliding_window > 0 ? sliding_window : INT_MAX;
+  prm.sinks = num_sinks;
+  if (soft_cap > 0.f) {
+    prm.soft_cap_on = 1;
+    prm.inv_cap_scale = sm_scale / soft_cap;
+    prm.cap_log2 = soft_cap * 1.4426950408889634f;
+  }
+  // pages of the longest list, the split unit: at most the request's, or the
+  // sinks' and the window's, which may start inside one
+  const long long pages = ((long long)max_kv + ps - 1) / ps;
+  const long long most = ((long long)num_sinks + ps - 1) / ps + ((long long)prm.window + ps - 1) / ps + 1;
+  prm.K = (int)std::min(pages, most);
+  prm.o = o;
+  prm.lse = lse;
+  prm.dev_status = dev_status;
+  return run_attend_cache(static_cast<cudaStream_t>(stream), prm);
 }
 
 int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8_t* cache, const int32_t* seq_lens,
@@ -462,6 +484,7 @@ int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8
                              const int32_t* sel, int K, int unit, int T, int S, int P, int PTW, int ps, int H, int Dk,
                              int Dv, float sm_scale, uint16_t* o, float* lse, void* ws, size_t ws_bytes,
                              int32_t* dev_status) {
+  (void)ws, (void)ws_bytes;  // taken as dsa_sparse_mla_decode takes them; this form needs none
   NvtxRange nvtx_range("dsa_sparse_mla_decode_q4");
   int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
   if (rc) return rc;
@@ -502,6 +525,7 @@ int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int3
   NvtxRange nvtx_range("dsa_build_page_tables");
   if (S < 0 || T < 0 || PTW < 0 || F < 0 || width < 0 || bt_stride < width) return DSA_ERR_INVALID_ARGUMENT;
   if (!ps_supported(ps) || S > kTablesMaxRequests || (long long)width * ps >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  if (T > (1 << 30) || PTW > (1 << 30)) return DSA_ERR_UNSUPPORTED;
   if (!cu_q_lens || !cu_kv_lens || !n_taken) return DSA_ERR_INVALID_ARGUMENT;
   if ((S > 0 && (!q_lens || !seq_lens)) || (S > 0 && width > 0 && !block_table) || (F > 0 && !free_pages) ||
       (PTW > 0 && !page_indices) || (T > 0 && (!token_seq || !positions || !slots)))
@@ -509,6 +533,16 @@ int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int3
   TablesParams p{q_lens, seq_lens, block_table, bt_stride, width, free_pages, F, S, T, PTW, ps, cu_q_lens, cu_kv_lens,
                  page_indices, token_seq, positions, slots, n_taken, dev_status, false};
   return run_page_tables(static_cast<cudaStream_t>(stream), p);
+}
+
+// Whether n0 x n1 rows of D elements, s0 and s1 elements apart, are disjoint.
+static bool rows_apart(long long n0, long long s0, long long n1, long long s1, long long D) {
+  s0 = s0 < 0 ? -s0 : s0;
+  s1 = s1 < 0 ? -s1 : s1;
+  if (n0 <= 1) return n1 <= 1 || s1 >= D;
+  if (n1 <= 1) return s0 >= D;
+  if (s0 < s1) std::swap(n0, n1), std::swap(s0, s1);  // s1: the inner rows
+  return s1 >= D && (s0 - D) / (n1 - 1) >= s1 && s0 >= D;
 }
 
 int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets, int T, int rot_dim,
@@ -528,6 +562,7 @@ int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets,
     if (T == 0 || g.H == 0) continue;
     if (!g.x || !g.y) return DSA_ERR_INVALID_ARGUMENT;
     if (g.x == g.y && (g.x_stride_t != g.y_stride_t || g.x_stride_h != g.y_stride_h)) return DSA_ERR_INVALID_ARGUMENT;
+    if (!rows_apart(T, g.y_stride_t, g.H, g.y_stride_h, g.D)) return DSA_ERR_INVALID_ARGUMENT;
     const uintptr_t es = g.dtype == DSA_DTYPE_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(g.x) % es || reinterpret_cast<uintptr_t>(g.y) % es) return DSA_ERR_ALIGNMENT;
   }

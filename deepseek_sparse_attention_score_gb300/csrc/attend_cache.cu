@@ -471,6 +471,10 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   tc_fence_after();
   griddep_wait();
   const uint32_t tmem = *tmem_slot;
+  if (t >= __ldg(prm.cu_q_lens + prm.S)) {  // a padding row behind the last request: left as it is
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;  // this warp's TMEM lanes
   const int r = (warp & 3) * 32 + lane;                          // and this thread's: a head row
   if (tid == 0) {

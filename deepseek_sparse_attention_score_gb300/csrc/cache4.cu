@@ -65,8 +65,9 @@ __global__ void __launch_bounds__(kRowThreads) q4_write_back_kernel(
   griddep_launch_dependents();
   griddep_wait();
   const int lane = lane_id();
-  const int t = blockIdx.x * kRowsPerCta + warp_id();
-  if (t >= T) return;
+  const long long row = (long long)blockIdx.x * kRowsPerCta + warp_id();
+  if (row >= min(T, __ldg(cu_q_lens + S))) return;  // past the end, or a padding row behind the last request
+  const int t = (int)row;
   // the row's loads do not depend on where it goes: issue them first
   const uint4* src = reinterpret_cast<const uint4*>(rows + (size_t)t * src_stride);
   const uint4 u = __ldg(src + 2 * lane), v = __ldg(src + 2 * lane + 1);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kRowThreads) q4_read_rows_kernel(
   griddep_launch_dependents();
   griddep_wait();
   const int lane = lane_id();
-  const int i = blockIdx.x * kRowsPerCta + warp_id();
+  const long long i = (long long)blockIdx.x * kRowsPerCta + warp_id();
   if (i >= N) return;
   const int slot = __ldg(slots + i);
   uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}, rp = make_uint4(0, 0, 0, 0);

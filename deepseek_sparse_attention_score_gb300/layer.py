@@ -200,7 +200,7 @@ class LayerRunner:
             abi.dsa_sparse_mla_decode_q4(self.q[layer], self.kv4[layer], *self.meta,
                                          (self.topk_pages if paged else self.topk)[slot],
                                          unit=self.ps if paged else 1, sm_scale=self.wl.sm_scale, o=self.o[layer],
-                                         ws=self.ws_att, dev_status=self.status)
+                                         dev_status=self.status)
         elif self.prefill:
             abi.dsa_sparse_mla_prefill_qblock(self.q[layer], self.kv[layer], *self.meta, self.units[slot],
                                               self.member[slot], self.counts[slot], QB=self.QB,

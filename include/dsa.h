@@ -387,8 +387,8 @@ DSA_API int dsa_topk_pages_from_tokens(dsa_stream_t stream, const int32_t* topk,
  * pages than PTW (those past the end, and block-table entries behind them,
  * are not written); a list that runs out sets DSA_STATUS_NO_PAGES, its
  * missing pages and their slots are -1 and n_taken says how many it takes.
- * Supported: ps in {32, 64, 128}, S <= 16384, width * ps < 2^31. Outputs
- * overlap no input. Needs no workspace.
+ * Supported: ps in {32, 64, 128}, S <= 16384, width * ps < 2^31, T and PTW
+ * up to 2^30. Outputs overlap no input. Needs no workspace.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int32_t* seq_lens,
                                   int32_t* block_table, int64_t bt_stride, int width, const int32_t* free_pages,
@@ -408,7 +408,8 @@ DSA_API int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, co
  *   x, y       [T, H, D] of `dtype` with element strides (*_stride_t,
  *              *_stride_h, 1). y == x (same strides) works in place and
  *              touches the rotated columns only; otherwise y receives the
- *              other columns too and must not overlap x
+ *              other columns too and must not overlap x. Rows of y must not
+ *              overlap each other
  *   positions  int32 [T]; a row with a negative position is left as it is
  *   freqs      fp64 [rot_dim / 2], radians per position (dsa_rope_freqs)
  * Angles are reduced in fp64; products are fp32, rounded once to `dtype`.
@@ -459,7 +460,8 @@ DSA_API int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor,
  *
  * dsa_q4_write_back is dsa_paged_write_back into such a cache: token t's row
  * goes to the slot of its position, every other row is left untouched, and a
- * token without a slot sets DSA_STATUS_BAD_METADATA and is skipped.
+ * token without a slot sets DSA_STATUS_BAD_METADATA and is skipped. T may be
+ * an upper bound: rows from cu_q_lens[S] on are padding and are ignored.
  *   rows   bf16 [T, src_stride], the first 576 columns
  *   cache  [P, ps, 416] bytes
  * dsa_q4_read_rows writes the values of N slots (page * ps + row, as
@@ -485,7 +487,8 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
  * is taken for symmetry with dsa_sparse_mla_decode and not used). Only rows of visible selected positions are read, in page units
  * too, so unwritten rows may hold anything. Prefill tokens go through it with
  * page units, one selection per token.
- * An entry listed twice counts twice.
+ * An entry listed twice counts twice. T may be an upper bound: rows of o and
+ * lse from cu_q_lens[S] on are left as they are.
  * Supported: as dsa_sparse_mla_decode, K <= 2^30, |sm_scale| * 185 finite in
  * fp32.
  * ------------------------------------------------------------------------ */
@@ -499,12 +502,15 @@ DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, con
  * Absorbed-MLA attention with a sliding window and sinks: dsa_dense_mla where
  * token t sees, of the positions j < seq_len with j <= pos(t), those with
  * j > pos(t) - sliding_window and the first num_sinks, j < num_sinks (a
- * position that is both counts once). num_sinks == 0 is dsa_dense_mla; with
- * sliding_window == 0 every position is visible and num_sinks changes nothing.
+ * position that is both counts once). With sliding_window == 0 every position
+ * is visible. T may be an upper bound: rows of o and lse from cu_q_lens[S] on
+ * are left as they are.
  * Only pages that hold a visible position are read, in runs of 32 rows (see
  * the finite-rows rule of dsa_sparse_mla_decode): a cache may drop the pages
  * between the sinks and the window.
- *   max_kv  as dsa_dense_mla;  ws  as there, not used with sinks
+ *   max_kv  as dsa_dense_mla
+ *   ws      taken as there and not used (may be NULL): split key lists are
+ *           merged inside clusters
  * Supported: as dsa_dense_mla; num_sinks >= 0.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,

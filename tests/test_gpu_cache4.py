@@ -186,15 +186,14 @@ def test_attention(dsa, ps, paged, q_lens, kv_lens, H, K):
 
 @pytest.mark.parametrize("K,unit", [(2048, 1), (2047, 1), (37, 64), (9, 64)])
 def test_long_selections_split(dsa, K, unit):
-    """One request: the selection is split over CTAs and merged; without a
-    workspace it is not."""
+    """One request: the selection is split over CTAs and merged, the same on
+    every run."""
     rg, cache, q = _batch([1, 1], [2600, 1900], 64, 32, seed=4)
     sel = _select(rg, K, unit, np.random.default_rng(1))
     o, lse = _check(dsa, rg, cache, q, sel, unit, "split")
     for _ in range(3):
         o2, lse2, _ = _run(dsa, rg, cache, q, sel, unit)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
-    _check(dsa, rg, cache, q, sel, unit, "one CTA", ws=torch.empty(1, dtype=torch.uint8, device=DEV))
 
 
 @pytest.mark.parametrize("unit", [1, 64])
@@ -214,6 +213,28 @@ def test_entries_listed_twice_count_twice(dsa, unit):
     sel = _select(rg, 60 if unit == 1 else 3, unit, np.random.default_rng(5))
     sel[:, 1], sel[0, 2] = sel[:, 0], sel[0, 0]
     _check(dsa, rg, cache, q, sel, unit, "twice")
+
+
+def test_padding_rows_are_left_alone(dsa):
+    """T as an upper bound of the tokens: three rows behind the last request."""
+    rg, cache, q = _batch([1, 4, 0], [300, 200, 64], 64, 16, seed=17)
+    sel = _select(rg, 130, 1, np.random.default_rng(7))
+    q2 = torch.cat([q, torch.full((3, 16, 576), float("nan"), dtype=torch.bfloat16)]).to(DEV)
+    sel2 = torch.from_numpy(np.concatenate([sel, np.zeros((3, 130), np.int32)])).to(DEV)
+    o, lse = torch.full((8, 16, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((8, 16), 7.0, device=DEV)
+    st = _status()
+    dsa.dsa_sparse_mla_decode_q4(q2, cache.to(DEV), *meta_to(rg, DEV), sel2, unit=1, sm_scale=DI.SM_SCALE, o=o,
+                                 lse=lse, dev_status=st)
+    assert st.item() == 0 and (o[5:] == 7).all() and (lse[5:] == 7).all()
+    flat = R.q4_values(cache.numpy().reshape(-1, 416))
+    R.check_attend(o[:5], lse[:5], R.attend(R.f64(q), R.token_keys(rg, flat, _positions(sel, 1)), DI.SM_SCALE),
+                   "padded")
+    # and in the write-back: rows behind the last request go nowhere
+    rows = _rows(8, 9)
+    a, b = (torch.zeros_like(cache, device=DEV) for _ in range(2))
+    dsa.dsa_q4_write_back(rows, a, *meta_to(rg, DEV), dev_status=st)
+    dsa.dsa_q4_write_back(rows[:5], b, *meta_to(rg, DEV), dev_status=st)
+    assert st.item() == 0 and torch.equal(a, b) and a.any()
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05])
@@ -267,22 +288,21 @@ def test_bad_pages_are_skipped(dsa):
     R.check_attend(o, lse, R.attend(R.f64(q), R.token_keys(rg, flat, lambda t: live[t]), DI.SM_SCALE), "bad pages")
 
 
-def test_two_captured_graphs_with_workspaces_of_their_own(dsa):
+def test_two_captured_graphs_at_once(dsa):
     rg, cache, q = _batch([1, 1], [1500, 900], 64, 16, seed=9)
     sel = _select(rg, 700, 1, np.random.default_rng(4))
     want, lse, _ = _run(dsa, rg, cache, q, sel, 1)
     dc, dq, ds, meta = cache.to(DEV), q.to(DEV), torch.from_numpy(sel).to(DEV), meta_to(rg, DEV)
     graphs = []
     for _ in range(2):
-        ws = torch.empty(dsa.dsa_sparse_mla_decode_workspace_size(2, 16), dtype=torch.uint8, device=DEV)
         o = torch.zeros_like(want)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            dsa.dsa_sparse_mla_decode_q4(dq, dc, *meta, ds, unit=1, sm_scale=DI.SM_SCALE, o=o, ws=ws)
-        graphs.append((g, o, ws, torch.cuda.Stream()))
+            dsa.dsa_sparse_mla_decode_q4(dq, dc, *meta, ds, unit=1, sm_scale=DI.SM_SCALE, o=o)
+        graphs.append((g, o, torch.cuda.Stream()))
     for _ in range(5):
-        for g, _, _, s in graphs:
+        for g, _, s in graphs:
             with torch.cuda.stream(s):
                 g.replay()
     torch.cuda.synchronize()
-    assert all(torch.equal(o, want) for _, o, _, _ in graphs)
+    assert all(torch.equal(o, want) for _, o, _ in graphs)

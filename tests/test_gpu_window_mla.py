@@ -71,7 +71,6 @@ def test_split_over_ctas(dsa, window, sinks):
     o, lse = _check(dsa, wl, window, sinks)
     o2, lse2, _ = _run(dsa, wl, window, sinks)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
-    _check(dsa, wl, window, sinks, ws=torch.empty(1, dtype=torch.uint8, device=DEV))
 
 
 @pytest.mark.parametrize("sinks", [0, 9])
@@ -79,12 +78,35 @@ def test_logit_cap(dsa, sinks):
     _check(dsa, DI.random_small(12, [1, 6], [400, 200], H=16), 90, sinks, cap=2.0)
 
 
-def test_no_sinks_is_the_dense_call(dsa):
+def test_row_stride_640(dsa):
     wl = DI.random_small(13, [1, 9], [700, 300], H=16)
-    o, lse, _ = _run(dsa, wl, 200, 0)
-    od, ld = dsa.dsa_dense_mla(wl.q[0].to(DEV), wl.kv[0].to(DEV), *meta_to(wl.rg, DEV), max_kv=700,
-                               sm_scale=wl.sm_scale, sliding_window=200, want_lse=True)
-    assert torch.equal(o, od) and torch.equal(lse, ld)
+    wide = torch.full((wl.rg.num_pages, 64, 640), float("nan"), dtype=torch.bfloat16)
+    wide[:, :, :576] = wl.kv[0]
+    o, lse = _check(dsa, wl, 200, 4)
+    o2, lse2, st = _run(dsa, wl, 200, 4, kv=wide)
+    assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 0), (200, 4)])
+def test_padding_rows_are_left_alone(dsa, window, sinks):
+    """T as an upper bound: queries and outputs of 3 rows more than tokens."""
+    wl = DI.random_small(17, [1, 9, 0], [700, 300, 64], H=16)
+    o, lse = _check(dsa, wl, window, sinks)
+    q = torch.cat([wl.q[0], torch.full((3, 16, 576), float("nan"), dtype=torch.bfloat16)]).to(DEV)
+    o2, lse2 = torch.full((13, 16, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((13, 16), 7.0, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dsa.dsa_window_mla(q, wl.kv[0].to(DEV), *meta_to(wl.rg, DEV), max_kv=700, sm_scale=wl.sm_scale,
+                       sliding_window=window, num_sinks=sinks, o=o2, lse=lse2, dev_status=st)
+    assert st.item() == 0 and (o2[10:] == 7).all() and (lse2[10:] == 7).all()
+    R.check_attend(o2[:10], lse2[:10], R.attend(R.f64(wl.q[0]), R.token_keys(
+        wl.rg, R.f64(wl.kv[0]).reshape(-1, 576), _visible(wl.rg, window, sinks)), wl.sm_scale), "padded")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+def test_scales_of_zero_and_below(dsa, scale):
+    wl = DI.random_small(18, [2], [300], H=16)
+    wl.sm_scale = scale
+    _check(dsa, wl, 100, 4)
 
 
 def test_pages_between_sinks_and_window_are_not_read(dsa):

@@ -39,6 +39,7 @@ def _tables(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(S=-1), INVALID), (dict(T=-1), INVALID), (dict(PTW=-1), INVALID), (dict(F=-1), INVALID),
+    (dict(T=(1 << 30) + 1), UNSUPPORTED), (dict(PTW=(1 << 30) + 1), UNSUPPORTED),
     (dict(width=-1), INVALID), (dict(bt_stride=7), INVALID), (dict(ps=48), UNSUPPORTED), (dict(ps=0), UNSUPPORTED),
     (dict(S=16385), UNSUPPORTED), (dict(width=1 << 25, bt_stride=1 << 25), UNSUPPORTED),
     (dict(q_lens=None), INVALID), (dict(seq_lens=None), INVALID), (dict(block_table=None), INVALID),
@@ -63,6 +64,10 @@ def _rope(n=1, T=4, rot=64, pos=_p(), freqs=_p(), **kw):
     (dict(rot_off=-1), INVALID), (dict(H=-1), INVALID), (dict(layout=2), INVALID), (dict(dtype=2), UNSUPPORTED),
     (dict(scale=math.nan), INVALID), (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(x=4097), ALIGNMENT),
     (dict(y=8194, dtype=1), ALIGNMENT), (dict(y=4096, y_stride_t=128), INVALID), (dict(pos=None), INVALID),
+    (dict(y_stride_t=0), INVALID), (dict(y_stride_t=63), INVALID),  # rows of y on top of each other
+    (dict(H=2, y_stride_t=64), INVALID), (dict(H=2, y_stride_t=127), INVALID),
+    (dict(H=2, y_stride_h=256, y_stride_t=64, T=5), INVALID), (dict(H=2, y_stride_h=0, y_stride_t=128), INVALID),
+    (dict(D=4097), UNSUPPORTED), (dict(H=65537), UNSUPPORTED),
     (dict(freqs=None), INVALID), (dict(H=1 << 26), UNSUPPORTED), (dict(T=0), OK), (dict(T=0, x=None), OK),
 ])
 def test_rope_host_checks(dsa, kw, code):
