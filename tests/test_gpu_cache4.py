@@ -306,3 +306,33 @@ def test_two_captured_graphs_at_once(dsa):
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for _, o, _ in graphs)
+
+
+def test_offsets_past_32_bits(dsa):
+    """A cache of 4.8 GB whose requests lie at its end."""
+    P, ps = 90112, 128
+    rg = DI.make_ragged([1, 130], [200, 300], ps, master_seed=3)
+    rg.page_indices = (P - 1 - rg.page_indices).astype(np.int32)
+    rg.num_pages = P
+    cache = torch.zeros((P, ps, 416), dtype=torch.uint8, device=DEV)
+    assert cache.numel() > 2**32
+    g = torch.Generator().manual_seed(18)
+    last = cache[-8:]
+    pool = R.q4_pack(torch.randn((8 * ps, 576), generator=g).to(torch.bfloat16))
+    last.copy_(torch.from_numpy(pool).view(8, ps, 416))
+    rows, st = _rows(rg.T, 19), _status()
+    dsa.dsa_q4_write_back(rows, cache, *meta_to(rg, DEV), dev_status=st)
+    slots = _slots(rg)
+    assert slots.min() * 416 > 2**32
+    out = dsa.dsa_q4_read_rows(cache, torch.from_numpy(slots.astype(np.int32)).to(DEV), dev_status=st)
+    flat = R.q4_values(last.cpu().numpy().reshape(-1, 416))
+    assert np.array_equal(R.f64(out), R.q4_values(R.q4_pack(rows)), equal_nan=True)
+    assert np.array_equal(R.f64(out), flat[slots - (P - 8) * ps], equal_nan=True)
+    # attention over rows that were there before: positions below the new ones
+    q = torch.randn((rg.T, 16, 576), generator=g).to(torch.bfloat16)
+    sel = np.tile(np.arange(0, 165, 5, dtype=np.int32), (rg.T, 1))
+    o, lse = dsa.dsa_sparse_mla_decode_q4(q.to(DEV), cache, *meta_to(rg, DEV), torch.from_numpy(sel).to(DEV), unit=1,
+                                          sm_scale=DI.SM_SCALE, want_lse=True, dev_status=st)
+    assert st.item() == 0
+    rg.page_indices = (rg.page_indices - (P - 8)).astype(np.int32)
+    R.check_attend(o, lse, R.attend(R.f64(q), R.token_keys(rg, flat, _positions(sel, 1)), DI.SM_SCALE), "far rows")

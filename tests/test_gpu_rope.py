@@ -132,3 +132,32 @@ def test_frequencies(dsa):
     f, m = dsa.dsa_rope_freqs(64)
     want = 10000.0 ** (-np.arange(0, 64, 2) / 64)
     assert m == 1.0 and np.allclose(f.numpy(), want, rtol=1e-15, atol=0)
+
+
+def test_offsets_past_32_bits(dsa):
+    """Rows 2^31 + 64 elements apart in both tensors."""
+    buf = torch.zeros(2**31 + 256, dtype=torch.bfloat16, device="cuda")
+    far = buf.as_strided((2, 1, 64), (2**31 + 64, 64, 1))
+    far.copy_(_x((2, 1, 64), torch.bfloat16, 3))
+    x = far.clone()
+    pos = torch.tensor([77, 1234], dtype=torch.int32, device="cuda")
+    freqs, _ = dsa.dsa_rope_freqs(64, device="cuda")
+    dsa.dsa_rope(dsa.RopeTarget(far), pos, freqs)
+    _check(far, x, pos, freqs, 0, "half", 1.0, False)
+
+
+def test_two_streams_at_once(dsa):
+    """Calls on two streams share nothing."""
+    freqs, _ = dsa.dsa_rope_freqs(64, device="cuda")
+    pos = torch.arange(500, dtype=torch.int32, device="cuda")
+    xs = [_x((500, 8, 64), torch.bfloat16, k) for k in range(2)]
+    ys = [torch.empty_like(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, x, y in zip(streams, xs, ys):
+            with torch.cuda.stream(s):
+                dsa.dsa_rope(dsa.RopeTarget(x, y), pos, freqs)
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        _check(y, x, pos, freqs, 0, "half", 1.0, False)

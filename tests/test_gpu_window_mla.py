@@ -123,3 +123,17 @@ def test_pages_between_sinks_and_window_are_not_read(dsa):
     meta[3] = torch.from_numpy(pages).to(DEV)
     o2, lse2, st = _run(dsa, wl, 130, 4, kv=kv, meta=meta)
     assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_offsets_past_32_bits(dsa):
+    """A cache of 4.8 GB whose requests lie at its end."""
+    wl = DI.random_small(19, [1, 3], [400, 200], H=16)
+    rg, P = wl.rg, 65536
+    big = torch.zeros((P, 64, 576), dtype=torch.bfloat16, device=DEV)
+    assert big.numel() * 2 > 2**32
+    big[P - rg.num_pages:] = wl.kv[0].to(DEV)
+    meta = meta_to(rg, DEV)
+    meta[3] = meta[3] + (P - rg.num_pages)
+    o, lse = _check(dsa, wl, 100, 4)
+    o2, lse2, st = _run(dsa, wl, 100, 4, kv=big, meta=meta)
+    assert st == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
