@@ -40,6 +40,7 @@ struct AttendParams {
   int32_t* dev_status;
   const uint8_t* kv4;  // run_attend_cache: the 4-bit cache [P, ps, kRow4Bytes], in the place of kv
   int sinks;           // dense mode with a window: the first `sinks` positions stay visible
+  int pack;            // neighbouring tokens of a CTA (set by run_attend_cache)
 };
 
 int attend_num_splits(int T, int H, int K, int mode);

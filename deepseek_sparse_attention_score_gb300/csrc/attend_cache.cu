@@ -3,7 +3,9 @@
 // mathematics and the split of the work are attend.cu's:
 //   S = Q K^T over 576 dims, online softmax, O += P V, V = the first 512 dims,
 // one CTA per query token, 128 heads and half of the value columns, in tiles
-// of 64 keys. 4-bit keys are 416-byte rows that sixteen copier warps turn into
+// of 64 keys. With 64 heads or fewer, neighbouring tokens of a request share a
+// CTA of the window form, 128 rows of (token, head): they see nearly the same
+// keys, and each row masks its own. 4-bit keys are 416-byte rows that sixteen copier warps turn into
 // bf16 column blocks on their way to shared memory; bf16 keys are runs of 32
 // rows of a page, fetched by one thread as TMA boxes.
 //
@@ -35,6 +37,7 @@ constexpr int kSubKeys = 32;  // keys resolved per step
 constexpr int kTile = 64, kSteps = kTile / kSubKeys;
 constexpr int kRing = 8;       // tiles resolved ahead (their rows are pulled into L2 meanwhile)
 constexpr int kMaxSplits = 8;  // CTAs of a portable cluster
+constexpr int kNoKeys = 0x7fffff00;  // the position of a run that holds no keys
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
 constexpr int kHeads = 128;
 
@@ -48,18 +51,20 @@ constexpr int OFF_Q = 0;  // dims 256-575
 constexpr int OFF_K = OFF_Q + 5 * kQBlk;
 constexpr int OFF_V = OFF_K + 2 * kKStage;
 constexpr int OFF_RING = OFF_V + 2 * kVStage;           // int32 [kRing][kTile] rows
-constexpr int OFF_MASK = OFF_RING + kRing * kTile * 4;  // uint32 [kRing][kSteps]
+constexpr int OFF_MASK = OFF_RING + kRing * kTile * 4;  // uint32 [kRing][kSteps]; bf16: a run's first position
 constexpr int OFF_END = OFF_MASK + kRing * kSteps * 4;  // uint32 [kRing]
 constexpr int OFF_BAR = OFF_END + kRing * 4;
 constexpr int kNumBars = 2 * kRing + 15;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;  // TMEM address, abort flag
-constexpr int kSmem = OFF_MISC + 16;
+constexpr int kSmem = OFF_MISC + 32;  // and the CTA's tokens
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_BAR % 8 == 0, "alignment");
 static_assert(4 * kQBlk <= 2 * kKStage, "the queries for TMEM land in the key stages");
 // after the last MMA: fp32 partial rows of 256 value columns, padded against
 // bank conflicts, their log-sums, and the weights of the splits
 constexpr int kStageLd = 256 + 4;
+constexpr int kOutLd = 512 + 16;  // bytes of a staged bf16 row
+static_assert(kHeads * kOutLd <= 2 * kKStage, "bf16 rows are staged in the key stages");
 constexpr int OFF_LSE = kHeads * kStageLd * 4;
 constexpr int OFF_WTS = OFF_LSE + kHeads * 4;
 static_assert(OFF_WTS + kMaxSplits * kHeads * 4 <= OFF_RING, "split stage");
@@ -104,14 +109,15 @@ struct KeyList {
   int phys, first_key;          // this lane's page (-1: none) and its first position
   int cur_phys, cur_key, sub;   // the page being walked and its next run
 
-  __device__ void init(const AttendParams& prm, int tok, int split) {
+  // the list of tokens tok .. tok + ntok - 1 of one request (ntok > 1: bf16)
+  __device__ void init(const AttendParams& prm, int tok, int ntok, int split) {
     p = &prm;
     t = tok;
     lg = 31 - __clz(prm.ps);
     const int s = seq_of_token_warp(prm.cu_q_lens, prm.S, tok);
     const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, 0x3fffffff, tok,
                                    prm.dev_status, s);
-    n_vis = g.n_vis;
+    n_vis = max(0, min(g.kv_len, g.pos + ntok));  // of the last token
     page_base = g.page_base;
     left = pend = 0;
     sub = prm.ps / kSubKeys;
@@ -143,9 +149,10 @@ struct KeyList {
     return pg;
   }
 
-  // The next 32 keys: this lane's row (-1: masked) and the mask of the rows;
-  // base: the first row of a run. False: the share is exhausted.
-  __device__ bool next(int& row, uint32_t& mask, int& base) {
+  // The next 32 keys: this lane's row (-1: masked) and the mask of the rows
+  // (bf16: of those that any token sees); base: the first row of a run and
+  // pos0: its position. False: the share is exhausted.
+  __device__ bool next(int& row, uint32_t& mask, int& base, int& pos0) {
     if (kCache == kCache4Bit && p->mode == kModeToken) return next_tokens(row, mask);
     while (true) {
       if (sub < (p->ps >> 5)) {
@@ -153,6 +160,7 @@ struct KeyList {
         bool v = key < n_vis;
         if constexpr (kCache == kCacheBf16) v = v && (key >= key_lo || key < p->sinks);
         base = (cur_phys << lg) + sub * kSubKeys;
+        pos0 = cur_key + sub * kSubKeys;
         ++sub;
         row = v ? (cur_phys << lg) + k0 : -1;
         mask = __ballot_sync(0xffffffffu, v);
@@ -423,10 +431,39 @@ __device__ __forceinline__ void copy_boxes(const CUtensorMap* kvmap, int half, u
   }
 }
 
+// The g-th run of up to G neighbouring tokens of one request, request by
+// request: its first token and length (0: there are fewer runs). One warp.
+__device__ __forceinline__ int2 token_run(const AttendParams& p, int g, int G) {
+  const int lane = lane_id();
+  long long before = 0;  // runs of the requests before
+  for (int s0 = 0; s0 < p.S; s0 += 32) {
+    const int s = s0 + lane;
+    const int q0 = s < p.S ? __ldg(p.cu_q_lens + s) : 0, q1 = s < p.S ? __ldg(p.cu_q_lens + s + 1) : 0;
+    const int n = q1 > q0 && q0 >= 0 ? (int)(((long long)q1 - q0 + G - 1) / G) : 0;
+    long long x = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    const long long k = g - (before + x - n);  // the run's number within this lane's request
+    const uint32_t has = __ballot_sync(0xffffffffu, k >= 0 && k < n);
+    if (has) {
+      const int src = __ffs(has) - 1;
+      const long long first = q0 + k * G;
+      const int t0 = (int)__shfl_sync(0xffffffffu, first, src);
+      const int len = (int)__shfl_sync(0xffffffffu, min((long long)G, min((long long)q1, (long long)p.T) - first), src);
+      return make_int2(t0, max(len, 0));
+    }
+    before += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return make_int2(0, 0);
+}
+
 template <int kCache>
 __global__ void __launch_bounds__(kThreads<kCache>, 1)
     cache_mla_kernel(const AttendParams prm, const __grid_constant__ CUtensorMap kvmap,
-                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
+                     const __grid_constant__ CUtensorMap qmap) {
   constexpr bool k4 = kCache == kCache4Bit;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // in every CTA alike
@@ -436,7 +473,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   griddep_launch_dependents();
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   const int half = blockIdx.x & 1, h0 = (blockIdx.x >> 1) * kHeads;
-  const int t = (int)blockIdx.y, split = blockIdx.z;  // the split is the rank in the cluster
+  const int split = blockIdx.z;  // the rank in the cluster
   int* ring_rows = reinterpret_cast<int*>(smem + OFF_RING);
   volatile uint32_t* ring_mask = reinterpret_cast<volatile uint32_t*>(smem + OFF_MASK);
   volatile uint32_t* ring_end = reinterpret_cast<volatile uint32_t*>(smem + OFF_END);
@@ -471,25 +508,40 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   tc_fence_after();
   griddep_wait();
   const uint32_t tmem = *tmem_slot;
-  if (t >= __ldg(prm.cu_q_lens + prm.S)) {  // a padding row behind the last request: left as it is
+  // this CTA's tokens t .. t + ntok - 1
+  int t = (int)blockIdx.y, ntok = t < __ldg(prm.cu_q_lens + prm.S) ? 1 : 0;
+  if constexpr (!k4) {
+    if (prm.pack > 1) {
+      volatile int* tokens = reinterpret_cast<volatile int*>(smem + OFF_MISC + 16);
+      if (warp == 0) {
+        const int2 run = token_run(prm, t, prm.pack);
+        if (lane == 0) tokens[0] = run.x, tokens[1] = run.y;
+      }
+      __syncthreads();
+      t = tokens[0];
+      ntok = tokens[1];
+    }
+  }
+  if (ntok == 0) {  // a padding row behind the last request: left as it is
     if (warp == 0) tmem_dealloc(tmem, kTmemCols);
     return;
   }
+  // rows r of the CTA are rows first_row + r of [T * H], below `rows`
+  const int first_row = t * prm.H + h0, rows = min(kHeads, ntok * prm.H - h0);
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;  // this warp's TMEM lanes
-  const int r = (warp & 3) * 32 + lane;                          // and this thread's: a head row
+  const int r = (warp & 3) * 32 + lane;                          // and this thread's: a row
   if (tid == 0) {
-    // query rows h0 .. h0 + 127 of token t (rows past H belong to the next
-    // token or lie past the tensor; their outputs are never stored): dims
-    // 0-255 wait in the unused key stages until they are moved into TMEM
+    // 128 query rows (those past `rows` belong to other tokens or lie past
+    // the tensor; their outputs are never stored): dims 0-255 wait in the unused key stages until they are moved into TMEM
     mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
 #pragma unroll 1
     for (int c = 0; c < 9; ++c)
       tma_load_2d(smem + (c < 4 ? OFF_K + c * kQBlk : OFF_Q + (c - 4) * kQBlk), &qmap, br.qbar(), c * 64,
-                  t * prm.H + h0);
+                  first_row);
   }
   // the generator resolves its first keys while the queries arrive
   KeyList<kCache> gen;
-  if (warp == 1) gen.init(prm, t, split);
+  if (warp == 1) gen.init(prm, t, ntok, split);
   if (warp >= 4 && warp < 8) {
     if (mbar_wait(br.qbar(), 0, abort_flag)) {
 #pragma unroll 1
@@ -527,9 +579,9 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       bool any = false;
 #pragma unroll 1
       for (int s = 0; s < kSteps; ++s) {
-        int row = -1, base = -kSubKeys;
+        int row = -1, base = -kSubKeys, pos0 = kNoKeys;
         uint32_t mask = 0;
-        if (more && !(more = gen.next(row, mask, base))) row = -1, mask = 0, base = -kSubKeys;
+        if (more && !(more = gen.next(row, mask, base, pos0))) row = -1, mask = 0, base = -kSubKeys, pos0 = kNoKeys;
         any |= mask != 0;
         if constexpr (k4) {
           ring_rows[slot * kTile + s * kSubKeys + lane] = row;
@@ -543,7 +595,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
         } else if (lane == 0) {
           ring_rows[slot * kTile + s] = base;  // the step's first row
         }
-        if (lane == 0) ring_mask[slot * kSteps + s] = mask;
+        if (lane == 0) ring_mask[slot * kSteps + s] = k4 ? mask : (uint32_t)pos0;
       }
       if (lane == 0) ring_end[slot] = any ? 0u : 1u;
       __syncwarp();
@@ -559,7 +611,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       copy_boxes(&kvmap, half, smem, ring_rows, ring_end, br, abort_flag);
   } else if (warp >= 4) {
     // --------------------------------------------------------------- softmax
-    // one head per thread; tiles of 4-bit keys hold them times 2^-7 (copy_keys)
+    // one row per thread; tiles of 4-bit keys hold them times 2^-7 (copy_keys)
     const bool capped = !k4 && prm.soft_cap_on;
     const float sl2 = k4 ? prm.scale_log2 * 128.f : capped ? 1.f : prm.scale_log2;
     auto load_s = [&](uint32_t ts, uint32_t (&s)[32]) {
@@ -571,6 +623,23 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
           s[j] = __float_as_uint(prm.cap_log2 * tanh_approx(__uint_as_float(s[j]) * prm.inv_cap_scale));
       }
     };
+    // bf16: this row's visible prefix and window
+    int see = 0, from = 0;
+    if constexpr (!k4) {
+      const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, 0x3fffffff, t,
+                                     nullptr, seq_of_token_warp(prm.cu_q_lens, prm.S, t));
+      const int pos = g.pos + (ntok > 1 ? r / prm.H : 0);
+      see = r < rows ? max(0, min(g.kv_len, pos + 1)) : 0;
+      from = max(0, pos - prm.window + 1);
+    }
+    auto mask_of = [&](uint32_t x) -> uint32_t {
+      if constexpr (k4) return x;
+      auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+      const int p0 = (int)x;
+      return below(see - p0) & (~below(from - p0) | below(prm.sinks - p0));
+    };
+    // whether a run is unmasked in every row of the warp
+    auto full = [&](uint32_t mk) -> bool { return k4 ? mk == 0xffffffffu : __all_sync(0xffffffffu, mk == 0xffffffffu); };
     float m_run = -INFINITY, l_run = 0.f;
     int n = 0;
     bool ok = true;
@@ -579,7 +648,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       const int slot = i % kRing;
       if (!(ok = mbar_wait(br.rfull(slot), (i / kRing) & 1, abort_flag))) break;
       if (ring_end[slot]) break;
-      const uint32_t mlo = ring_mask[slot * kSteps], mhi = ring_mask[slot * kSteps + 1];
+      const uint32_t mlo = mask_of(ring_mask[slot * kSteps]), mhi = mask_of(ring_mask[slot * kSteps + 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(br.rempty(slot));
       if (!(ok = mbar_wait(br.sfull(i & 1), (i >> 1) & 1, abort_flag))) break;
@@ -593,7 +662,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
         uint32_t s[32];
         load_s(tS + 32 * h, s);
         const uint32_t mk = h ? mhi : mlo;
-        if (mk == 0xffffffffu) {
+        if (full(mk)) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]) * sl2);
         } else {
@@ -635,7 +704,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
           s[2 * c] = __float_as_uint(ex2_approx(x0));
           s[2 * c + 1] = __float_as_uint(ex2_approx(x1));
         }
-        if (mk != 0xffffffffu) {
+        if (!full(mk)) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) s[j] = ((mk >> j) & 1u) ? s[j] : 0u;
         }
@@ -675,15 +744,13 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       }
     };
     if (prm.nsplit == 1) {
-      // the warp stages its 32 head rows as bf16 in the idle key stages
-      // (swizzled boxes of 64 columns), one lane writes them with TMA stores;
-      // rows past H lie outside the tensor map and are not written
-      uint8_t* stg = smem + OFF_K + (warp & 3) * 16384;
+      // the warp stages its 32 rows as bf16 in the idle key stages and writes
+      // them one contiguous 512-byte row at a time
+      uint8_t* stg = smem + OFF_K + (warp & 3) * (32 * kOutLd);
 #pragma unroll 1
       for (int c0 = 0; c0 < 256; c0 += 32) {
         uint32_t o[32];
         load_o(c0, o);
-        const uint32_t box = smem_u32(stg) + (uint32_t)(c0 / 64) * 4096u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t pk[4];
@@ -693,20 +760,17 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
                                                       __uint_as_float(o[8 * j + 2 * e + 1]) * inv_l);
             pk[e] = *reinterpret_cast<uint32_t*>(&b2);
           }
-          st_shared_v4(box + sw128_offset((uint32_t)lane, (uint32_t)((c0 & 32) / 8 + j)), pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(stg + lane * kOutLd + c0 * 2 + j * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      const int hw = h0 + (warp & 3) * 32;  // first head row of this warp
-      if (lane == 0 && hw < prm.H) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) tma_store_3d(&omap, stg + c * 4096, half * 256 + c * 64, hw, t);
-        bulk_commit();
-        bulk_wait_read();
-      }
-      __syncwarp();
-      if (half == 0 && h0 + r < prm.H && prm.lse) prm.lse[(size_t)t * prm.H + h0 + r] = lse_v;
+      const int w0 = (warp & 3) * 32, nw = min(32, rows - w0);
+      uint16_t* orow = prm.o + ((size_t)first_row + w0) * kDv + half * 256;
+#pragma unroll 8
+      for (int i = 0; i < nw; ++i)
+        reinterpret_cast<uint4*>(orow + (size_t)i * kDv)[lane] =
+            *reinterpret_cast<const uint4*>(stg + i * kOutLd + lane * 16);
+      if (half == 0 && r < rows && prm.lse) prm.lse[(size_t)first_row + r] = lse_v;
     } else {
       // split keys: normalised partial rows and their log-sums in shared
       // memory (the queries' and keys' places, idle after the last PV)
@@ -743,7 +807,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
     __syncwarp();
     cluster_sync_all();
     const int Z = prm.nsplit, share = kHeads / Z, row0 = split * share;
-    const int nrows = max(0, min(share, prm.H - h0 - row0));
+    const int nrows = max(0, min(share, rows - row0));
     const uint32_t smem0 = smem_u32(smem);
     float* wts = reinterpret_cast<float*>(smem + OFF_WTS);
     if (tid < nrows) {
@@ -764,10 +828,10 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
 #pragma unroll
       for (int z = 0; z < kMaxSplits; ++z) wts[z * kHeads + tid] = lz[z] * inv;
       if (half == 0 && prm.lse)
-        prm.lse[(size_t)t * prm.H + h0 + row0 + tid] = some ? mx + logf(tot) : -INFINITY;
+        prm.lse[(size_t)first_row + row0 + tid] = some ? mx + logf(tot) : -INFINITY;
     }
     __syncthreads();
-    uint16_t* orow = prm.o + ((size_t)t * prm.H + h0 + row0) * kDv + half * 256;
+    uint16_t* orow = prm.o + ((size_t)first_row + row0) * kDv + half * 256;
 #pragma unroll 1
     for (int i = warp; i < nrows; i += kThreads<kCache> / 32) {
       float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -797,7 +861,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   }
 }
 
-using Kernel = void (*)(AttendParams, CUtensorMap, CUtensorMap, CUtensorMap);
+using Kernel = void (*)(AttendParams, CUtensorMap, CUtensorMap);
 
 // How many clusters of 2^lz CTAs the current device runs at once (a cluster
 // lies in one GPC, so this is less than SMs / 2^lz); asked once per device.
@@ -830,8 +894,7 @@ int clusters_at_once(Kernel kern, bool k4, int lz) {
 // request, z = 1 / 2 / 4 / 8: 128 keys 10.9 / 11.3 / 12.3 / 14.5 us, 256 keys
 // 15.0 / 13.1 / 12.5 / 14.7, 1024 keys 35 / 23.7 / 18.0 / 16.5; 8 requests of
 // 2048 keys 64 / 39 / 27.9 / 46.9 (16 clusters of eight are more than fit).
-int num_splits(Kernel kern, bool k4, int T, int H, long long keys) {
-  const long long clusters = 2LL * T * ((H + kHeads - 1) / kHeads);
+int num_splits(Kernel kern, bool k4, long long clusters, long long keys) {
   int lz = 0;
   while (lz < 3 && (keys >> (lz + 1)) >= (lz == 2 ? 128 : 64) && clusters <= clusters_at_once(kern, k4, lz + 1)) ++lz;
   return 1 << lz;
@@ -842,16 +905,22 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
   if (prm.T == 0 || prm.H == 0) return DSA_OK;
   if (prm.ps < kSubKeys || (prm.ps & (prm.ps - 1))) return DSA_ERR_UNSUPPORTED;  // pages: 2^n rows, n >= 5
   const bool k4 = prm.kv4 != nullptr;
-  CUtensorMap kvmap{}, qmap, omap;  // kvmap: the bf16 cache; 4-bit rows are read without one
+  CUtensorMap kvmap{}, qmap;  // kvmap: the bf16 cache; 4-bit rows are read without one
   if (!k4 && !encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, kSubKeys, kDk))
     return DSA_ERR_CUDA;
   if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kHeads, kDk)) return DSA_ERR_CUDA;
-  if (!encode_bf16_3d(&omap, prm.o, kDv, (uint64_t)prm.H, (uint64_t)prm.T, 32)) return DSA_ERR_CUDA;
   const Kernel kern = k4 ? cache_mla_kernel<kCache4Bit> : cache_mla_kernel<kCacheBf16>;
   set_smem_attr_once(reinterpret_cast<const void*>(kern), kSmem);
-  prm.nsplit = num_splits(kern, k4, prm.T, prm.H, (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps));
+  // Neighbouring tokens share a CTA where they fit and a request has two on
+  // average: 2049 tokens, window 1024, 16 heads: 137 us with eight tokens a
+  // CTA, 894 with one. A CTA finds its run by a scan over the requests, 32 at a
+  // time, which 1024 of them bound.
+  prm.pack = !k4 && prm.H <= kHeads / 2 && prm.S <= 1024 && prm.T >= 2 * prm.S ? kHeads / prm.H : 1;
+  const long long runs = std::min<long long>(prm.T, (prm.T + (long long)prm.S * (prm.pack - 1)) / prm.pack);
+  const int cols = 2 * ((prm.H + kHeads - 1) / kHeads);
+  prm.nsplit = num_splits(kern, k4, cols * runs, (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * ((prm.H + kHeads - 1) / kHeads), prm.T, prm.nsplit);
+  cfg.gridDim = dim3(cols, (unsigned)runs, prm.nsplit);
   cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16>);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
@@ -864,7 +933,7 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
   attr[1].val.clusterDim.z = prm.nsplit;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, prm, kvmap, qmap, omap) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, prm, kvmap, qmap) != cudaSuccess) {
     (void)cudaGetLastError();
     return DSA_ERR_CUDA;
   }

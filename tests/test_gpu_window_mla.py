@@ -65,6 +65,22 @@ def test_heads_and_one_token(dsa, H):
     _check(dsa, DI.random_small(H + 1, [2], [900], H=H), 333, 5)
 
 
+@pytest.mark.parametrize("H", [1, 3, 43, 64, 65])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 1), (100, 4), (0, 0), (300, 70)])
+def test_neighbouring_tokens_share_a_block(dsa, H, window, sinks):
+    """Up to 64 heads: runs of 128 / H tokens, at the ends of requests shorter
+    ones; a row sees its own window only."""
+    _check(dsa, DI.random_small(40 + H, [70, 3, 0, 131, 1], [400, 3, 64, 131, 200], H=H, page_size=32), window, sinks)
+
+
+def test_many_requests_of_two_tokens(dsa):
+    n = 1030  # past the requests that a block searches: one token each
+    wl = DI.random_small(45, [2] * n, [2 + s % 40 for s in range(n)], H=2, page_size=32)
+    _check(dsa, wl, 8, 2)
+    wl = DI.random_small(46, [3] * 200, [3 + s % 40 for s in range(200)], H=2, page_size=32)
+    _check(dsa, wl, 8, 2)
+
+
 @pytest.mark.parametrize("window,sinks", [(1000, 4), (700, 200), (64, 64)])
 def test_split_over_ctas(dsa, window, sinks):
     wl = DI.random_small(11, [1, 1], [2600, 1500], H=24)
