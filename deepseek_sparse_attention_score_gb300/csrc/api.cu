@@ -444,6 +444,7 @@ int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, i
   if (rc) return rc;
   if (max_kv < 1 || sliding_window < 0 || num_sinks < 0) return DSA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(sm_scale) || !std::isfinite(soft_cap) || soft_cap < 0.f) return DSA_ERR_INVALID_ARGUMENT;
+  if ((long long)T * H >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
   if (T == 0 || H == 0) return DSA_OK;
   AttendParams prm{};
   prm.q = q;
@@ -492,7 +493,7 @@ int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8
   if (rc) return rc;
   if (K < 1 || (T > 0 && !sel)) return DSA_ERR_INVALID_ARGUMENT;
   if (unit != 1 && unit != ps) return DSA_ERR_INVALID_ARGUMENT;
-  if (K > (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  if (K > (1 << 30) || (long long)T * H >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
   AttendParams prm{};
   prm.scale_log2 = sm_scale * 1.4426950408889634f;
   if (!std::isfinite(prm.scale_log2 * 128.f)) return DSA_ERR_INVALID_ARGUMENT;  // the kernel's logit factor

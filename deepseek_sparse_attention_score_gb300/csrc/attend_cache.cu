@@ -5,9 +5,9 @@
 // one CTA per query token, 128 heads and half of the value columns, in tiles
 // of 64 keys. With 64 heads or fewer, neighbouring tokens of a request share a
 // CTA of the window form, 128 rows of (token, head): they see nearly the same
-// keys, and each row masks its own. 4-bit keys are 416-byte rows that sixteen copier warps turn into
-// bf16 column blocks on their way to shared memory; bf16 keys are runs of 32
-// rows of a page, fetched by one thread as TMA boxes.
+// keys, and each row masks its own. 4-bit keys are 416-byte rows that sixteen
+// copier warps turn into bf16 column blocks on their way to shared memory;
+// bf16 keys are runs of 32 rows of a page, fetched by one thread as TMA boxes.
 //
 // Roles: warp 0 issues the MMAs, warp 1 resolves the keys (KeyList), warps
 // 4-7 move the queries' first 256 dims into TMEM and run the softmax, others
@@ -39,7 +39,7 @@ constexpr int kRing = 8;       // tiles resolved ahead (their rows are pulled in
 constexpr int kMaxSplits = 8;  // CTAs of a portable cluster
 constexpr int kNoKeys = 0x7fffff00;  // the position of a run that holds no keys
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
-constexpr int kHeads = 128;
+constexpr int kHeads = 128;  // rows of a CTA: heads, or heads of neighbouring tokens
 
 // shared memory: 128-byte-swizzled blocks of 64 columns. The queries' dims
 // 0-255 live in TMEM. A tile is nine blocks of keys: the four of this CTA's
@@ -234,9 +234,9 @@ struct Bars {
   __device__ __forceinline__ uint64_t* fin() const { return b + 2 * kRing + 14; }            // commit while unwinding
 };
 
-// The MMA issuer (one converged warp). Per tile i: QK^T(i) over the K part, then over
-// the V part, then PV(i - 1), so that the softmax of a tile runs beside the
-// next tile's QK^T.
+// The MMA issuer (one converged warp). Per tile i: QK^T(i) over the K part,
+// then over the V part, then PV(i - 1), so that the softmax of a tile runs
+// beside the next tile's QK^T.
 __device__ __forceinline__ void issue_mmas(int half, uint32_t tmem, uint32_t smem0, const Bars& br,
                                            volatile const uint32_t* ring_end, volatile int* abort_flag) {
   const uint32_t lead = elect_one();
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       __syncwarp();
       const int w0 = (warp & 3) * 32, nw = min(32, rows - w0);
       uint16_t* orow = prm.o + ((size_t)first_row + w0) * kDv + half * 256;
-#pragma unroll 8
+#pragma unroll 4
       for (int i = 0; i < nw; ++i)
         reinterpret_cast<uint4*>(orow + (size_t)i * kDv)[lane] =
             *reinterpret_cast<const uint4*>(stg + i * kOutLd + lane * 16);

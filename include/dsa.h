@@ -489,8 +489,8 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
  * page units, one selection per token.
  * An entry listed twice counts twice. T may be an upper bound: rows of o and
  * lse from cu_q_lens[S] on are left as they are.
- * Supported: as dsa_sparse_mla_decode, K <= 2^30, |sm_scale| * 185 finite in
- * fp32.
+ * Supported: as dsa_sparse_mla_decode, K <= 2^30, T * H < 2^31, |sm_scale| *
+ * 185 finite in fp32.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8_t* cache,
                                      const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
@@ -505,13 +505,15 @@ DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, con
  * position that is both counts once). With sliding_window == 0 every position
  * is visible. T may be an upper bound: rows of o and lse from cu_q_lens[S] on
  * are left as they are.
- * Only pages that hold a visible position are read, in runs of 32 rows (see
- * the finite-rows rule of dsa_sparse_mla_decode): a cache may drop the pages
- * between the sinks and the window.
+ * Only pages that hold a visible position are read, in runs of 32 rows: a
+ * cache may drop the pages between the sinks and the window. The finite-rows
+ * rule of dsa_sparse_mla_decode holds for these runs and, with H <= 64, for
+ * those of the up to 128 / H neighbouring tokens of the same request, which
+ * are computed together.
  *   max_kv  as dsa_dense_mla
  *   ws      taken as there and not used (may be NULL): split key lists are
  *           merged inside clusters
- * Supported: as dsa_dense_mla; num_sinks >= 0.
+ * Supported: as dsa_dense_mla; num_sinks >= 0, T * H < 2^31.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
                            const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,

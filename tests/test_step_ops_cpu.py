@@ -113,7 +113,7 @@ def _attend(**kw):
     (dict(K=0), INVALID), (dict(K=(1 << 30) + 1), UNSUPPORTED), (dict(sel=None), INVALID),
     (dict(sm_scale=math.inf), INVALID),
     (dict(sm_scale=3e36), INVALID), (dict(cache=_p(4104)), ALIGNMENT), (dict(cache=None), INVALID),
-    (dict(o=None), INVALID), (dict(T=65536, S=65536), UNSUPPORTED), (dict(H=-1), INVALID), (dict(H=0), OK),
+    (dict(o=None), INVALID), (dict(T=65536, S=65536), UNSUPPORTED), (dict(T=65535, H=32769), UNSUPPORTED), (dict(H=-1), INVALID), (dict(H=0), OK),
     (dict(T=0, S=0, P=0, PTW=0), OK),
 ])
 def test_decode_q4_host_checks(dsa, kw, code):
@@ -129,7 +129,7 @@ def _window(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(cap=-1.0), INVALID), (dict(cap=math.inf), INVALID),
     (dict(max_kv=0), INVALID), (dict(ps=100), UNSUPPORTED), (dict(kv=_p(4100)), ALIGNMENT),
-    (dict(row_stride=600), UNSUPPORTED), (dict(sm_scale=math.nan), INVALID), (dict(T=0, S=0, P=0, PTW=0), OK),
+    (dict(T=65535, H=32769), UNSUPPORTED), (dict(row_stride=600), UNSUPPORTED), (dict(sm_scale=math.nan), INVALID), (dict(T=0, S=0, P=0, PTW=0), OK),
 ])
 def test_window_host_checks(dsa, kw, code):
     assert dsa.lib().dsa_window_mla(*_window(**kw)) == code
