@@ -462,6 +462,7 @@ DSA_API int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor,
  * goes to the slot of its position, every other row is left untouched, and a
  * token without a slot sets DSA_STATUS_BAD_METADATA and is skipped. T may be
  * an upper bound: rows from cu_q_lens[S] on are padding and are ignored.
+ * Tokens write distinct rows whenever the metadata is valid.
  *   rows   bf16 [T, src_stride], the first 576 columns
  *   cache  [P, ps, 416] bytes
  * dsa_q4_read_rows writes the values of N slots (page * ps + row, as
