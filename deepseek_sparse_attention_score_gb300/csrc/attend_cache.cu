@@ -3,11 +3,17 @@
 // mathematics and the split of the work are attend.cu's:
 //   S = Q K^T over 576 dims, online softmax, O += P V, V = the first 512 dims,
 // one CTA per query token, 128 heads and half of the value columns, in tiles
-// of 64 keys. With 64 heads or fewer, neighbouring tokens of a request share a
-// CTA of the window form, 128 rows of (token, head): they see nearly the same
-// keys, and each row masks its own. 4-bit keys are 416-byte rows that sixteen
-// copier warps turn into bf16 column blocks on their way to shared memory;
-// bf16 keys are runs of 32 rows of a page, fetched by one thread as TMA boxes.
+// of 64 keys. With 64 heads or fewer half of those 128 rows would be empty:
+//  - neighbouring tokens of a request share a CTA of the window form, 128 rows
+//    of (token, head): they see nearly the same keys, and each row masks its own;
+//  - a token by itself takes one CTA instead of two (kBoth): its queries stand
+//    in rows 0-63 and again in rows 64-127, P is written twice, once with the
+//    lower and once with the upper rows zero, and PV adds lower P times the
+//    first 256 value columns and upper P times the others into the same TMEM
+//    columns. QK^T, the keys' fetch and their unpacking happen once.
+// 4-bit keys are 416-byte rows that sixteen copier warps turn into bf16 column
+// blocks on their way to shared memory; bf16 keys are runs of 32 rows of a page,
+// fetched by one thread as TMA boxes.
 //
 // Roles: warp 0 issues the MMAs, warp 1 resolves the keys (KeyList), warps
 // 4-7 move the queries' first 256 dims into TMEM and run the softmax, others
@@ -236,14 +242,18 @@ struct Bars {
 
 // The MMA issuer (one converged warp). Per tile i: QK^T(i) over the K part,
 // then over the V part, then PV(i - 1), so that the softmax of a tile runs
-// beside the next tile's QK^T.
+// beside the next tile's QK^T. With kBoth PV reads the K part as well, which
+// then stays as long as the V part.
+template <bool kBoth>
 __device__ __forceinline__ void issue_mmas(int half, uint32_t tmem, uint32_t smem0, const Bars& br,
                                            volatile const uint32_t* ring_end, volatile int* abort_flag) {
   const uint32_t lead = elect_one();
   const uint64_t dq = make_sdesc(smem0 + OFF_Q, 16, 1024, kSwizzle128B);
   const uint64_t dk = make_sdesc(smem0 + OFF_K, 16, 1024, kSwizzle128B);
   const uint64_t dv = make_sdesc(smem0 + OFF_V, 16, 1024, kSwizzle128B);
-  const uint64_t dvn = make_sdesc(smem0 + OFF_V, kBlk, 1024, kSwizzle128B);  // MN-major: blocks kBlk apart
+  // MN-major, as operands of PV: blocks kBlk apart
+  const uint64_t dkn = make_sdesc(smem0 + OFF_K, kBlk, 1024, kSwizzle128B);
+  const uint64_t dvn = make_sdesc(smem0 + OFF_V, kBlk, 1024, kSwizzle128B);
   // N column blocks of keys from b against the query blocks in TMEM (0-3), or
   // in shared memory from a
   auto blocks_ts = [&](uint32_t tS, uint64_t b, uint32_t acc) {
@@ -281,11 +291,11 @@ __device__ __forceinline__ void issue_mmas(int half, uint32_t tmem, uint32_t sme
       fence_proxy_async_smem();
       tc_fence_after();
       // value half 0: dims 256-575 are the K part, dims 0-255 the V part;
-      // half 1: dims 0-255 and the rotary block, then dims 256-511
+      // half 1 and kBoth: dims 0-255 and the rotary block, then dims 256-511
       if (half) blocks_ts(tS, kb, 0u);
       else blocks_ss(tS, dq, kb, 0u, Four{});
       blocks_ss(tS, dq + 4 * (kQBlk >> 4), kb + 4 * (kBlk >> 4), 1u, One{});
-      commit(br.empty(0, st));
+      if (!kBoth) commit(br.empty(0, st));
       issued = true;
       if (!(ok = wait(br.full(1, st), ph))) break;
       fence_proxy_async_smem();
@@ -299,10 +309,16 @@ __device__ __forceinline__ void issue_mmas(int half, uint32_t tmem, uint32_t sme
       if (!(ok = wait(br.pfull(sj), (j >> 1) & 1))) break;
       tc_fence_after();
       const uint32_t tP = tmem + kColS + (uint32_t)sj * kTile;
-      const uint64_t vb = dvn + (uint64_t)(sj * (kVStage >> 4));
+      auto pv = [&](uint32_t a, uint64_t b, uint32_t acc) {
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        umma_bf16_ts_lead(lead, tmem + kColO, tP + k * 8, vb + (uint64_t)(k * 128), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+        for (int k = 0; k < kTile / 16; ++k, acc = 1u)
+          umma_bf16_ts_lead(lead, tmem + kColO, a + k * 8, b + (uint64_t)(k * 128), kIdescPV, acc);
+      };
+      if (kBoth) {  // the K part holds the first 256 value columns
+        pv(tP, dkn + (uint64_t)(sj * (kKStage >> 4)), j > 0 ? 1u : 0u);
+        commit(br.empty(0, sj));
+      }
+      pv(tP + (kBoth ? 32 : 0), dvn + (uint64_t)(sj * (kVStage >> 4)), kBoth || j > 0 ? 1u : 0u);
       commit(br.empty(1, sj));
       commit(br.pvdone());
     }
@@ -460,7 +476,8 @@ __device__ __forceinline__ int2 token_run(const AttendParams& p, int g, int G) {
   return make_int2(0, 0);
 }
 
-template <int kCache>
+// kBoth: H <= 64, a CTA has both value halves
+template <int kCache, bool kBoth>
 __global__ void __launch_bounds__(kThreads<kCache>, 1)
     cache_mla_kernel(const AttendParams prm, const __grid_constant__ CUtensorMap kvmap,
                      const __grid_constant__ CUtensorMap qmap) {
@@ -472,7 +489,9 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   }
   griddep_launch_dependents();
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
-  const int half = blockIdx.x & 1, h0 = (blockIdx.x >> 1) * kHeads;
+  constexpr int kRows = kBoth ? kHeads / 2 : kHeads;  // output rows of the CTA
+  // kBoth loads and multiplies as value half 1 does
+  const int half = kBoth ? 1 : blockIdx.x & 1, h0 = kBoth ? 0 : (blockIdx.x >> 1) * kHeads;
   const int split = blockIdx.z;  // the rank in the cluster
   int* ring_rows = reinterpret_cast<int*>(smem + OFF_RING);
   volatile uint32_t* ring_mask = reinterpret_cast<volatile uint32_t*>(smem + OFF_MASK);
@@ -527,17 +546,20 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
     return;
   }
   // rows r of the CTA are rows first_row + r of [T * H], below `rows`
-  const int first_row = t * prm.H + h0, rows = min(kHeads, ntok * prm.H - h0);
+  const int first_row = t * prm.H + h0, rows = min(kRows, ntok * prm.H - h0);
+  auto value_half = [&](int r) { return kBoth ? r / kRows : half; };  // of TMEM lane r
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;  // this warp's TMEM lanes
   const int r = (warp & 3) * 32 + lane;                          // and this thread's: a row
   if (tid == 0) {
-    // 128 query rows (those past `rows` belong to other tokens or lie past
-    // the tensor; their outputs are never stored): dims 0-255 wait in the unused key stages until they are moved into TMEM
+    // the query rows, with kBoth twice (those past `rows` belong to other tokens
+    // or lie past the tensor; their outputs are never stored): dims 0-255 wait
+    // in the unused key stages until they are moved into TMEM
     mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
 #pragma unroll 1
     for (int c = 0; c < 9; ++c)
-      tma_load_2d(smem + (c < 4 ? OFF_K + c * kQBlk : OFF_Q + (c - 4) * kQBlk), &qmap, br.qbar(), c * 64,
-                  first_row);
+      for (int k = 0; k < kHeads / kRows; ++k)
+        tma_load_2d(smem + (c < 4 ? OFF_K + c * kQBlk : OFF_Q + (c - 4) * kQBlk) + k * (kQBlk / 2), &qmap, br.qbar(),
+                    c * 64, first_row);
   }
   // the generator resolves its first keys while the queries arrive
   KeyList<kCache> gen;
@@ -566,7 +588,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   tc_fence_after();
 
   if (warp == 0) {
-    issue_mmas(half, __shfl_sync(0xffffffffu, tmem, 0), smem_u32(smem), br, ring_end, abort_flag);
+    issue_mmas<kBoth>(half, __shfl_sync(0xffffffffu, tmem, 0), smem_u32(smem), br, ring_end, abort_flag);
   } else if (warp == 1) {
     // ---------------------------------------------------------- key generator
     bool more = true;
@@ -611,7 +633,8 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       copy_boxes(&kvmap, half, smem, ring_rows, ring_end, br, abort_flag);
   } else if (warp >= 4) {
     // --------------------------------------------------------------- softmax
-    // one row per thread; tiles of 4-bit keys hold them times 2^-7 (copy_keys)
+    // one row per thread (kBoth: two threads, one per value half); tiles of
+    // 4-bit keys hold them times 2^-7 (copy_keys)
     const bool capped = !k4 && prm.soft_cap_on;
     const float sl2 = k4 ? prm.scale_log2 * 128.f : capped ? 1.f : prm.scale_log2;
     auto load_s = [&](uint32_t ts, uint32_t (&s)[32]) {
@@ -629,7 +652,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, 0x3fffffff, t,
                                      nullptr, seq_of_token_warp(prm.cu_q_lens, prm.S, t));
       const int pos = g.pos + (ntok > 1 ? r / prm.H : 0);
-      see = r < rows ? max(0, min(g.kv_len, pos + 1)) : 0;
+      see = r % kRows < rows ? max(0, min(g.kv_len, pos + 1)) : 0;
       from = max(0, pos - prm.window + 1);
     }
     auto mask_of = [&](uint32_t x) -> uint32_t {
@@ -692,8 +715,12 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       }
       const uint64_t sl2x2 = f32x2_pack(sl2, sl2), nm2 = f32x2_pack(-m_use, -m_use);
       uint64_t ps2[2] = {0ull, 0ull};  // packed (0.f, 0.f)
+      // P goes over the halves of S that both passes have read: columns 0-31,
+      // or for the upper value half columns 32-63, starting with S's upper half
+      const int upper = kBoth ? r >> 6 : 0;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int hh = 0; hh < 2; ++hh) {
+        const int h = hh ^ upper;
         uint32_t s[32], pw[16];
         load_s(tS + 32 * h, s);
         const uint32_t mk = h ? mhi : mlo;
@@ -715,7 +742,12 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
           __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);  // P as a bf16 operand
           pw[c] = *reinterpret_cast<uint32_t*>(&b2);
         }
-        tmem_st16(tS + 16 * h, pw);  // over the half of S that both passes have read
+        tmem_st16(tS + 32 * upper + 16 * h, pw);
+      }
+      if (kBoth) {  // the other half's P has zeros in this row
+        const uint32_t zero[16] = {};
+        tmem_st16(tS + 32 * (upper ^ 1), zero);
+        tmem_st16(tS + 32 * (upper ^ 1) + 16, zero);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -764,13 +796,13 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
         }
       }
       __syncwarp();
-      const int w0 = (warp & 3) * 32, nw = min(32, rows - w0);
-      uint16_t* orow = prm.o + ((size_t)first_row + w0) * kDv + half * 256;
+      const int w0 = (warp & 3) * 32 % kRows, nw = min(32, rows - w0);
+      uint16_t* orow = prm.o + ((size_t)first_row + w0) * kDv + value_half((warp & 3) * 32) * 256;
 #pragma unroll 4
       for (int i = 0; i < nw; ++i)
         reinterpret_cast<uint4*>(orow + (size_t)i * kDv)[lane] =
             *reinterpret_cast<const uint4*>(stg + i * kOutLd + lane * 16);
-      if (half == 0 && r < rows && prm.lse) prm.lse[(size_t)first_row + r] = lse_v;
+      if (value_half(r) == 0 && r < rows && prm.lse) prm.lse[(size_t)first_row + r] = lse_v;
     } else {
       // split keys: normalised partial rows and their log-sums in shared
       // memory (the queries' and keys' places, idle after the last PV)
@@ -807,7 +839,8 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
     __syncwarp();
     cluster_sync_all();
     const int Z = prm.nsplit, share = kHeads / Z, row0 = split * share;
-    const int nrows = max(0, min(share, rows - row0));
+    // lanes row0 .. row0 + share - 1; with kBoth they are rows of one value half
+    const int out0 = row0 % kRows, nrows = max(0, min(share, rows - out0)), vh = value_half(row0);
     const uint32_t smem0 = smem_u32(smem);
     float* wts = reinterpret_cast<float*>(smem + OFF_WTS);
     if (tid < nrows) {
@@ -827,11 +860,11 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       const float inv = some ? 1.f / tot : 0.f;
 #pragma unroll
       for (int z = 0; z < kMaxSplits; ++z) wts[z * kHeads + tid] = lz[z] * inv;
-      if (half == 0 && prm.lse)
-        prm.lse[(size_t)first_row + row0 + tid] = some ? mx + logf(tot) : -INFINITY;
+      if (vh == 0 && prm.lse)
+        prm.lse[(size_t)first_row + out0 + tid] = some ? mx + logf(tot) : -INFINITY;
     }
     __syncthreads();
-    uint16_t* orow = prm.o + ((size_t)first_row + row0) * kDv + half * 256;
+    uint16_t* orow = prm.o + ((size_t)first_row + out0) * kDv + vh * 256;
 #pragma unroll 1
     for (int i = warp; i < nrows; i += kThreads<kCache> / 32) {
       float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
@@ -865,11 +898,12 @@ using Kernel = void (*)(AttendParams, CUtensorMap, CUtensorMap);
 
 // How many clusters of 2^lz CTAs the current device runs at once (a cluster
 // lies in one GPC, so this is less than SMs / 2^lz); asked once per device.
-int clusters_at_once(Kernel kern, bool k4, int lz) {
-  static std::atomic<int> cached[64][2][4];
+int clusters_at_once(Kernel kern, bool k4, bool both, int lz) {
+  static std::atomic<int> cached[64][4][4];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = cached[dev][k4][lz].load(std::memory_order_relaxed);
+  std::atomic<int>& slot = cached[dev][2 * both + k4][lz];
+  int n = slot.load(std::memory_order_relaxed);
   if (n) return n - 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1 << lz);
@@ -885,7 +919,7 @@ int clusters_at_once(Kernel kern, bool k4, int lz) {
     (void)cudaGetLastError();
     return 0;
   }
-  cached[dev][k4][lz].store(n + 1, std::memory_order_relaxed);
+  slot.store(n + 1, std::memory_order_relaxed);
   return n;
 }
 
@@ -894,10 +928,11 @@ int clusters_at_once(Kernel kern, bool k4, int lz) {
 // request, z = 1 / 2 / 4 / 8: 128 keys 10.9 / 11.3 / 12.3 / 14.5 us, 256 keys
 // 15.0 / 13.1 / 12.5 / 14.7, 1024 keys 35 / 23.7 / 18.0 / 16.5; 8 requests of
 // 2048 keys 64 / 39 / 27.9 / 46.9 (16 clusters of eight are more than fit).
-int num_splits(Kernel kern, bool k4, long long clusters, long long keys) {
+int log2_splits(Kernel kern, bool k4, bool both, long long clusters, long long keys) {
   int lz = 0;
-  while (lz < 3 && (keys >> (lz + 1)) >= (lz == 2 ? 128 : 64) && clusters <= clusters_at_once(kern, k4, lz + 1)) ++lz;
-  return 1 << lz;
+  while (lz < 3 && (keys >> (lz + 1)) >= (lz == 2 ? 128 : 64) && clusters <= clusters_at_once(kern, k4, both, lz + 1))
+    ++lz;
+  return lz;
 }
 }  // namespace
 
@@ -908,17 +943,36 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
   CUtensorMap kvmap{}, qmap;  // kvmap: the bf16 cache; 4-bit rows are read without one
   if (!k4 && !encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, kSubKeys, kDk))
     return DSA_ERR_CUDA;
-  if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kHeads, kDk)) return DSA_ERR_CUDA;
-  const Kernel kern = k4 ? cache_mla_kernel<kCache4Bit> : cache_mla_kernel<kCacheBf16>;
-  set_smem_attr_once(reinterpret_cast<const void*>(kern), kSmem);
   // Neighbouring tokens share a CTA where they fit and a request has two on
   // average: 2049 tokens, window 1024, 16 heads: 137 us with eight tokens a
   // CTA, 894 with one. A CTA finds its run by a scan over the requests, 32 at a
   // time, which 1024 of them bound.
   prm.pack = !k4 && prm.H <= kHeads / 2 && prm.S <= 1024 && prm.T >= 2 * prm.S ? kHeads / prm.H : 1;
   const long long runs = std::min<long long>(prm.T, (prm.T + (long long)prm.S * (prm.pack - 1)) / prm.pack);
-  const int cols = 2 * ((prm.H + kHeads - 1) / kHeads);
-  prm.nsplit = num_splits(kern, k4, cols * runs, (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps));
+  // One CTA per token of up to 64 heads (kBoth) does twice the PV work and
+  // takes 1.2 to 1.3 times as long, so it is taken where two CTAs per token in
+  // as many splits would not all run at once. Measured with two / one, 4-bit
+  // cache, 2048 keys each, 64 heads: 1 request 19.4 / 23.2 us, 16 requests 26.6
+  // / 30.8, 48 requests 66.4 / 50.4; 16 heads: 8 requests 24.5 / 20.4, 32
+  // requests 39.8 / 30.1; window 4096, 32 requests 67.2 / 56.0.
+  const auto choose = [&](bool one) -> Kernel {
+    if (k4) return one ? cache_mla_kernel<kCache4Bit, true> : cache_mla_kernel<kCache4Bit, false>;
+    return one ? cache_mla_kernel<kCacheBf16, true> : cache_mla_kernel<kCacheBf16, false>;
+  };
+  const long long keys = (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps);
+  bool both = prm.H <= kHeads / 2 && prm.pack == 1;
+  int lz = 0;
+  if (both) {
+    for (const bool one : {false, true}) set_smem_attr_once(reinterpret_cast<const void*>(choose(one)), kSmem);
+    lz = log2_splits(choose(true), k4, true, runs, keys);
+    both = 2 * runs > clusters_at_once(choose(false), k4, false, lz);
+  }
+  const Kernel kern = choose(both);
+  set_smem_attr_once(reinterpret_cast<const void*>(kern), kSmem);
+  const int cols = both ? 1 : 2 * ((prm.H + kHeads - 1) / kHeads);
+  if (!both) lz = log2_splits(kern, k4, false, cols * runs, keys);
+  prm.nsplit = 1 << lz;
+  if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, both ? kHeads / 2 : kHeads, kDk)) return DSA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cols, (unsigned)runs, prm.nsplit);
   cfg.blockDim = dim3(k4 ? kThreads<kCache4Bit> : kThreads<kCacheBf16>);

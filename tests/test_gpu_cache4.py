@@ -196,6 +196,24 @@ def test_long_selections_split(dsa, K, unit):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("H", [1, 33, 64, 65])
+@pytest.mark.parametrize("S,K,unit", [(12, 1024, 1), (24, 512, 1), (24, 9, 64), (48, 130, 1), (90, 63, 1), (160, 1, 64)])
+def test_many_requests(dsa, S, K, unit, H):
+    """More requests than run at once in two CTAs each: up to 64 heads take one,
+    over 8, 4, 2 and 1 splits. Some rows select nothing, one has a NaN query."""
+    kv = [1 + (K * unit + 97 * s) % (K * unit + 64) for s in range(S)]
+    rg, cache, q = _batch([1] * S, kv, 64, H, seed=S + H)
+    sel = _select(rg, K, unit, np.random.default_rng(S), empty=(1, S - 1))
+    o, lse = _check(dsa, rg, cache, q, sel, unit, f"{S} requests")
+    assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    q[2, H // 2, 3] = float("nan")  # its own row only
+    o2, lse2, st = _run(dsa, rg, cache, q, sel, unit)
+    row = torch.zeros((S, H), dtype=torch.bool, device=DEV)
+    row[2, H // 2] = True
+    assert st == 0 and torch.isnan(o2[row]).all() and torch.isnan(lse2[row]).all()
+    assert torch.equal(o[~row], o2[~row]) and torch.equal(lse[~row], lse2[~row])
+
+
 @pytest.mark.parametrize("unit", [1, 64])
 def test_rows_that_select_nothing(dsa, unit):
     rg, cache, q = _batch([1, 1, 1], [300, 500, 64], 64, 16, seed=5)

@@ -89,6 +89,16 @@ def test_split_over_ctas(dsa, window, sinks):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("H", [1, 33, 64, 65])
+@pytest.mark.parametrize("S,window,sinks,cap", [(12, 1100, 4, 0.0), (24, 450, 70, 0.0), (48, 66, 1, 2.0), (90, 10, 0, 0.0),
+                                                (160, 64, 9, 0.0)])
+def test_many_requests_of_one_token(dsa, S, window, sinks, cap, H):
+    """More requests than run at once in two CTAs each: up to 64 heads take
+    one, over 8, 4, 2 and 1 splits."""
+    kv = [1 + 97 * s % (window + 200) for s in range(S)]
+    _check(dsa, DI.random_small(50 + S, [1] * S, kv, H=H), window, sinks, cap=cap)
+
+
 @pytest.mark.parametrize("sinks", [0, 9])
 def test_logit_cap(dsa, sinks):
     _check(dsa, DI.random_small(12, [1, 6], [400, 200], H=16), 90, sinks, cap=2.0)
