@@ -269,9 +269,7 @@ __device__ __forceinline__ void issue_mmas(int half, uint32_t tmem, uint32_t sme
   };
   using One = std::integral_constant<int, 1>;
   using Four = std::integral_constant<int, 4>;
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // the same answer in every lane
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait_warp(bar, parity, abort_flag); };
   auto commit = [&](uint64_t* bar) {
     if (lead) umma_commit(bar);
     __syncwarp();
@@ -379,7 +377,7 @@ __device__ __forceinline__ void copy_keys(const uint8_t* __restrict__ cache, int
   };
   // whether there is a tile i (the list may end, or a wait give up)
   auto tile = [&](int i) -> bool {
-    return mbar_wait(br.rfull(i % kRing), (i / kRing) & 1, abort_flag) && !ring_end[i % kRing];
+    return mbar_wait_warp(br.rfull(i % kRing), (i / kRing) & 1, abort_flag) && !ring_end[i % kRing];
   };
   Part cur, nxt;
   bool have = tile(0);
@@ -389,7 +387,7 @@ __device__ __forceinline__ void copy_keys(const uint8_t* __restrict__ cache, int
     const int i = u >> 1, part = u & 1, st = i & 1;
     const bool more = !part || tile(i + 1);
     if (more) load(nxt, i + part, part ^ 1);
-    if (!mbar_wait(br.empty(part, st), ((i >> 1) & 1) ^ 1, abort_flag)) break;
+    if (!mbar_wait_warp(br.empty(part, st), ((i >> 1) & 1) ^ 1, abort_flag)) break;
     const uint32_t base = smem0 + (part ? OFF_V + st * kVStage : OFF_K + st * kKStage);
     const uint32_t d = base + (g >> 2) * kBlk;
 #pragma unroll
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
   KeyList<kCache> gen;
   if (warp == 1) gen.init(prm, t, ntok, split);
   if (warp >= 4 && warp < 8) {
-    if (mbar_wait(br.qbar(), 0, abort_flag)) {
+    if (mbar_wait_warp(br.qbar(), 0, abort_flag)) {
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         const uint8_t* row = smem + OFF_K + c * kQBlk + r * 128;
@@ -669,12 +667,12 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const int slot = i % kRing;
-      if (!(ok = mbar_wait(br.rfull(slot), (i / kRing) & 1, abort_flag))) break;
+      if (!(ok = mbar_wait_warp(br.rfull(slot), (i / kRing) & 1, abort_flag))) break;
       if (ring_end[slot]) break;
       const uint32_t mlo = mask_of(ring_mask[slot * kSteps]), mhi = mask_of(ring_mask[slot * kSteps + 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(br.rempty(slot));
-      if (!(ok = mbar_wait(br.sfull(i & 1), (i >> 1) & 1, abort_flag))) break;
+      if (!(ok = mbar_wait_warp(br.sfull(i & 1), (i >> 1) & 1, abort_flag))) break;
       tc_fence_after();
       const uint32_t tS = tmem + lane_base + kColS + (uint32_t)(i & 1) * 64;
       // Two passes over S in TMEM, 32 keys at a time: the largest logit, then
@@ -700,7 +698,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       const float alpha = need ? exp2f(m_run - m_new) : 1.f;
       if (i > 0 && __any_sync(0xffffffffu, need)) {
         // rescaling O waits until PV(i - 1) has added into it
-        if (!(ok = mbar_wait(br.pvdone(), (i - 1) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait_warp(br.pvdone(), (i - 1) & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
@@ -760,7 +758,7 @@ __global__ void __launch_bounds__(kThreads<kCache>, 1)
       n = i + 1;
     }
     // -------------------------------------------------------------- epilogue
-    if (ok && n > 0) ok = mbar_wait(br.pvdone(), (n - 1) & 1, abort_flag);
+    if (ok && n > 0) ok = mbar_wait_warp(br.pvdone(), (n - 1) & 1, abort_flag);
     tc_fence_after();
     const bool have_o = n > 0 && ok;
     const bool some = l_run != 0.f;  // a sum of weights is never negative; NaN counts

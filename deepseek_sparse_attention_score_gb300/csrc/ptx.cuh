@@ -77,6 +77,16 @@ __device__ __forceinline__ bool mbar_wait_limit(uint64_t* bar, uint32_t parity, 
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   return mbar_wait_limit(bar, parity, abort_flag, kWaitTimeoutClocks);
 }
+// The wait of a whole warp, with the same answer in every lane. A wait may
+// give up in some lanes and be met in others; a warp whose loop holds votes or
+// the tensor memory's warp-wide instructions has to leave it as one.
+__device__ __forceinline__ bool mbar_wait_warp_limit(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                     long long limit_clocks) {
+  return __all_sync(0xffffffffu, mbar_wait_limit(bar, parity, abort_flag, limit_clocks));
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait_warp_limit(bar, parity, abort_flag, kWaitTimeoutClocks);
+}
 
 // Bounded wait that ignores the abort flag: used while unwinding, to let
 // copies or MMAs already in flight land before shared memory or TMEM is

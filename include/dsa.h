@@ -527,7 +527,9 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * sets DSA_STATUS_TIMEOUT in the status word, unwinds and returns instead of
  * hanging or trapping. This entry runs one such wait on a barrier that
  * nothing arrives on, bounded by limit_clocks SM clocks (1 .. 1e10), so a
- * test can check that the status is set and the context stays usable.
+ * test can check that the status is set and the context stays usable; and one
+ * of a whole warp that runs out in half of its lanes, which sets
+ * DSA_STATUS_INTERNAL too if any lane takes it for met.
  *   dev_status  device int32, required */
 DSA_API int dsa_selftest_wait_timeout(dsa_stream_t stream, long long limit_clocks, int32_t* dev_status);
 
