@@ -485,7 +485,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
   if (warp >= 4 && warp < 8) {
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    if (mbar_wait(qbar, 0, abort_flag)) {
+    if (mbar_wait_warp(qbar, 0, abort_flag)) {
 #pragma unroll 1
       for (int c = 0; c < kQTmemBlocks; ++c) {
         const uint8_t* row = qstage + c * 16384 + r * 128;
@@ -689,10 +689,10 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
     bool ok = true;
     for (int i = 0;; ++i) {
       const int vs = i % kVStages;
-      if (!(ok = mbar_wait(vfull + vs, (i / kVStages) & 1, abort_flag))) break;
+      if (!(ok = mbar_wait_warp(vfull + vs, (i / kVStages) & 1, abort_flag))) break;
       if (vst_end[vs]) break;
       const uint32_t mlo = vst_mask[2 * vs], mhi = vst_mask[2 * vs + 1];
-      if (!(ok = mbar_wait(sfull + (i & 1), (i >> 1) & 1, abort_flag))) break;
+      if (!(ok = mbar_wait_warp(sfull + (i & 1), (i >> 1) & 1, abort_flag))) break;
       tc_fence_after();
       const uint32_t tS = tmem + lane_base + kColS + (uint32_t)(i & 1) * kTileKeys;
       uint32_t sa[32], sb[32];
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
       // rescaling O must wait until PV(i-1) has added into it; P(i) goes to
       // the other S buffer than P(i-1), so without a rescale nothing waits
       if (i > 0 && __any_sync(0xffffffffu, need)) {
-        if (!(ok = mbar_wait(pempty, (i - 1) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait_warp(pempty, (i - 1) & 1, abort_flag))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < kDvHalf / 32; ++c) {
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
       n = i + 1;
     }
     // epilogue
-    if (ok && n > 0) ok = mbar_wait(pempty, (n - 1) & 1, abort_flag);
+    if (ok && n > 0) ok = mbar_wait_warp(pempty, (n - 1) & 1, abort_flag);
     tc_fence_after();
     const int h = h0 + r;
     const bool hv = h < prm.H;

@@ -27,6 +27,8 @@ def _between(text, first, last):
     ("attend_cache.cu", "gen.init(prm, t, ntok, split)", "tmem_st_wait();"),  # the queries' move into tensor memory
     ("attend_cache.cu", "void copy_keys(", "// The copier of the bf16 cache"),
     ("attend_cache.cu", "void issue_mmas(", "// A copier warp:"),
+    ("attend.cu", "- softmax\n", "const bool have_o"),
+    ("attend.cu", "if (warp >= 4 && warp < 8) {", "tmem_st_wait();"),
 ])
 def test_whole_warps_wait_as_one(name, first, last):
     part = _between(_source(name), first, last)
