@@ -637,9 +637,11 @@ class RopeTarget:
     .. ``rot_off + rot_dim - 1`` (all after ``rot_off`` by default) into ``y``
     of the same shape, or in place without one. ``layout``: "interleaved"
     pairs (2i, 2i+1) or "half" pairs (i, i + rot_dim/2). ``scale`` multiplies
-    the rotated columns. Holds its tensors; may be kept and used again."""
+    the rotated columns. Holds its tensors and may be kept and used again:
+    a call packs it anew when their storage, shape or strides have changed
+    since it was made (resize_, set_, .data)."""
 
-    __slots__ = ("x", "y", "rot_dim", "c")
+    __slots__ = ("x", "y", "rot_dim", "args", "c", "shape", "xp", "xs", "yp", "ys")
 
     def __init__(self, x, y=None, *, rot_off=0, rot_dim=None, layout="half", scale=1.0):
         if y is None:
@@ -654,13 +656,20 @@ class RopeTarget:
         if lay is None:
             raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
         _, H, D = shape
-        xt, xh, xd = x.stride()
-        yt, yh, yd = y.stride()
+        xt, xh, xd = xs = x.stride()
+        yt, yh, yd = ys = y.stride()
         if D > 1 and (xd != 1 or yd != 1):
             raise ValueError("the columns of x and y must be contiguous")
-        self.x, self.y = x, y
+        xp, yp = x.data_ptr(), y.data_ptr()
+        self.x, self.y, self.args = x, y, (rot_off, rot_dim, layout, scale)
         self.rot_dim = D - rot_off if rot_dim is None else rot_dim
-        self.c = _rope_target(x.data_ptr(), y.data_ptr(), xt, xh, yt, yh, H, D, rot_off, lay, dtype, scale)
+        self.c = _rope_target(xp, yp, xt, xh, yt, yh, H, D, rot_off, lay, dtype, scale)
+        self.shape, self.xp, self.xs, self.yp, self.ys = shape, xp, xs, yp, ys
+
+    def repack(self):
+        """Pack the tensors as they are now, with the checks of a new target."""
+        off, dim, layout, scale = self.args
+        self.__init__(self.x, self.y, rot_off=off, rot_dim=dim, layout=layout, scale=scale)
 
 
 def dsa_rope(targets, positions, freqs, *, inverse=False):
@@ -676,8 +685,12 @@ def dsa_rope(targets, positions, freqs, *, inverse=False):
     _need(freqs, "freqs", torch.float64, dev, 1)
     T, rot = positions.numel(), 2 * freqs.numel()
     for g in ts:
-        if g.x.device != dev or g.x.shape[0] != T:
-            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(g.x.shape)} on {g.x.device}")
+        x, y = g.x, g.y
+        if (x.data_ptr() != g.xp or x.stride() != g.xs or x.shape != g.shape or
+                y is not x and (y.data_ptr() != g.yp or y.stride() != g.ys or y.shape != g.shape)):
+            g.repack()
+        if x.device != dev or g.shape[0] != T:
+            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(x.shape)} on {x.device}")
         if g.rot_dim != rot:
             raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
     _launch(dev, "dsa_rope", b"".join([g.c for g in ts]), len(ts), T, rot, a_pos, freqs.data_ptr(), 1 if inverse else 0)
