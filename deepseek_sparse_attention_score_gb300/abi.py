@@ -56,6 +56,7 @@ EXPORTS = (
     "dsa_launch_count",
     "dsa_sparse_mla_decode_noalloc",
     "dsa_build_page_tables",
+    "dsa_build_page_tables_next",
     "dsa_rope",
     "dsa_rope_freqs",
     "dsa_q4_write_back",
@@ -126,6 +127,8 @@ def lib() -> ctypes.CDLL:
                                           _P, _P, _Z, _P]
     L.dsa_selftest_wait_timeout.argtypes = [_P, ctypes.c_longlong, _P]
     L.dsa_build_page_tables.argtypes = [_P, _P, _P, _P, _L, _I, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]
+    L.dsa_build_page_tables_next.argtypes = [_P, _P, _P, _P, _L, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                                             _P, _P]
     L.dsa_rope.argtypes = [_P, _P, _I, _I, _I, _P, _P, _I]
     L.dsa_rope_freqs.argtypes = [_I, _D, _I, _D, _I, _D, _D, _P, _P]
     L.dsa_q4_write_back.argtypes = [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]
@@ -578,8 +581,8 @@ class PageTables(NamedTuple):
     n_taken: torch.Tensor       # [1], pages taken from the free list
 
 
-def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, PTW, ps=64, out=None,
-                          dev_status=None):
+def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, PTW, ps=64, free_state=None,
+                          out=None, dev_status=None):
     """A step's ragged metadata and slot map from its requests' lengths.
 
     ``q_lens`` [S] new tokens and ``seq_lens`` [S] positions with them;
@@ -589,7 +592,13 @@ def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, 
     tokens and page-table entries (the rest is -1); with ``T`` the number of
     tokens, ``(seq_lens, out.cu_q_lens, out.cu_kv_lens, out.page_indices)`` is
     the metadata of every other call. ``out``: a :class:`PageTables` to write
-    into."""
+    into.
+
+    A call takes from the first entry of ``free_pages`` on. For a sequence of
+    steps over one list pass ``free_state``, int32 [3 + 2 S], zeros before the
+    first (dsa_build_page_tables_next): each step then takes the pages behind
+    those of the steps before, and a step with the last one's lengths is that
+    step again."""
     dev = q_lens.device
     a_q, a_seq = _i32(q_lens, "q_lens", dev), _i32(seq_lens, "seq_lens", dev)
     S = q_lens.numel()
@@ -606,6 +615,10 @@ def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, 
     F, a_free = 0, None
     if free_pages is not None:
         F, a_free = free_pages.numel(), _i32(free_pages, "free_pages", dev)
+    entry, state = "dsa_build_page_tables", ()
+    if free_state is not None:
+        entry, state = "dsa_build_page_tables_next", (_i32(free_state, "free_state", dev),)
+        _shape(free_state, "free_state", (3 + 2 * S,))
     T, PTW = int(T), int(PTW)
     if T < 0 or PTW < 0:
         raise ValueError("T and PTW must not be negative")
@@ -620,8 +633,8 @@ def dsa_build_page_tables(q_lens, seq_lens, block_table, free_pages=None, *, T, 
             _need(getattr(out, name), f"out.{name}", torch.int32, dev, 1)
             _shape(getattr(out, name), f"out.{name}", (n,))
     cu_q, cu_kv, pages, seq, pos, slots, taken = out
-    _launch(dev, "dsa_build_page_tables", a_q, a_seq, block_table.data_ptr(), max(W, bt_stride) if S > 1 else W, W,
-            a_free, F, S, T, PTW, int(ps), cu_q.data_ptr(), cu_kv.data_ptr(), pages.data_ptr(), seq.data_ptr(),
+    _launch(dev, entry, a_q, a_seq, block_table.data_ptr(), max(W, bt_stride) if S > 1 else W, W,
+            a_free, F, *state, S, T, PTW, int(ps), cu_q.data_ptr(), cu_kv.data_ptr(), pages.data_ptr(), seq.data_ptr(),
             pos.data_ptr(), slots.data_ptr(), taken.data_ptr(), _status(dev_status, dev))
     return out
 

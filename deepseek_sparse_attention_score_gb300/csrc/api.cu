@@ -523,6 +523,16 @@ int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int3
                           int64_t bt_stride, int width, const int32_t* free_pages, int F, int S, int T, int PTW,
                           int ps, int32_t* cu_q_lens, int32_t* cu_kv_lens, int32_t* page_indices, int32_t* token_seq,
                           int32_t* positions, int32_t* slots, int32_t* n_taken, int32_t* dev_status) {
+  return dsa_build_page_tables_next(stream, q_lens, seq_lens, block_table, bt_stride, width, free_pages, F, nullptr, S,
+                                    T, PTW, ps, cu_q_lens, cu_kv_lens, page_indices, token_seq, positions, slots,
+                                    n_taken, dev_status);
+}
+
+int dsa_build_page_tables_next(dsa_stream_t stream, const int32_t* q_lens, const int32_t* seq_lens,
+                               int32_t* block_table, int64_t bt_stride, int width, const int32_t* free_pages, int F,
+                               int32_t* free_state, int S, int T, int PTW, int ps, int32_t* cu_q_lens,
+                               int32_t* cu_kv_lens, int32_t* page_indices, int32_t* token_seq, int32_t* positions,
+                               int32_t* slots, int32_t* n_taken, int32_t* dev_status) {
   NvtxRange nvtx_range("dsa_build_page_tables");
   if (S < 0 || T < 0 || PTW < 0 || F < 0 || width < 0 || bt_stride < width) return DSA_ERR_INVALID_ARGUMENT;
   if (!ps_supported(ps) || S > kTablesMaxRequests || (long long)width * ps >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
@@ -531,8 +541,8 @@ int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, const int3
   if ((S > 0 && (!q_lens || !seq_lens)) || (S > 0 && width > 0 && !block_table) || (F > 0 && !free_pages) ||
       (PTW > 0 && !page_indices) || (T > 0 && (!token_seq || !positions || !slots)))
     return DSA_ERR_INVALID_ARGUMENT;
-  TablesParams p{q_lens, seq_lens, block_table, bt_stride, width, free_pages, F, S, T, PTW, ps, cu_q_lens, cu_kv_lens,
-                 page_indices, token_seq, positions, slots, n_taken, dev_status, false};
+  TablesParams p{q_lens, seq_lens, block_table, bt_stride, width, free_pages, free_state, F, S, T, PTW, ps, cu_q_lens,
+                 cu_kv_lens, page_indices, token_seq, positions, slots, n_taken, dev_status, false};
   return run_page_tables(static_cast<cudaStream_t>(stream), p);
 }
 

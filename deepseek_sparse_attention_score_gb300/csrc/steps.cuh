@@ -19,6 +19,7 @@ struct TablesParams {
   long long bt_stride;
   int width;
   const int32_t* free_pages;
+  int32_t* free_state;  // [3 + 2 S], or null: the list is used from its start
   int F, S, T, PTW, ps;
   int32_t* cu_q_lens;
   int32_t* cu_kv_lens;

@@ -17,6 +17,12 @@
 // the block table, whose new entries other CTAs may still be writing. What
 // bounds it is latency: the launch, one round trip for the lengths, the scan,
 // one for the pages.
+//
+// With a free_state the list goes on where the last step stopped. A step with
+// the last one's lengths is that step again and takes its pages again, so a
+// call can be repeated; any other starts behind them. Every CTA reads the
+// state and finds the same start; the CTA that arrives last, when no other
+// will read it any more, writes the new one.
 #include <climits>
 
 #include "common.cuh"
@@ -43,6 +49,10 @@ __device__ __forceinline__ Sums shfl_up(Sums a, int d) {
   return {__shfl_up_sync(0xffffffffu, a.q, d), __shfl_up_sync(0xffffffffu, a.need, d),
           __shfl_up_sync(0xffffffffu, a.grow, d)};
 }
+
+// free_state: CTAs that have read it, list entries that the steps before the
+// last one used and that the last one used, its q_lens and its seq_lens
+enum : int { kStateArrived = 0, kStateUsed = 1, kStateTaken = 2, kStateLens = 3 };
 
 // Lengths of request s; one that cannot be right counts as empty.
 __device__ __forceinline__ bool lens_of(const TablesParams& p, int s, int& q, int& n) {
@@ -79,10 +89,14 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
   const int per = (p.S + kTbThreads - 1) / kTbThreads;
   const int s0 = min(p.S, tid * per), s1 = min(p.S, s0 + per);
   Sums mine = {0, 0, 0};
-  bool bad = false;
+  bool bad = false, moved = false;
   for (int s = s0; s < s1; ++s) {
     int q, n;
     bad |= !lens_of(p, s, q, n);
+    if (p.free_state) {
+      const volatile int* last = p.free_state + kStateLens + s;
+      moved |= last[0] != __ldg(p.q_lens + s) || last[p.S] != __ldg(p.seq_lens + s);
+    }
     const int need = pages_of(n, p.ps, lg);
     mine = mine + Sums{q, need, need - pages_of(n - q, p.ps, lg)};
   }
@@ -122,7 +136,35 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
     cp[p.S] = min(all.need, top_pages);
     cg[p.S] = all.grow;
   }
-  __syncthreads();
+  int start = 0, used = 0;  // list entries used before this step, and by it
+  if (p.free_state) {
+    const volatile int* st = p.free_state;
+    const int before = st[kStateUsed], taken = st[kStateTaken];
+    moved = __syncthreads_or(moved);
+    start = max(0, min(p.F, moved ? add_sat(max(before, 0), max(taken, 0)) : before));
+    used = min(all.grow, p.F - start);
+    __shared__ int s_last;
+    if (tid == 0) {
+      __threadfence();
+      s_last = atomicAdd(p.free_state + kStateArrived, 1) == (int)gridDim.x - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (s_last) {
+      if (tid == 0) {
+        p.free_state[kStateArrived] = 0;
+        p.free_state[kStateUsed] = start;
+        p.free_state[kStateTaken] = used;
+      }
+      if (moved)
+        for (int s = tid; s < p.S; s += kTbThreads) {
+          p.free_state[kStateLens + s] = __ldg(p.q_lens + s);
+          p.free_state[kStateLens + p.S + s] = __ldg(p.seq_lens + s);
+        }
+    }
+  } else {
+    __syncthreads();
+  }
   const int total_q = cq[p.S], total_p = cp[p.S];
   if (blockIdx.x == 0) {
     for (int s = tid; s <= p.S; s += kTbThreads) {
@@ -132,12 +174,12 @@ __global__ void __launch_bounds__(kTbThreads) page_tables_kernel(const TablesPar
     if (tid == 0) {
       *p.n_taken = cg[p.S];
       if (all.q > p.T || all.need > p.PTW) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
-      if (all.grow > p.F) set_status(p.dev_status, DSA_STATUS_NO_PAGES);
+      if (all.grow > p.F - start) set_status(p.dev_status, DSA_STATUS_NO_PAGES);
     }
     if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
   }
   auto taken = [&](int s, int i) {  // page i of those that request s takes
-    const long long k = (long long)cg[s] + i;
+    const long long k = (long long)start + cg[s] + i;
     return k < p.F ? __ldg(p.free_pages + k) : -1;
   };
 

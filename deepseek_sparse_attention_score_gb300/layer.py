@@ -26,7 +26,8 @@ from . import abi
 
 
 class LayerRunner:
-    def __init__(self, wl, device, page_budget=None, prefill=None, cache_bits=16, tables=False, rope=None):
+    def __init__(self, wl, device, page_budget=None, prefill=None, cache_bits=16, tables=False, rope=None,
+                 spare_pages=(), PTW=None, max_kv=None):
         """``wl``: a dsa_inputs.Workload whose tensors already live on ``device``
         (or on the CPU; they are moved). ``page_budget``: decode page-budget
         mode with that many pages. ``prefill``: force the prefill path
@@ -36,6 +37,14 @@ class LayerRunner:
         through the 4-bit decode call, one by one instead of by query blocks).
         ``tables``: build the metadata every step with dsa_build_page_tables,
         from ``lens`` (q_lens, seq_lens), ``block_table`` and ``free_pages``.
+        Lengths that the caller advances between steps (also between replays
+        of a captured one) make each step take its pages behind those of the
+        steps before; a step with unchanged lengths is the last one again
+        (``free_state``, see dsa_build_page_tables). Room to grow:
+        ``spare_pages``, page ids that later steps may take; ``PTW``, the
+        page-table entries (by default the workload's and the spare pages);
+        ``max_kv``, the longest length a request may reach (by default the
+        workload's longest).
         ``rope``: (freqs, scale, layout), with ``tables``: the workload's
         rotary columns (the last 64 of latent rows and queries, the first 64
         of indexer queries and keys) are taken as not rotated yet, and every
@@ -44,13 +53,17 @@ class LayerRunner:
             raise ValueError(f"cache_bits must be 4 or 16, got {cache_bits}")
         if rope is not None and not tables:
             raise ValueError("rope needs the positions that tables=True finds")
+        if not tables and (len(spare_pages) or PTW is not None or max_kv is not None):
+            raise ValueError("spare_pages, PTW and max_kv are for tables=True")
         rg = wl.rg
         self.wl = wl
         self.dev = torch.device(device)
         dev = self.dev
         self.rg = rg
         self.T, self.S, self.P, self.PTW, self.ps = rg.T, rg.S, rg.num_pages, rg.PTW, rg.page_size
-        self.max_kv = max(1, rg.max_kv)
+        self.max_kv = max(1, rg.max_kv, max_kv or 0)
+        if tables:
+            self.PTW = max(rg.PTW, rg.PTW + len(spare_pages) if PTW is None else PTW)
         self.k = wl.k
         self.k_pages = wl.k_pages if page_budget is None else page_budget
         self.page_budget = page_budget
@@ -78,7 +91,7 @@ class LayerRunner:
         if cache_bits == 4:
             self.kv4 = [self._quantised(c) for c in self.kv]
             self.kv = None
-        self.tables = self._make_tables(rg) if tables else None
+        self.tables = self._make_tables(rg, spare_pages) if tables else None
         self.rope = None
         if rope is not None:
             freqs, scale, layout = rope
@@ -125,14 +138,14 @@ class LayerRunner:
                               torch.arange(P, dtype=torch.int32, device=self.dev))
         return out
 
-    def _make_tables(self, rg):
+    def _make_tables(self, rg, spare_pages):
         """Inputs and outputs of dsa_build_page_tables for the workload's
         batch: the pages that its new tokens are the first to need wait in
-        ``free_pages``, the others in ``block_table``. ``meta`` becomes the
-        outputs."""
+        ``free_pages``, the spare ones behind them, the others in
+        ``block_table``. ``meta`` becomes the outputs."""
         had = -(-(rg.seq_lens - rg.q_lens) // self.ps)
         need = -(-rg.seq_lens // self.ps)
-        bt = torch.full((self.S, max(1, int(need.max(initial=0)))), -1, dtype=torch.int32)
+        bt = torch.full((self.S, -(-self.max_kv // self.ps)), -1, dtype=torch.int32)
         free = []
         for s in range(self.S):
             pages = rg.page_indices[rg.cu_kv_lens[s] // self.ps:][: need[s]]
@@ -140,7 +153,8 @@ class LayerRunner:
             free.extend(pages[had[s]:].tolist())
         self.lens = [torch.from_numpy(rg.q_lens.astype("int32")).to(self.dev), self.meta[0]]
         self.block_table = bt.to(self.dev)
-        self.free_pages = torch.tensor(free, dtype=torch.int32, device=self.dev)
+        self.free_pages = torch.tensor(free + list(spare_pages), dtype=torch.int32, device=self.dev)
+        self.free_state = torch.zeros(3 + 2 * self.S, dtype=torch.int32, device=self.dev)
         i32 = lambda n: torch.empty(n, dtype=torch.int32, device=self.dev)
         out = abi.PageTables(i32(self.S + 1), i32(self.S + 1), i32(self.PTW), i32(self.T), i32(self.T), i32(self.T),
                              i32(1))
@@ -152,7 +166,8 @@ class LayerRunner:
         """The step's metadata from its lengths (with ``tables``)."""
         if self.tables is not None:
             abi.dsa_build_page_tables(*self.lens, self.block_table, self.free_pages, T=self.T, PTW=self.PTW,
-                                      ps=self.ps, out=self.tables, dev_status=self.status)
+                                      ps=self.ps, free_state=self.free_state, out=self.tables,
+                                      dev_status=self.status)
 
     def rotate(self, layer):
         """The layer's queries, latent rows and indexer keys at their

@@ -381,7 +381,9 @@ DSA_API int dsa_topk_pages_from_tokens(dsa_stream_t stream, const int32_t* topk,
  *   n_taken      int32 [1] out     pages this step takes from the list
  * cu_q_lens, cu_kv_lens and page_indices are the metadata of the other calls
  * when T is the number of tokens. The call reads no state of its own: run
- * again on the same inputs it writes the same values.
+ * again on the same inputs it writes the same values. It always takes from the
+ * list's first entry on: before the next step that takes pages the caller
+ * passes the rest of the list, or uses dsa_build_page_tables_next.
  * Device conditions: a request with q < 0, seq < q or seq > width * ps counts
  * as empty and sets DSA_STATUS_BAD_METADATA, as do more tokens than T or more
  * pages than PTW (those past the end, and block-table entries behind them,
@@ -395,6 +397,30 @@ DSA_API int dsa_build_page_tables(dsa_stream_t stream, const int32_t* q_lens, co
                                   int F, int S, int T, int PTW, int ps, int32_t* cu_q_lens, int32_t* cu_kv_lens,
                                   int32_t* page_indices, int32_t* token_seq, int32_t* positions, int32_t* slots,
                                   int32_t* n_taken, int32_t* dev_status);
+/* The same for a sequence of steps over one free list. A step's pages stay in
+ * the block table and must not be handed out again, so the list goes on where
+ * the last step stopped:
+ *   free_state  int32 [3 + 2 S] in/out, zeros before the first step on a list
+ *               (and again whenever the list is filled anew), or NULL: the
+ *               call above, every step from the list's first entry
+ *                 [0]  for the call's own use
+ *                 [1]  entries that the steps before the last one used
+ *                 [2]  entries that the last one used
+ *                 [3, 3 + S) and [3 + S, 3 + 2 S)  its q_lens and seq_lens
+ * A step with exactly the lengths of the last one is that step again (a retry,
+ * a replay of a captured graph) and takes the same pages; any other starts
+ * behind them. Where equal lengths do mean a new step (every request was
+ * replaced by another of its lengths, and the old ones keep their pages), fill
+ * the remembered lengths with -1. Pages of a step that is taken back stay
+ * used. DSA_STATUS_NO_PAGES is set when fewer than the step takes are left.
+ * Steps on one state run one after another. */
+DSA_API int dsa_build_page_tables_next(dsa_stream_t stream, const int32_t* q_lens, const int32_t* seq_lens,
+                                       int32_t* block_table, int64_t bt_stride, int width,
+                                       const int32_t* free_pages, int F, int32_t* free_state, int S, int T, int PTW,
+                                       int ps, int32_t* cu_q_lens, int32_t* cu_kv_lens, int32_t* page_indices,
+                                       int32_t* token_seq, int32_t* positions, int32_t* slots, int32_t* n_taken,
+                                       int32_t* dev_status);
+
 
 /* ------------------------------------------------------------------------
  * Rotary positions (no counterpart on the pages, whose queries and rows
