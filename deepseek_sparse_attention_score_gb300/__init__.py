@@ -12,6 +12,7 @@ from .abi import (  # noqa: F401
     dsa_q4_read_rows,
     dsa_q4_write_back,
     dsa_rope,
+    dsa_rope_attention_scales,
     dsa_rope_freqs,
     dsa_sparse_mla_decode_q4,
     dsa_window_mla,

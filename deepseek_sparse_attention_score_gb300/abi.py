@@ -59,6 +59,7 @@ EXPORTS = (
     "dsa_build_page_tables_next",
     "dsa_rope",
     "dsa_rope_freqs",
+    "dsa_rope_attention_scales",
     "dsa_q4_write_back",
     "dsa_q4_read_rows",
     "dsa_sparse_mla_decode_q4",
@@ -131,6 +132,7 @@ def lib() -> ctypes.CDLL:
                                              _P, _P]
     L.dsa_rope.argtypes = [_P, _P, _I, _I, _I, _P, _P, _I]
     L.dsa_rope_freqs.argtypes = [_I, _D, _I, _D, _I, _D, _D, _P, _P]
+    L.dsa_rope_attention_scales.argtypes = [_D, _D, _D, _P, _P]
     L.dsa_q4_write_back.argtypes = [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]
     L.dsa_q4_read_rows.argtypes = [_P, _P, _I, _I, _P, _I, _P, _I, _P]
     L.dsa_sparse_mla_decode_q4.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F,
@@ -713,8 +715,11 @@ def dsa_rope(targets, positions, freqs, *, inverse=False):
 def dsa_rope_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, orig_max_pos=4096, beta_fast=32.0,
                    beta_slow=1.0, device=None):
     """Frequencies (fp64 [rot_dim / 2], radians per position) of the rotary
-    pairs and the factor that goes with them, scaled for long contexts:
-    "none", "linear" (all divided by ``factor``) or "yarn" (by parts)."""
+    pairs, scaled for long contexts: "none", "linear" (all divided by
+    ``factor``) or "yarn" (by parts); and YaRN's factor 0.1 ln(factor) + 1 (or
+    1), the scale of queries and keys whose columns all rotate. For the heads
+    here, of which 64 of 576 columns rotate, see
+    :func:`dsa_rope_attention_scales`."""
     if scaling not in _ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
     freqs = torch.empty(max(0, int(rot_dim) // 2), dtype=torch.float64)
@@ -723,6 +728,18 @@ def dsa_rope_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, orig_ma
                               float(beta_fast), float(beta_slow), _addr(freqs), ctypes.byref(ms))
     _check("dsa_rope_freqs", rc)
     return (freqs if device is None else freqs.to(device)), ms.value
+
+
+def dsa_rope_attention_scales(factor, *, mscale=1.0, mscale_all_dim=1.0):
+    """YaRN's factors for a head of which a part rotates: the scale of the
+    rotated columns of queries and keys (:class:`RopeTarget`), and what
+    ``sm_scale`` is multiplied by. ``mscale`` and ``mscale_all_dim``: the
+    model's coefficients."""
+    rotated, logits = ctypes.c_double(), ctypes.c_double()
+    rc = lib().dsa_rope_attention_scales(float(factor), float(mscale), float(mscale_all_dim), ctypes.byref(rotated),
+                                         ctypes.byref(logits))
+    _check("dsa_rope_attention_scales", rc)
+    return rotated.value, logits.value
 
 
 def _rows576(t, name, dev):

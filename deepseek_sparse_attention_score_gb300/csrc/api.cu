@@ -609,6 +609,15 @@ int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor, int ori
   return DSA_OK;
 }
 
+int dsa_rope_attention_scales(double factor, double mscale, double mscale_all_dim, double* rotated, double* logits) {
+  if (!rotated || !logits || !std::isfinite(factor) || factor < 1.0) return DSA_ERR_INVALID_ARGUMENT;
+  const double m = 0.1 * mscale * std::log(factor) + 1.0, all = 0.1 * mscale_all_dim * std::log(factor) + 1.0;
+  if (!std::isfinite(m) || !std::isfinite(all) || !(all > 0.0)) return DSA_ERR_INVALID_ARGUMENT;
+  *rotated = m / all;
+  *logits = all * all;
+  return DSA_OK;
+}
+
 int dsa_q4_write_back(dsa_stream_t stream, const uint16_t* rows, int src_stride, uint8_t* cache,
                       const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
                       const int32_t* page_indices, int T, int S, int P, int PTW, int ps, int32_t* dev_status) {

@@ -48,7 +48,9 @@ class LayerRunner:
         ``rope``: (freqs, scale, layout), with ``tables``: the workload's
         rotary columns (the last 64 of latent rows and queries, the first 64
         of indexer queries and keys) are taken as not rotated yet, and every
-        step rotates its tokens'; indexer columns pair by halves."""
+        step rotates its tokens'; indexer columns pair by halves. ``scale`` is
+        that of the rotated columns alone: YaRN's temperature of the logits
+        belongs in the workload's ``sm_scale`` (dsa_rope_attention_scales)."""
         if cache_bits not in (4, 16):
             raise ValueError(f"cache_bits must be 4 or 16, got {cache_bits}")
         if rope is not None and not tables:

@@ -464,12 +464,24 @@ DSA_API int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets /* host
  *       times within orig_max_pos keep their frequency, those below beta_slow
  *       turns are divided by factor, a linear ramp over the pair index between
  *   freqs   host fp64 [rot_dim / 2] out
- *   mscale  host out or NULL: the factor that goes with it for the rotated
- *           columns of queries and keys, 0.1 ln(factor) + 1 (YaRN, factor > 1)
- *           or 1 */
+ *   mscale  host out or NULL: YaRN's factor m = 0.1 ln(factor) + 1, else 1.
+ *           Its square is a temperature of the whole logit. As the scale of
+ *           the rotated columns of queries and keys it is that only where all
+ *           columns rotate; a head of which a part rotates (here 64 of 576
+ *           columns) takes dsa_rope_attention_scales */
 enum dsa_rope_scaling { DSA_ROPE_SCALE_NONE = 0, DSA_ROPE_SCALE_LINEAR = 1, DSA_ROPE_SCALE_YARN = 2 };
 DSA_API int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor, int orig_max_pos, double beta_fast,
                            double beta_slow, double* freqs, double* mscale);
+/* YaRN's factors for a head of which only a part rotates (host only). With
+ * m(c) = 0.1 c ln(factor) + 1 and a model's two coefficients (mscale and
+ * mscale_all_dim of its configuration):
+ *   rotated  host out: m(mscale) / m(mscale_all_dim), the scale of the rotated
+ *            columns of queries and keys (dsa_rope_target.scale); 1 when the
+ *            coefficients are equal
+ *   logits   host out: m(mscale_all_dim)^2, the factor of sm_scale
+ * factor >= 1 (1: both are 1); m(mscale_all_dim) > 0. */
+DSA_API int dsa_rope_attention_scales(double factor, double mscale, double mscale_all_dim, double* rotated,
+                                      double* logits);
 
 /* ------------------------------------------------------------------------
  * 4-bit latent cache: the rows [c_kv(512) | k_rope(64)] in 416 bytes instead
