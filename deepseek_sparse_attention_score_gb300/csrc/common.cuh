@@ -27,7 +27,8 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu_q_lens, int S, int
 
 // Warp-cooperative version of seq_of_token: 32 boundaries per step, so a
 // batch of S requests resolves in ceil(log32(S)) dependent loads. All lanes
-// must call it with the same t; every lane gets the result.
+// must call it with the same t; every lane gets the result, which lies in
+// [0, S) whatever the boundaries hold.
 __device__ __forceinline__ int seq_of_token_warp(const int32_t* cu_q_lens, int S, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = S;  // answer in [lo, hi)
@@ -36,7 +37,9 @@ __device__ __forceinline__ int seq_of_token_warp(const int32_t* cu_q_lens, int S
     const int idx = lo + lane * step;
     const bool le = idx < hi && __ldg(cu_q_lens + idx) <= t;
     const uint32_t m = __ballot_sync(0xffffffffu, le);
-    const int last = 31 - __clz(m);  // lane 0 always qualifies (cu_q_lens[lo] <= t)
+    // lane 0 qualifies (cu_q_lens[lo] <= t) unless the first request of all
+    // starts behind t, which valid metadata never has
+    const int last = 31 - __clz(m | 1u);
     lo = lo + last * step;
     hi = min(hi, lo + step);
   }
