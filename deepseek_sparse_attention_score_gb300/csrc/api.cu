@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -445,6 +446,7 @@ int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, i
   if (max_kv < 1 || sliding_window < 0 || num_sinks < 0) return DSA_ERR_INVALID_ARGUMENT;
   if (!std::isfinite(sm_scale) || !std::isfinite(soft_cap) || soft_cap < 0.f) return DSA_ERR_INVALID_ARGUMENT;
   if ((long long)T * H >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  if (!std::isfinite(sm_scale * 1.4426950408889634f)) return DSA_ERR_INVALID_ARGUMENT;  // the kernel's logit factor
   if (T == 0 || H == 0) return DSA_OK;
   AttendParams prm{};
   prm.q = q;
@@ -464,9 +466,12 @@ int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, i
   prm.mode = kModeDense;
   prm.window = sliding_window > 0 ? sliding_window : INT_MAX;
   prm.sinks = num_sinks;
-  if (soft_cap > 0.f) {
+  // c tanh(l / c) is l to fp32 accuracy where |l| < 2^-12 c; from 2^60 on that
+  // is every logit that a softmax can tell apart, and l / c would underflow.
+  // A tiny cap's factor stops at the largest number, so that 0 stays 0.
+  if (soft_cap > 0.f && soft_cap < 0x1p60f) {
     prm.soft_cap_on = 1;
-    prm.inv_cap_scale = sm_scale / soft_cap;
+    prm.inv_cap_scale = std::min(std::max(sm_scale / soft_cap, -FLT_MAX), FLT_MAX);
     prm.cap_log2 = soft_cap * 1.4426950408889634f;
   }
   // pages of the longest list, the split unit: at most the request's, or the

@@ -552,7 +552,8 @@ DSA_API int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, con
  *   max_kv  as dsa_dense_mla
  *   ws      taken as there and not used (may be NULL): split key lists are
  *           merged inside clusters
- * Supported: as dsa_dense_mla; num_sinks >= 0, T * H < 2^31.
+ * Supported: as dsa_dense_mla; num_sinks >= 0, T * H < 2^31, any soft_cap
+ * (from 2^60 on the logits stay as they are), |sm_scale| * 1.5 finite in fp32.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
                            const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
