@@ -921,14 +921,18 @@ int clusters_at_once(Kernel kern, bool k4, bool both, int lz) {
   return n;
 }
 
-// Splits of a key list: a power of two up to eight, as long as all clusters
-// run at once and a split keeps 64 keys (128 among eight). Measured, one
+// Splits of a list of n entries (tokens, or pages of ps keys): a power of two
+// up to eight, as long as all clusters run at once, 64 keys are left for each
+// split on average (128 among eight) and the longest share gets shorter: pages
+// are dealt out whole, so one page is not split. Measured, one
 // request, z = 1 / 2 / 4 / 8: 128 keys 10.9 / 11.3 / 12.3 / 14.5 us, 256 keys
 // 15.0 / 13.1 / 12.5 / 14.7, 1024 keys 35 / 23.7 / 18.0 / 16.5; 8 requests of
 // 2048 keys 64 / 39 / 27.9 / 46.9 (16 clusters of eight are more than fit).
-int log2_splits(Kernel kern, bool k4, bool both, long long clusters, long long keys) {
+int log2_splits(Kernel kern, bool k4, bool both, long long clusters, long long n, int unit) {
+  const auto longest = [&](int lz) { return (n + (1 << lz) - 1) >> lz; };
   int lz = 0;
-  while (lz < 3 && (keys >> (lz + 1)) >= (lz == 2 ? 128 : 64) && clusters <= clusters_at_once(kern, k4, both, lz + 1))
+  while (lz < 3 && ((n * unit) >> (lz + 1)) >= (lz == 2 ? 128 : 64) && longest(lz + 1) < longest(lz) &&
+         clusters <= clusters_at_once(kern, k4, both, lz + 1))
     ++lz;
   return lz;
 }
@@ -957,18 +961,18 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
     if (k4) return one ? cache_mla_kernel<kCache4Bit, true> : cache_mla_kernel<kCache4Bit, false>;
     return one ? cache_mla_kernel<kCacheBf16, true> : cache_mla_kernel<kCacheBf16, false>;
   };
-  const long long keys = (long long)prm.K * (prm.mode == kModeToken ? 1 : prm.ps);
+  const int unit = prm.mode == kModeToken ? 1 : prm.ps;
   bool both = prm.H <= kHeads / 2 && prm.pack == 1;
   int lz = 0;
   if (both) {
     for (const bool one : {false, true}) set_smem_attr_once(reinterpret_cast<const void*>(choose(one)), kSmem);
-    lz = log2_splits(choose(true), k4, true, runs, keys);
+    lz = log2_splits(choose(true), k4, true, runs, prm.K, unit);
     both = 2 * runs > clusters_at_once(choose(false), k4, false, lz);
   }
   const Kernel kern = choose(both);
   set_smem_attr_once(reinterpret_cast<const void*>(kern), kSmem);
   const int cols = both ? 1 : 2 * ((prm.H + kHeads - 1) / kHeads);
-  if (!both) lz = log2_splits(kern, k4, false, cols * runs, keys);
+  if (!both) lz = log2_splits(kern, k4, false, cols * runs, prm.K, unit);
   prm.nsplit = 1 << lz;
   if (!encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, both ? kHeads / 2 : kHeads, kDk)) return DSA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
