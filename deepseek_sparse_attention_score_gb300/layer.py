@@ -114,14 +114,15 @@ class LayerRunner:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws_idx = torch.empty(max(1, abi.dsa_indexer_workspace_size(T, self.S, self.max_kv, self.ps)),
                                   dtype=torch.uint8, device=dev)
-        self.ws_att = torch.empty(max(1, abi.dsa_sparse_mla_decode_workspace_size(T, H)), dtype=torch.uint8,
-                                  device=dev)
+        if cache_bits == 16:  # the split scratch of the bf16 decode; the 4-bit form merges inside clusters
+            self.ws_att = torch.empty(max(1, abi.dsa_sparse_mla_decode_workspace_size(T, H)), dtype=torch.uint8,
+                                      device=dev)
         nl = len(self.types)
         self.topk = [torch.empty((T, self.k), dtype=torch.int32, device=dev) for _ in range(self.num_full)]
         self.topk_pages = [torch.empty((T, self.k_pages), dtype=torch.int32, device=dev)
                            for _ in range(self.num_full)]
         self.o = [torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev) for _ in range(nl)]
-        if self.prefill:
+        if self.prefill and cache_bits == 16:  # query blocks; 4-bit prefill tokens attend one by one
             self.QB = wl.QB
             self.u_max = wl.u_max if wl.u_max > 0 else min(self.QB * self.k_pages, self.PTW)
             nqb = (T + self.QB - 1) // self.QB
