@@ -429,8 +429,9 @@ DSA_API int dsa_build_page_tables_next(dsa_stream_t stream, const int32_t* q_len
  * with (a, b) the elements (2i, 2i+1) (DSA_ROPE_INTERLEAVED) or
  * (i, i + rot_dim/2) (DSA_ROPE_HALF) of columns [rot_off, rot_off + rot_dim).
  * `inverse` != 0 turns by the negative angle: that call maps an output's
- * gradient to the input's. Every target of a call is rotated in one launch:
- * a layer's queries, latent rows, indexer queries and indexer keys.
+ * gradient to the input's. The targets of a call are rotated in one launch (a
+ * layer's queries, latent rows, indexer queries and indexer keys), in two if
+ * only some of them lie on 16 bytes.
  *   x, y       [T, H, D] of `dtype` with element strides (*_stride_t,
  *              *_stride_h, 1). y == x (same strides) works in place and
  *              touches the rotated columns only; otherwise y receives the
@@ -440,7 +441,9 @@ DSA_API int dsa_build_page_tables_next(dsa_stream_t stream, const int32_t* q_len
  *   freqs      fp64 [rot_dim / 2], radians per position (dsa_rope_freqs)
  * Angles are reduced in fp64; products are fp32, rounded once to `dtype`.
  * Supported: 1 to 8 targets, even rot_dim <= 512, H <= 65536, D <= 4096. Any strides and alignment
- * of whole elements; 16-byte aligned rows and columns move 16 bytes at a time.
+ * of whole elements; a target moves 16 bytes at a time if its addresses,
+ * strides, D, rot_off and rot_dim / 2 are multiples of 16 bytes, else element by
+ * element.
  * ------------------------------------------------------------------------ */
 enum dsa_dtype { DSA_DTYPE_BF16 = 0, DSA_DTYPE_F32 = 1 };
 enum dsa_rope_layout { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 };
