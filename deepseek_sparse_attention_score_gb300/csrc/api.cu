@@ -8,6 +8,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -41,8 +42,10 @@ void set_smem_attr_once(const void* func, int bytes) {
   };
   static Entry done[64];
   static int ndone = 0;
+  static std::mutex lock;  // calls may come from several threads at once
   int dev = 0;
   cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> hold(lock);
   for (int i = 0; i < ndone; ++i)
     if (done[i].f == func && done[i].dev == dev) return;
   cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
