@@ -241,21 +241,12 @@ def prepare(case, seed):
             sel[rng.integers(0, S)] = -1  # a row that selects nothing
             sel[:, 0] = -1
         st.update(sel=_ints(sel), q=_randn(gen, S, case["H"], DK), seq_np=seq,
-                  o=torch.empty(S, case["H"], NOPE, device=DEV, dtype=torch.bfloat16), ws=_workspace(S, case["H"]))
+                  o=torch.empty(S, case["H"], NOPE, device=DEV, dtype=torch.bfloat16))
     else:
         st.update(_ragged(q, seq, case["ps"], rng))
         st.update(q=_randn(gen, st["T"], case["H"], DK), kv=_randn(gen, st["P"], case["ps"], DK), seq_np=seq,
-                  o=torch.empty(st["T"], case["H"], NOPE, device=DEV, dtype=torch.bfloat16),
-                  ws=_workspace(st["T"], case["H"]))
+                  o=torch.empty(st["T"], case["H"], NOPE, device=DEV, dtype=torch.bfloat16))
     return st
-
-
-def _workspace(T, H):
-    """The attention's split workspace: a user's program keeps one."""
-    if not own:
-        return None
-    import deepseek_sparse_attention_score_gb300 as dsa
-    return torch.empty(max(1, dsa.dsa_sparse_mla_decode_workspace_size(T, H)), device=DEV, dtype=torch.uint8)
 
 
 # ------------------------------------------------------------------- passes
@@ -286,9 +277,9 @@ def _run_own(op, case, st):
     if op == "q4_attend":
         return dsa.dsa_sparse_mla_decode_q4(st["q"], st["cache"], *_meta(st), st["sel"],
                                             unit=1 if case["unit"] == "token" else case["ps"], sm_scale=SM_SCALE,
-                                            o=st["o"], want_lse=True, ws=st["ws"])
+                                            o=st["o"], want_lse=True)
     return dsa.dsa_window_mla(st["q"], st["kv"], *_meta(st), max_kv=case["kv_max"], sliding_window=case["window"],
-                              num_sinks=case["sinks"], sm_scale=SM_SCALE, o=st["o"], want_lse=True, ws=st["ws"])
+                              num_sinks=case["sinks"], sm_scale=SM_SCALE, o=st["o"], want_lse=True)
 
 
 def _run_plain(op, case, st):
