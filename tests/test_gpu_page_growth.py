@@ -168,3 +168,29 @@ def test_runner_refusals(dsa):
     for kw in (dict(spare_pages=[1]), dict(PTW=4), dict(max_kv=100)):
         with pytest.raises(ValueError):
             LayerRunner(wl, DEV, **kw)
+
+
+def test_no_requests_and_the_largest_number(dsa):
+    state, st = torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = dsa.dsa_build_page_tables(_i32([]), _i32([]), torch.zeros((0, 4), dtype=torch.int32, device=DEV), _i32([3]), T=2,
+                                    PTW=2, free_state=state, dev_status=st)
+    torch.cuda.synchronize()
+    assert state.cpu().tolist() == [0, 0, 0] and st.item() == 0 and (out.slots == -1).all()
+    S = 16384
+    run = Steps(dsa, S, width=3, F=3 * S, T=S, PTW=3 * S)
+    seq = np.arange(S) % 60 + 1
+    assert run(np.ones(S), seq) == 0  # from an empty block table: a request's first page comes with its first tokens
+    assert run(np.ones(S), seq + 1) == 0 and run(np.ones(S), seq + 1) == 0
+    assert run(np.ones(S), np.full(S, 65)) == 0
+    held = run.bt[run.bt >= 0]
+    assert len(np.unique(held)) == len(held)
+
+
+def test_a_list_that_is_not_given(dsa):
+    """No free list: steps that take no page, and one that would."""
+    run = Steps(dsa, 2, width=2, F=0, T=4, PTW=4)
+    run.bt[:, 0] = [4, 7]
+    run.g_bt.copy_(_i32(run.bt))
+    run.g_free = None
+    assert run([1, 1], [5, 64]) == 0 and run([1, 1], [6, 64]) == 0
+    assert run([1, 1], [7, 65]) == NO_PAGES
