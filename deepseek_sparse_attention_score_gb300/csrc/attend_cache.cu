@@ -23,7 +23,7 @@
 //
 // The loops are rolled. Five roles share the SM's instruction cache; with
 // attend.cu's unrolled loops it hit 60% of the time here and warps waited for
-// instructions more than for anything else, rolled it hits 96%.
+// instructions more than for anything else, rolled it hits 95%.
 #include <atomic>
 #include <type_traits>
 
@@ -87,7 +87,7 @@ constexpr uint32_t kColO = 256;
 template <int kCache>
 constexpr int kCopyWarps = kCache == kCache4Bit ? 16 : 1;
 // the 4-bit copiers are warps 8-23; the TMA issuer is warp 2, away from the MMA
-// issuer's quarter of the SM (as warp 8 it cost 4%: 928 against 895 us for 2049
+// issuer's quarter of the SM (as warp 8 it costs 4%: 924 against 885 us for 2049
 // tokens; for the 4-bit copiers it made no difference where they were)
 template <int kCache>
 constexpr int kThreads = (kCache == kCache4Bit ? 8 + kCopyWarps<kCache> : 8) * 32;
@@ -924,10 +924,13 @@ int clusters_at_once(Kernel kern, bool k4, bool both, int lz) {
 // Splits of a list of n entries (tokens, or pages of ps keys): a power of two
 // up to eight, as long as all clusters run at once, 64 keys are left for each
 // split on average (128 among eight) and the longest share gets shorter: pages
-// are dealt out whole, so one page is not split. Measured, one
-// request, z = 1 / 2 / 4 / 8: 128 keys 10.9 / 11.3 / 12.3 / 14.5 us, 256 keys
-// 15.0 / 13.1 / 12.5 / 14.7, 1024 keys 35 / 23.7 / 18.0 / 16.5; 8 requests of
-// 2048 keys 64 / 39 / 27.9 / 46.9 (16 clusters of eight are more than fit).
+// are dealt out whole, so one page is not split. Measured, 4-bit cache, z = 1 /
+// 2 / 4 / 8, 128 heads: one request of 128 keys 12.5 / 13.4 / 14.3 / 16.6 us,
+// 256 keys 17.1 / 15.7 / 14.6 / 16.8, 1024 keys 40.9 / 28.0 / 20.9 / 19.1, 8
+// requests of 2048 keys 72.4 / 44.2 / 29.4 / 46.2 (16 clusters of eight are more
+// than fit); 16 heads, one request of 128 keys 11.7 / 11.6 / 11.5 / 13.0, 256
+// keys 16.1 / 13.8 / 11.9 / 12.9. One page of 128 keys, 8 requests: 13.7 us in
+// two splits and 10.8 in one with 128 heads, 12.1 and 10.1 with 16.
 int log2_splits(Kernel kern, bool k4, bool both, long long clusters, long long n, int unit) {
   const auto longest = [&](int lz) { return (n + (1 << lz) - 1) >> lz; };
   int lz = 0;
@@ -946,17 +949,19 @@ int run_attend_cache(cudaStream_t stream, AttendParams prm) {
   if (!k4 && !encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, kSubKeys, kDk))
     return DSA_ERR_CUDA;
   // Neighbouring tokens share a CTA where they fit and a request has two on
-  // average: 2049 tokens, window 1024, 16 heads: 137 us with eight tokens a
-  // CTA, 894 with one. A CTA finds its run by a scan over the requests, 32 at a
-  // time, which 1024 of them bound.
+  // average: 2049 tokens, window 1024: 134 us with eight tokens a CTA against
+  // 597 with one for 16 heads, 461 against 611 for 64, 20 against 590 for one.
+  // A CTA finds its run by a scan over the requests, 32 at a time, which 1024 of
+  // them bound.
   prm.pack = !k4 && prm.H <= kHeads / 2 && prm.S <= 1024 && prm.T >= 2 * prm.S ? kHeads / prm.H : 1;
   const long long runs = std::min<long long>(prm.T, (prm.T + (long long)prm.S * (prm.pack - 1)) / prm.pack);
   // One CTA per token of up to 64 heads (kBoth) does twice the PV work and
-  // takes 1.2 to 1.3 times as long, so it is taken where two CTAs per token in
+  // takes 1.1 to 1.2 times as long, so it is taken where two CTAs per token in
   // as many splits would not all run at once. Measured with two / one, 4-bit
-  // cache, 2048 keys each, 64 heads: 1 request 19.4 / 23.2 us, 16 requests 26.6
-  // / 30.8, 48 requests 66.4 / 50.4; 16 heads: 8 requests 24.5 / 20.4, 32
-  // requests 39.8 / 30.1; window 4096, 32 requests 67.2 / 56.0.
+  // cache, 2048 keys each, 64 heads: 1 request 20.6 / 24.4 us, 16 requests 29.0
+  // / 32.8, 48 requests 73.3 / 51.9; 16 heads: 1 request 19.5 / 20.7, 8 requests
+  // 27.0 / 21.7, 32 requests 43.5 / 31.1; window 4096 and 64 sinks, 32 requests
+  // of 16 heads 67.4 / 57.8.
   const auto choose = [&](bool one) -> Kernel {
     if (k4) return one ? cache_mla_kernel<kCache4Bit, true> : cache_mla_kernel<kCache4Bit, false>;
     return one ? cache_mla_kernel<kCacheBf16, true> : cache_mla_kernel<kCacheBf16, false>;

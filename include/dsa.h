@@ -292,6 +292,9 @@ DSA_API int dsa_indexer_topk_approx(dsa_stream_t stream, const uint16_t* q, cons
  *   max_kv  an upper bound on seq_lens (host-known), sizes the key splits
  *   ws      workspace of dsa_sparse_mla_decode_workspace_size(T, H, Dv) bytes
  * Supported: as dsa_sparse_mla_decode; sliding_window >= 0, soft_cap >= 0.
+ * With a sliding window dsa_window_mla (num_sinks = 0) computes the same and
+ * is the faster call, most of all with 64 heads or fewer, where it takes
+ * neighbouring tokens together.
  * ------------------------------------------------------------------------ */
 DSA_API int dsa_dense_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
                           const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
@@ -497,7 +500,11 @@ DSA_API int dsa_rope_attention_scales(double factor, double mscale, double mscal
  * e2m1 (both to the nearest, ties to even, saturating); the value is code *
  * scale, exact in bf16. A group with an infinity or a NaN gets the scale NaN
  * and zero codes and reads back as NaN,
- * one with max|x| <= 6 * 2^-10 as zeros.
+ * one with max|x| <= 6 * 2^-10 as zeros. Scales below 2^-6 are subnormal and
+ * coarser: 4 significant bits for max|x| >= 0.094, then 3, 2 and 1 below 0.094,
+ * 0.047 and 0.024. There is no second scale: a layer whose latent rows are that
+ * small is written times a power of two, with the queries' first 512 dims and
+ * the output times its inverse, which changes nothing else.
  *
  * dsa_q4_write_back is dsa_paged_write_back into such a cache: token t's row
  * goes to the slot of its position, every other row is left untouched, and a
