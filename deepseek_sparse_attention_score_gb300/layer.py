@@ -40,7 +40,8 @@ class LayerRunner:
         Lengths that the caller advances between steps (also between replays
         of a captured one) make each step take its pages behind those of the
         steps before; a step with unchanged lengths is the last one again
-        (``free_state``, see dsa_build_page_tables). Room to grow:
+        (``free_state``, see dsa_build_page_tables; zero it when
+        ``free_pages`` is filled anew). Room to grow:
         ``spare_pages``, page ids that later steps may take; ``PTW``, the
         page-table entries (by default the workload's and the spare pages);
         ``max_kv``, the longest length a request may reach (by default the
@@ -58,6 +59,8 @@ class LayerRunner:
         if not tables and (len(spare_pages) or PTW is not None or max_kv is not None):
             raise ValueError("spare_pages, PTW and max_kv are for tables=True")
         rg = wl.rg
+        if PTW is not None and PTW < rg.PTW or max_kv is not None and max_kv < rg.max_kv:
+            raise ValueError(f"the workload needs {rg.PTW} page-table entries and lengths of {rg.max_kv}")
         self.wl = wl
         self.dev = torch.device(device)
         dev = self.dev
@@ -65,7 +68,7 @@ class LayerRunner:
         self.T, self.S, self.P, self.PTW, self.ps = rg.T, rg.S, rg.num_pages, rg.PTW, rg.page_size
         self.max_kv = max(1, rg.max_kv, max_kv or 0)
         if tables:
-            self.PTW = max(rg.PTW, rg.PTW + len(spare_pages) if PTW is None else PTW)
+            self.PTW = rg.PTW + len(spare_pages) if PTW is None else PTW
         self.k = wl.k
         self.k_pages = wl.k_pages if page_budget is None else page_budget
         self.page_budget = page_budget

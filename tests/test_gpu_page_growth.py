@@ -168,6 +168,9 @@ def test_runner_refusals(dsa):
     for kw in (dict(spare_pages=[1]), dict(PTW=4), dict(max_kv=100)):
         with pytest.raises(ValueError):
             LayerRunner(wl, DEV, **kw)
+    for kw in (dict(PTW=0), dict(max_kv=63)):
+        with pytest.raises(ValueError):
+            LayerRunner(wl, DEV, tables=True, **kw)
 
 
 def test_no_requests_and_the_largest_number(dsa):
