@@ -49,3 +49,13 @@ def test_a_wait_that_runs_out_in_half_of_a_warp():
     dsa.dsa_selftest_wait_timeout(st, limit_clocks=2_000_000)  # about a millisecond for each of its two waits
     torch.cuda.synchronize()
     assert st.item() == 8  # DSA_STATUS_TIMEOUT, and no lane took the second wait for met
+
+
+@pytest.mark.parametrize("name,first,last", [
+    ("attend_cache.cu", "void copy_boxes(", "// The g-th run of"),
+    ("attend.cu", "- gather\n", "- softmax\n"),
+])
+def test_copies_in_flight_are_waited_for_when_unwinding(name, first, last):
+    """A thread that issues TMA boxes and gives up waits (bounded) until they
+    have landed: shared memory must not be written after its block has gone."""
+    assert re.search(r"\b(mbar_wait_drain|drain_boxes)\(", _between(_source(name), first, last))
