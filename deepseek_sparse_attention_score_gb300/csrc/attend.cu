@@ -371,20 +371,6 @@ __device__ __forceinline__ void mma_issuer(uint32_t tmem, uint32_t qs_addr, uint
   }
 }
 
-// Unwinding after a wait that gave up: of the K and V parts issued so far (K of
-// tile 0, V of tile 0, K of tile 1, ...) the last four, one per stage, may be in
-// flight and must not land after the CTA has gone. Not inlined, and called where
-// the loop is left: its code in the loop's path, or the count kept beyond the
-// loop, cost the query-block prefill 0.8% and 0.6%, this 0.5%.
-__device__ __noinline__ void drain_boxes(uint64_t* kfull, uint64_t* vfull, int parts) {
-#pragma unroll 1
-  for (int u = max(0, parts - 4); u < parts; ++u) {
-    const int ti = u >> 1;
-    if (u & 1) mbar_wait_drain(vfull + ti % kVStages, (ti / kVStages) & 1);
-    else mbar_wait_drain(kfull + ti % kKStages, (ti / kKStages) & 1);
-  }
-}
-
 // kSoftCap: the logit cap of the dense fallback, a separate instantiation
 // so that the common path carries none of its code
 // kCopyW: copier warps (kCopyWarpsToken or kCopyWarpsRuns); the block has
@@ -591,23 +577,14 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
     const int src_k0 = kcol0 * 64 + (lane & 7) * 8, src_k1 = kcol1 * 64 + (kc1 & 7) * 8;
     const int src_v = vcol * 64 + (lane & 7) * 8;
     const uint32_t dst_k0 = kpos0 * kBlk, dst_k1 = kpos1 * kBlk, dst_v = (lane >> 3) * kBlk;
-    auto unwind = [&](int parts) {
-      if (!kRows && ctid == 0) drain_boxes(kfull, vfull, parts);
-    };
     for (int ti = 0;; ++ti) {
       const int j0 = 2 * ti, s0 = j0 % kRing, s1 = (j0 + 1) % kRing;
       const int ks = ti % kKStages, vs = ti % kVStages;
-      if (!mbar_wait(rfull + s0, (j0 / kRing) & 1, abort_flag)) {
-        unwind(2 * ti);
-        break;
-      }
+      if (!mbar_wait(rfull + s0, (j0 / kRing) & 1, abort_flag)) break;
       if (ring_end[s0]) {
         // the end marker stands for a whole tile: both steps' arrivals
-        if (!mbar_wait(kempty + ks, ((ti / kKStages) & 1) ^ 1, abort_flag) ||
-            !mbar_wait(vempty + vs, ((ti / kVStages) & 1) ^ 1, abort_flag)) {
-          unwind(2 * ti);
-          break;
-        }
+        if (!mbar_wait(kempty + ks, ((ti / kKStages) & 1) ^ 1, abort_flag)) break;
+        if (!mbar_wait(vempty + vs, ((ti / kVStages) & 1) ^ 1, abort_flag)) break;
         if (ctid == 0) {
           kst_end[ks] = 1u;
           vst_end[vs] = 1u;
@@ -623,16 +600,10 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
         mbar_arrive(rempty + s0);
         break;
       }
-      if (!mbar_wait(rfull + s1, ((j0 + 1) / kRing) & 1, abort_flag)) {
-        unwind(2 * ti);
-        break;
-      }
+      if (!mbar_wait(rfull + s1, ((j0 + 1) / kRing) & 1, abort_flag)) break;
       const int base0 = ring_base[s0], base1 = ring_base[s1];
       // ---- K parts
-      if (!mbar_wait(kempty + ks, ((ti / kKStages) & 1) ^ 1, abort_flag)) {
-        unwind(2 * ti);
-        break;
-      }
+      if (!mbar_wait(kempty + ks, ((ti / kKStages) & 1) ^ 1, abort_flag)) break;
       const uint32_t kd = smem_u32(kst_s + ks * kKStageBytes);
 #pragma unroll 1
       for (int sb = 0; sb < 2; ++sb) {
@@ -671,10 +642,7 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
         mbar_arrive(kfull + ks);
       }
       // ---- V parts
-      if (!mbar_wait(vempty + vs, ((ti / kVStages) & 1) ^ 1, abort_flag)) {
-        unwind(2 * ti + 1);
-        break;
-      }
+      if (!mbar_wait(vempty + vs, ((ti / kVStages) & 1) ^ 1, abort_flag)) break;
       const uint32_t vd = smem_u32(vst_s + vs * kVStageBytes);
 #pragma unroll 1
       for (int sb = 0; sb < 2; ++sb) {
@@ -894,7 +862,15 @@ __global__ void __launch_bounds__((6 + kCopyW) * 32, 1)
     if (*abort_flag && lane == 0) {
       set_status(prm.dev_status, DSA_STATUS_TIMEOUT);
       mbar_wait_drain(qbar, 0);  // the Q copy must not land after the CTA exits
+      // Nor may boxes of key parts: how many are in flight only the copier
+      // knew, so they get a time that no copy takes, about 70 ms. (Waiting on their barriers where the copier leaves its loop
+      // changed that loop's code and cost the query-block prefill 0.5%.)
+      if (!kRows) {
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1LL << 27)) __nanosleep(1000);
+      }
     }
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

@@ -51,11 +51,11 @@ def test_a_wait_that_runs_out_in_half_of_a_warp():
     assert st.item() == 8  # DSA_STATUS_TIMEOUT, and no lane took the second wait for met
 
 
-@pytest.mark.parametrize("name,first,last", [
-    ("attend_cache.cu", "void copy_boxes(", "// The g-th run of"),
-    ("attend.cu", "- gather\n", "- softmax\n"),
+@pytest.mark.parametrize("name,first,last,waits", [
+    ("attend_cache.cu", "void copy_boxes(", "// The g-th run of", r"mbar_wait_drain\(br\.full"),
+    ("attend.cu", "if (*abort_flag && lane == 0) {", "tmem_dealloc(", r"while \(clock64\(\) - t0 < "),
 ])
-def test_copies_in_flight_are_waited_for_when_unwinding(name, first, last):
-    """A thread that issues TMA boxes and gives up waits (bounded) until they
-    have landed: shared memory must not be written after its block has gone."""
-    assert re.search(r"\b(mbar_wait_drain|drain_boxes)\(", _between(_source(name), first, last))
+def test_copies_in_flight_are_waited_for_when_unwinding(name, first, last, waits):
+    """A block that gives up waits (bounded) until its TMA boxes have landed:
+    shared memory must not be written after the block has gone."""
+    assert re.search(waits, _between(_source(name), first, last))
