@@ -455,11 +455,11 @@ __global__ void __launch_bounds__(IdxCfg<NQ>::THREADS, 1)
         }
       }
       const int qb = it & 1;
-      if (!(ok = mbar_wait(qfull + qb, (it >> 1) & 1, abort_flag))) break;
+      if (!(ok = mbar_wait_warp(qfull + qb, (it >> 1) & 1, abort_flag))) break;
       const float* wq = w_s + qb * C::N;
       for (int tile = kb / 128; tile * 128 < ke; ++tile, ++dt) {
         const int db = dt & 1;
-        if (!(ok = mbar_wait(dfull + db, (dt >> 1) & 1, abort_flag))) break;
+        if (!(ok = mbar_wait_warp(dfull + db, (dt >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         const int key = tile * 128 + quad * 32 + lane;
         uint32_t r[QPW][32];

@@ -28,6 +28,7 @@ def _between(text, first, last):
     ("attend_cache.cu", "void copy_keys(", "// The copier of the bf16 cache"),
     ("attend_cache.cu", "void issue_mmas(", "// A copier warp:"),
     ("attend.cu", "- softmax\n", "const bool have_o"),
+    ("indexer.cu", "- epilogue\n", "tmem_dealloc("),
     ("attend.cu", "if (warp >= 4 && warp < 8) {", "tmem_st_wait();"),
 ])
 def test_whole_warps_wait_as_one(name, first, last):
