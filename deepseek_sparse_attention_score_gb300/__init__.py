@@ -5,6 +5,7 @@ in ``include/dsa.h``); :mod:`.abi` is its thin Python binding and
 :mod:`.layer` chains the calls into one DSA layer step.
 """
 from .abi import (  # noqa: F401
+    AppendTarget,
     DSAError,
     PageTables,
     RopeTarget,
@@ -12,6 +13,7 @@ from .abi import (  # noqa: F401
     dsa_q4_read_rows,
     dsa_q4_write_back,
     dsa_rope,
+    dsa_rope_append,
     dsa_rope_attention_scales,
     dsa_rope_freqs,
     dsa_sparse_mla_decode_q4,

@@ -64,6 +64,7 @@ EXPORTS = (
     "dsa_q4_read_rows",
     "dsa_sparse_mla_decode_q4",
     "dsa_window_mla",
+    "dsa_rope_append",
 )
 Q4_ROW_BYTES = 416  # one row of the 4-bit latent cache
 
@@ -86,6 +87,9 @@ _L = ctypes.c_int64
 # rot_off, layout, dtype, scale (72 bytes without padding). Packed bytes: a
 # ctypes.Structure takes four times as long to fill.
 _rope_target = struct.Struct("=QQqqqqiiiiif").pack
+# dsa_append_target: x, x_rot, cache, x_stride, x_rot_stride, cache_stride, D,
+# rot_off, layout, format, scale (68 bytes, padded to 72)
+_append_target = struct.Struct("=QQQqqqiiiif4x").pack
 
 
 def lib() -> ctypes.CDLL:
@@ -139,6 +143,7 @@ def lib() -> ctypes.CDLL:
                                            _P, _P, _P, _Z, _P]
     L.dsa_window_mla.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _F,
                                  _P, _P, _P, _Z, _P]
+    L.dsa_rope_append.argtypes = [_P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _P]
     L.dsa_device_sm_count.argtypes = []
     L.dsa_launch_count.argtypes = []
     L.dsa_launch_count.restype = ctypes.c_longlong
@@ -687,6 +692,20 @@ class RopeTarget:
         self.__init__(self.x, self.y, rot_off=off, rot_dim=dim, layout=layout, scale=scale)
 
 
+def _rope_targets(targets, T, rot, dev):
+    """The packed targets of a call, each as its tensors are now."""
+    for g in targets:
+        x, y = g.x, g.y
+        if (x.data_ptr() != g.xp or x.stride() != g.xs or x.shape != g.shape or
+                y is not x and (y.data_ptr() != g.yp or y.stride() != g.ys or y.shape != g.shape)):
+            g.repack()
+        if x.device != dev or g.shape[0] != T:
+            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(x.shape)} on {x.device}")
+        if g.rot_dim != rot:
+            raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
+    return b"".join([g.c for g in targets])
+
+
 def dsa_rope(targets, positions, freqs, *, inverse=False):
     """Rotate the rows of one or several :class:`RopeTarget` in one launch.
     ``positions`` int32 [T] (rows with a negative one are left alone),
@@ -699,17 +718,105 @@ def dsa_rope(targets, positions, freqs, *, inverse=False):
     a_pos = _i32(positions, "positions", dev)
     _need(freqs, "freqs", torch.float64, dev, 1)
     T, rot = positions.numel(), 2 * freqs.numel()
+    packed = _rope_targets(ts, T, rot, dev)
+    _launch(dev, "dsa_rope", packed, len(ts), T, rot, a_pos, freqs.data_ptr(), 1 if inverse else 0)
+    return ts[0].y if one else [g.y for g in ts]
+
+
+class AppendTarget:
+    """Rows that one :func:`dsa_rope_append` call writes into a paged cache:
+    ``x`` [T, D] (bf16, contiguous columns), rotated in columns ``rot_off`` ..
+    ``rot_off + rot_dim - 1`` (all after ``rot_off`` by default), into
+    ``cache`` [P, ps, >= D] (bf16) or a 4-bit latent cache [P, ps, 416]
+    (uint8; D 576, of which the last 64 rotate). With ``x_rot`` [T, rot_dim]
+    the rotated columns come from there and ``x`` holds only the others.
+    ``layout`` and ``scale`` as for :class:`RopeTarget`. May be kept and used
+    again, as a :class:`RopeTarget`."""
+
+    __slots__ = ("x", "cache", "x_rot", "rot_dim", "args", "c", "was")
+
+    def __init__(self, x, cache, *, x_rot=None, rot_off=0, rot_dim=None, layout="half", scale=1.0):
+        dev = getattr(cache, "device", None)
+        for name, t in (("x", x), ("x_rot", x_rot)):
+            if name == "x_rot" and t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
+                raise TypeError(f"{name} must be a bf16 tensor [T, D]")
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            if t.shape[1] > 1 and t.stride(1) != 1:
+                raise ValueError(f"the columns of {name} must be contiguous")
+        q4 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
+        if q4:
+            P, ps = _cache4(cache, dev)
+        else:
+            _need(cache, "cache", torch.bfloat16, dev, 3)
+            P, ps, _ = cache.shape
+        lay = _ROPE_LAYOUTS.get(layout)
+        if lay is None:
+            raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
+        T, D = x.shape
+        if x_rot is not None:
+            if x_rot.shape[0] != T:
+                raise ValueError(f"x_rot must have {T} rows like x, got {x_rot.shape[0]}")
+            if rot_dim not in (None, x_rot.shape[1]):
+                raise ValueError(f"x_rot has {x_rot.shape[1]} columns, rot_dim is {rot_dim}")
+            D += x_rot.shape[1]
+        self.x, self.cache, self.x_rot, self.args = x, cache, x_rot, (rot_off, rot_dim, layout, scale)
+        self.rot_dim = x_rot.shape[1] if x_rot is not None else D - rot_off if rot_dim is None else rot_dim
+        row = Q4_ROW_BYTES if q4 else cache.shape[2]
+        if not q4 and D > row:
+            raise ValueError(f"cache rows have {row} columns, {D} are written")
+        self.c = _append_target(x.data_ptr(), 0 if x_rot is None else x_rot.data_ptr(), cache.data_ptr(),
+                                x.stride(0) if T > 1 else -(-x.shape[1] // 8) * 8,
+                                0 if x_rot is None else x_rot.stride(0) if T > 1 else self.rot_dim, row, D, rot_off,
+                                lay, 1 if q4 else 0, scale)
+        self.was = self._now()
+
+    def _now(self):
+        r = self.x_rot
+        return (self.x.data_ptr(), self.x.shape, self.x.stride(), self.cache.data_ptr(), self.cache.shape,
+                r is not None and (r.data_ptr(), r.shape, r.stride()))
+
+    def repack(self):
+        """Pack the tensors as they are now, with the checks of a new target."""
+        off, dim, layout, scale = self.args
+        self.__init__(self.x, self.cache, x_rot=self.x_rot, rot_off=off, rot_dim=dim, layout=layout, scale=scale)
+
+
+def dsa_rope_append(targets, positions, slots, freqs, *, rotate=(), dev_status=None):
+    """Write the rows of one or several :class:`AppendTarget` into their paged
+    caches, rotated on the way: row t for position ``positions[t]`` into cache
+    row ``slots[t]`` (both int32 [T], as :func:`dsa_build_page_tables` makes
+    them; a row where either is negative is written nowhere). The
+    :class:`RopeTarget` in ``rotate``, such as the layer's queries, turn in the
+    same launch, as :func:`dsa_rope` turns them. ``freqs``: fp64 [rot_dim / 2].
+    Returns the caches, one or a list as ``targets`` came."""
+    one = isinstance(targets, AppendTarget)
+    ts = [targets] if one else list(targets)
+    rs = [rotate] if isinstance(rotate, RopeTarget) else list(rotate)
+    dev = positions.device
+    a_pos, a_slots = _i32(positions, "positions", dev), _i32(slots, "slots", dev)
+    _need(freqs, "freqs", torch.float64, dev, 1)
+    T, rot = positions.numel(), 2 * freqs.numel()
+    if slots.numel() != T:
+        raise ValueError(f"slots must have {T} entries like positions, got {slots.numel()}")
+    if not ts:
+        raise ValueError("dsa_rope_append needs a target")
+    pages = ts[0].cache.shape[:2]
     for g in ts:
-        x, y = g.x, g.y
-        if (x.data_ptr() != g.xp or x.stride() != g.xs or x.shape != g.shape or
-                y is not x and (y.data_ptr() != g.yp or y.stride() != g.ys or y.shape != g.shape)):
+        if g._now() != g.was:
             g.repack()
-        if x.device != dev or g.shape[0] != T:
-            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(x.shape)} on {x.device}")
+        if g.x.device != dev or g.x.shape[0] != T:
+            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(g.x.shape)} on {g.x.device}")
         if g.rot_dim != rot:
             raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
-    _launch(dev, "dsa_rope", b"".join([g.c for g in ts]), len(ts), T, rot, a_pos, freqs.data_ptr(), 1 if inverse else 0)
-    return ts[0].y if one else [g.y for g in ts]
+        if g.cache.shape[:2] != pages:
+            raise ValueError(f"the caches need the same pages, got {tuple(g.cache.shape[:2])} and {tuple(pages)}")
+    _launch(dev, "dsa_rope_append", b"".join([g.c for g in ts]), len(ts),
+            _rope_targets(rs, T, rot, dev) if rs else None, len(rs), T, rot, a_pos, a_slots, freqs.data_ptr(),
+            pages[0], pages[1], _status(dev_status, dev))
+    return ts[0].cache if one else [g.cache for g in ts]
 
 
 def dsa_rope_freqs(rot_dim, *, base=10000.0, scaling="none", factor=1.0, orig_max_pos=4096, beta_fast=32.0,

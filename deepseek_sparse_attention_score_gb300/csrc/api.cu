@@ -12,6 +12,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "append.cuh"
 #include "attend.cuh"
 #include "common.cuh"
 #include "indexer.cuh"
@@ -564,10 +565,7 @@ static bool rows_apart(long long n0, long long s0, long long n1, long long s1, l
   return s1 >= D && (s0 - D) / (n1 - 1) >= s1 && s0 >= D;
 }
 
-int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets, int T, int rot_dim,
-             const int32_t* positions, const double* freqs, int inverse) {
-  NvtxRange nvtx_range("dsa_rope");
-  if (T < 0 || !targets || n_targets < 1) return DSA_ERR_INVALID_ARGUMENT;
+static int rope_check(const dsa_rope_target* targets, int n_targets, int T, int rot_dim) {
   if (n_targets > kRopeMaxTargets) return DSA_ERR_UNSUPPORTED;
   if (rot_dim < 2 || rot_dim % 2) return DSA_ERR_INVALID_ARGUMENT;
   if (rot_dim > kRopeMaxDim) return DSA_ERR_UNSUPPORTED;
@@ -585,9 +583,57 @@ int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets,
     const uintptr_t es = g.dtype == DSA_DTYPE_F32 ? 4 : 2;
     if (reinterpret_cast<uintptr_t>(g.x) % es || reinterpret_cast<uintptr_t>(g.y) % es) return DSA_ERR_ALIGNMENT;
   }
+  return DSA_OK;
+}
+
+int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets, int T, int rot_dim,
+             const int32_t* positions, const double* freqs, int inverse) {
+  NvtxRange nvtx_range("dsa_rope");
+  if (T < 0 || !targets || n_targets < 1) return DSA_ERR_INVALID_ARGUMENT;
+  const int rc = rope_check(targets, n_targets, T, rot_dim);
+  if (rc) return rc;
   if (T == 0) return DSA_OK;
   if (!positions || !freqs) return DSA_ERR_INVALID_ARGUMENT;
   return run_rope(static_cast<cudaStream_t>(stream), targets, n_targets, T, rot_dim, positions, freqs, inverse != 0);
+}
+
+int dsa_rope_append(dsa_stream_t stream, const dsa_append_target* append, int n_append, const dsa_rope_target* rotate,
+                    int n_rotate, int T, int rot_dim, const int32_t* positions, const int32_t* slots,
+                    const double* freqs, int P, int ps, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_rope_append");
+  if (T < 0 || P < 0 || !append || n_append < 1 || n_rotate < 0 || (n_rotate > 0 && !rotate))
+    return DSA_ERR_INVALID_ARGUMENT;
+  if (n_append > kAppendMaxTargets || !ps_supported(ps) || (long long)P * ps >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+  const int rc = rope_check(rotate, n_rotate, T, rot_dim);
+  if (rc) return rc;
+  if (rot_dim % 16) return DSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_append; ++i) {
+    const dsa_append_target& g = append[i];
+    if (g.rot_off < 0 || (long long)g.rot_off + rot_dim > g.D) return DSA_ERR_INVALID_ARGUMENT;
+    if ((g.layout != DSA_ROPE_INTERLEAVED && g.layout != DSA_ROPE_HALF) || !std::isfinite(g.scale))
+      return DSA_ERR_INVALID_ARGUMENT;
+    if (g.format != DSA_CACHE_BF16 && g.format != DSA_CACHE_Q4) return DSA_ERR_UNSUPPORTED;
+    const bool q4 = g.format == DSA_CACHE_Q4, split = g.x_rot != nullptr;
+    if (q4 && (g.D != 576 || g.rot_off != 512 || rot_dim != 64)) return DSA_ERR_UNSUPPORTED;
+    if (g.D > kRopeMaxColumns || g.D % 8 || g.rot_off % 8) return DSA_ERR_UNSUPPORTED;
+    if (T == 0) continue;
+    const int pass = g.D - rot_dim;
+    const bool reads_x = !split || pass > 0;
+    if ((reads_x && !g.x) || (P > 0 && !g.cache)) return DSA_ERR_INVALID_ARGUMENT;
+    // a single row's strides are never stepped over
+    if (T > 1 && ((reads_x && g.x_stride < (split ? pass : g.D)) || (split && g.x_rot_stride < rot_dim)))
+      return DSA_ERR_INVALID_ARGUMENT;
+    if (!q4 && g.cache_stride < g.D) return DSA_ERR_INVALID_ARGUMENT;
+    if ((reads_x && g.x_stride % 8) || (split && g.x_rot_stride % 8) || (!q4 && g.cache_stride % 8))
+      return DSA_ERR_UNSUPPORTED;
+    if ((reads_x && !aligned16(g.x)) || !aligned16(g.x_rot) || !aligned16(g.cache)) return DSA_ERR_ALIGNMENT;
+    for (int j = 0; j < i; ++j)
+      if (P > 0 && append[j].cache == g.cache) return DSA_ERR_INVALID_ARGUMENT;
+  }
+  if (T == 0) return DSA_OK;
+  if (!positions || !slots || !freqs) return DSA_ERR_INVALID_ARGUMENT;
+  return run_rope_append(static_cast<cudaStream_t>(stream), rotate, n_rotate, append, n_append, T, rot_dim, positions,
+                         slots, freqs, (long long)P * ps, dev_status);
 }
 
 int dsa_rope_freqs(int rot_dim, double base, int scaling, double factor, int orig_max_pos, double beta_fast,

@@ -22,41 +22,6 @@ namespace {
 constexpr int kRowThreads = 128;  // 4 rows per CTA
 constexpr int kRowsPerCta = kRowThreads / 32;
 
-// code pair e2m1(hi) << 4 | e2m1(lo), to the nearest even, saturating
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
-      : "=r"(r)
-      : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_of(float x) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
-  return r & 0xffu;
-}
-// 8 bf16 (four words) and 1/s -> one word of codes: dims 0, 2, 4, 6 in
-// nibbles 0..3, dims 1, 3, 5, 7 in nibbles 4..7.
-//
-// x * r with r = 1/s rounded is within 2^-22 of x / s. x has 8 significant
-// bits, s 4 and a boundary between two codes 3, so x / s is either exactly a
-// boundary or at least 2^-8 away from it: rounding the product to 16 bits
-// puts the first kind back on the boundary and moves none of the second over
-// it, as an exact division would, at a fraction of its cost.
-__device__ __forceinline__ uint32_t quantise8(const uint32_t (&x)[4], float r) {
-  float e[4], o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(x[i] << 16) * r, b = __uint_as_float(x[i] & 0xffff0000u) * r;
-    e[i] = __uint_as_float((__float_as_uint(a) + 0x80u) & 0xffffff00u);
-    o[i] = __uint_as_float((__float_as_uint(b) + 0x80u) & 0xffffff00u);
-  }
-  return e2m1_pair(e[0], e[1]) | (e2m1_pair(e[2], e[3]) << 8) | (e2m1_pair(o[0], o[1]) << 16) |
-         (e2m1_pair(o[2], o[3]) << 24);
-}
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
 __global__ void __launch_bounds__(kRowThreads) q4_write_back_kernel(
     const uint16_t* __restrict__ rows, long long src_stride, uint8_t* __restrict__ cache,
     const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu_q_lens,
@@ -89,20 +54,8 @@ __global__ void __launch_bounds__(kRowThreads) q4_write_back_kernel(
   }
   uint8_t* dst = cache + ((size_t)pg * ps + (size_t)(pos % ps)) * kRow4Bytes;
   const uint32_t x0[4] = {u.x, u.y, u.z, u.w}, x1[4] = {v.x, v.y, v.z, v.w};
-  // the largest magnitude as an integer of the bf16 bits: the order of the
-  // values, with infinities and NaN on top
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max_u16x2(m, max_u16x2(x0[i] & 0x7fff7fffu, x1[i] & 0x7fff7fffu));
-  const uint32_t top = max(m & 0xffffu, m >> 16);
-  uint32_t sb = 0x7fu;  // NaN, with zero codes
-  uint2 code = make_uint2(0u, 0u);
-  if (top < 0x7f80u) {
-    sb = e4m3_of(__fdiv_rn(__uint_as_float(top << 16), 6.f));
-    const float sc = e4m3_value(sb);
-    const float r = sc > 0.f ? __frcp_rn(sc) : 0.f;
-    code = make_uint2(quantise8(x0, r), quantise8(x1, r));
-  }
+  uint32_t sb;
+  const uint2 code = quantise16(x0, x1, sb);
   reinterpret_cast<uint2*>(dst)[lane] = code;
   dst[kRow4Codes + lane] = (uint8_t)sb;
   if (lane < kRow4Rope / 16) reinterpret_cast<uint4*>(dst + kRow4Codes + kRow4Scales)[lane] = rp;

@@ -27,7 +27,7 @@ from . import abi
 
 class LayerRunner:
     def __init__(self, wl, device, page_budget=None, prefill=None, cache_bits=16, tables=False, rope=None,
-                 spare_pages=(), PTW=None, max_kv=None):
+                 spare_pages=(), PTW=None, max_kv=None, append=False):
         """``wl``: a dsa_inputs.Workload whose tensors already live on ``device``
         (or on the CPU; they are moved). ``page_budget``: decode page-budget
         mode with that many pages. ``prefill``: force the prefill path
@@ -51,11 +51,16 @@ class LayerRunner:
         of indexer queries and keys) are taken as not rotated yet, and every
         step rotates its tokens'; indexer columns pair by halves. ``scale`` is
         that of the rotated columns alone: YaRN's temperature of the logits
-        belongs in the workload's ``sm_scale`` (dsa_rope_attention_scales)."""
+        belongs in the workload's ``sm_scale`` (dsa_rope_attention_scales).
+        ``append``, with ``rope``: the rows are rotated on their way into the
+        caches, in one launch with the queries (dsa_rope_append), and
+        ``new_kv`` and ``new_k`` stay as they are."""
         if cache_bits not in (4, 16):
             raise ValueError(f"cache_bits must be 4 or 16, got {cache_bits}")
         if rope is not None and not tables:
             raise ValueError("rope needs the positions that tables=True finds")
+        if append and rope is None:
+            raise ValueError("append is for rows that rope rotates")
         if not tables and (len(spare_pages) or PTW is not None or max_kv is not None):
             raise ValueError("spare_pages, PTW and max_kv are for tables=True")
         rg = wl.rg
@@ -97,7 +102,7 @@ class LayerRunner:
             self.kv4 = [self._quantised(c) for c in self.kv]
             self.kv = None
         self.tables = self._make_tables(rg, spare_pages) if tables else None
-        self.rope = None
+        self.rope = self.append = None
         if rope is not None:
             freqs, scale, layout = rope
             self.rope = torch.as_tensor(freqs, dtype=torch.float64).to(dev)
@@ -108,12 +113,22 @@ class LayerRunner:
             # layer -> what it rotates; the indexer's queries with the first layer
             self.rope_targets = []
             for layer in range(len(self.types)):
-                g = [turn(self.q[layer], qk, scale, layout), turn(self.new_kv[layer], qk, scale, layout)]
-                if self.full_slot[layer] >= 0:
-                    g.append(turn(self.new_k[self.full_slot[layer]], ki, 1.0, "half"))
+                g = [turn(self.q[layer], qk, scale, layout)]
+                if not append:
+                    g.append(turn(self.new_kv[layer], qk, scale, layout))
+                    if self.full_slot[layer] >= 0:
+                        g.append(turn(self.new_k[self.full_slot[layer]], ki, 1.0, "half"))
                 if layer == 0:
                     g.append(turn(self.q_idx, ki, 1.0, "half"))
                 self.rope_targets.append(g)
+            if append:
+                self.append = []
+                for layer, slot in enumerate(self.full_slot):
+                    g = [abi.AppendTarget(self.new_kv[layer], (self.kv4 if cache_bits == 4 else self.kv)[layer],
+                                          rot_off=512, layout=layout, scale=scale)]
+                    if slot >= 0:
+                        g.append(abi.AppendTarget(self.new_k[slot], self.kcache[slot], rot_dim=64))
+                    self.append.append(g)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.ws_idx = torch.empty(max(1, abi.dsa_indexer_workspace_size(T, self.S, self.max_kv, self.ps)),
                                   dtype=torch.uint8, device=dev)
@@ -177,13 +192,19 @@ class LayerRunner:
 
     def rotate(self, layer):
         """The layer's queries, latent rows and indexer keys at their
-        positions (with ``rope``)."""
-        if self.rope is not None:
+        positions (with ``rope``; with ``append`` the rows go into the caches
+        as well)."""
+        if self.append is not None:
+            abi.dsa_rope_append(self.append[layer], self.tables.positions, self.tables.slots, self.rope,
+                                rotate=self.rope_targets[layer], dev_status=self.status)
+        elif self.rope is not None:
             abi.dsa_rope(self.rope_targets[layer], self.tables.positions, self.rope)
 
     def write_back(self, layer):
         """The layer's new latent rows, and on a full layer its new indexer
         keys, into their slots of the paged caches."""
+        if self.append is not None:  # rotate() has written them
+            return
         if self.cache_bits == 4:
             abi.dsa_q4_write_back(self.new_kv[layer], self.kv4[layer], *self.meta, dev_status=self.status)
             if self.full_slot[layer] >= 0:

@@ -529,6 +529,56 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
                              uint16_t* rows, int dst_stride, int32_t* dev_status);
 
 /* ------------------------------------------------------------------------
+ * Appending rows to the paged caches with the rotary positions applied on the
+ * way (no counterpart on the pages, whose rows arrive rotated): dsa_rope of a
+ * step's new rows and their write-back in one pass, and in the same launch
+ * dsa_rope of other targets, such as the layer's queries. Row t of an append
+ * target goes to cache row slots[t] (page * ps + row, as dsa_build_page_tables
+ * numbers them); every other row of the cache, and the columns of a row from D
+ * on, are left untouched.
+ *   append     host [n_append], 1 to 4 targets; all caches have P pages of ps
+ *              rows
+ *     x, x_stride          bf16 [T, D]; with x_rot, [T, D - rot_dim]: the
+ *                          columns that do not rotate, without a gap
+ *     x_rot, x_rot_stride  bf16 [T, rot_dim]: the rotated columns when they are
+ *                          a tensor of their own, else NULL
+ *     cache, cache_stride  DSA_CACHE_BF16: bf16 [P, ps, cache_stride], written
+ *                          in place; DSA_CACHE_Q4: bytes [P, ps, 416], the row
+ *                          quantised as dsa_q4_write_back does (the stride is
+ *                          not read; D 576, rot_off 512, rot_dim 64)
+ *     D, rot_off           columns [rot_off, rot_off + rot_dim) rotate
+ *     layout, scale        as in dsa_rope_target
+ *   rotate     host [n_rotate], 0 to 8 targets of dsa_rope (NULL with 0)
+ *   positions  int32 [T], slots int32 [T]: a row where either is negative
+ *              (padding) is appended nowhere; the targets of `rotate` follow
+ *              the position alone
+ *   freqs      fp64 [rot_dim / 2]
+ * A slot >= P * ps sets DSA_STATUS_BAD_INDEX and its row is skipped. Slots of
+ * a call are distinct: of rows with one slot any may win, 16 bytes at a time.
+ * No source may overlap a cache or an output. Angles, products and rounding are
+ * those of dsa_rope.
+ * Supported: rot_dim a multiple of 16 up to 512, D <= 4096, D, rot_off and the
+ * strides multiples of 8, 16-byte aligned rows and caches, P * ps < 2^31.
+ * Targets of `rotate` that do not lie on 16 bytes take a second launch.
+ * Needs no workspace.
+ * ------------------------------------------------------------------------ */
+enum dsa_cache_format { DSA_CACHE_BF16 = 0, DSA_CACHE_Q4 = 1 };
+typedef struct dsa_append_target {
+  const void* x;
+  const void* x_rot;
+  void* cache;
+  int64_t x_stride, x_rot_stride, cache_stride;
+  int32_t D, rot_off;
+  int32_t layout; /* dsa_rope_layout */
+  int32_t format; /* dsa_cache_format */
+  float scale;
+} dsa_append_target;
+DSA_API int dsa_rope_append(dsa_stream_t stream, const dsa_append_target* append /* host */, int n_append,
+                            const dsa_rope_target* rotate /* host */, int n_rotate, int T, int rot_dim,
+                            const int32_t* positions, const int32_t* slots, const double* freqs, int P, int ps,
+                            int32_t* dev_status);
+
+/* ------------------------------------------------------------------------
  * Sparse absorbed-MLA attention over the 4-bit latent cache: as
  * dsa_sparse_mla_decode (token or page units, lse, empty rows,
  * reproducibility) with `cache` [P, ps, 416] bytes in the place of kv and
