@@ -733,50 +733,56 @@ class AppendTarget:
     ``layout`` and ``scale`` as for :class:`RopeTarget`. May be kept and used
     again, as a :class:`RopeTarget`."""
 
-    __slots__ = ("x", "cache", "x_rot", "rot_dim", "args", "c", "was")
+    __slots__ = ("x", "cache", "x_rot", "rot_dim", "args", "c", "was", "place")
 
     def __init__(self, x, cache, *, x_rot=None, rot_off=0, rot_dim=None, layout="half", scale=1.0):
-        dev = getattr(cache, "device", None)
-        for name, t in (("x", x), ("x_rot", x_rot)):
-            if name == "x_rot" and t is None:
-                continue
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 2:
-                raise TypeError(f"{name} must be a bf16 tensor [T, D]")
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, expected {dev}")
-            if t.shape[1] > 1 and t.stride(1) != 1:
-                raise ValueError(f"the columns of {name} must be contiguous")
-        q4 = isinstance(cache, torch.Tensor) and cache.dtype == torch.uint8
+        if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+            raise TypeError("cache must be a tensor [P, ps, row]")
+        dev, (P, ps, row), cp = cache.device, cache.shape, cache.data_ptr()
+        q4 = cache.dtype is torch.uint8
         if q4:
-            P, ps = _cache4(cache, dev)
-        else:
-            _need(cache, "cache", torch.bfloat16, dev, 3)
-            P, ps, _ = cache.shape
+            _cache4(cache, dev)
+        elif cache.dtype is not torch.bfloat16:
+            raise TypeError(f"cache must be bf16, or uint8 for 4-bit rows, got {cache.dtype}")
+        elif not cache.is_contiguous():
+            raise ValueError("cache must be contiguous")
         lay = _ROPE_LAYOUTS.get(layout)
         if lay is None:
             raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUTS)}, got {layout!r}")
-        T, D = x.shape
+        (T, D), xp, xs = self._rows("x", x, dev)
+        r = None
         if x_rot is not None:
-            if x_rot.shape[0] != T:
-                raise ValueError(f"x_rot must have {T} rows like x, got {x_rot.shape[0]}")
-            if rot_dim not in (None, x_rot.shape[1]):
-                raise ValueError(f"x_rot has {x_rot.shape[1]} columns, rot_dim is {rot_dim}")
-            D += x_rot.shape[1]
-        self.x, self.cache, self.x_rot, self.args = x, cache, x_rot, (rot_off, rot_dim, layout, scale)
-        self.rot_dim = x_rot.shape[1] if x_rot is not None else D - rot_off if rot_dim is None else rot_dim
-        row = Q4_ROW_BYTES if q4 else cache.shape[2]
-        if not q4 and D > row:
+            r = (n, R), rp, rs = self._rows("x_rot", x_rot, dev)
+            if n != T:
+                raise ValueError(f"x_rot must have {T} rows like x, got {n}")
+            if rot_dim is not None and rot_dim != R:
+                raise ValueError(f"x_rot has {R} columns, rot_dim is {rot_dim}")
+            D, rot, rp, rs = D + R, R, rp, rs[0] if T > 1 else 0
+        else:
+            rot, rp, rs = D - rot_off if rot_dim is None else rot_dim, 0, 0
+        if D > row and not q4:
             raise ValueError(f"cache rows have {row} columns, {D} are written")
-        self.c = _append_target(x.data_ptr(), 0 if x_rot is None else x_rot.data_ptr(), cache.data_ptr(),
-                                x.stride(0) if T > 1 else -(-x.shape[1] // 8) * 8,
-                                0 if x_rot is None else x_rot.stride(0) if T > 1 else self.rot_dim, row, D, rot_off,
-                                lay, 1 if q4 else 0, scale)
-        self.was = self._now()
+        self.x, self.cache, self.x_rot, self.args = x, cache, x_rot, (rot_off, rot_dim, layout, scale)
+        self.rot_dim = rot
+        self.c = _append_target(xp, rp, cp, xs[0] if T > 1 else 0, rs, row, D, rot_off, lay, q4, scale)
+        self.was = x.shape, xp, xs, cp, cache.shape, r
+        self.place = T, rot, P, ps, dev
+
+    @staticmethod
+    def _rows(name, t, dev):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 2:
+            raise TypeError(f"{name} must be a bf16 tensor [T, D]")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        shape, strides = t.shape, t.stride()
+        if strides[1] != 1 and shape[1] > 1:
+            raise ValueError(f"the columns of {name} must be contiguous")
+        return shape, t.data_ptr(), strides
 
     def _now(self):
-        r = self.x_rot
-        return (self.x.data_ptr(), self.x.shape, self.x.stride(), self.cache.data_ptr(), self.cache.shape,
-                r is not None and (r.data_ptr(), r.shape, r.stride()))
+        x, c, r = self.x, self.cache, self.x_rot
+        return (x.shape, x.data_ptr(), x.stride(), c.data_ptr(), c.shape,
+                None if r is None else (r.shape, r.data_ptr(), r.stride()))
 
     def repack(self):
         """Pack the tensors as they are now, with the checks of a new target."""
@@ -795,27 +801,27 @@ def dsa_rope_append(targets, positions, slots, freqs, *, rotate=(), dev_status=N
     one = isinstance(targets, AppendTarget)
     ts = [targets] if one else list(targets)
     rs = [rotate] if isinstance(rotate, RopeTarget) else list(rotate)
+    if not ts:
+        raise ValueError("dsa_rope_append needs a target")
     dev = positions.device
     a_pos, a_slots = _i32(positions, "positions", dev), _i32(slots, "slots", dev)
-    _need(freqs, "freqs", torch.float64, dev, 1)
+    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or freqs.device != dev or not freqs.is_contiguous():
+        _need(freqs, "freqs", torch.float64, dev, 1)
     T, rot = positions.numel(), 2 * freqs.numel()
     if slots.numel() != T:
         raise ValueError(f"slots must have {T} entries like positions, got {slots.numel()}")
-    if not ts:
-        raise ValueError("dsa_rope_append needs a target")
-    pages = ts[0].cache.shape[:2]
     for g in ts:
         if g._now() != g.was:
             g.repack()
-        if g.x.device != dev or g.x.shape[0] != T:
-            raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(g.x.shape)} on {g.x.device}")
-        if g.rot_dim != rot:
-            raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
-        if g.cache.shape[:2] != pages:
-            raise ValueError(f"the caches need the same pages, got {tuple(g.cache.shape[:2])} and {tuple(pages)}")
+        if g.place != (T, rot, P := ts[0].place[2], ps := ts[0].place[3], dev):
+            if g.x.device != dev or g.x.shape[0] != T:
+                raise ValueError(f"a target needs {T} rows on {dev}, got {tuple(g.x.shape)} on {g.x.device}")
+            if g.rot_dim != rot:
+                raise ValueError(f"a target rotates {g.rot_dim} columns, freqs are for {rot}")
+            raise ValueError(f"the caches need the same pages, got {tuple(g.cache.shape[:2])} and {(P, ps)}")
     _launch(dev, "dsa_rope_append", b"".join([g.c for g in ts]), len(ts),
-            _rope_targets(rs, T, rot, dev) if rs else None, len(rs), T, rot, a_pos, a_slots, freqs.data_ptr(),
-            pages[0], pages[1], _status(dev_status, dev))
+            _rope_targets(rs, T, rot, dev) if rs else None, len(rs), T, rot, a_pos, a_slots, freqs.data_ptr(), P, ps,
+            _status(dev_status, dev))
     return ts[0].cache if one else [g.cache for g in ts]
 
 

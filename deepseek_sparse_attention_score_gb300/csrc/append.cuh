@@ -8,6 +8,7 @@
 namespace dsa {
 
 constexpr int kAppendMaxTargets = 4;
+constexpr int kAppendTokens = 8;  // of one warp, at most
 
 struct AppendTarget {
   const uint16_t* x;   // columns that pass, and with !split the rotated ones among them
@@ -17,13 +18,15 @@ struct AppendTarget {
   long long cache_stride;  // bytes of a cache row
   int rot_at;              // byte of a cache row where the rotated columns start
   int rot_off, pass;       // first rotated column; columns that pass (4 bits: none, they are quantised)
-  int rot_units, first;    // units that rotate; units of the targets before
-  int half, split, q4;
+  int first;               // units of the targets before
+  int half, split;
   float scale;
 };
 struct AppendParams {
   AppendTarget tg[kAppendMaxTargets];
+  int q4[kAppendMaxTargets], n_q4;  // targets that are quantised
   int n, units, rot_dim, T;
+  int tokens;  // of a warp
   unsigned append_ctas;
   long long rows;  // of each cache: pages * page size
   const int32_t* positions;

@@ -84,7 +84,7 @@ def test_wrapper_refusals():
     i32, f = torch.zeros(3, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
     g = A(x, cache, rot_dim=64)
     for make, err in ((lambda: A(x.float(), cache), TypeError), (lambda: A(x[0], cache), TypeError),
-                      (lambda: A(x, cache.float()), TypeError), (lambda: A(x, cache[0]), ValueError),
+                      (lambda: A(x, cache.float()), TypeError), (lambda: A(x, cache[0]), TypeError),
                       (lambda: A(x, cache[:, :, :64]), ValueError), (lambda: A(x.t(), cache), ValueError),
                       (lambda: A(x, cache, layout="quarter"), ValueError),
                       (lambda: A(x, cache, x_rot=x[:2]), ValueError),
