@@ -18,6 +18,8 @@ from .abi import (  # noqa: F401
     dsa_rope_freqs,
     dsa_sparse_mla_decode_q4,
     dsa_window_mla,
+    dsa_prefix_mla,
+    dsa_prefix_mla_workspace_size,
     dsa_build_block_union,
     dsa_device_sm_count,
     dsa_launch_count,

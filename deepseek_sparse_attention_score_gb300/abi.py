@@ -65,6 +65,8 @@ EXPORTS = (
     "dsa_sparse_mla_decode_q4",
     "dsa_window_mla",
     "dsa_rope_append",
+    "dsa_prefix_mla_workspace_size",
+    "dsa_prefix_mla",
 )
 Q4_ROW_BYTES = 416  # one row of the 4-bit latent cache
 
@@ -144,12 +146,17 @@ def lib() -> ctypes.CDLL:
     L.dsa_window_mla.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _I, _F,
                                  _P, _P, _P, _Z, _P]
     L.dsa_rope_append.argtypes = [_P, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _P]
+    L.dsa_prefix_mla_workspace_size.argtypes = [_I, _I, _I]
+    L.dsa_prefix_mla_workspace_size.restype = _Z
+    L.dsa_prefix_mla.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P,
+                                 _P, _P, _Z, _P]
     L.dsa_device_sm_count.argtypes = []
     L.dsa_launch_count.argtypes = []
     L.dsa_launch_count.restype = ctypes.c_longlong
     for name in EXPORTS:
         if name not in ("dsa_indexer_workspace_size", "dsa_sparse_mla_decode_workspace_size",
-                        "dsa_launch_count", "dsa_indexer_topk_approx_workspace_size"):
+                        "dsa_launch_count", "dsa_indexer_topk_approx_workspace_size",
+                        "dsa_prefix_mla_workspace_size"):
             getattr(L, name).restype = _I
     _lib = L
     return L
@@ -954,4 +961,42 @@ def dsa_window_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, *, max_
     _launch(dev, "dsa_window_mla", _addr(q), _addr(kv), row_stride, *meta, int(max_kv), T, S, P, PTW, ps, H, Dk, Dv,
             float(sm_scale), int(sliding_window), int(num_sinks), float(soft_cap), _addr(o), _addr(lse), None, 0,
             _status(dev_status, dev))
+    return (o, lse) if lse is not None else o
+
+
+def dsa_prefix_mla_workspace_size(T, H, G=1):
+    return int((_lib or lib()).dsa_prefix_mla_workspace_size(int(T), int(H), int(G)))
+
+
+def dsa_prefix_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, prefix_lens, group_offsets=None, *, max_kv,
+                   sm_scale, o=None, lse=None, want_lse=False, ws=None, dev_status=None, Dv=512):
+    """Causal absorbed-MLA over all positions, as :func:`dsa_dense_mla`, of
+    requests that share a prefix: the requests ``group_offsets[g]`` ..
+    ``group_offsets[g + 1] - 1`` (int32 [G + 1]; None: all are one group) hold
+    the same rows in their first ``prefix_lens[g]`` positions (int32 [G]), which
+    are read once for all of them, through the first one's pages. ``ws``: at
+    least ``dsa_prefix_mla_workspace_size(T, H, G)`` bytes, one for each call
+    that may run at once; allocated if None. ``q`` may have padding rows behind
+    the last token, whose outputs are left as they are."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev, 3)
+    _need(kv, "kv", torch.bfloat16, dev, 3)
+    T, H, Dk = q.shape
+    P, ps, row_stride = kv.shape
+    S, PTW, meta = _ragged(dev, seq_lens, cu_q_lens, cu_kv_lens, page_indices)
+    a_prefix, G = _i32(prefix_lens, "prefix_lens", dev), prefix_lens.numel()
+    a_groups = None
+    if group_offsets is not None:
+        a_groups = _i32(group_offsets, "group_offsets", dev)
+        if group_offsets.numel() != G + 1:
+            raise ValueError(f"group_offsets needs {G + 1} entries for {G} prefixes")
+    elif G != 1:
+        raise ValueError(f"without group_offsets there is one prefix, got {G}")
+    o, lse = _attend_out(dev, T, H, Dv, o, lse, want_lse)
+    if ws is None:
+        ws = torch.empty(dsa_prefix_mla_workspace_size(T, H, G), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    _launch(dev, "dsa_prefix_mla", _addr(q), _addr(kv), row_stride, *meta, a_prefix, a_groups, G, int(max_kv), T, S, P,
+            PTW, ps, H, Dk, Dv, float(sm_scale), _addr(o), _addr(lse), _addr(ws), ws.numel(), _status(dev_status, dev))
     return (o, lse) if lse is not None else o

@@ -16,6 +16,7 @@
 #include "attend.cuh"
 #include "common.cuh"
 #include "indexer.cuh"
+#include "prefix.cuh"
 #include "steps.cuh"
 
 namespace dsa {
@@ -487,6 +488,53 @@ int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, i
   prm.lse = lse;
   prm.dev_status = dev_status;
   return run_attend_cache(static_cast<cudaStream_t>(stream), prm);
+}
+
+size_t dsa_prefix_mla_workspace_size(int T, int H, int G) {
+  if (T <= 0 || H <= 0 || G <= 0 || (long long)T * H >= kPrefixMaxRows || G > kPrefixMaxGroups) return 0;
+  return prefix_workspace_bytes(T, H, G);
+}
+
+int dsa_prefix_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride, const int32_t* seq_lens,
+                   const int32_t* cu_q_lens, const int32_t* cu_kv_lens, const int32_t* page_indices,
+                   const int32_t* prefix_lens, const int32_t* group_offsets, int G, int max_kv, int T, int S, int P,
+                   int PTW, int ps, int H, int Dk, int Dv, float sm_scale, uint16_t* o, float* lse, void* ws,
+                   size_t ws_bytes, int32_t* dev_status) {
+  NvtxRange nvtx_range("dsa_prefix_mla");
+  int rc = check_meta(seq_lens, cu_q_lens, cu_kv_lens, page_indices, T, S, P, PTW, ps);
+  if (rc) return rc;
+  rc = attend_check(q, kv, row_stride, T, H, Dk, Dv, o);
+  if (rc) return rc;
+  if (G < 1 || max_kv < 1 || (G > 1 && !group_offsets)) return DSA_ERR_INVALID_ARGUMENT;
+  if (G > kPrefixMaxGroups || max_kv > (1 << 30) || (long long)T * H >= kPrefixMaxRows) return DSA_ERR_UNSUPPORTED;
+  if (!std::isfinite(sm_scale * 1.4426950408889634f)) return DSA_ERR_INVALID_ARGUMENT;  // the kernel's logit factor
+  if (T == 0 || H == 0) return DSA_OK;
+  if (!prefix_lens) return DSA_ERR_INVALID_ARGUMENT;
+  if (!ws || ws_bytes < prefix_workspace_bytes(T, H, G)) return DSA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return DSA_ERR_ALIGNMENT;
+  PrefixParams prm{};
+  prm.q = q;
+  prm.kv = kv;
+  prm.row_stride = row_stride;
+  prm.seq_lens = seq_lens;
+  prm.cu_q_lens = cu_q_lens;
+  prm.cu_kv_lens = cu_kv_lens;
+  prm.page_indices = page_indices;
+  prm.prefix_lens = prefix_lens;
+  prm.group_offsets = group_offsets;
+  prm.G = G;
+  prm.max_kv = max_kv;
+  prm.T = T;
+  prm.S = S;
+  prm.P = P;
+  prm.PTW = PTW;
+  prm.ps = ps;
+  prm.H = H;
+  prm.scale_log2 = sm_scale * 1.4426950408889634f;
+  prm.o = o;
+  prm.lse = lse;
+  prm.dev_status = dev_status;
+  return run_prefix_mla(static_cast<cudaStream_t>(stream), prm, ws);
 }
 
 int dsa_sparse_mla_decode_q4(dsa_stream_t stream, const uint16_t* q, const uint8_t* cache, const int32_t* seq_lens,

@@ -1,0 +1,868 @@
+// Absorbed-MLA attention of requests that share a prefix, whose keys are read
+// once for all of them. Per group of requests, and with rows (token, head):
+//   S = Q K^T over 576 dims, online softmax, O += P V, V = the first 512 dims.
+// The rows of a group are cut into tiles of 256, of any tokens and heads, since
+// [T, H] rows lie one behind another. A tile's keys are a list of key tiles of
+// 128: the prefix, read through the page table of the group's first request,
+// then the own positions of each request that has rows in the tile, which the
+// rows of others mask.
+//
+// A pair of CTAs takes a row tile and half of the value columns: each has 128
+// rows, and the MMAs of 256 rows (cta_group::2) read half of a key tile from
+// each one's shared memory, so each fetches half. All of O is 512 columns of
+// fp32, the whole TMEM, so both value halves compute S.
+//
+// Work: the key tiles of all row tiles and both halves in a row, dealt to the
+// pairs in equal shares, wherever a share ends. A list that was divided leaves
+// its parts in the workspace (at most two per pair) and a second kernel merges
+// them, in order, so outputs are the same on every run.
+//
+// Roles of a CTA: warp 0 issues the MMAs (rank 0 only), warp 1 resolves keys and
+// copies the K blocks and queries, warp 2 the V blocks, warps 4-7 run the
+// softmax, a row per thread.
+//
+// Per key tile i: QK^T(i), nine blocks of 64 dims, then PV(i - 1). S is read into
+// registers at once and P goes to shared memory, so that QK^T(i + 1) runs beside
+// the softmax of tile i.
+#include <algorithm>
+
+#include "common.cuh"
+#include "prefix.cuh"
+
+namespace dsa {
+
+namespace {
+constexpr int kDk = 576, kDv = 512;
+constexpr int kRows = 128, kTileRows = 2 * kRows;  // of a CTA, of a pair
+constexpr int kKeys = 128, kHalfKeys = 64;         // of a key tile, of one CTA's K blocks
+constexpr int kBlk = kHalfKeys * 128;              // 64 keys x 64 dims
+constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims
+constexpr int kSlots = 10;                         // K blocks in flight (nine a tile)
+constexpr int kVStages = 2, kVStage = 2 * kBlk;    // 64 keys x 128 dims
+constexpr int kDescs = 4;
+constexpr int kThreads = 256;
+constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
+constexpr int kNoRow = -64;               // a box from here on lies outside the cache and lands as zeros
+
+// What the softmax and the copiers know of a key tile.
+struct KeyTile {
+  int row[4];  // cache row of each 32 keys, or kNoRow
+  int pos;     // of the first key
+  int seg;     // -1: prefix; else the request whose own keys they are
+  int valid;   // bit g: keys 32 g .. hold positions
+  int pad;
+};
+
+constexpr int OFF_Q = 0;  // dims 256-575
+constexpr int OFF_P = OFF_Q + 5 * kQBlk;
+constexpr int OFF_K = OFF_P + 2 * kQBlk;
+constexpr int OFF_V = OFF_K + kSlots * kBlk;
+constexpr int OFF_DESC = OFF_V + kVStages * kVStage;
+constexpr int OFF_BAR = OFF_DESC + kDescs * (int)sizeof(KeyTile);
+constexpr int kNumBars = 2 * kSlots + 2 * kVStages + 2 * kDescs + 7;
+constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
+constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_DESC % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+static_assert(4 * kQBlk <= kSlots * kBlk, "the queries for TMEM land in the K blocks");
+constexpr int kOutLd = 512 + 16;      // bytes of a staged bf16 row
+constexpr int kPartLd = 64 * 4 + 16;  // and of 64 staged fp32 columns
+static_assert(kRows * kOutLd <= kSlots * kBlk && kRows * kPartLd <= kSlots * kBlk, "rows are staged in the K blocks");
+
+constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, kKeys, false, false);
+constexpr uint32_t kIdescPV = make_idesc_bf16(kTileRows, 256, false, true);
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
+
+struct Bars {
+  uint64_t* b;
+  // leader's: both CTAs' copies
+  __device__ __forceinline__ uint64_t* kfull(int s) const { return b + s; }
+  __device__ __forceinline__ uint64_t* vfull(int s) const { return b + 2 * kSlots + s; }
+  // each CTA's: commits
+  __device__ __forceinline__ uint64_t* kempty(int s) const { return b + kSlots + s; }
+  __device__ __forceinline__ uint64_t* vempty(int s) const { return b + 2 * kSlots + kVStages + s; }
+  // each CTA's: key tiles resolved, and read
+  __device__ __forceinline__ uint64_t* dfull(int s) const { return b + 2 * kSlots + 2 * kVStages + s; }
+  __device__ __forceinline__ uint64_t* dempty(int s) const { return b + 2 * kSlots + 2 * kVStages + kDescs + s; }
+  __device__ __forceinline__ uint64_t* rest(int k) const { return b + 2 * kSlots + 2 * kVStages + 2 * kDescs + k; }
+  __device__ __forceinline__ uint64_t* sfull() const { return rest(0); }   // each: commit
+  __device__ __forceinline__ uint64_t* pvdone() const { return rest(1); }  // each: commit
+  __device__ __forceinline__ uint64_t* sempty() const { return rest(2); }  // leader's: softmax warps of both
+  __device__ __forceinline__ uint64_t* pfull() const { return rest(3); }   // leader's: softmax warps of both
+  __device__ __forceinline__ uint64_t* qready() const { return rest(4); }  // leader's: softmax warps of both
+  __device__ __forceinline__ uint64_t* qbar() const { return rest(5); }    // each: the queries' copies
+  __device__ __forceinline__ uint64_t* qmoved() const { return rest(6); }  // each: softmax warps
+};
+
+// ------------------------------------------------------------- the work list
+__device__ __forceinline__ int request_kv(const PrefixParams& p, int s) {
+  return min(max(__ldg(p.seq_lens + s), 0), p.max_kv);
+}
+__device__ __forceinline__ int group_begin(const PrefixParams& p, int g) {
+  return p.group_offsets ? min(max(__ldg(p.group_offsets + g), 0), p.S) : g ? p.S : 0;
+}
+// Positions that group g (not empty) reads through its first request.
+__device__ __forceinline__ int group_prefix(const PrefixParams& p, int g) {
+  return min(max(__ldg(p.prefix_lens + g), 0), request_kv(p, min(group_begin(p, g), p.S - 1)));
+}
+// Request s's own keys for rows of tokens up to `last`: from position `start`
+// (a page's first) to `end`.
+struct Own {
+  int start, end;
+  __device__ __forceinline__ int tiles() const { return end > start ? (end - start + kKeys - 1) / kKeys : 0; }
+};
+__device__ __forceinline__ Own own_keys(const PrefixParams& p, int s, int last, int prefix) {
+  const int q0 = __ldg(p.cu_q_lens + s), q1 = __ldg(p.cu_q_lens + s + 1);
+  Own w{0, 0};
+  if (q1 <= q0 || last < q0) return w;
+  const int kv = request_kv(p, s);
+  const int end = min(kv, kv - (q1 - q0) + min(last, q1 - 1) - q0 + 1);
+  if (end > prefix) w.start = prefix & -p.ps, w.end = end;
+  return w;
+}
+
+// One CTA lays out the row tiles and counts their key tiles.
+constexpr int kPlanThreads = 1024;
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+  // inclusive, of one value per thread
+  const int lane = lane_id(), w = warp_id();
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += y;
+  }
+  if (lane == 31) warp_sums[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    long long x = warp_sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    warp_sums[lane] = x;
+  }
+  __syncthreads();
+  if (w) v += warp_sums[w - 1];
+  total = warp_sums[31];
+  __syncthreads();
+  return v;
+}
+
+// Tokens of group g: [x, y), within [0, T), none if the metadata is out of order.
+__device__ __forceinline__ int2 group_tokens(const PrefixParams& p, int g) {
+  const int a = group_begin(p, g), b = group_begin(p, g + 1);
+  if (b <= a) return make_int2(0, 0);
+  return make_int2(__ldg(p.cu_q_lens + a), __ldg(p.cu_q_lens + b));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ long long warp_sums[32];
+  const int tid = threadIdx.x;
+  long long total;
+  int bad = 0;
+  long long tiles = 0;
+  for (int g0 = 0; g0 < p.G; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    long long n = 0;
+    if (g < p.G) {
+      const int2 t = group_tokens(p, g);
+      const int raw0 = p.group_offsets ? __ldg(p.group_offsets + g) : 0;
+      const int raw1 = p.group_offsets ? __ldg(p.group_offsets + g + 1) : p.S;
+      bool ok = raw0 >= 0 && raw1 >= raw0 && raw1 <= p.S && t.x >= 0 && t.y >= t.x && t.y <= p.T;
+      if (g == 0 && raw0 != 0) ok = false;
+      if (g == p.G - 1 && raw1 != p.S) bad = 1;  // requests behind the last group: no rows of theirs are written
+      if (ok) n = ((long long)(t.y - t.x) * p.H + kTileRows - 1) / kTileRows;
+      else bad = 1;
+      if (ok && raw1 > raw0) {
+        const int want = __ldg(p.prefix_lens + g);
+        if (want < 0 || want != group_prefix(p, g)) bad = 1;
+      }
+    }
+    const long long end = block_scan(n, warp_sums, total);
+    if (g < p.G) p.tile_base[g] = (int)min(tiles + end - n, (long long)p.max_tiles);
+    tiles += total;
+  }
+  if (tiles > p.max_tiles) bad = 1;
+  const int ntiles = (int)min(tiles, (long long)p.max_tiles);
+  if (tid == 0) p.tile_base[p.G] = *p.num_tiles = ntiles;
+  __syncthreads();
+  long long units = 0;
+  for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    long long n = 0;
+    if (i < ntiles) {
+      int lo = 0, hi = p.G - 1;  // the group with tile_base[g] <= i < tile_base[g + 1]
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.tile_base[mid] <= i) lo = mid;
+        else hi = mid - 1;
+      }
+      const int2 t = group_tokens(p, lo);
+      const int first = t.x * p.H + (i - p.tile_base[lo]) * kTileRows, rows = min(kTileRows, t.y * p.H - first);
+      const int ta = first / p.H, tb = (first + rows - 1) / p.H, prefix = group_prefix(p, lo);
+      const int s0 = seq_of_token(p.cu_q_lens, p.S, ta);
+      n = (prefix + kKeys - 1) / kKeys;
+      for (int s = s0; s < p.S && __ldg(p.cu_q_lens + s) <= tb; ++s) n += own_keys(p, s, tb, prefix).tiles();
+      n = max(n, 1LL);  // rows without any key still have an output
+      p.tiles[i] = make_int4(first, rows, lo, s0);
+    }
+    const long long end = block_scan(n, warp_sums, total);
+    if (i < ntiles) p.unit_base[i] = units + end - n;
+    units += total;
+  }
+  if (tid == 0) p.unit_base[ntiles] = units;
+  if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
+}
+
+// The units (key tiles of row tiles, both halves) and the shares they are dealt in.
+struct Shares {
+  long long units;
+  int n;
+  __device__ __forceinline__ long long begin(int k) const { return units * k / n; }
+  __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * n - 1) / units); }
+};
+__device__ __forceinline__ Shares make_shares(const PrefixParams& p) {
+  Shares s;
+  s.units = 2 * p.unit_base[*p.num_tiles];
+  s.n = (int)min((long long)p.pairs, s.units);
+  return s;
+}
+// The list (row tile and value half) of unit u: units [begin, end).
+struct List {
+  int tile, half;
+  long long begin, end;
+};
+__device__ __forceinline__ List list_of(const PrefixParams& p, long long u) {
+  int lo = 0, hi = *p.num_tiles - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (2 * p.unit_base[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const long long a = p.unit_base[lo], n = p.unit_base[lo + 1] - a;
+  List l;
+  l.tile = lo;
+  l.half = u >= 2 * a + n;
+  l.begin = 2 * a + (l.half ? n : 0);
+  l.end = l.begin + n;
+  return l;
+}
+
+// The key tiles of a list from tile k on, resolved by one whole warp.
+struct KeyCursor {
+  const PrefixParams* p;
+  int prefix, last, s, seg;  // last token; next request; the segment (-1: prefix)
+  int pos, end, left, page_base, lg;
+  int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
+
+  __device__ __forceinline__ void open(int sg, int first, int stop, int tiles, int request) {
+    seg = sg;
+    pos = first;
+    end = stop;
+    left = tiles;
+    page_base = __ldg(p->cu_kv_lens + request) >> lg;
+    win = -64;
+  }
+  __device__ void init(const PrefixParams& prm, const int4 tile, int k) {
+    p = &prm;
+    lg = 31 - __clz(prm.ps);
+    prefix = group_prefix(prm, tile.z);
+    last = (tile.x + tile.y - 1) / prm.H;
+    s = tile.w;
+    left = 0;
+    const int np = (prefix + kKeys - 1) / kKeys;
+    if (k < np) {
+      open(-1, k * kKeys, prefix, np - k, group_begin(prm, tile.z));
+    } else {
+      next_request(k - np);
+    }
+  }
+  // the request that holds own tile k, counted from request s on
+  __device__ void next_request(int k) {
+    for (; s < p->S && __ldg(p->cu_q_lens + s) <= last; ++s) {
+      const Own w = own_keys(*p, s, last, prefix);
+      const int n = w.tiles();
+      if (k < n) {
+        open(s, w.start + k * kKeys, w.end, n - k, s);
+        ++s;
+        return;
+      }
+      k -= n;
+    }
+    seg = p->S;  // no keys: the only tile of rows that see none
+    pos = end = 0;
+    left = 1;
+    win = 0;
+    page = -1;
+  }
+  // The next key tile, in every lane.
+  __device__ KeyTile next() {
+    if (!left) next_request(0);
+    --left;
+    KeyTile t;
+    t.pos = pos;
+    t.seg = seg;
+    t.valid = 0;
+    t.pad = 0;
+    const int e0 = pos >> lg;
+    if (pos < end && (e0 < win || ((pos + kKeys - 1) >> lg) >= win + 32)) {
+      win = e0;
+      const int e = win + lane_id();
+      page = -1;
+      if ((long long)e << lg < end) {
+        const long long ent = (long long)page_base + e;
+        if (ent < 0 || ent >= p->PTW) {
+          set_status(p->dev_status, DSA_STATUS_BAD_METADATA);
+        } else {
+          page = __ldg(p->page_indices + ent);
+          if (page < 0 || page >= p->P) {
+            set_status(p->dev_status, DSA_STATUS_BAD_METADATA);
+            page = -1;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int at = pos + 32 * g, pg = __shfl_sync(0xffffffffu, page, ((at >> lg) - win) & 31);
+      const bool ok = at < end && pg >= 0;
+      t.row[g] = ok ? (pg << lg) + (at & (p->ps - 1)) : kNoRow;
+      t.valid |= ok ? 1 << g : 0;
+    }
+    pos += kKeys;
+    return t;
+  }
+};
+
+// 64 keys x 64 dims as boxes of min(ps, 64) rows.
+__device__ __forceinline__ void copy_block(uint32_t dst, const CUtensorMap* map, uint32_t bar, int dim, int r0, int r1,
+                                           bool two) {
+  tma_load_2d_pair(dst, map, bar, dim, r0);
+  if (two) tma_load_2d_pair(dst + kBlk / 2, map, bar, dim, r1);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_mla_kernel(const __grid_constant__ PrefixParams prm, const __grid_constant__ CUtensorMap kvmap,
+                      const __grid_constant__ CUtensorMap qmap) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // in every CTA alike
+    if (threadIdx.x == 0) set_status(prm.dev_status, DSA_STATUS_INTERNAL);
+    return;
+  }
+  griddep_launch_dependents();
+  const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
+  const uint32_t rank = cluster_rank(), smem0 = smem_u32(smem);
+  const int pair = blockIdx.x >> 1;
+  const Bars br{reinterpret_cast<uint64_t*>(smem + OFF_BAR)};
+  KeyTile* descs = reinterpret_cast<KeyTile*>(smem + OFF_DESC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) mbar_init(br.kfull(s), 1), mbar_init(br.kempty(s), 1);
+    for (int s = 0; s < kVStages; ++s) mbar_init(br.vfull(s), 1), mbar_init(br.vempty(s), 1);
+    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), 5);
+    mbar_init(br.sfull(), 1);
+    mbar_init(br.pvdone(), 1);
+    mbar_init(br.sempty(), 8);
+    mbar_init(br.pfull(), 8);
+    mbar_init(br.qready(), 8);
+    mbar_init(br.qbar(), 1);
+    mbar_init(br.qmoved(), 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync_all();
+  tc_fence_after();
+  griddep_wait();
+  const uint32_t tmem = *tmem_slot;
+  const Shares shares = make_shares(prm);
+  auto leader = [&](uint64_t* bar) { return cluster_addr(smem_u32(bar), 0); };
+  // a role that gives up tells both CTAs
+  auto give_up = [&]() {
+    if (lane == 0) {
+      *abort_flag = 1;
+      st_cluster_u32(cluster_addr(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1);
+    }
+    __syncwarp();
+  };
+  // every role counts what it has passed since the kernel began: a barrier's
+  // phase is that number's parity
+  uint32_t kc = 0, vc = 0, tc = 0, uc = 0;  // K blocks, V stages, key tiles, lists
+  const long long u_end = pair < shares.n ? shares.begin(pair + 1) : 0;
+  long long u = pair < shares.n ? shares.begin(pair) : 0;
+#pragma unroll 1
+  while (u < u_end) {
+    const List list = list_of(prm, u);
+    const int4 tile = prm.tiles[list.tile];
+    const int k0 = (int)(u - list.begin), n = (int)(min(u_end, list.end) - u);
+    const bool whole = k0 == 0 && u + n == list.end;
+    const int slot_out = u == shares.begin(pair) ? 2 * pair : 2 * pair + 1;
+    const int row0 = tile.x + (int)rank * kRows;               // this CTA's first row of [T * H]
+    const int rows = min(kRows, tile.y - (int)rank * kRows);   // <= 0: none
+    if (warp == 0) {
+      // -------------------------------------------------------- MMA issuer
+      if (rank == 0) {
+        const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = make_sdesc(smem0 + OFF_Q, 16, 1024, kSwizzle128B);
+        const uint64_t dp = make_sdesc(smem0 + OFF_P, 16, 1024, kSwizzle128B);
+        const uint64_t dk = make_sdesc(smem0 + OFF_K, 16, 1024, kSwizzle128B);
+        const uint64_t dv = make_sdesc(smem0 + OFF_V, kBlk, 1024, kSwizzle128B);  // MN-major
+        auto commit = [&](uint64_t* bar) {
+          if (lead) umma_commit_pair(bar, 3);
+          __syncwarp();
+        };
+        bool ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; ok && i <= n; ++i) {
+          if (i < n) {
+            // S is free once the tile before has been read into registers
+            if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 9; ++b, ++kc) {
+              const int slot = kc % kSlots;
+              if (!(ok = mbar_wait_warp(br.kfull(slot), (kc / kSlots) & 1, abort_flag))) break;
+              tc_fence_after();
+              const uint64_t kb = dk + (uint64_t)(slot * (kBlk >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t acc = b || k ? 1u : 0u;
+                if (b < 4) umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + b * 32 + k * 8, kb + k * 2, kIdescQK, acc);
+                else umma_pair_ss_lead(lead, tm + kColS, dq + (uint64_t)((b - 4) * (kQBlk >> 4) + k * 2), kb + k * 2,
+                                       kIdescQK, acc);
+              }
+              commit(br.kempty(slot));
+            }
+            if (!ok) break;
+            commit(br.sfull());
+            ++tc;
+          }
+          if (i > 0) {
+            if (!(ok = mbar_wait_warp_cluster(br.pfull(), (tc - (i < n ? 2 : 1)) & 1, abort_flag))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int s = 0; s < kVStages; ++s) {
+              if (!(ok = mbar_wait_warp(br.vfull(s), (vc / kVStages) & 1, abort_flag))) break;
+              ++vc;
+              tc_fence_after();
+              const uint64_t vb = dv + (uint64_t)(s * (kVStage >> 4)), pb = dp + (uint64_t)(s * (kQBlk >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_pair_ss_lead(lead, tm + kColO, pb + k * 2, vb + k * 128, kIdescPV, i > 1 || s || k ? 1u : 0u);
+              commit(br.vempty(s));
+            }
+            if (!ok) break;
+            commit(br.pvdone());
+          }
+        }
+        if (!ok) give_up();
+      }
+    } else if (warp == 1) {
+      // ------------------------------------ queries, key tiles and K blocks
+      if (lane == 0) {
+        mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
+#pragma unroll 1
+        for (int c = 0; c < 9; ++c)
+          tma_load_2d(smem + (c < 4 ? OFF_K + c * kQBlk : OFF_Q + (c - 4) * kQBlk), &qmap, br.qbar(), c * 64, row0);
+      }
+      KeyCursor cur;
+      cur.init(prm, tile, k0);
+      const bool two = prm.ps == 32;
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++tc) {
+        const KeyTile t = cur.next();
+        const int ds = tc % kDescs;
+        if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
+        if (lane == 0) {
+          descs[ds] = t;
+          mbar_arrive(br.dfull(ds));
+        }
+        __syncwarp();
+        // the queries for TMEM have left the K blocks
+        if (i == 0 && !(ok = mbar_wait_warp(br.qmoved(), uc & 1, abort_flag))) break;
+#pragma unroll 1
+        for (int b = 0; b < 9; ++b, ++kc) {
+          const int slot = kc % kSlots;
+          if (!(ok = mbar_wait_warp(br.kempty(slot), ((kc / kSlots) & 1) ^ 1, abort_flag))) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(br.kfull(slot), 2 * kBlk);
+            copy_block(smem0 + OFF_K + slot * kBlk, &kvmap, leader(br.kfull(slot)), b * 64,
+                       rank ? t.row[2] : t.row[0], rank ? t.row[3] : t.row[1], two);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (!ok) give_up();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ V blocks
+      const bool two = prm.ps == 32;
+      const int dim = list.half * 256 + (int)rank * 128;
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++tc) {
+        const int ds = tc % kDescs;
+        if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
+        const KeyTile t = descs[ds];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(br.dempty(ds));
+        // the queries for TMEM lie in the K blocks alone
+#pragma unroll 1
+        for (int s = 0; s < kVStages; ++s, ++vc) {
+          if (!(ok = mbar_wait_warp(br.vempty(s), ((vc / kVStages) & 1) ^ 1, abort_flag))) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(br.vfull(s), 2 * kVStage);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              copy_block(smem0 + OFF_V + s * kVStage + c * kBlk, &kvmap, leader(br.vfull(s)), dim + c * 64,
+                         s ? t.row[2] : t.row[0], s ? t.row[3] : t.row[1], two);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (!ok) give_up();
+    } else if (warp >= 4) {
+      // ------------------------------------------------------------- softmax
+      const int r = (warp & 3) * 32 + lane;  // TMEM lane and row
+      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
+      bool ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
+      if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const uint8_t* row = smem + OFF_K + c * kQBlk + r * 128;
+          uint32_t v[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + ((j ^ (r & 7)) << 4));
+            v[4 * j] = x.x;
+            v[4 * j + 1] = x.y;
+            v[4 * j + 2] = x.z;
+            v[4 * j + 3] = x.w;
+          }
+          tmem_st32(tmem + lane_base + kColQ + c * 32, v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        fence_proxy_async_smem();  // the blocks are written by copies again
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(br.qmoved());
+          mbar_arrive_cluster(leader(br.qready()));
+        }
+        __syncwarp();
+      }
+      // this row's request and visible positions
+      int my_s = -2, see = 0;
+      const int prefix = group_prefix(prm, tile.z);
+      if (r < rows) {
+        const int t = (row0 + r) / prm.H;
+        int s = tile.w;
+        while (s + 1 < prm.S && __ldg(prm.cu_q_lens + s + 1) <= t) ++s;
+        const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, prm.max_kv, t,
+                                       prm.dev_status, s);
+        my_s = s;
+        see = g.n_vis;
+      }
+      const float sl2 = prm.scale_log2;
+      float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i, ++tc) {
+        const int ds = tc % kDescs;
+        if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
+        const int p0 = descs[ds].pos, seg = descs[ds].seg, valid = descs[ds].valid;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(br.dempty(ds));
+        const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
+        const int lo = seg < 0 ? 0 : prefix - p0;
+        auto below = [](int k) -> uint32_t { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };
+        uint32_t mask[4];
+        bool full = true;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) & ~below(lo - 32 * g) : 0u;
+          full = full && mask[g] == 0xffffffffu;
+        }
+        full = __all_sync(0xffffffffu, full);
+        if (!(ok = mbar_wait_warp(br.sfull(), tc & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) tmem_ld32(tmem + lane_base + kColS + 32 * g, s[g]);
+        tmem_ld_wait_regs(s[0]);
+#pragma unroll
+        for (int g = 1; g < 4; ++g) reg_fence(s[g]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(a_sempty);
+        __syncwarp();
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // a masked key is left out of maximum and weights, whatever its logit is
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = __uint_as_float(s[g][j]) * sl2;
+            mx[j & 3] = full || ((mask[g] >> j) & 1u) ? fmaxf(mx[j & 3], x) : mx[j & 3];
+          }
+        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        const bool need = m_new > m_run + kRescaleThreshold;  // also true when m_run == -inf
+        const float m_use = need ? m_new : m_run;
+        const float alpha = need ? exp2f(m_run - m_new) : 1.f;
+        const float m_sub = m_use == -INFINITY ? 0.f : m_use;
+        const uint64_t sl2x2 = f32x2_pack(sl2, sl2), nm2 = f32x2_pack(-m_sub, -m_sub);
+        uint64_t ps2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float x0, x1;
+            f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[g][2 * c]), __uint_as_float(s[g][2 * c + 1])), sl2x2, nm2),
+                         x0, x1);
+            x0 = ex2_approx(x0);
+            x1 = ex2_approx(x1);
+            if (!full) {
+              x0 = (mask[g] >> (2 * c)) & 1u ? x0 : 0.f;
+              x1 = (mask[g] >> (2 * c + 1)) & 1u ? x1 : 0.f;
+            }
+            ps2[c & 1] = fadd2(ps2[c & 1], f32x2_pack(x0, x1));
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(x0, x1);  // P as a bf16 operand
+            s[g][c] = *reinterpret_cast<uint32_t*>(&b2);
+          }
+        }
+        // P's buffer and O are free once PV of the tile before has run
+        if (i > 0 && !(ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag))) break;
+        if (i > 0 && __any_sync(0xffffffffu, need)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tmem + lane_base + kColO + c * 32, ov);
+            tmem_ld_wait_regs(ov);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+            tmem_st32(tmem + lane_base + kColO + c * 32, ov);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_shared_v4(smem0 + OFF_P + (g >> 1) * kQBlk + sw128_offset(r, (g & 1) * 4 + c), s[g][4 * c],
+                         s[g][4 * c + 1], s[g][4 * c + 2], s[g][4 * c + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(a_pfull);
+        __syncwarp();
+        float pa, pb;
+        f32x2_unpack(fadd2(ps2[0], ps2[1]), pa, pb);
+        l_run = l_run * alpha + (pa + pb);
+        m_run = m_use;
+      }
+      // ------------------------------------------------------------ epilogue
+      if (ok) ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
+      if (ok) {
+        tc_fence_after();
+        const bool some = l_run != 0.f;  // a sum of weights is never negative; NaN counts
+        const float inv_l = some ? 1.f / l_run : 0.f;
+        const float lse2 = some ? m_run + log2f(l_run) : -INFINITY;
+        const int w0 = (warp & 3) * 32, nw = min(32, rows - w0);
+        if (whole) {
+          uint8_t* stg = smem + OFF_K + (warp & 3) * (32 * kOutLd);
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_base + kColO + c0, o);
+            tmem_ld_wait_regs(o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * e]) * inv_l,
+                                                          __uint_as_float(o[8 * j + 2 * e + 1]) * inv_l);
+                pk[e] = *reinterpret_cast<uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(stg + lane * kOutLd + c0 * 2 + j * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+          __syncwarp();
+          uint16_t* orow = prm.o + ((size_t)row0 + w0) * kDv + list.half * 256;
+#pragma unroll 4
+          for (int k = 0; k < nw; ++k)
+            reinterpret_cast<uint4*>(orow + (size_t)k * kDv)[lane] =
+                *reinterpret_cast<const uint4*>(stg + k * kOutLd + lane * 16);
+          if (list.half == 0 && r < rows && prm.lse) prm.lse[(size_t)row0 + r] = lse2 * 0.69314718055994531f;
+        } else {
+          // normalised partial rows and their log-sums
+          uint8_t* stg = smem + OFF_K + (warp & 3) * (32 * kPartLd);
+          const size_t out_row = (size_t)slot_out * kTileRows + rank * kRows + w0;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 256; c0 += 64) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lane_base + kColO + c0 + 32 * h, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                *reinterpret_cast<float4*>(stg + lane * kPartLd + h * 128 + v * 16) =
+                    make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int k = lane >> 4; k < nw; k += 2)
+              *reinterpret_cast<float4*>(prm.part_o + (out_row + k) * 256 + c0 + (lane & 15) * 4) =
+                  *reinterpret_cast<const float4*>(stg + k * kPartLd + (lane & 15) * 16);
+            __syncwarp();
+          }
+          if (r < rows) prm.part_lse[out_row + lane] = lse2;
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();  // the staged rows' place is written by copies again
+      } else {
+        give_up();
+      }
+    }
+    // both CTAs are done with the list: their MMAs have run and their copies landed
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after();
+    if (*abort_flag) break;
+    // a role that does not count by itself keeps up
+    if (warp != 1 && !(warp == 0 && rank == 0)) kc += 9 * n;
+    u += n;
+    ++uc;
+  }
+  if (*abort_flag) {
+    // unwinding: copies and MMAs in flight land within microseconds; wait longer
+    const long long t0 = clock64();
+    while (clock64() - t0 < 4000000) __nanosleep(1000);
+    if (tid == 0) set_status(prm.dev_status, DSA_STATUS_TIMEOUT);
+  }
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 0) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// Merges a list that was divided: block x looks at the end of share x and takes
+// the list that it cuts, if it is the first to; a warp takes a row.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const Shares sh = make_shares(p);
+  const int x = blockIdx.x, lane = lane_id();
+  if (x + 1 >= sh.n) return;
+  const long long u = sh.begin(x + 1);
+  const List l = list_of(p, u);
+  if (l.begin == u) return;  // the share ends with a list
+  const int k0 = sh.of(l.begin), k1 = sh.of(l.end - 1);
+  if (k0 != x) return;
+  const int4 tile = p.tiles[l.tile];
+  const int r = blockIdx.y * kMergeWarps + warp_id();
+  if (r >= tile.y) return;
+  auto row_of = [&](int k) { return ((size_t)(sh.begin(k) >= l.begin ? 2 * k : 2 * k + 1)) * kTileRows + r; };
+  float mx = -INFINITY, tot = 0.f;
+  for (int k = k0 + lane; k <= k1; k += 32) mx = fmaxf(mx, p.part_lse[row_of(k)]);
+  mx = warp_max_f32(mx);
+  for (int k = k0 + lane; k <= k1; k += 32) {
+    const float v = p.part_lse[row_of(k)];
+    tot += v == -INFINITY ? 0.f : exp2f(v - mx);  // NaN stays NaN
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, d);
+  const bool some = tot != 0.f;
+  const float inv = some ? 1.f / tot : 0.f;
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+  for (int k = k0; k <= k1; ++k) {
+    const size_t row = row_of(k);
+    const float v = p.part_lse[row], w = v == -INFINITY ? 0.f : exp2f(v - mx) * inv;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + row * 256);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 y = src[32 * h + lane];
+      acc[h].x = fmaf(w, y.x, acc[h].x);
+      acc[h].y = fmaf(w, y.y, acc[h].y);
+      acc[h].z = fmaf(w, y.z, acc[h].z);
+      acc[h].w = fmaf(w, y.w, acc[h].w);
+    }
+  }
+  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.x + r) * kDv + l.half * 256);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc[h].x, acc[h].y), hi = __floats2bfloat162_rn(acc[h].z, acc[h].w);
+    dst[32 * h + lane] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  }
+  if (l.half == 0 && lane == 0 && p.lse)
+    p.lse[(size_t)tile.x + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
+}
+
+int max_tiles_of(int T, int H, int G) { return (int)(((long long)T * H + kTileRows - 1) / kTileRows) + G; }
+int max_pairs() { return std::max(1, sm_count() / 2); }
+struct Layout {
+  size_t tile_base, tiles, unit_base, num_tiles, part_o, part_lse, bytes;
+};
+Layout layout_of(int T, int H, int G) {
+  const size_t nt = (size_t)max_tiles_of(T, H, G), slots = 2 * (size_t)max_pairs();
+  Layout l;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align_up(bytes, 256);
+    return here;
+  };
+  l.tile_base = take(((size_t)G + 1) * 4);
+  l.tiles = take(nt * 16);
+  l.unit_base = take((nt + 1) * 8);
+  l.num_tiles = take(4);
+  l.part_lse = take(slots * kTileRows * 4);
+  l.part_o = take(slots * kTileRows * 256 * 4);
+  l.bytes = at;
+  return l;
+}
+}  // namespace
+
+size_t prefix_workspace_bytes(int T, int H, int G) { return layout_of(T, H, G).bytes; }
+
+int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
+  const Layout l = layout_of(prm.T, prm.H, prm.G);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  prm.tile_base = reinterpret_cast<int32_t*>(w + l.tile_base);
+  prm.tiles = reinterpret_cast<int4*>(w + l.tiles);
+  prm.unit_base = reinterpret_cast<long long*>(w + l.unit_base);
+  prm.num_tiles = reinterpret_cast<int*>(w + l.num_tiles);
+  prm.part_o = reinterpret_cast<float*>(w + l.part_o);
+  prm.part_lse = reinterpret_cast<float*>(w + l.part_lse);
+  prm.max_tiles = max_tiles_of(prm.T, prm.H, prm.G);
+  prm.pairs = max_pairs();
+  CUtensorMap kvmap, qmap;
+  if (!encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, std::min(prm.ps, kHalfKeys),
+                      kDk) ||
+      !encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kRows, kDk))
+    return DSA_ERR_CUDA;
+  set_smem_attr_once(reinterpret_cast<const void*>(prefix_mla_kernel), kSmem);
+  DSA_LAUNCH_PDL(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, prm);
+  DSA_LAUNCH_PDL(prefix_mla_kernel, dim3(2 * prm.pairs), dim3(kThreads), kSmem, stream, prm, kvmap, qmap);
+  DSA_LAUNCH_PDL(prefix_merge_kernel, dim3(prm.pairs, kTileRows / kMergeWarps), dim3(kMergeWarps * 32), 0, stream, prm);
+  return DSA_OK;
+}
+
+}  // namespace dsa

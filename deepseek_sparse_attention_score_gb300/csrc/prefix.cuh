@@ -1,0 +1,41 @@
+// Attention of requests that share a prefix (prefix.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace dsa {
+
+constexpr long long kPrefixMaxRows = (1LL << 31) - (1 << 16);  // T * H: a tile ends past them
+constexpr int kPrefixMaxGroups = 1 << 20;
+
+struct PrefixParams {
+  const uint16_t* q;   // bf16 [T, H, 576]
+  const uint16_t* kv;  // bf16 [P, ps, row_stride]
+  int row_stride;
+  const int32_t* seq_lens;
+  const int32_t* cu_q_lens;
+  const int32_t* cu_kv_lens;
+  const int32_t* page_indices;
+  const int32_t* prefix_lens;    // [G]
+  const int32_t* group_offsets;  // [G + 1], or null: one group of all requests
+  int G, max_kv, T, S, P, PTW, ps, H;
+  float scale_log2;  // sm_scale * log2(e)
+  uint16_t* o;       // bf16 [T, H, 512]
+  float* lse;        // [T, H] or null
+  int32_t* dev_status;
+  // workspace (set by run_prefix_mla)
+  int32_t* tile_base;  // [G + 1] tiles of the groups before
+  int4* tiles;         // first row, rows, group, first request
+  long long* unit_base;  // [tiles + 1] key tiles of the tiles before
+  int* num_tiles;
+  float* part_o;    // [2 * pairs][256][256]
+  float* part_lse;  // [2 * pairs][256], log2
+  int max_tiles, pairs;
+};
+
+size_t prefix_workspace_bytes(int T, int H, int G);
+// ws: at least that many bytes.
+int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws);
+
+}  // namespace dsa

@@ -621,6 +621,42 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
                            int Dk, int Dv, float sm_scale, int sliding_window, int num_sinks, float soft_cap,
                            uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status);
 
+/* ------------------------------------------------------------------------
+ * Absorbed-MLA attention of requests that share a prefix (no counterpart on
+ * the pages): dsa_dense_mla without window and cap, where the keys that a group
+ * of requests has in common are read once for all of its queries.
+ * Groups are runs of requests: group g has the requests group_offsets[g] ..
+ * group_offsets[g + 1] - 1, whose first prefix_lens[g] positions hold the same
+ * rows: the same pages, or copies of them. Those positions are read through the
+ * page table of the group's first request, the positions from prefix_lens[g] on
+ * through each request's own. Visible are, as ever, j <= pos(t), j < seq_len: a
+ * request may be shorter than the prefix or have new tokens inside it.
+ *   prefix_lens    int32 [G], 0 (nothing shared) .. the first request's length
+ *   group_offsets  int32 [G + 1], 0 .. S in order; NULL with G == 1: one group
+ *   max_kv         upper bound of seq_lens (a longer one is clamped and flagged)
+ *   ws             workspace of dsa_prefix_mla_workspace_size(T, H, G) bytes,
+ *                  16-byte aligned: calls that may run at once, captured graphs
+ *                  among them, need one each
+ *   T may be an upper bound: rows of o and lse from cu_q_lens[S] on are left as
+ *   they are.
+ * Device conditions: a prefix below 0 or longer than its group's first request
+ * is clamped to that (each request reads the rest through its own pages) and
+ * sets DSA_STATUS_BAD_METADATA, as does a group whose requests or tokens are
+ * out of order or out of range, whose rows are not written.
+ * Cache contents: of pages that hold a visible position runs of min(ps, 64) rows
+ * are read; rows of a run past the visible length must hold finite values (see
+ * dsa_sparse_mla_decode).
+ * Outputs are the same on every run.
+ * Supported: as dsa_dense_mla; 1 <= G <= 2^20, T * H < 2^31 - 2^16, max_kv <=
+ * 2^30, |sm_scale| * 1.5 finite in fp32.
+ * ------------------------------------------------------------------------ */
+DSA_API size_t dsa_prefix_mla_workspace_size(int T, int H, int G);
+DSA_API int dsa_prefix_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
+                           const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* cu_kv_lens,
+                           const int32_t* page_indices, const int32_t* prefix_lens, const int32_t* group_offsets, int G,
+                           int max_kv, int T, int S, int P, int PTW, int ps, int H, int Dk, int Dv, float sm_scale,
+                           uint16_t* o, float* lse, void* ws, size_t ws_bytes, int32_t* dev_status);
+
 /* Self-test of failure detection; the source pages have no counterpart.
  * Every pipeline wait in these kernels is bounded: when it runs out, the CTA
  * sets DSA_STATUS_TIMEOUT in the status word, unwinds and returns instead of
