@@ -18,8 +18,8 @@
 // them, in order, so outputs are the same on every run.
 //
 // Roles of a CTA: warp 0 issues the MMAs (rank 0 only), warp 1 resolves keys and
-// copies the K blocks and queries, warp 2 the V blocks, warps 4-7 run the
-// softmax, a row per thread.
+// copies the K blocks and queries, warp 2 the V blocks, warps 4-11 run the
+// softmax, a row and half of a key tile's columns per thread.
 //
 // Per key tile i: QK^T(i), nine blocks of 64 dims, then PV(i - 1). S is read into
 // registers at once and P goes to shared memory, so that QK^T(i + 1) runs beside
@@ -37,10 +37,11 @@ constexpr int kRows = 128, kTileRows = 2 * kRows;  // of a CTA, of a pair
 constexpr int kKeys = 128, kHalfKeys = 64;         // of a key tile, of one CTA's K blocks
 constexpr int kBlk = kHalfKeys * 128;              // 64 keys x 64 dims
 constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims
-constexpr int kSlots = 10;                         // K blocks in flight (nine a tile)
+constexpr int kSlots = 9;                          // K blocks in flight: a tile's
 constexpr int kVStages = 2, kVStage = 2 * kBlk;    // 64 keys x 128 dims
 constexpr int kDescs = 4;
-constexpr int kThreads = 256;
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = (4 + kSoftWarps) * 32;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
 constexpr int kNoRow = -64;               // a box from here on lies outside the cache and lands as zeros
 
@@ -58,16 +59,16 @@ constexpr int OFF_P = OFF_Q + 5 * kQBlk;
 constexpr int OFF_K = OFF_P + 2 * kQBlk;
 constexpr int OFF_V = OFF_K + kSlots * kBlk;
 constexpr int OFF_DESC = OFF_V + kVStages * kVStage;
-constexpr int OFF_BAR = OFF_DESC + kDescs * (int)sizeof(KeyTile);
-constexpr int kNumBars = 2 * kSlots + 2 * kVStages + 2 * kDescs + 7;
+constexpr int OFF_ROW = OFF_DESC + kDescs * (int)sizeof(KeyTile);  // float [2][2][kRows]: maxima of the two halves
+constexpr int OFF_BAR = OFF_ROW + 4 * kRows * 4;
+constexpr int kNumBars = 2 * kSlots + 2 * kVStages + 2 * kDescs + 7 + kSoftWarps / 2;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_DESC % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 static_assert(4 * kQBlk <= kSlots * kBlk, "the queries for TMEM land in the K blocks");
-constexpr int kOutLd = 512 + 16;      // bytes of a staged bf16 row
-constexpr int kPartLd = 64 * 4 + 16;  // and of 64 staged fp32 columns
-static_assert(kRows * kOutLd <= kSlots * kBlk && kRows * kPartLd <= kSlots * kBlk, "rows are staged in the K blocks");
+constexpr int kStageLd = 256 + 16;  // bytes of a staged row: 128 bf16 or 64 fp32 columns
+static_assert(kSoftWarps * 32 * kStageLd <= kSlots * kBlk, "rows are staged in the K blocks");
 
 constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, kKeys, false, false);
 constexpr uint32_t kIdescPV = make_idesc_bf16(kTileRows, 256, false, true);
@@ -93,6 +94,7 @@ struct Bars {
   __device__ __forceinline__ uint64_t* qready() const { return rest(4); }  // leader's: softmax warps of both
   __device__ __forceinline__ uint64_t* qbar() const { return rest(5); }    // each: the queries' copies
   __device__ __forceinline__ uint64_t* qmoved() const { return rest(6); }  // each: softmax warps
+  __device__ __forceinline__ uint64_t* met(int w) const { return rest(7 + w); }  // each: two warps with the same rows
 };
 
 // ------------------------------------------------------------- the work list
@@ -364,14 +366,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) mbar_init(br.kfull(s), 1), mbar_init(br.kempty(s), 1);
     for (int s = 0; s < kVStages; ++s) mbar_init(br.vfull(s), 1), mbar_init(br.vempty(s), 1);
-    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), 5);
+    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps + 1);
     mbar_init(br.sfull(), 1);
     mbar_init(br.pvdone(), 1);
-    mbar_init(br.sempty(), 8);
-    mbar_init(br.pfull(), 8);
-    mbar_init(br.qready(), 8);
+    mbar_init(br.sempty(), 2 * kSoftWarps);
+    mbar_init(br.pfull(), 2 * kSoftWarps);
+    mbar_init(br.qready(), 2 * kSoftWarps);
     mbar_init(br.qbar(), 1);
-    mbar_init(br.qmoved(), 4);
+    mbar_init(br.qmoved(), kSoftWarps);
+    for (int w = 0; w < kSoftWarps / 2; ++w) mbar_init(br.met(w), 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -397,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   };
   // every role counts what it has passed since the kernel began: a barrier's
   // phase is that number's parity
-  uint32_t kc = 0, vc = 0, tc = 0, uc = 0;  // K blocks, V stages, key tiles, lists
+  uint32_t tc = 0, uc = 0, mc = 0;  // key tiles, lists, exchanges of two softmax warps
   const long long u_end = pair < shares.n ? shares.begin(pair + 1) : 0;
   long long u = pair < shares.n ? shares.begin(pair) : 0;
 #pragma unroll 1
@@ -429,12 +432,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // S is free once the tile before has been read into registers
             if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < 9; ++b, ++kc) {
-              const int slot = kc % kSlots;
-              if (!(ok = mbar_wait_warp(br.kfull(slot), (kc / kSlots) & 1, abort_flag))) break;
-              tc_fence_after();
-              const uint64_t kb = dk + (uint64_t)(slot * (kBlk >> 4));
+#pragma unroll
+            for (int b = 0; b < kSlots; ++b) {
+              ok = ok && mbar_wait_warp(br.kfull(b), tc & 1, abort_flag);
+              if (!ok) break;
+              const uint64_t kb = dk + (uint64_t)(b * (kBlk >> 4));
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t acc = b || k ? 1u : 0u;
@@ -442,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 else umma_pair_ss_lead(lead, tm + kColS, dq + (uint64_t)((b - 4) * (kQBlk >> 4) + k * 2), kb + k * 2,
                                        kIdescQK, acc);
               }
-              commit(br.kempty(slot));
+              commit(br.kempty(b));
             }
             if (!ok) break;
             commit(br.sfull());
@@ -451,11 +453,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (i > 0) {
             if (!(ok = mbar_wait_warp_cluster(br.pfull(), (tc - (i < n ? 2 : 1)) & 1, abort_flag))) break;
             tc_fence_after();
-#pragma unroll 1
+#pragma unroll
             for (int s = 0; s < kVStages; ++s) {
-              if (!(ok = mbar_wait_warp(br.vfull(s), (vc / kVStages) & 1, abort_flag))) break;
-              ++vc;
-              tc_fence_after();
+              ok = ok && mbar_wait_warp(br.vfull(s), (tc - (i < n ? 2 : 1)) & 1, abort_flag);
+              if (!ok) break;
               const uint64_t vb = dv + (uint64_t)(s * (kVStage >> 4)), pb = dp + (uint64_t)(s * (kQBlk >> 4));
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -493,12 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the queries for TMEM have left the K blocks
         if (i == 0 && !(ok = mbar_wait_warp(br.qmoved(), uc & 1, abort_flag))) break;
 #pragma unroll 1
-        for (int b = 0; b < 9; ++b, ++kc) {
-          const int slot = kc % kSlots;
-          if (!(ok = mbar_wait_warp(br.kempty(slot), ((kc / kSlots) & 1) ^ 1, abort_flag))) break;
+        for (int b = 0; b < kSlots; ++b) {
+          if (!(ok = mbar_wait_warp(br.kempty(b), (tc & 1) ^ 1, abort_flag))) break;
           if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(br.kfull(slot), 2 * kBlk);
-            copy_block(smem0 + OFF_K + slot * kBlk, &kvmap, leader(br.kfull(slot)), b * 64,
+            if (rank == 0) mbar_arrive_expect_tx(br.kfull(b), 2 * kBlk);
+            copy_block(smem0 + OFF_K + b * kBlk, &kvmap, leader(br.kfull(b)), b * 64,
                        rank ? t.row[2] : t.row[0], rank ? t.row[3] : t.row[1], two);
           }
           __syncwarp();
@@ -520,8 +520,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(br.dempty(ds));
         // the queries for TMEM lie in the K blocks alone
 #pragma unroll 1
-        for (int s = 0; s < kVStages; ++s, ++vc) {
-          if (!(ok = mbar_wait_warp(br.vempty(s), ((vc / kVStages) & 1) ^ 1, abort_flag))) break;
+        for (int s = 0; s < kVStages; ++s) {
+          if (!(ok = mbar_wait_warp(br.vempty(s), (tc & 1) ^ 1, abort_flag))) break;
           if (lane == 0) {
             if (rank == 0) mbar_arrive_expect_tx(br.vfull(s), 2 * kVStage);
 #pragma unroll
@@ -536,13 +536,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) give_up();
     } else if (warp >= 4) {
       // ------------------------------------------------------------- softmax
-      const int r = (warp & 3) * 32 + lane;  // TMEM lane and row
+      const int r = (warp & 3) * 32 + lane, hh = (warp - 4) >> 2;  // TMEM lane and row; half of the columns
       const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
+      float* row_buf = reinterpret_cast<float*>(smem + OFF_ROW) + r;
+      // the two warps that share 32 rows wait for each other (not by a named
+      // barrier: that wait would have no limit)
+      auto meet = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(br.met(warp & 3));
+        return mbar_wait_warp(br.met(warp & 3), mc++ & 1, abort_flag);
+      };
       bool ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
       if (ok) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
           const uint8_t* row = smem + OFF_K + c * kQBlk + r * 128;
           uint32_t v[32];
 #pragma unroll
@@ -578,77 +586,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         see = g.n_vis;
       }
       const float sl2 = prm.scale_log2;
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's columns
 #pragma unroll 1
       for (int i = 0; ok && i < n; ++i, ++tc) {
         const int ds = tc % kDescs;
         if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-        const int p0 = descs[ds].pos, seg = descs[ds].seg, valid = descs[ds].valid;
+        const int p0 = descs[ds].pos + hh * 64, seg = descs[ds].seg, valid = descs[ds].valid >> (2 * hh);
         __syncwarp();
         if (lane == 0) mbar_arrive(br.dempty(ds));
         const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
         const int lo = seg < 0 ? 0 : prefix - p0;
         auto below = [](int k) -> uint32_t { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };
-        uint32_t mask[4];
-        bool full = true;
+        uint32_t mask[2];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) & ~below(lo - 32 * g) : 0u;
-          full = full && mask[g] == 0xffffffffu;
-        }
-        full = __all_sync(0xffffffffu, full);
+        for (int g = 0; g < 2; ++g) mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) & ~below(lo - 32 * g) : 0u;
+        const bool full = __all_sync(0xffffffffu, (mask[0] & mask[1]) == 0xffffffffu);
         if (!(ok = mbar_wait_warp(br.sfull(), tc & 1, abort_flag))) break;
         tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_ld32(tmem + lane_base + kColS + 32 * g, s[g]);
+        uint32_t s[2][32];
+        tmem_ld32(tmem + lane_base + kColS + 64 * hh, s[0]);
+        tmem_ld32(tmem + lane_base + kColS + 64 * hh + 32, s[1]);
         tmem_ld_wait_regs(s[0]);
-#pragma unroll
-        for (int g = 1; g < 4; ++g) reg_fence(s[g]);
+        reg_fence(s[1]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(a_sempty);
-        __syncwarp();
+        // scaled logits, those of masked keys -inf: they are left out of maximum
+        // and weights, whatever they are
+        if (full) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[g][j] = __float_as_uint(__uint_as_float(s[g][j]) * sl2);
+        } else {
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              s[g][j] = (mask[g] >> j) & 1u ? __float_as_uint(__uint_as_float(s[g][j]) * sl2) : 0xff800000u;
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        // a masked key is left out of maximum and weights, whatever its logit is
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x = __uint_as_float(s[g][j]) * sl2;
-            mx[j & 3] = full || ((mask[g] >> j) & 1u) ? fmaxf(mx[j & 3], x) : mx[j & 3];
-          }
-        const float m_new = fmaxf(m_run, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          for (int j = 0; j < 32; j += 2)
+            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[g][j]), __uint_as_float(s[g][j + 1]));
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        float* xch = row_buf + (tc & 1) * 2 * kRows;
+        xch[hh * kRows] = mine;
+        if (!(ok = meet())) break;
+        const float m_new = fmaxf(m_run, fmaxf(mine, xch[(hh ^ 1) * kRows]));
         const bool need = m_new > m_run + kRescaleThreshold;  // also true when m_run == -inf
         const float m_use = need ? m_new : m_run;
         const float alpha = need ? exp2f(m_run - m_new) : 1.f;
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;
-        const uint64_t sl2x2 = f32x2_pack(sl2, sl2), nm2 = f32x2_pack(-m_sub, -m_sub);
+        const float m_sub = m_use == -INFINITY ? 0.f : m_use;  // a row without keys so far: its weights are 2^-inf
+        const uint64_t nm2 = f32x2_pack(-m_sub, -m_sub);
         uint64_t ps2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             float x0, x1;
-            f32x2_unpack(ffma2(f32x2_pack(__uint_as_float(s[g][2 * c]), __uint_as_float(s[g][2 * c + 1])), sl2x2, nm2),
-                         x0, x1);
+            f32x2_unpack(fadd2(f32x2_pack(__uint_as_float(s[g][2 * c]), __uint_as_float(s[g][2 * c + 1])), nm2), x0, x1);
             x0 = ex2_approx(x0);
             x1 = ex2_approx(x1);
-            if (!full) {
-              x0 = (mask[g] >> (2 * c)) & 1u ? x0 : 0.f;
-              x1 = (mask[g] >> (2 * c + 1)) & 1u ? x1 : 0.f;
-            }
             ps2[c & 1] = fadd2(ps2[c & 1], f32x2_pack(x0, x1));
             __nv_bfloat162 b2 = __floats2bfloat162_rn(x0, x1);  // P as a bf16 operand
             s[g][c] = *reinterpret_cast<uint32_t*>(&b2);
           }
-        }
         // P's buffer and O are free once PV of the tile before has run
         if (i > 0 && !(ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag))) break;
         if (i > 0 && __any_sync(0xffffffffu, need)) {
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 4 * hh; c < 4 * hh + 4; ++c) {
             uint32_t ov[32];
             tmem_ld32(tmem + lane_base + kColO + c * 32, ov);
             tmem_ld_wait_regs(ov);
@@ -660,34 +671,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_before();
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            st_shared_v4(smem0 + OFF_P + (g >> 1) * kQBlk + sw128_offset(r, (g & 1) * 4 + c), s[g][4 * c],
-                         s[g][4 * c + 1], s[g][4 * c + 2], s[g][4 * c + 3]);
+            st_shared_v4(smem0 + OFF_P + hh * kQBlk + sw128_offset(r, g * 4 + c), s[g][4 * c], s[g][4 * c + 1],
+                         s[g][4 * c + 2], s[g][4 * c + 3]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(a_pfull);
-        __syncwarp();
         float pa, pb;
         f32x2_unpack(fadd2(ps2[0], ps2[1]), pa, pb);
         l_run = l_run * alpha + (pa + pb);
         m_run = m_use;
       }
       // ------------------------------------------------------------ epilogue
-      if (ok) ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
+      float* xch = row_buf + (tc & 1) * 2 * kRows;
+      xch[hh * kRows] = l_run;
+      ok = ok && meet() && mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
       if (ok) {
         tc_fence_after();
-        const bool some = l_run != 0.f;  // a sum of weights is never negative; NaN counts
-        const float inv_l = some ? 1.f / l_run : 0.f;
-        const float lse2 = some ? m_run + log2f(l_run) : -INFINITY;
+        const float l = xch[0] + xch[kRows];
+        const bool some = l != 0.f;  // a sum of weights is never negative; NaN counts
+        const float inv_l = some ? 1.f / l : 0.f;
+        const float lse2 = some ? m_run + log2f(l) : -INFINITY;
+        // the warp stages 32 rows of its 128 columns in the idle K blocks and
+        // writes them two rows at a time
         const int w0 = (warp & 3) * 32, nw = min(32, rows - w0);
+        uint8_t* stg = smem + OFF_K + (warp - 4) * (32 * kStageLd);
+        const uint32_t col = tmem + lane_base + kColO + 128 * hh;
         if (whole) {
-          uint8_t* stg = smem + OFF_K + (warp & 3) * (32 * kOutLd);
 #pragma unroll 1
-          for (int c0 = 0; c0 < 256; c0 += 32) {
+          for (int c0 = 0; c0 < 128; c0 += 32) {
             uint32_t o[32];
-            tmem_ld32(tmem + lane_base + kColO + c0, o);
+            tmem_ld32(col + c0, o);
             tmem_ld_wait_regs(o);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -698,41 +714,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                                           __uint_as_float(o[8 * j + 2 * e + 1]) * inv_l);
                 pk[e] = *reinterpret_cast<uint32_t*>(&b2);
               }
-              *reinterpret_cast<uint4*>(stg + lane * kOutLd + c0 * 2 + j * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              *reinterpret_cast<uint4*>(stg + lane * kStageLd + c0 * 2 + j * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
           __syncwarp();
-          uint16_t* orow = prm.o + ((size_t)row0 + w0) * kDv + list.half * 256;
+          uint16_t* out = prm.o + ((size_t)row0 + w0) * kDv + list.half * 256 + hh * 128 + (lane & 15) * 8;
 #pragma unroll 4
-          for (int k = 0; k < nw; ++k)
-            reinterpret_cast<uint4*>(orow + (size_t)k * kDv)[lane] =
-                *reinterpret_cast<const uint4*>(stg + k * kOutLd + lane * 16);
-          if (list.half == 0 && r < rows && prm.lse) prm.lse[(size_t)row0 + r] = lse2 * 0.69314718055994531f;
+          for (int k = lane >> 4; k < nw; k += 2)
+            *reinterpret_cast<uint4*>(out + (size_t)k * kDv) =
+                *reinterpret_cast<const uint4*>(stg + k * kStageLd + (lane & 15) * 16);
+          if (list.half == 0 && hh == 0 && r < rows && prm.lse) prm.lse[(size_t)row0 + r] = lse2 * 0.69314718055994531f;
         } else {
           // normalised partial rows and their log-sums
-          uint8_t* stg = smem + OFF_K + (warp & 3) * (32 * kPartLd);
           const size_t out_row = (size_t)slot_out * kTileRows + rank * kRows + w0;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 256; c0 += 64) {
+          for (int c0 = 0; c0 < 128; c0 += 64) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               uint32_t o[32];
-              tmem_ld32(tmem + lane_base + kColO + c0 + 32 * h, o);
+              tmem_ld32(col + c0 + 32 * h, o);
               tmem_ld_wait_regs(o);
 #pragma unroll
               for (int v = 0; v < 8; ++v)
-                *reinterpret_cast<float4*>(stg + lane * kPartLd + h * 128 + v * 16) =
+                *reinterpret_cast<float4*>(stg + lane * kStageLd + h * 128 + v * 16) =
                     make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
             }
             __syncwarp();
+            float* out = prm.part_o + out_row * 256 + hh * 128 + c0 + (lane & 15) * 4;
 #pragma unroll 4
             for (int k = lane >> 4; k < nw; k += 2)
-              *reinterpret_cast<float4*>(prm.part_o + (out_row + k) * 256 + c0 + (lane & 15) * 4) =
-                  *reinterpret_cast<const float4*>(stg + k * kPartLd + (lane & 15) * 16);
+              *reinterpret_cast<float4*>(out + (size_t)k * 256) =
+                  *reinterpret_cast<const float4*>(stg + k * kStageLd + (lane & 15) * 16);
             __syncwarp();
           }
-          if (r < rows) prm.part_lse[out_row + lane] = lse2;
+          if (hh == 0 && r < rows) prm.part_lse[out_row + lane] = lse2;
         }
         tc_fence_before();
         fence_proxy_async_smem();  // the staged rows' place is written by copies again
@@ -745,8 +761,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     if (*abort_flag) break;
-    // a role that does not count by itself keeps up
-    if (warp != 1 && !(warp == 0 && rank == 0)) kc += 9 * n;
     u += n;
     ++uc;
   }

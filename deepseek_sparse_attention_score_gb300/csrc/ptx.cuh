@@ -464,6 +464,12 @@ __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// The largest of three, ignoring NaN as fmaxf does.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // Maximum of one fp32 value over the full warp (every lane gets it).
 __device__ __forceinline__ float warp_max_f32(float v) {
   float r;
