@@ -282,8 +282,13 @@ __device__ __forceinline__ uint32_t elect_one() {
 // 128 rows of A and D, and half of B's columns, at the same shared-memory and
 // TMEM addresses. The CTA of rank 0 issues. Barriers that both sides count on
 // are named by their address in the cluster (cluster_addr).
+//
+// Such arrivals hand over no memory from CTA to CTA: what they announce is in
+// TMEM (ordered by the tcgen05 fences), or in the announcing CTA's own shared
+// memory, where a proxy fence has passed it to the MMAs. So they need no cluster
+// scope, with which one waits 1.2 K cycles for the copies in flight.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // mbar_wait_warp for a barrier that the other CTA arrives on as well.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
