@@ -432,18 +432,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // S is free once the tile before has been read into registers
             if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
             tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < kSlots; ++b) {
-              ok = ok && mbar_wait_warp(br.kfull(b), tc & 1, abort_flag);
-              if (!ok) break;
+            // small loops: other roles share the instruction cache
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              if (!(ok = mbar_wait_warp(br.kfull(b), tc & 1, abort_flag))) break;
               const uint64_t kb = dk + (uint64_t)(b * (kBlk >> 4));
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t acc = b || k ? 1u : 0u;
-                if (b < 4) umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + b * 32 + k * 8, kb + k * 2, kIdescQK, acc);
-                else umma_pair_ss_lead(lead, tm + kColS, dq + (uint64_t)((b - 4) * (kQBlk >> 4) + k * 2), kb + k * 2,
-                                       kIdescQK, acc);
-              }
+              for (int k = 0; k < 4; ++k)
+                umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + b * 32 + k * 8, kb + k * 2, kIdescQK, b || k ? 1u : 0u);
+              commit(br.kempty(b));
+            }
+            if (!ok) break;
+#pragma unroll 1
+            for (int b = 4; b < kSlots; ++b) {
+              if (!(ok = mbar_wait_warp(br.kfull(b), tc & 1, abort_flag))) break;
+              const uint64_t kb = dk + (uint64_t)(b * (kBlk >> 4)), qb = dq + (uint64_t)((b - 4) * (kQBlk >> 4));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + k * 2, kIdescQK, 1u);
               commit(br.kempty(b));
             }
             if (!ok) break;
@@ -453,10 +458,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (i > 0) {
             if (!(ok = mbar_wait_warp_cluster(br.pfull(), (tc - (i < n ? 2 : 1)) & 1, abort_flag))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kVStages; ++s) {
-              ok = ok && mbar_wait_warp(br.vfull(s), (tc - (i < n ? 2 : 1)) & 1, abort_flag);
-              if (!ok) break;
+              if (!(ok = mbar_wait_warp(br.vfull(s), (tc - (i < n ? 2 : 1)) & 1, abort_flag))) break;
               const uint64_t vb = dv + (uint64_t)(s * (kVStage >> 4)), pb = dp + (uint64_t)(s * (kQBlk >> 4));
 #pragma unroll
               for (int k = 0; k < 4; ++k)
