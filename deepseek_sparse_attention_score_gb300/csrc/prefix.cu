@@ -3,28 +3,31 @@
 //   S = Q K^T over 576 dims, online softmax, O += P V, V = the first 512 dims.
 // The rows of a group are cut into tiles of 256, of any tokens and heads, since
 // [T, H] rows lie one behind another. A tile's keys are a list of key tiles of
-// 128: the prefix, read through the page table of the group's first request,
+// 256: the prefix, read through the page table of the group's first request,
 // then the own positions of each request that has rows in the tile, which the
 // rows of others mask.
 //
-// A pair of CTAs takes a row tile and half of the value columns: each has 128
-// rows, and the MMAs of 256 rows (cta_group::2) read half of a key tile from
-// each one's shared memory, so each fetches half. All of O is 512 columns of
-// fp32, the whole TMEM, so both value halves compute S.
+// A cluster of four CTAs takes a row tile: CTA (c, r) = rank 2c + r has rows
+// 128r .. of it, value columns 256c .. (128 rows of all 512 columns in fp32 would
+// be the whole TMEM) and computes S for keys 128c .. of a key tile, so that no
+// product is computed twice; it gives its weights P to CTA (1 - c, r), which
+// needs them for the other value columns, and the two agree on the rows' maxima.
+// The MMAs are those of the pairs (c, 0), (c, 1): 256 rows, and either CTA
+// fetches half of the keys' operands.
 //
-// Work: the key tiles of all row tiles and both halves in a row, dealt to the
-// pairs in equal shares, wherever a share ends. A list that was divided leaves
-// its parts in the workspace (at most two per pair) and a second kernel merges
-// them, in order, so outputs are the same on every run.
+// Work: the key tiles of all row tiles in a row, dealt to the clusters in equal
+// shares, wherever a share ends. A list that was divided leaves its parts in the
+// workspace (at most two per cluster) and a second kernel merges them, in order,
+// so outputs are the same on every run.
 //
-// Roles of a CTA: warp 0 issues the MMAs (rank 0 only), warp 1 resolves keys and
-// copies the K blocks and queries, warp 2 the V blocks, warps 4-11 run the
-// softmax, a row and half of a key tile's columns per thread.
+// Roles of a CTA: warp 0 issues the MMAs (r = 0), warp 1 resolves keys and copies
+// them and the queries, warp 3 passes on that the other half's P has arrived,
+// warps 4-11 run the softmax, a row and half of its columns of S per thread.
 //
-// Per key tile i: QK^T(i), nine blocks of 64 dims, then PV(i - 1). S is read into
-// registers at once and P goes to shared memory, so that QK^T(i + 1) runs beside
-// the softmax of tile i.
+// Per key tile i: QK^T(i), then PV(i - 1). S is read into registers at once and P
+// goes to shared memory, so that QK^T(i + 1) runs beside the softmax of tile i.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "prefix.cuh"
@@ -33,68 +36,71 @@ namespace dsa {
 
 namespace {
 constexpr int kDk = 576, kDv = 512;
-constexpr int kRows = 128, kTileRows = 2 * kRows;  // of a CTA, of a pair
-constexpr int kKeys = 128, kHalfKeys = 64;         // of a key tile, of one CTA's K blocks
-constexpr int kBlk = kHalfKeys * 128;              // 64 keys x 64 dims
-constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims
-constexpr int kSlots = 9;                          // K blocks in flight: a tile's
-constexpr int kVStages = 2, kVStage = 2 * kBlk;    // 64 keys x 128 dims
-constexpr int kDescs = 4;
+constexpr int kRows = 128, kTileRows = 2 * kRows;  // of a CTA, of a cluster
+constexpr int kKeys = 256, kRuns = kKeys / 32;     // of a key tile, and its runs of 32 keys
+constexpr int kBlk = 64 * 128;                     // 64 keys x 64 dims
+constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (queries) or keys (P)
+// Stages of a key tile: five of two K blocks (64 keys of this CTA, 128 dims; the
+// last has one block), then four of V (64 keys, 128 dims of this CTA)
+constexpr int kStages = 5, kStage = 2 * kBlk;
+constexpr int kKStages = 5, kVStages = 4;
+constexpr int kDescs = 2;
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = (4 + kSoftWarps) * 32;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
 constexpr int kNoRow = -64;               // a box from here on lies outside the cache and lands as zeros
 
-// What the softmax and the copiers know of a key tile.
+// What the softmax and the copier know of a key tile.
 struct KeyTile {
-  int row[4];  // cache row of each 32 keys, or kNoRow
-  int pos;     // of the first key
-  int seg;     // -1: prefix; else the request whose own keys they are
-  int valid;   // bit g: keys 32 g .. hold positions
-  int pad;
+  int row[kRuns];  // cache row of each run of 32 keys, or kNoRow
+  int pos;         // of the first key
+  int seg;         // -1: prefix; else the request whose own keys they are
+  int valid;       // bit g: run g holds positions
 };
 
 constexpr int OFF_Q = 0;  // dims 256-575
-constexpr int OFF_P = OFF_Q + 5 * kQBlk;
-constexpr int OFF_K = OFF_P + 2 * kQBlk;
-constexpr int OFF_V = OFF_K + kSlots * kBlk;
-constexpr int OFF_DESC = OFF_V + kVStages * kVStage;
-constexpr int OFF_ROW = OFF_DESC + kDescs * (int)sizeof(KeyTile);  // float [2][2][kRows]: maxima of the two halves
-constexpr int OFF_BAR = OFF_ROW + 4 * kRows * 4;
-constexpr int kNumBars = 2 * kSlots + 2 * kVStages + 2 * kDescs + 7 + kSoftWarps / 2;
+constexpr int OFF_P = OFF_Q + 5 * kQBlk;  // four blocks of 64 keys
+constexpr int OFF_RING = OFF_P + 4 * kQBlk;
+constexpr int OFF_LOCAL = OFF_RING + kStages * kStage;   // float [2][kRows]: maxima of the two halves of S's columns
+constexpr int OFF_REMOTE = OFF_LOCAL + 2 * kRows * 4;    // float [2][kRows]: those of the other keys, two tiles
+constexpr int OFF_DESC = OFF_REMOTE + 2 * kRows * 4;
+constexpr int OFF_BAR = (OFF_DESC + kDescs * (int)sizeof(KeyTile) + 7) & ~7;
+constexpr int kNumBars = 2 * kStages + 2 * kDescs + 9 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
-static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_DESC % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
-static_assert(4 * kQBlk <= kSlots * kBlk, "the queries for TMEM land in the K blocks");
+static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_DESC % 16 == 0, "alignment");
+static_assert(4 * kQBlk <= kStages * kStage, "the queries for TMEM land in the ring");
 constexpr int kStageLd = 256 + 16;  // bytes of a staged row: 128 bf16 or 64 fp32 columns
-static_assert(kSoftWarps * 32 * kStageLd <= kSlots * kBlk, "rows are staged in the K blocks");
+static_assert(kSoftWarps * 32 * kStageLd <= kStages * kStage, "rows are staged in the ring");
 
-constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, kKeys, false, false);
+constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, 128, false, false);
 constexpr uint32_t kIdescPV = make_idesc_bf16(kTileRows, 256, false, true);
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 384;
 
 struct Bars {
   uint64_t* b;
-  // leader's: both CTAs' copies
-  __device__ __forceinline__ uint64_t* kfull(int s) const { return b + s; }
-  __device__ __forceinline__ uint64_t* vfull(int s) const { return b + 2 * kSlots + s; }
-  // each CTA's: commits
-  __device__ __forceinline__ uint64_t* kempty(int s) const { return b + kSlots + s; }
-  __device__ __forceinline__ uint64_t* vempty(int s) const { return b + 2 * kSlots + kVStages + s; }
+  // the pair's first CTA's: both CTAs' copies
+  __device__ __forceinline__ uint64_t* full(int s) const { return b + s; }
+  // each CTA's: commits of its pair
+  __device__ __forceinline__ uint64_t* empty(int s) const { return b + kStages + s; }
   // each CTA's: key tiles resolved, and read
-  __device__ __forceinline__ uint64_t* dfull(int s) const { return b + 2 * kSlots + 2 * kVStages + s; }
-  __device__ __forceinline__ uint64_t* dempty(int s) const { return b + 2 * kSlots + 2 * kVStages + kDescs + s; }
-  __device__ __forceinline__ uint64_t* rest(int k) const { return b + 2 * kSlots + 2 * kVStages + 2 * kDescs + k; }
-  __device__ __forceinline__ uint64_t* sfull() const { return rest(0); }   // each: commit
-  __device__ __forceinline__ uint64_t* pvdone() const { return rest(1); }  // each: commit
-  __device__ __forceinline__ uint64_t* sempty() const { return rest(2); }  // leader's: softmax warps of both
-  __device__ __forceinline__ uint64_t* pfull() const { return rest(3); }   // leader's: softmax warps of both
-  __device__ __forceinline__ uint64_t* qready() const { return rest(4); }  // leader's: softmax warps of both
+  __device__ __forceinline__ uint64_t* dfull(int s) const { return b + 2 * kStages + s; }
+  __device__ __forceinline__ uint64_t* dempty(int s) const { return b + 2 * kStages + kDescs + s; }
+  __device__ __forceinline__ uint64_t* rest(int k) const { return b + 2 * kStages + 2 * kDescs + k; }
+  __device__ __forceinline__ uint64_t* sfull() const { return rest(0); }   // each: commit of its pair
+  __device__ __forceinline__ uint64_t* pvdone() const { return rest(1); }  // each: commits of both pairs
+  __device__ __forceinline__ uint64_t* sempty() const { return rest(2); }  // pair's: softmax warps of both CTAs
+  __device__ __forceinline__ uint64_t* pfull() const { return rest(3); }   // pair's: those, and the other half's P
+  __device__ __forceinline__ uint64_t* qready() const { return rest(4); }  // pair's: softmax warps of both CTAs
   __device__ __forceinline__ uint64_t* qbar() const { return rest(5); }    // each: the queries' copies
   __device__ __forceinline__ uint64_t* qmoved() const { return rest(6); }  // each: softmax warps
-  __device__ __forceinline__ uint64_t* met(int w) const { return rest(7 + w); }  // each: two warps with the same rows
+  __device__ __forceinline__ uint64_t* ppeer() const { return rest(7); }   // each: P from the other half
+  __device__ __forceinline__ uint64_t* lbar() const { return rest(8); }    // each: sums of weights from the other half
+  __device__ __forceinline__ uint64_t* local(int w) const { return rest(9 + w); }  // each: two warps of the same rows
+  // each: those two and the maxima of the other half
+  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(13 + 4 * k + w); }
 };
 
 // ------------------------------------------------------------- the work list
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
 }
 
-// The units (key tiles of row tiles, both halves) and the shares they are dealt in.
+// The units (key tiles of row tiles) and the shares they are dealt in.
 struct Shares {
   long long units;
   int n;
@@ -229,29 +235,23 @@ struct Shares {
 };
 __device__ __forceinline__ Shares make_shares(const PrefixParams& p) {
   Shares s;
-  s.units = 2 * p.unit_base[*p.num_tiles];
-  s.n = (int)min((long long)p.pairs, s.units);
+  s.units = p.unit_base[*p.num_tiles];
+  s.n = (int)min((long long)p.shares, s.units);
   return s;
 }
-// The list (row tile and value half) of unit u: units [begin, end).
+// The list (of a row tile) that holds unit u: units [begin, end).
 struct List {
-  int tile, half;
+  int tile;
   long long begin, end;
 };
 __device__ __forceinline__ List list_of(const PrefixParams& p, long long u) {
   int lo = 0, hi = *p.num_tiles - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (2 * p.unit_base[mid] <= u) lo = mid;
+    if (p.unit_base[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
-  const long long a = p.unit_base[lo], n = p.unit_base[lo + 1] - a;
-  List l;
-  l.tile = lo;
-  l.half = u >= 2 * a + n;
-  l.begin = 2 * a + (l.half ? n : 0);
-  l.end = l.begin + n;
-  return l;
+  return {lo, p.unit_base[lo], p.unit_base[lo + 1]};
 }
 
 // The key tiles of a list from tile k on, resolved by one whole warp.
@@ -309,7 +309,6 @@ struct KeyCursor {
     t.pos = pos;
     t.seg = seg;
     t.valid = 0;
-    t.pad = 0;
     const int e0 = pos >> lg;
     if (pos < end && (e0 < win || ((pos + kKeys - 1) >> lg) >= win + 32)) {
       win = e0;
@@ -329,7 +328,7 @@ struct KeyCursor {
       }
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < kRuns; ++g) {
       const int at = pos + 32 * g, pg = __shfl_sync(0xffffffffu, page, ((at >> lg) - win) & 31);
       const bool ok = at < end && pg >= 0;
       t.row[g] = ok ? (pg << lg) + (at & (p->ps - 1)) : kNoRow;
@@ -347,7 +346,7 @@ __device__ __forceinline__ void copy_block(uint32_t dst, const CUtensorMap* map,
   if (two) tma_load_2d_pair(dst + kBlk / 2, map, bar, dim, r1);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_mla_kernel(const __grid_constant__ PrefixParams prm, const __grid_constant__ CUtensorMap kvmap,
                       const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -357,24 +356,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   griddep_launch_dependents();
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
-  const uint32_t rank = cluster_rank(), smem0 = smem_u32(smem);
-  const int pair = blockIdx.x >> 1;
+  const int rank = (int)cluster_rank(), c = rank >> 1, r = rank & 1, share = blockIdx.x >> 2;
+  const uint32_t smem0 = smem_u32(smem);
   const Bars br{reinterpret_cast<uint64_t*>(smem + OFF_BAR)};
   KeyTile* descs = reinterpret_cast<KeyTile*>(smem + OFF_DESC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) mbar_init(br.kfull(s), 1), mbar_init(br.kempty(s), 1);
-    for (int s = 0; s < kVStages; ++s) mbar_init(br.vfull(s), 1), mbar_init(br.vempty(s), 1);
-    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps + 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(br.full(s), 1), mbar_init(br.empty(s), 1);
+    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps);
     mbar_init(br.sfull(), 1);
-    mbar_init(br.pvdone(), 1);
+    mbar_init(br.pvdone(), 2);
     mbar_init(br.sempty(), 2 * kSoftWarps);
-    mbar_init(br.pfull(), 2 * kSoftWarps);
+    mbar_init(br.pfull(), 2 * kSoftWarps + 2);
     mbar_init(br.qready(), 2 * kSoftWarps);
     mbar_init(br.qbar(), 1);
     mbar_init(br.qmoved(), kSoftWarps);
-    for (int w = 0; w < kSoftWarps / 2; ++w) mbar_init(br.met(w), 2);
+    mbar_init(br.ppeer(), 1);
+    mbar_init(br.lbar(), kSoftWarps);
+    for (int w = 0; w < 4; ++w) {
+      mbar_init(br.local(w), 2);
+      for (int k = 0; k < 2; ++k) mbar_init(br.remote(w, k), 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -389,70 +392,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   griddep_wait();
   const uint32_t tmem = *tmem_slot;
   const Shares shares = make_shares(prm);
-  auto leader = [&](uint64_t* bar) { return cluster_addr(smem_u32(bar), 0); };
-  // a role that gives up tells both CTAs
+  auto leader = [&](uint64_t* bar) { return cluster_addr(smem_u32(bar), rank & 2); };  // of the pair
+  auto other = [&](uint32_t a) { return cluster_addr(a, rank ^ 2); };  // CTA (1 - c, r)
+  // a role that gives up tells all CTAs
   auto give_up = [&]() {
-    if (lane == 0) {
-      *abort_flag = 1;
-      st_cluster_u32(cluster_addr(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1);
-    }
+    if (lane < 4) st_cluster_u32(cluster_addr(smem_u32(const_cast<int*>(abort_flag)), lane), 1);
     __syncwarp();
   };
   // every role counts what it has passed since the kernel began: a barrier's
   // phase is that number's parity
-  uint32_t tc = 0, uc = 0, mc = 0;  // key tiles, lists, exchanges of two softmax warps
-  const long long u_end = pair < shares.n ? shares.begin(pair + 1) : 0;
-  long long u = pair < shares.n ? shares.begin(pair) : 0;
+  uint32_t tc = 0, uc = 0, fc = 0;  // key tiles, lists, stages
+  const long long u_end = share < shares.n ? shares.begin(share + 1) : 0;
+  long long u = share < shares.n ? shares.begin(share) : 0;
 #pragma unroll 1
   while (u < u_end) {
     const List list = list_of(prm, u);
     const int4 tile = prm.tiles[list.tile];
     const int k0 = (int)(u - list.begin), n = (int)(min(u_end, list.end) - u);
     const bool whole = k0 == 0 && u + n == list.end;
-    const int slot_out = u == shares.begin(pair) ? 2 * pair : 2 * pair + 1;
-    const int row0 = tile.x + (int)rank * kRows;               // this CTA's first row of [T * H]
-    const int rows = min(kRows, tile.y - (int)rank * kRows);   // <= 0: none
+    const int slot_out = u == shares.begin(share) ? 2 * share : 2 * share + 1;
+    const int row0 = tile.x + r * kRows;              // this CTA's first row of [T * H]
+    const int rows = min(kRows, tile.y - r * kRows);  // <= 0: none
     if (warp == 0) {
       // -------------------------------------------------------- MMA issuer
-      if (rank == 0) {
+      if (r == 0) {
         const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t dq = make_sdesc(smem0 + OFF_Q, 16, 1024, kSwizzle128B);
         const uint64_t dp = make_sdesc(smem0 + OFF_P, 16, 1024, kSwizzle128B);
-        const uint64_t dk = make_sdesc(smem0 + OFF_K, 16, 1024, kSwizzle128B);
-        const uint64_t dv = make_sdesc(smem0 + OFF_V, kBlk, 1024, kSwizzle128B);  // MN-major
-        auto commit = [&](uint64_t* bar) {
-          if (lead) umma_commit_pair(bar, 3);
+        const uint64_t dk = make_sdesc(smem0 + OFF_RING, 16, 1024, kSwizzle128B);
+        const uint64_t dv = make_sdesc(smem0 + OFF_RING, kBlk, 1024, kSwizzle128B);  // MN-major
+        const uint16_t pair = (uint16_t)(3 << rank);
+        auto commit = [&](uint64_t* bar, uint16_t to) {
+          if (lead) umma_commit_pair(bar, to);
           __syncwarp();
+        };
+        uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
+        auto arrived = [&]() { return mbar_wait_warp(br.full(slot), phase, abort_flag); };
+        auto pass = [&]() {
+          commit(br.empty(slot), pair);
+          if (++slot == kStages) slot = 0, phase ^= 1;
         };
         bool ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
         tc_fence_after();
 #pragma unroll 1
         for (int i = 0; ok && i <= n; ++i) {
+          // small loops: the roles share the instruction cache
           if (i < n) {
             // S is free once the tile before has been read into registers
             if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
             tc_fence_after();
-            // small loops: other roles share the instruction cache
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-              if (!(ok = mbar_wait_warp(br.kfull(b), tc & 1, abort_flag))) break;
-              const uint64_t kb = dk + (uint64_t)(b * (kBlk >> 4));
+            for (int j = 0; j < 2; ++j) {
+              if (!(ok = arrived())) break;
+              const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4));
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + b * 32 + k * 8, kb + k * 2, kIdescQK, b || k ? 1u : 0u);
-              commit(br.kempty(b));
+              for (int k = 0; k < 8; ++k)
+                umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + j * 64 + k * 8,
+                                  kb + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, kIdescQK, j || k ? 1u : 0u);
+              pass();
             }
             if (!ok) break;
 #pragma unroll 1
-            for (int b = 4; b < kSlots; ++b) {
-              if (!(ok = mbar_wait_warp(br.kfull(b), tc & 1, abort_flag))) break;
-              const uint64_t kb = dk + (uint64_t)(b * (kBlk >> 4)), qb = dq + (uint64_t)((b - 4) * (kQBlk >> 4));
+            for (int j = 4; j < 9; j += 2) {  // K blocks j and, but for the last, j + 1
+              if (!(ok = arrived())) break;
+              const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4)), qb = dq + (uint64_t)((j - 4) * (kQBlk >> 4));
 #pragma unroll
               for (int k = 0; k < 4; ++k) umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + k * 2, kIdescQK, 1u);
-              commit(br.kempty(b));
+              if (j < 8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  umma_pair_ss_lead(lead, tm + kColS, qb + (kQBlk >> 4) + k * 2, kb + (kBlk >> 4) + k * 2, kIdescQK, 1u);
+              }
+              pass();
             }
             if (!ok) break;
-            commit(br.sfull());
+            commit(br.sfull(), pair);
             ++tc;
           }
           if (i > 0) {
@@ -460,116 +474,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int s = 0; s < kVStages; ++s) {
-              if (!(ok = mbar_wait_warp(br.vfull(s), (tc - (i < n ? 2 : 1)) & 1, abort_flag))) break;
-              const uint64_t vb = dv + (uint64_t)(s * (kVStage >> 4)), pb = dp + (uint64_t)(s * (kQBlk >> 4));
+              if (!(ok = arrived())) break;
+              const uint64_t vb = dv + (uint64_t)(slot * (kStage >> 4)), pb = dp + (uint64_t)(s * (kQBlk >> 4));
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 umma_pair_ss_lead(lead, tm + kColO, pb + k * 2, vb + k * 128, kIdescPV, i > 1 || s || k ? 1u : 0u);
-              commit(br.vempty(s));
+              pass();
             }
             if (!ok) break;
-            commit(br.pvdone());
+            commit(br.pvdone(), 15);
           }
         }
         if (!ok) give_up();
       }
     } else if (warp == 1) {
-      // ------------------------------------ queries, key tiles and K blocks
+      // ------------------------------------------- queries and keys
       if (lane == 0) {
         mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
 #pragma unroll 1
-        for (int c = 0; c < 9; ++c)
-          tma_load_2d(smem + (c < 4 ? OFF_K + c * kQBlk : OFF_Q + (c - 4) * kQBlk), &qmap, br.qbar(), c * 64, row0);
+        for (int b = 0; b < 9; ++b)
+          tma_load_2d(smem + (b < 4 ? OFF_RING + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
       }
       KeyCursor cur;
       cur.init(prm, tile, k0);
       const bool two = prm.ps == 32;
-      bool ok = true;
-#pragma unroll 1
-      for (int i = 0; i < n; ++i, ++tc) {
-        const KeyTile t = cur.next();
-        const int ds = tc % kDescs;
-        if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
+      uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
+      // a stage of two blocks of 64 keys, from dim d0 on (one: only the first)
+      auto load = [&](int d0, int r0, int r1, bool one) -> bool {
+        if (!mbar_wait_warp(br.empty(slot), phase ^ 1, abort_flag)) return false;
         if (lane == 0) {
-          descs[ds] = t;
-          mbar_arrive(br.dfull(ds));
+          const uint32_t bar = leader(br.full(slot)), dst = smem0 + OFF_RING + slot * kStage;
+          if (r == 0) mbar_arrive_expect_tx(br.full(slot), one ? kStage : 2 * kStage);
+          copy_block(dst, &kvmap, bar, d0, r0, r1, two);
+          if (!one) copy_block(dst + kBlk, &kvmap, bar, d0 + 64, r0, r1, two);
         }
         __syncwarp();
-        // the queries for TMEM have left the K blocks
-        if (i == 0 && !(ok = mbar_wait_warp(br.qmoved(), uc & 1, abort_flag))) break;
+        if (++slot == kStages) slot = 0, phase ^= 1;
+        return true;
+      };
+      KeyTile t{}, before{};
+      bool ok = true;
 #pragma unroll 1
-        for (int b = 0; b < kSlots; ++b) {
-          if (!(ok = mbar_wait_warp(br.kempty(b), (tc & 1) ^ 1, abort_flag))) break;
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {
+          t = cur.next();
+          const int ds = tc % kDescs;
+          if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
           if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(br.kfull(b), 2 * kBlk);
-            copy_block(smem0 + OFF_K + b * kBlk, &kvmap, leader(br.kfull(b)), b * 64,
-                       rank ? t.row[2] : t.row[0], rank ? t.row[3] : t.row[1], two);
+            descs[ds] = t;
+            mbar_arrive(br.dfull(ds));
           }
           __syncwarp();
+          ++tc;
+          // the queries for TMEM have left the ring
+          if (i == 0 && !(ok = mbar_wait_warp(br.qmoved(), uc & 1, abort_flag))) break;
+          const int g = 4 * c + 2 * r;  // this CTA's 64 keys
+          int r0 = t.row[0], r1 = t.row[1];
+#pragma unroll
+          for (int h = 2; h < kRuns; h += 2)
+            if (h == g) r0 = t.row[h], r1 = t.row[h + 1];
+#pragma unroll 1
+          for (int j = 0; ok && j < kKStages; ++j) ok = load(j * 128, r0, r1, j == kKStages - 1);
+          if (!ok) break;
         }
-        if (!ok) break;
+        if (i > 0) {
+#pragma unroll
+          for (int s = 0; s < kVStages; ++s)
+            ok = ok && load(c * 256 + r * 128, before.row[2 * s], before.row[2 * s + 1], false);
+        }
+        before = t;
       }
       if (!ok) give_up();
-    } else if (warp == 2) {
-      // ------------------------------------------------------------ V blocks
-      const bool two = prm.ps == 32;
-      const int dim = list.half * 256 + (int)rank * 128;
+    } else if (warp == 3) {
+      // --------------------------- P of the other half, for the MMA issuer
+      const uint32_t a_pfull = leader(br.pfull());
       bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++tc) {
-        const int ds = tc % kDescs;
-        if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-        const KeyTile t = descs[ds];
+        if (lane == 0) mbar_arrive_expect_tx(br.ppeer(), 2 * kQBlk);
+        if (!(ok = mbar_wait_warp(br.ppeer(), tc & 1, abort_flag))) break;
+        if (lane == 0) mbar_arrive_cluster(a_pfull);
         __syncwarp();
-        if (lane == 0) mbar_arrive(br.dempty(ds));
-        // the queries for TMEM lie in the K blocks alone
-#pragma unroll 1
-        for (int s = 0; s < kVStages; ++s) {
-          if (!(ok = mbar_wait_warp(br.vempty(s), (tc & 1) ^ 1, abort_flag))) break;
-          if (lane == 0) {
-            if (rank == 0) mbar_arrive_expect_tx(br.vfull(s), 2 * kVStage);
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              copy_block(smem0 + OFF_V + s * kVStage + c * kBlk, &kvmap, leader(br.vfull(s)), dim + c * 64,
-                         s ? t.row[2] : t.row[0], s ? t.row[3] : t.row[1], two);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
       }
       if (!ok) give_up();
     } else if (warp >= 4) {
       // ------------------------------------------------------------- softmax
-      const int r = (warp & 3) * 32 + lane, hh = (warp - 4) >> 2;  // TMEM lane and row; half of the columns
-      const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+      const int q = warp & 3, hh = (warp - 4) >> 2;  // 32 TMEM lanes (rows); half of S's columns
+      const int row = q * 32 + lane;
+      const uint32_t lane_base = (uint32_t)(q * 32) << 16;
       const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
-      float* row_buf = reinterpret_cast<float*>(smem + OFF_ROW) + r;
-      // the two warps that share 32 rows wait for each other (not by a named
-      // barrier: that wait would have no limit)
-      auto meet = [&]() -> bool {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(br.met(warp & 3));
-        return mbar_wait_warp(br.met(warp & 3), mc++ & 1, abort_flag);
-      };
+      // this warp's part of P, 32 rows x 64 keys, here and at the other half
+      const uint32_t p_blk = smem0 + OFF_P + (2 * c + hh) * kQBlk, p_run = p_blk + q * 32 * 128;
       bool ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
       if (ok) {
 #pragma unroll 1
-        for (int c = 2 * hh; c < 2 * hh + 2; ++c) {
-          const uint8_t* row = smem + OFF_K + c * kQBlk + r * 128;
+        for (int b = 2 * hh; b < 2 * hh + 2; ++b) {
+          const uint8_t* src = smem + OFF_RING + b * kQBlk + row * 128;
           uint32_t v[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row + ((j ^ (r & 7)) << 4));
+            const uint4 x = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
             v[4 * j] = x.x;
             v[4 * j + 1] = x.y;
             v[4 * j + 2] = x.z;
             v[4 * j + 3] = x.w;
           }
-          tmem_st32(tmem + lane_base + kColQ + c * 32, v);
+          tmem_st32(tmem + lane_base + kColQ + b * 32, v);
         }
         tmem_st_wait();
         tc_fence_before();
-        fence_proxy_async_smem();  // the blocks are written by copies again
+        fence_proxy_async_smem();  // the ring is written by copies again
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(br.qmoved());
@@ -580,8 +594,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // this row's request and visible positions
       int my_s = -2, see = 0;
       const int prefix = group_prefix(prm, tile.z);
-      if (r < rows) {
-        const int t = (row0 + r) / prm.H;
+      if (row < rows) {
+        const int t = (row0 + row) / prm.H;
         int s = tile.w;
         while (s + 1 < prm.S && __ldg(prm.cu_q_lens + s + 1) <= t) ++s;
         const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, prm.max_kv, t,
@@ -591,11 +605,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const float sl2 = prm.scale_log2;
       float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's columns
+      float* mx_local = reinterpret_cast<float*>(smem + OFF_LOCAL) + row;
 #pragma unroll 1
       for (int i = 0; ok && i < n; ++i, ++tc) {
         const int ds = tc % kDescs;
         if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-        const int p0 = descs[ds].pos + hh * 64, seg = descs[ds].seg, valid = descs[ds].valid >> (2 * hh);
+        const int p0 = descs[ds].pos + c * 128 + hh * 64, seg = descs[ds].seg;
+        const int valid = descs[ds].valid >> (4 * c + 2 * hh);
         __syncwarp();
         if (lane == 0) mbar_arrive(br.dempty(ds));
         const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
@@ -635,11 +651,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; j += 2)
             mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[g][j]), __uint_as_float(s[g][j + 1]));
-        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        float* xch = row_buf + (tc & 1) * 2 * kRows;
-        xch[hh * kRows] = mine;
-        if (!(ok = meet())) break;
-        const float m_new = fmaxf(m_run, fmaxf(mine, xch[(hh ^ 1) * kRows]));
+        // The row's maximum over the tile: first with the warp of the other
+        // columns, then one of the two tells the CTA of the other keys. The other
+        // CTA sends tile i + 2's when PV(i) has run, so after this one has read
+        // tile i's: two places are enough. One local place is: the second barrier
+        // is passed when both warps have read. All waits have limits, which named
+        // barriers' have not.
+        mx_local[hh * kRows] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(br.local(q));
+        if (!(ok = mbar_wait_warp(br.local(q), tc & 1, abort_flag))) break;
+        const float mine = fmaxf(mx_local[0], mx_local[kRows]);
+        const uint32_t a_mx = smem0 + OFF_REMOTE + ((tc & 1) * kRows + row) * 4;
+        uint64_t* rbar = br.remote(q, tc & 1);
+        if (hh == 0) st_async_f32(other(a_mx), mine, other(smem_u32(rbar)));
+        __syncwarp();
+        if (lane == 0) {
+          if (hh == 0) mbar_arrive_expect_tx(rbar, 32 * 4);
+          else mbar_arrive(rbar);
+        }
+        if (!(ok = mbar_wait_warp(rbar, (tc >> 1) & 1, abort_flag))) break;
+        const float m_new = max3(m_run, mine, *reinterpret_cast<volatile float*>(smem + (a_mx - smem0)));
         const bool need = m_new > m_run + kRescaleThreshold;  // also true when m_run == -inf
         const float m_use = need ? m_new : m_run;
         const float alpha = need ? exp2f(m_run - m_new) : 1.f;
@@ -649,27 +681,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
+          for (int k = 0; k < 16; ++k) {
             float x0, x1;
-            f32x2_unpack(fadd2(f32x2_pack(__uint_as_float(s[g][2 * c]), __uint_as_float(s[g][2 * c + 1])), nm2), x0, x1);
+            f32x2_unpack(fadd2(f32x2_pack(__uint_as_float(s[g][2 * k]), __uint_as_float(s[g][2 * k + 1])), nm2), x0, x1);
             x0 = ex2_approx(x0);
             x1 = ex2_approx(x1);
-            ps2[c & 1] = fadd2(ps2[c & 1], f32x2_pack(x0, x1));
+            ps2[k & 1] = fadd2(ps2[k & 1], f32x2_pack(x0, x1));
             __nv_bfloat162 b2 = __floats2bfloat162_rn(x0, x1);  // P as a bf16 operand
-            s[g][c] = *reinterpret_cast<uint32_t*>(&b2);
+            s[g][k] = *reinterpret_cast<uint32_t*>(&b2);
           }
-        // P's buffer and O are free once PV of the tile before has run
+        // P's places, here and at the other half, and O are free once both
+        // pairs' PV of the tile before have run
         if (i > 0 && !(ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag))) break;
         if (i > 0 && __any_sync(0xffffffffu, need)) {
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 4 * hh; c < 4 * hh + 4; ++c) {
+          for (int k = 4 * hh; k < 4 * hh + 4; ++k) {
             uint32_t ov[32];
-            tmem_ld32(tmem + lane_base + kColO + c * 32, ov);
+            tmem_ld32(tmem + lane_base + kColO + k * 32, ov);
             tmem_ld_wait_regs(ov);
 #pragma unroll
             for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-            tmem_st32(tmem + lane_base + kColO + c * 32, ov);
+            tmem_st32(tmem + lane_base + kColO + k * 32, ov);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -677,31 +710,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            st_shared_v4(smem0 + OFF_P + hh * kQBlk + sw128_offset(r, g * 4 + c), s[g][4 * c], s[g][4 * c + 1],
-                         s[g][4 * c + 2], s[g][4 * c + 3]);
+          for (int k = 0; k < 4; ++k)
+            st_shared_v4(p_blk + sw128_offset(row, g * 4 + k), s[g][4 * k], s[g][4 * k + 1], s[g][4 * k + 2],
+                         s[g][4 * k + 3]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(a_pfull);
+        if (lane == 0) {
+          bulk_store_cluster(other(p_run), p_run, 32 * 128, other(smem_u32(br.ppeer())));
+          mbar_arrive_cluster(a_pfull);
+        }
         float pa, pb;
         f32x2_unpack(fadd2(ps2[0], ps2[1]), pa, pb);
         l_run = l_run * alpha + (pa + pb);
         m_run = m_use;
       }
       // ------------------------------------------------------------ epilogue
-      float* xch = row_buf + (tc & 1) * 2 * kRows;
-      xch[hh * kRows] = l_run;
-      ok = ok && meet() && mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
+      ok = ok && mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
+      if (ok) {
+        // the sum of a row's weights: four parts, in the idle P blocks
+        const uint32_t a_l = smem0 + OFF_P + ((2 * c + hh) * kRows + row) * 4;
+        st_async_f32(other(a_l), l_run, other(smem_u32(br.lbar())));
+        *reinterpret_cast<float*>(smem + (a_l - smem0)) = l_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(br.lbar(), 32 * 4);
+        ok = mbar_wait_warp(br.lbar(), uc & 1, abort_flag);
+      }
       if (ok) {
         tc_fence_after();
-        const float l = xch[0] + xch[kRows];
+        const volatile float* lp = reinterpret_cast<const volatile float*>(smem + OFF_P) + row;
+        const float l = (lp[0] + lp[kRows]) + (lp[2 * kRows] + lp[3 * kRows]);
         const bool some = l != 0.f;  // a sum of weights is never negative; NaN counts
         const float inv_l = some ? 1.f / l : 0.f;
         const float lse2 = some ? m_run + log2f(l) : -INFINITY;
-        // the warp stages 32 rows of its 128 columns in the idle K blocks and
-        // writes them two rows at a time
-        const int w0 = (warp & 3) * 32, nw = min(32, rows - w0);
-        uint8_t* stg = smem + OFF_K + (warp - 4) * (32 * kStageLd);
+        // the warp stages 32 rows of its 128 columns in the idle ring and writes
+        // them two rows at a time
+        const int w0 = q * 32, nw = min(32, rows - w0);
+        uint8_t* stg = smem + OFF_RING + (warp - 4) * (32 * kStageLd);
         const uint32_t col = tmem + lane_base + kColO + 128 * hh;
         if (whole) {
 #pragma unroll 1
@@ -722,15 +766,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          uint16_t* out = prm.o + ((size_t)row0 + w0) * kDv + list.half * 256 + hh * 128 + (lane & 15) * 8;
+          uint16_t* out = prm.o + ((size_t)row0 + w0) * kDv + c * 256 + hh * 128 + (lane & 15) * 8;
 #pragma unroll 4
           for (int k = lane >> 4; k < nw; k += 2)
             *reinterpret_cast<uint4*>(out + (size_t)k * kDv) =
                 *reinterpret_cast<const uint4*>(stg + k * kStageLd + (lane & 15) * 16);
-          if (list.half == 0 && hh == 0 && r < rows && prm.lse) prm.lse[(size_t)row0 + r] = lse2 * 0.69314718055994531f;
+          if (c == 0 && hh == 0 && row < rows && prm.lse) prm.lse[(size_t)row0 + row] = lse2 * 0.69314718055994531f;
         } else {
           // normalised partial rows and their log-sums
-          const size_t out_row = (size_t)slot_out * kTileRows + rank * kRows + w0;
+          const size_t out_row = (size_t)slot_out * kTileRows + r * kRows + w0;
 #pragma unroll 1
           for (int c0 = 0; c0 < 128; c0 += 64) {
 #pragma unroll 1
@@ -745,14 +789,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
             }
             __syncwarp();
-            float* out = prm.part_o + out_row * 256 + hh * 128 + c0 + (lane & 15) * 4;
+            float* out = prm.part_o + out_row * kDv + c * 256 + hh * 128 + c0 + (lane & 15) * 4;
 #pragma unroll 4
             for (int k = lane >> 4; k < nw; k += 2)
-              *reinterpret_cast<float4*>(out + (size_t)k * 256) =
+              *reinterpret_cast<float4*>(out + (size_t)k * kDv) =
                   *reinterpret_cast<const float4*>(stg + k * kStageLd + (lane & 15) * 16);
             __syncwarp();
           }
-          if (hh == 0 && r < rows) prm.part_lse[out_row + lane] = lse2;
+          if (c == 0 && hh == 0 && row < rows) prm.part_lse[out_row + lane] = lse2;
         }
         tc_fence_before();
         fence_proxy_async_smem();  // the staged rows' place is written by copies again
@@ -760,11 +804,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         give_up();
       }
     }
-    // both CTAs are done with the list: their MMAs have run and their copies landed
+    // all CTAs are done with the list: their MMAs have run and their copies landed
     __syncwarp();
     cluster_sync_all();
     tc_fence_after();
     if (*abort_flag) break;
+    fc += (kKStages + kVStages) * n;
     u += n;
     ++uc;
   }
@@ -780,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Merges a list that was divided: block x looks at the end of share x and takes
-// the list that it cuts, if it is the first to; a warp takes a row.
+// the list that it cuts, if it is the first to; a warp takes half a row.
 constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
   griddep_launch_dependents();
@@ -794,7 +839,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   const int k0 = sh.of(l.begin), k1 = sh.of(l.end - 1);
   if (k0 != x) return;
   const int4 tile = p.tiles[l.tile];
-  const int r = blockIdx.y * kMergeWarps + warp_id();
+  const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1;
   if (r >= tile.y) return;
   auto row_of = [&](int k) { return ((size_t)(sh.begin(k) >= l.begin ? 2 * k : 2 * k + 1)) * kTileRows + r; };
   float mx = -INFINITY, tot = 0.f;
@@ -812,34 +857,60 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
 #pragma unroll 4
   for (int k = k0; k <= k1; ++k) {
     const size_t row = row_of(k);
-    const float v = p.part_lse[row], w = v == -INFINITY ? 0.f : exp2f(v - mx) * inv;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + row * 256);
+    const float v = p.part_lse[row], wt = v == -INFINITY ? 0.f : exp2f(v - mx) * inv;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + row * kDv + half * 256);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 y = src[32 * h + lane];
-      acc[h].x = fmaf(w, y.x, acc[h].x);
-      acc[h].y = fmaf(w, y.y, acc[h].y);
-      acc[h].z = fmaf(w, y.z, acc[h].z);
-      acc[h].w = fmaf(w, y.w, acc[h].w);
+      acc[h].x = fmaf(wt, y.x, acc[h].x);
+      acc[h].y = fmaf(wt, y.y, acc[h].y);
+      acc[h].z = fmaf(wt, y.z, acc[h].z);
+      acc[h].w = fmaf(wt, y.w, acc[h].w);
     }
   }
-  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.x + r) * kDv + l.half * 256);
+  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.x + r) * kDv + half * 256);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc[h].x, acc[h].y), hi = __floats2bfloat162_rn(acc[h].z, acc[h].w);
     dst[32 * h + lane] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
   }
-  if (l.half == 0 && lane == 0 && p.lse)
+  if (half == 0 && lane == 0 && p.lse)
     p.lse[(size_t)tile.x + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
 }
 
 int max_tiles_of(int T, int H, int G) { return (int)(((long long)T * H + kTileRows - 1) / kTileRows) + G; }
-int max_pairs() { return std::max(1, sm_count() / 2); }
+int max_shares() { return std::max(1, sm_count() / 4); }
+// Clusters that the current device runs at once (a cluster lies in one GPC, so
+// there are fewer than SMs / 4), asked once per device.
+int clusters_at_once() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return max_shares();
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4 * max_shares());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 4;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, prefix_mla_kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return max_shares();
+  }
+  n = std::min(n, max_shares());
+  cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 struct Layout {
   size_t tile_base, tiles, unit_base, num_tiles, part_o, part_lse, bytes;
 };
 Layout layout_of(int T, int H, int G) {
-  const size_t nt = (size_t)max_tiles_of(T, H, G), slots = 2 * (size_t)max_pairs();
+  const size_t nt = (size_t)max_tiles_of(T, H, G), slots = 2 * (size_t)max_shares();
   Layout l;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -852,7 +923,7 @@ Layout layout_of(int T, int H, int G) {
   l.unit_base = take((nt + 1) * 8);
   l.num_tiles = take(4);
   l.part_lse = take(slots * kTileRows * 4);
-  l.part_o = take(slots * kTileRows * 256 * 4);
+  l.part_o = take(slots * kTileRows * kDv * 4);
   l.bytes = at;
   return l;
 }
@@ -870,16 +941,17 @@ int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
   prm.part_o = reinterpret_cast<float*>(w + l.part_o);
   prm.part_lse = reinterpret_cast<float*>(w + l.part_lse);
   prm.max_tiles = max_tiles_of(prm.T, prm.H, prm.G);
-  prm.pairs = max_pairs();
   CUtensorMap kvmap, qmap;
-  if (!encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, std::min(prm.ps, kHalfKeys),
+  if (!encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, std::min(prm.ps, 64),
                       kDk) ||
       !encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kRows, kDk))
     return DSA_ERR_CUDA;
   set_smem_attr_once(reinterpret_cast<const void*>(prefix_mla_kernel), kSmem);
+  prm.shares = clusters_at_once();
   DSA_LAUNCH_PDL(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, prm);
-  DSA_LAUNCH_PDL(prefix_mla_kernel, dim3(2 * prm.pairs), dim3(kThreads), kSmem, stream, prm, kvmap, qmap);
-  DSA_LAUNCH_PDL(prefix_merge_kernel, dim3(prm.pairs, kTileRows / kMergeWarps), dim3(kMergeWarps * 32), 0, stream, prm);
+  DSA_LAUNCH_PDL(prefix_mla_kernel, dim3(4 * prm.shares), dim3(kThreads), kSmem, stream, prm, kvmap, qmap);
+  DSA_LAUNCH_PDL(prefix_merge_kernel, dim3(prm.shares, 2 * kTileRows / kMergeWarps), dim3(kMergeWarps * 32), 0, stream,
+                 prm);
   return DSA_OK;
 }
 

@@ -29,9 +29,9 @@ struct PrefixParams {
   int4* tiles;         // first row, rows, group, first request
   long long* unit_base;  // [tiles + 1] key tiles of the tiles before
   int* num_tiles;
-  float* part_o;    // [2 * pairs][256][256]
-  float* part_lse;  // [2 * pairs][256], log2
-  int max_tiles, pairs;
+  float* part_o;    // [2 * shares][256][512]
+  float* part_lse;  // [2 * shares][256], log2
+  int max_tiles, shares;
 };
 
 size_t prefix_workspace_bytes(int T, int H, int G);

@@ -278,10 +278,10 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 
 // ------------------------------- tcgen05 and copies of a pair of CTAs
-// The two CTAs of a cluster work as one on 256 rows (cta_group::2): each holds
-// 128 rows of A and D, and half of B's columns, at the same shared-memory and
-// TMEM addresses. The CTA of rank 0 issues. Barriers that both sides count on
-// are named by their address in the cluster (cluster_addr).
+// Two CTAs of a cluster, of ranks 2k and 2k + 1, work as one on 256 rows
+// (cta_group::2): each holds 128 rows of A and D, and half of B's columns, at the
+// same shared-memory and TMEM addresses. The even one issues. Barriers that both
+// sides count on are named by their address in the cluster (cluster_addr).
 //
 // Such arrivals hand over no memory from CTA to CTA: what they announce is in
 // TMEM (ordered by the tcgen05 fences), or in the announcing CTA's own shared
@@ -318,6 +318,18 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "[%2];" ::"r"(dst),
       "l"(map), "r"(bar), "r"(x), "r"(y)
       : "memory");
+}
+// Asynchronous stores into another CTA's shared memory, counted on a barrier
+// there: one word, and a run of `bytes` (16-byte aligned, a multiple of 16) of
+// this CTA's shared memory.
+__device__ __forceinline__ void st_async_f32(uint32_t dst, float v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(dst), "f"(v), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 // One warp of each CTA calls these.
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
