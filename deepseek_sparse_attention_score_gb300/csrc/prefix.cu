@@ -41,7 +41,8 @@ constexpr int kKeys = 256, kRuns = kKeys / 32;     // of a key tile, and its run
 constexpr int kBlk = 64 * 128;                     // 64 keys x 64 dims
 constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (queries) or keys (P)
 // Stages of a key tile: five of two K blocks (64 keys of this CTA, 128 dims; the
-// last has one block), then four of V (64 keys, 128 dims of this CTA)
+// last has one block), then four of V (64 keys, 128 dims of this CTA), first the
+// keys whose P this CTA computes
 constexpr int kStages = 5, kStage = 2 * kBlk;
 constexpr int kKStages = 5, kVStages = 4;
 constexpr int kDescs = 2;
@@ -65,7 +66,7 @@ constexpr int OFF_LOCAL = OFF_RING + kStages * kStage;   // float [2][kRows]: ma
 constexpr int OFF_REMOTE = OFF_LOCAL + 2 * kRows * 4;    // float [2][kRows]: those of the other keys, two tiles
 constexpr int OFF_DESC = OFF_REMOTE + 2 * kRows * 4;
 constexpr int OFF_BAR = (OFF_DESC + kDescs * (int)sizeof(KeyTile) + 7) & ~7;
-constexpr int kNumBars = 2 * kStages + 2 * kDescs + 9 + 4 + 8;
+constexpr int kNumBars = 2 * kStages + 2 * kDescs + 10 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -92,15 +93,16 @@ struct Bars {
   __device__ __forceinline__ uint64_t* sfull() const { return rest(0); }   // each: commit of its pair
   __device__ __forceinline__ uint64_t* pvdone() const { return rest(1); }  // each: commits of both pairs
   __device__ __forceinline__ uint64_t* sempty() const { return rest(2); }  // pair's: softmax warps of both CTAs
-  __device__ __forceinline__ uint64_t* pfull() const { return rest(3); }   // pair's: those, and the other half's P
+  __device__ __forceinline__ uint64_t* pfull() const { return rest(3); }   // pair's: softmax warps of both CTAs
   __device__ __forceinline__ uint64_t* qready() const { return rest(4); }  // pair's: softmax warps of both CTAs
   __device__ __forceinline__ uint64_t* qbar() const { return rest(5); }    // each: the queries' copies
   __device__ __forceinline__ uint64_t* qmoved() const { return rest(6); }  // each: softmax warps
   __device__ __forceinline__ uint64_t* ppeer() const { return rest(7); }   // each: P from the other half
   __device__ __forceinline__ uint64_t* lbar() const { return rest(8); }    // each: sums of weights from the other half
-  __device__ __forceinline__ uint64_t* local(int w) const { return rest(9 + w); }  // each: two warps of the same rows
+  __device__ __forceinline__ uint64_t* pother() const { return rest(9); }  // pair's: P of the other half, both CTAs
+  __device__ __forceinline__ uint64_t* local(int w) const { return rest(10 + w); }  // each: two warps of the same rows
   // each: those two and the maxima of the other half
-  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(13 + 4 * k + w); }
+  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(14 + 4 * k + w); }
 };
 
 // ------------------------------------------------------------- the work list
@@ -368,7 +370,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(br.sfull(), 1);
     mbar_init(br.pvdone(), 2);
     mbar_init(br.sempty(), 2 * kSoftWarps);
-    mbar_init(br.pfull(), 2 * kSoftWarps + 2);
+    mbar_init(br.pfull(), 2 * kSoftWarps);
+    mbar_init(br.pother(), 2);
     mbar_init(br.qready(), 2 * kSoftWarps);
     mbar_init(br.qbar(), 1);
     mbar_init(br.qmoved(), kSoftWarps);
@@ -470,12 +473,18 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             ++tc;
           }
           if (i > 0) {
-            if (!(ok = mbar_wait_warp_cluster(br.pfull(), (tc - (i < n ? 2 : 1)) & 1, abort_flag))) break;
-            tc_fence_after();
+            // the keys whose P was computed here, then those whose P comes from
+            // the other half, which takes longer
+            const uint32_t parity = (tc - (i < n ? 2 : 1)) & 1;
 #pragma unroll 1
             for (int s = 0; s < kVStages; ++s) {
+              if (!(s & 1)) {
+                if (!(ok = mbar_wait_warp_cluster(s ? br.pother() : br.pfull(), parity, abort_flag))) break;
+                tc_fence_after();
+              }
               if (!(ok = arrived())) break;
-              const uint64_t vb = dv + (uint64_t)(slot * (kStage >> 4)), pb = dp + (uint64_t)(s * (kQBlk >> 4));
+              const uint64_t vb = dv + (uint64_t)(slot * (kStage >> 4));
+              const uint64_t pb = dp + (uint64_t)(((rank + s) & 3) * (kQBlk >> 4));  // rank = 2c
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 umma_pair_ss_lead(lead, tm + kColO, pb + k * 2, vb + k * 128, kIdescPV, i > 1 || s || k ? 1u : 0u);
@@ -540,20 +549,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         if (i > 0) {
 #pragma unroll
           for (int s = 0; s < kVStages; ++s)
-            ok = ok && load(c * 256 + r * 128, before.row[2 * s], before.row[2 * s + 1], false);
+            ok = ok && load(c * 256 + r * 128, c ? before.row[(2 * s + 4) & 7] : before.row[2 * s],
+                            c ? before.row[(2 * s + 5) & 7] : before.row[2 * s + 1], false);
         }
         before = t;
       }
       if (!ok) give_up();
     } else if (warp == 3) {
       // --------------------------- P of the other half, for the MMA issuer
-      const uint32_t a_pfull = leader(br.pfull());
+      const uint32_t a_pother = leader(br.pother());
       bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++tc) {
         if (lane == 0) mbar_arrive_expect_tx(br.ppeer(), 2 * kQBlk);
         if (!(ok = mbar_wait_warp(br.ppeer(), tc & 1, abort_flag))) break;
-        if (lane == 0) mbar_arrive_cluster(a_pfull);
+        if (lane == 0) mbar_arrive_cluster(a_pother);
         __syncwarp();
       }
       if (!ok) give_up();
