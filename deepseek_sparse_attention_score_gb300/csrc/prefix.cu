@@ -40,8 +40,8 @@ constexpr int kRows = 128, kTileRows = 2 * kRows;  // of a CTA, of a cluster
 constexpr int kKeys = 256, kRuns = kKeys / 32;     // of a key tile, and its runs of 32 keys
 constexpr int kBlk = 64 * 128;                     // 64 keys x 64 dims
 constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (queries) or keys (P)
-// Stages of a key tile: five of two K blocks (64 keys of this CTA, 128 dims; the
-// last has one block), then four of V (64 keys, 128 dims of this CTA), first the
+// Stages of a key tile: five of two K blocks (64 keys of this CTA, dims 64j and
+// 256 + 64j; the last has dims 512 alone), then four of V (64 keys, 128 dims of this CTA), first the
 // keys whose P this CTA computes
 constexpr int kStages = 5, kStage = 2 * kBlk;
 constexpr int kKStages = 5, kVStages = 4;
@@ -60,18 +60,17 @@ struct KeyTile {
 };
 
 constexpr int OFF_Q = 0;  // dims 256-575
-constexpr int OFF_P = OFF_Q + 5 * kQBlk;  // four blocks of 64 keys
+constexpr int OFF_P = OFF_Q + 5 * kQBlk;  // four blocks of 64 keys; before, the queries for TMEM: dims 0-255
 constexpr int OFF_RING = OFF_P + 4 * kQBlk;
 constexpr int OFF_LOCAL = OFF_RING + kStages * kStage;   // float [2][kRows]: maxima of the two halves of S's columns
 constexpr int OFF_REMOTE = OFF_LOCAL + 2 * kRows * 4;    // float [2][kRows]: those of the other keys, two tiles
 constexpr int OFF_DESC = OFF_REMOTE + 2 * kRows * 4;
 constexpr int OFF_BAR = (OFF_DESC + kDescs * (int)sizeof(KeyTile) + 7) & ~7;
-constexpr int kNumBars = 2 * kStages + 2 * kDescs + 10 + 4 + 8;
+constexpr int kNumBars = 2 * kStages + 2 * kDescs + 9 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_DESC % 16 == 0, "alignment");
-static_assert(4 * kQBlk <= kStages * kStage, "the queries for TMEM land in the ring");
 constexpr int kStageLd = 256 + 16;  // bytes of a staged row: 128 bf16 or 64 fp32 columns
 static_assert(kSoftWarps * 32 * kStageLd <= kStages * kStage, "rows are staged in the ring");
 
@@ -96,13 +95,12 @@ struct Bars {
   __device__ __forceinline__ uint64_t* pfull() const { return rest(3); }   // pair's: softmax warps of both CTAs
   __device__ __forceinline__ uint64_t* qready() const { return rest(4); }  // pair's: softmax warps of both CTAs
   __device__ __forceinline__ uint64_t* qbar() const { return rest(5); }    // each: the queries' copies
-  __device__ __forceinline__ uint64_t* qmoved() const { return rest(6); }  // each: softmax warps
-  __device__ __forceinline__ uint64_t* ppeer() const { return rest(7); }   // each: P from the other half
-  __device__ __forceinline__ uint64_t* lbar() const { return rest(8); }    // each: sums of weights from the other half
-  __device__ __forceinline__ uint64_t* pother() const { return rest(9); }  // pair's: P of the other half, both CTAs
-  __device__ __forceinline__ uint64_t* local(int w) const { return rest(10 + w); }  // each: two warps of the same rows
+  __device__ __forceinline__ uint64_t* ppeer() const { return rest(6); }   // each: P from the other half
+  __device__ __forceinline__ uint64_t* lbar() const { return rest(7); }    // each: sums of weights from the other half
+  __device__ __forceinline__ uint64_t* pother() const { return rest(8); }  // pair's: P of the other half, both CTAs
+  __device__ __forceinline__ uint64_t* local(int w) const { return rest(9 + w); }  // each: two warps of the same rows
   // each: those two and the maxima of the other half
-  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(14 + 4 * k + w); }
+  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(13 + 4 * k + w); }
 };
 
 // ------------------------------------------------------------- the work list
@@ -122,17 +120,15 @@ struct Own {
   int start, end;
   __device__ __forceinline__ int tiles() const { return end > start ? (end - start + kKeys - 1) / kKeys : 0; }
 };
-__device__ __forceinline__ Own own_keys(const PrefixParams& p, int s, int last, int prefix) {
-  const int q0 = __ldg(p.cu_q_lens + s), q1 = __ldg(p.cu_q_lens + s + 1);
+__device__ __forceinline__ Own own_keys(const PrefixParams& p, int q0, int q1, int seq_len, int last, int prefix) {
   Own w{0, 0};
   if (q1 <= q0 || last < q0) return w;
-  const int kv = request_kv(p, s);
+  const int kv = min(max(seq_len, 0), p.max_kv);
   const int end = min(kv, kv - (q1 - q0) + min(last, q1 - 1) - q0 + 1);
   if (end > prefix) w.start = prefix & -p.ps, w.end = end;
   return w;
 }
 
-// One CTA lays out the row tiles and counts their key tiles.
 constexpr int kPlanThreads = 1024;
 __device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
   // inclusive, of one value per thread
@@ -160,18 +156,32 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return v;
 }
 
-// Tokens of group g: [x, y), within [0, T), none if the metadata is out of order.
+// Tokens of group g: [x, y), none if it has no requests.
 __device__ __forceinline__ int2 group_tokens(const PrefixParams& p, int g) {
   const int a = group_begin(p, g), b = group_begin(p, g + 1);
   if (b <= a) return make_int2(0, 0);
   return make_int2(__ldg(p.cu_q_lens + a), __ldg(p.cu_q_lens + b));
 }
 
+// One CTA lays out the row tiles, counts their key tiles, a warp per row tile and
+// a lane per request, and deals them out. The requests' offsets and lengths are
+// read many times: they wait in shared memory, if they fit.
+constexpr int kPlanRequests = 4096;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
   __shared__ long long warp_sums[32];
-  const int tid = threadIdx.x;
+  __shared__ int32_t s_cu_q[kPlanRequests + 1], s_seq[kPlanRequests];
+  const int tid = threadIdx.x, lane = lane_id();
+  const int32_t *cu_q = p.cu_q_lens, *seq = p.seq_lens;
+  if (p.S <= kPlanRequests) {
+    for (int i = tid; i <= p.S; i += kPlanThreads) {
+      s_cu_q[i] = __ldg(p.cu_q_lens + i);
+      if (i < p.S) s_seq[i] = __ldg(p.seq_lens + i);
+    }
+    cu_q = s_cu_q;
+    seq = s_seq;
+  }
   long long total;
   int bad = 0;
   long long tiles = 0;
@@ -198,62 +208,71 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   }
   if (tiles > p.max_tiles) bad = 1;
   const int ntiles = (int)min(tiles, (long long)p.max_tiles);
-  if (tid == 0) p.tile_base[p.G] = *p.num_tiles = ntiles;
+  if (tid == 0) p.tile_base[p.G] = ntiles;
+  __syncthreads();
+  for (int i = warp_id(); i < ntiles; i += kPlanThreads / 32) {
+    int lo = 0, hi = p.G - 1;  // the group with tile_base[g] <= i < tile_base[g + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.tile_base[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    const int2 t = group_tokens(p, lo);
+    const int first = t.x * p.H + (i - p.tile_base[lo]) * kTileRows, rows = min(kTileRows, t.y * p.H - first);
+    const int ta = first / p.H, tb = (first + rows - 1) / p.H, prefix = group_prefix(p, lo);
+    int s0 = 0, top = p.S;  // the request of token ta
+    while (top - s0 > 1) {
+      const int mid = (s0 + top) >> 1;
+      if (cu_q[mid] <= ta) s0 = mid;
+      else top = mid;
+    }
+    int n = 0;
+    for (int b = s0; b < p.S; b += 32) {
+      const int s = b + lane;
+      const bool in = s < p.S && cu_q[s] <= tb;
+      if (in) n += own_keys(p, cu_q[s], cu_q[s + 1], seq[s], tb, prefix).tiles();
+      if (!__all_sync(0xffffffffu, in)) break;
+    }
+    n = __reduce_add_sync(0xffffffffu, n) + (prefix + kKeys - 1) / kKeys;
+    if (lane == 0) {
+      p.unit_base[i] = max(n, 1);  // rows without any key still have an output
+      PrefixTile r{};
+      r.row0 = first;
+      r.rows = rows;
+      r.s0 = s0;
+      r.last = tb;
+      r.prefix = prefix;
+      r.page_base = __ldg(p.cu_kv_lens + group_begin(p, lo)) / p.ps;
+      p.tiles[i] = r;
+    }
+  }
   __syncthreads();
   long long units = 0;
   for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    long long n = 0;
-    if (i < ntiles) {
-      int lo = 0, hi = p.G - 1;  // the group with tile_base[g] <= i < tile_base[g + 1]
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.tile_base[mid] <= i) lo = mid;
-        else hi = mid - 1;
-      }
-      const int2 t = group_tokens(p, lo);
-      const int first = t.x * p.H + (i - p.tile_base[lo]) * kTileRows, rows = min(kTileRows, t.y * p.H - first);
-      const int ta = first / p.H, tb = (first + rows - 1) / p.H, prefix = group_prefix(p, lo);
-      const int s0 = seq_of_token(p.cu_q_lens, p.S, ta);
-      n = (prefix + kKeys - 1) / kKeys;
-      for (int s = s0; s < p.S && __ldg(p.cu_q_lens + s) <= tb; ++s) n += own_keys(p, s, tb, prefix).tiles();
-      n = max(n, 1LL);  // rows without any key still have an output
-      p.tiles[i] = make_int4(first, rows, lo, s0);
-    }
-    const long long end = block_scan(n, warp_sums, total);
+    const long long n = i < ntiles ? p.unit_base[i] : 0, end = block_scan(n, warp_sums, total);
     if (i < ntiles) p.unit_base[i] = units + end - n;
     units += total;
   }
   if (tid == 0) p.unit_base[ntiles] = units;
-  if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
-}
-
-// The units (key tiles of row tiles) and the shares they are dealt in.
-struct Shares {
-  long long units;
-  int n;
-  __device__ __forceinline__ long long begin(int k) const { return units * k / n; }
-  __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * n - 1) / units); }
-};
-__device__ __forceinline__ Shares make_shares(const PrefixParams& p) {
-  Shares s;
-  s.units = p.unit_base[*p.num_tiles];
-  s.n = (int)min((long long)p.shares, s.units);
-  return s;
-}
-// The list (of a row tile) that holds unit u: units [begin, end).
-struct List {
-  int tile;
-  long long begin, end;
-};
-__device__ __forceinline__ List list_of(const PrefixParams& p, long long u) {
-  int lo = 0, hi = *p.num_tiles - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.unit_base[mid] <= u) lo = mid;
-    else hi = mid - 1;
+  __syncthreads();
+  const int n = (int)min((long long)p.shares, units);
+  for (int k = tid; k <= p.shares; k += kPlanThreads) {
+    PrefixShare r{};
+    if (k < n) {
+      r.begin = units * k / n;
+      r.end = units * (k + 1) / n;
+      int lo = 0, hi = ntiles - 1;  // the tile that holds unit `begin`
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.unit_base[mid] <= r.begin) lo = mid;
+        else hi = mid - 1;
+      }
+      r.tile = lo;
+    }
+    p.share[k] = r;
   }
-  return {lo, p.unit_base[lo], p.unit_base[lo + 1]};
+  if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
 }
 
 // The key tiles of a list from tile k on, resolved by one whole warp.
@@ -263,24 +282,24 @@ struct KeyCursor {
   int pos, end, left, page_base, lg;
   int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
 
-  __device__ __forceinline__ void open(int sg, int first, int stop, int tiles, int request) {
+  __device__ __forceinline__ void open(int sg, int first, int stop, int tiles, int base) {
     seg = sg;
     pos = first;
     end = stop;
     left = tiles;
-    page_base = __ldg(p->cu_kv_lens + request) >> lg;
+    page_base = base;
     win = -64;
   }
-  __device__ void init(const PrefixParams& prm, const int4 tile, int k) {
+  __device__ void init(const PrefixParams& prm, const PrefixTile& tile, int k) {
     p = &prm;
     lg = 31 - __clz(prm.ps);
-    prefix = group_prefix(prm, tile.z);
-    last = (tile.x + tile.y - 1) / prm.H;
-    s = tile.w;
+    prefix = tile.prefix;
+    last = tile.last;
+    s = tile.s0;
     left = 0;
     const int np = (prefix + kKeys - 1) / kKeys;
     if (k < np) {
-      open(-1, k * kKeys, prefix, np - k, group_begin(prm, tile.z));
+      open(-1, k * kKeys, prefix, np - k, tile.page_base);
     } else {
       next_request(k - np);
     }
@@ -288,10 +307,10 @@ struct KeyCursor {
   // the request that holds own tile k, counted from request s on
   __device__ void next_request(int k) {
     for (; s < p->S && __ldg(p->cu_q_lens + s) <= last; ++s) {
-      const Own w = own_keys(*p, s, last, prefix);
+      const Own w = own_keys(*p, __ldg(p->cu_q_lens + s), __ldg(p->cu_q_lens + s + 1), __ldg(p->seq_lens + s), last, prefix);
       const int n = w.tiles();
       if (k < n) {
-        open(s, w.start + k * kKeys, w.end, n - k, s);
+        open(s, w.start + k * kKeys, w.end, n - k, __ldg(p->cu_kv_lens + s) >> lg);
         ++s;
         return;
       }
@@ -374,7 +393,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(br.pother(), 2);
     mbar_init(br.qready(), 2 * kSoftWarps);
     mbar_init(br.qbar(), 1);
-    mbar_init(br.qmoved(), kSoftWarps);
     mbar_init(br.ppeer(), 1);
     mbar_init(br.lbar(), kSoftWarps);
     for (int w = 0; w < 4; ++w) {
@@ -394,7 +412,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   griddep_wait();
   const uint32_t tmem = *tmem_slot;
-  const Shares shares = make_shares(prm);
+  const PrefixShare work = prm.share[share];
   auto leader = [&](uint64_t* bar) { return cluster_addr(smem_u32(bar), rank & 2); };  // of the pair
   auto other = [&](uint32_t a) { return cluster_addr(a, rank ^ 2); };  // CTA (1 - c, r)
   // a role that gives up tells all CTAs
@@ -405,17 +423,16 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   // every role counts what it has passed since the kernel began: a barrier's
   // phase is that number's parity
   uint32_t tc = 0, uc = 0, fc = 0;  // key tiles, lists, stages
-  const long long u_end = share < shares.n ? shares.begin(share + 1) : 0;
-  long long u = share < shares.n ? shares.begin(share) : 0;
+  int ti = work.tile;
 #pragma unroll 1
-  while (u < u_end) {
-    const List list = list_of(prm, u);
-    const int4 tile = prm.tiles[list.tile];
-    const int k0 = (int)(u - list.begin), n = (int)(min(u_end, list.end) - u);
-    const bool whole = k0 == 0 && u + n == list.end;
-    const int slot_out = u == shares.begin(share) ? 2 * share : 2 * share + 1;
-    const int row0 = tile.x + r * kRows;              // this CTA's first row of [T * H]
-    const int rows = min(kRows, tile.y - r * kRows);  // <= 0: none
+  for (long long u = work.begin; u < work.end; ++ti) {
+    const PrefixTile tile = prm.tiles[ti];
+    const long long list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
+    const int k0 = (int)(u - list0), n = (int)(min(work.end, list1) - u);
+    const bool whole = k0 == 0 && u + n == list1;
+    const int slot_out = u == work.begin ? 2 * share : 2 * share + 1;
+    const int row0 = tile.row0 + r * kRows;              // this CTA's first row of [T * H]
+    const int rows = min(kRows, tile.rows - r * kRows);  // <= 0: none
     if (warp == 0) {
       // -------------------------------------------------------- MMA issuer
       if (r == 0) {
@@ -444,27 +461,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             // S is free once the tile before has been read into registers
             if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
             tc_fence_after();
+            // queries in TMEM and in shared memory by turns: the latter's reads and
+            // the copies into shared memory together are near its bandwidth
 #pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < kKStages; ++j) {
               if (!(ok = arrived())) break;
-              const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4));
+              const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4)), qb = dq + (uint64_t)(j * (kQBlk >> 4));
+              if (j < 4) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + j * 64 + k * 8,
-                                  kb + (k >> 2) * (kBlk >> 4) + (k & 3) * 2, kIdescQK, j || k ? 1u : 0u);
-              pass();
-            }
-            if (!ok) break;
-#pragma unroll 1
-            for (int j = 4; j < 9; j += 2) {  // K blocks j and, but for the last, j + 1
-              if (!(ok = arrived())) break;
-              const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4)), qb = dq + (uint64_t)((j - 4) * (kQBlk >> 4));
+                for (int k = 0; k < 4; ++k) {
+                  umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + j * 32 + k * 8, kb + k * 2, kIdescQK, j || k ? 1u : 0u);
+                  umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + (kBlk >> 4) + k * 2, kIdescQK, 1u);
+                }
+              } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + k * 2, kIdescQK, 1u);
-              if (j < 8) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_pair_ss_lead(lead, tm + kColS, qb + (kQBlk >> 4) + k * 2, kb + (kBlk >> 4) + k * 2, kIdescQK, 1u);
+                for (int k = 0; k < 4; ++k) umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + k * 2, kIdescQK, 1u);
               }
               pass();
             }
@@ -502,20 +513,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
 #pragma unroll 1
         for (int b = 0; b < 9; ++b)
-          tma_load_2d(smem + (b < 4 ? OFF_RING + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
+          tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
       }
       KeyCursor cur;
       cur.init(prm, tile, k0);
       const bool two = prm.ps == 32;
       uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
-      // a stage of two blocks of 64 keys, from dim d0 on (one: only the first)
-      auto load = [&](int d0, int r0, int r1, bool one) -> bool {
+      // a stage of two blocks of 64 keys, dims d0 .. and d1 .. (one: only the first)
+      auto load = [&](int d0, int d1, int r0, int r1, bool one) -> bool {
         if (!mbar_wait_warp(br.empty(slot), phase ^ 1, abort_flag)) return false;
         if (lane == 0) {
           const uint32_t bar = leader(br.full(slot)), dst = smem0 + OFF_RING + slot * kStage;
           if (r == 0) mbar_arrive_expect_tx(br.full(slot), one ? kStage : 2 * kStage);
           copy_block(dst, &kvmap, bar, d0, r0, r1, two);
-          if (!one) copy_block(dst + kBlk, &kvmap, bar, d0 + 64, r0, r1, two);
+          if (!one) copy_block(dst + kBlk, &kvmap, bar, d1, r0, r1, two);
         }
         __syncwarp();
         if (++slot == kStages) slot = 0, phase ^= 1;
@@ -535,21 +546,20 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           ++tc;
-          // the queries for TMEM have left the ring
-          if (i == 0 && !(ok = mbar_wait_warp(br.qmoved(), uc & 1, abort_flag))) break;
           const int g = 4 * c + 2 * r;  // this CTA's 64 keys
           int r0 = t.row[0], r1 = t.row[1];
 #pragma unroll
           for (int h = 2; h < kRuns; h += 2)
             if (h == g) r0 = t.row[h], r1 = t.row[h + 1];
 #pragma unroll 1
-          for (int j = 0; ok && j < kKStages; ++j) ok = load(j * 128, r0, r1, j == kKStages - 1);
+          for (int j = 0; ok && j < kKStages; ++j)
+            ok = j < 4 ? load(j * 64, 256 + j * 64, r0, r1, false) : load(512, 0, r0, r1, true);
           if (!ok) break;
         }
         if (i > 0) {
 #pragma unroll
           for (int s = 0; s < kVStages; ++s)
-            ok = ok && load(c * 256 + r * 128, c ? before.row[(2 * s + 4) & 7] : before.row[2 * s],
+            ok = ok && load(c * 256 + r * 128, c * 256 + r * 128 + 64, c ? before.row[(2 * s + 4) & 7] : before.row[2 * s],
                             c ? before.row[(2 * s + 5) & 7] : before.row[2 * s + 1], false);
         }
         before = t;
@@ -575,11 +585,31 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
       // this warp's part of P, 32 rows x 64 keys, here and at the other half
       const uint32_t p_blk = smem0 + OFF_P + (2 * c + hh) * kQBlk, p_run = p_blk + q * 32 * 128;
+      // this row's request and visible positions
+      int my_s = -2, see = 0;
+      const int prefix = tile.prefix;
+      if (row < rows) {
+        const int t = (row0 + row) / prm.H;
+        int s = tile.s0, top = prm.S;  // cu_q_lens[s] <= t < cu_q_lens[top]
+        for (int step = 1; s + step < top; step *= 2) {
+          if (__ldg(prm.cu_q_lens + s + step) > t) top = s + step;
+          else s += step;
+        }
+        while (top - s > 1) {
+          const int mid = (s + top) >> 1;
+          if (__ldg(prm.cu_q_lens + mid) > t) top = mid;
+          else s = mid;
+        }
+        const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, prm.max_kv, t,
+                                       prm.dev_status, s);
+        my_s = s;
+        see = g.n_vis;
+      }
       bool ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
       if (ok) {
 #pragma unroll 1
         for (int b = 2 * hh; b < 2 * hh + 2; ++b) {
-          const uint8_t* src = smem + OFF_RING + b * kQBlk + row * 128;
+          const uint8_t* src = smem + OFF_P + b * kQBlk + row * 128;
           uint32_t v[32];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -593,25 +623,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        fence_proxy_async_smem();  // the ring is written by copies again
+        // The other half's copies of P write here next: of these 32 rows, after it
+        // has had this warp's maxima of the first tile.
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(br.qmoved());
-          mbar_arrive_cluster(leader(br.qready()));
-        }
+        if (lane == 0) mbar_arrive_cluster(leader(br.qready()));
         __syncwarp();
-      }
-      // this row's request and visible positions
-      int my_s = -2, see = 0;
-      const int prefix = group_prefix(prm, tile.z);
-      if (row < rows) {
-        const int t = (row0 + row) / prm.H;
-        int s = tile.w;
-        while (s + 1 < prm.S && __ldg(prm.cu_q_lens + s + 1) <= t) ++s;
-        const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, prm.max_kv, t,
-                                       prm.dev_status, s);
-        my_s = s;
-        see = g.n_vis;
       }
       const float sl2 = prm.scale_log2;
       float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's columns
@@ -840,18 +857,18 @@ constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const Shares sh = make_shares(p);
   const int x = blockIdx.x, lane = lane_id();
-  if (x + 1 >= sh.n) return;
-  const long long u = sh.begin(x + 1);
-  const List l = list_of(p, u);
-  if (l.begin == u) return;  // the share ends with a list
-  const int k0 = sh.of(l.begin), k1 = sh.of(l.end - 1);
-  if (k0 != x) return;
-  const int4 tile = p.tiles[l.tile];
+  const PrefixShare cut = p.share[x + 1];
+  if (cut.end == cut.begin) return;
+  const long long begin = p.unit_base[cut.tile], end = p.unit_base[cut.tile + 1];
+  if (begin == cut.begin || p.share[x].begin > begin) return;  // nothing is cut, or an earlier share's end cuts it first
+  const PrefixTile tile = p.tiles[cut.tile];
   const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1;
-  if (r >= tile.y) return;
-  auto row_of = [&](int k) { return ((size_t)(sh.begin(k) >= l.begin ? 2 * k : 2 * k + 1)) * kTileRows + r; };
+  if (r >= tile.rows) return;
+  const int k0 = x;
+  int k1 = x + 1;
+  while (p.share[k1].end < end) ++k1;
+  auto row_of = [&](int k) { return ((size_t)(p.share[k].begin >= begin ? 2 * k : 2 * k + 1)) * kTileRows + r; };
   float mx = -INFINITY, tot = 0.f;
   for (int k = k0 + lane; k <= k1; k += 32) mx = fmaxf(mx, p.part_lse[row_of(k)]);
   mx = warp_max_f32(mx);
@@ -878,14 +895,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
       acc[h].w = fmaf(wt, y.w, acc[h].w);
     }
   }
-  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.x + r) * kDv + half * 256);
+  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.row0 + r) * kDv + half * 256);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc[h].x, acc[h].y), hi = __floats2bfloat162_rn(acc[h].z, acc[h].w);
     dst[32 * h + lane] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
   }
   if (half == 0 && lane == 0 && p.lse)
-    p.lse[(size_t)tile.x + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
+    p.lse[(size_t)tile.row0 + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
 }
 
 int max_tiles_of(int T, int H, int G) { return (int)(((long long)T * H + kTileRows - 1) / kTileRows) + G; }
@@ -917,7 +934,7 @@ int clusters_at_once() {
   return n;
 }
 struct Layout {
-  size_t tile_base, tiles, unit_base, num_tiles, part_o, part_lse, bytes;
+  size_t tile_base, tiles, unit_base, share, part_o, part_lse, bytes;
 };
 Layout layout_of(int T, int H, int G) {
   const size_t nt = (size_t)max_tiles_of(T, H, G), slots = 2 * (size_t)max_shares();
@@ -929,9 +946,9 @@ Layout layout_of(int T, int H, int G) {
     return here;
   };
   l.tile_base = take(((size_t)G + 1) * 4);
-  l.tiles = take(nt * 16);
+  l.tiles = take(nt * sizeof(PrefixTile));
   l.unit_base = take((nt + 1) * 8);
-  l.num_tiles = take(4);
+  l.share = take((slots / 2 + 1) * sizeof(PrefixShare));
   l.part_lse = take(slots * kTileRows * 4);
   l.part_o = take(slots * kTileRows * kDv * 4);
   l.bytes = at;
@@ -945,9 +962,9 @@ int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
   const Layout l = layout_of(prm.T, prm.H, prm.G);
   uint8_t* w = static_cast<uint8_t*>(ws);
   prm.tile_base = reinterpret_cast<int32_t*>(w + l.tile_base);
-  prm.tiles = reinterpret_cast<int4*>(w + l.tiles);
+  prm.tiles = reinterpret_cast<PrefixTile*>(w + l.tiles);
   prm.unit_base = reinterpret_cast<long long*>(w + l.unit_base);
-  prm.num_tiles = reinterpret_cast<int*>(w + l.num_tiles);
+  prm.share = reinterpret_cast<PrefixShare*>(w + l.share);
   prm.part_o = reinterpret_cast<float*>(w + l.part_o);
   prm.part_lse = reinterpret_cast<float*>(w + l.part_lse);
   prm.max_tiles = max_tiles_of(prm.T, prm.H, prm.G);

@@ -9,6 +9,20 @@ namespace dsa {
 constexpr long long kPrefixMaxRows = (1LL << 31) - (1 << 16);  // T * H: a tile ends past them
 constexpr int kPrefixMaxGroups = 1 << 20;
 
+// A row tile: 256 rows or fewer of one group.
+struct alignas(16) PrefixTile {
+  int row0, rows;      // of [T * H]
+  int s0, last;        // first request, last token
+  int prefix;          // positions read through the group's first request
+  int page_base;       // and where its page-table entries start
+  int pad[2];
+};
+// What a cluster works on: units [begin, end), from row tile `tile` on.
+struct alignas(16) PrefixShare {
+  long long begin, end;
+  int tile, pad[3];
+};
+
 struct PrefixParams {
   const uint16_t* q;   // bf16 [T, H, 576]
   const uint16_t* kv;  // bf16 [P, ps, row_stride]
@@ -25,10 +39,10 @@ struct PrefixParams {
   float* lse;        // [T, H] or null
   int32_t* dev_status;
   // workspace (set by run_prefix_mla)
-  int32_t* tile_base;  // [G + 1] tiles of the groups before
-  int4* tiles;         // first row, rows, group, first request
+  int32_t* tile_base;    // [G + 1] tiles of the groups before
+  PrefixTile* tiles;
   long long* unit_base;  // [tiles + 1] key tiles of the tiles before
-  int* num_tiles;
+  PrefixShare* share;    // [shares + 1], those past the work empty
   float* part_o;    // [2 * shares][256][512]
   float* part_lse;  // [2 * shares][256], log2
   int max_tiles, shares;
