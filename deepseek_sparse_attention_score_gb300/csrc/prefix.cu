@@ -20,8 +20,8 @@
 // workspace (at most two per cluster) and a second kernel merges them, in order,
 // so outputs are the same on every run.
 //
-// Roles of a CTA: warp 0 issues the MMAs (r = 0), warp 1 resolves keys and copies
-// them and the queries, warp 3 passes on that the other half's P has arrived,
+// Roles of a CTA: warp 0 issues the MMAs (r = 0), warp 1 copies queries and keys,
+// warp 2 resolves the keys a few tiles ahead, warp 3 passes on that the other half's P has arrived,
 // warps 4-11 run the softmax, a row and half of its columns of S per thread.
 //
 // Per key tile i: QK^T(i), then PV(i - 1). S is read into registers at once and P
@@ -45,7 +45,7 @@ constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (querie
 // keys whose P this CTA computes
 constexpr int kStages = 5, kStage = 2 * kBlk;
 constexpr int kKStages = 5, kVStages = 4;
-constexpr int kDescs = 2;
+constexpr int kDescs = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = (4 + kSoftWarps) * 32;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
@@ -166,12 +166,17 @@ __device__ __forceinline__ int2 group_tokens(const PrefixParams& p, int g) {
 // One CTA lays out the row tiles, counts their key tiles, a warp per row tile and
 // a lane per request, and deals them out. The requests' offsets and lengths are
 // read many times: they wait in shared memory, if they fit.
-constexpr int kPlanRequests = 4096;
+constexpr int kPlanRequests = 3584;
+constexpr int kPlanTiles = 1024;
+// A list that starts inside a share costs about as much as this many key tiles:
+// the pipeline runs empty, the outputs are written, the next queries fetched.
+constexpr int kListCost = 4;
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
   __shared__ long long warp_sums[32];
   __shared__ int32_t s_cu_q[kPlanRequests + 1], s_seq[kPlanRequests];
+  __shared__ long long s_base[kPlanTiles + 1];  // unit_base, if it fits
   const int tid = threadIdx.x, lane = lane_id();
   const int32_t *cu_q = p.cu_q_lens, *seq = p.seq_lens;
   if (p.S <= kPlanRequests) {
@@ -209,6 +214,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   if (tiles > p.max_tiles) bad = 1;
   const int ntiles = (int)min(tiles, (long long)p.max_tiles);
   if (tid == 0) p.tile_base[p.G] = ntiles;
+  long long* base = ntiles <= kPlanTiles ? s_base : p.unit_base;
   __syncthreads();
   for (int i = warp_id(); i < ntiles; i += kPlanThreads / 32) {
     int lo = 0, hi = p.G - 1;  // the group with tile_base[g] <= i < tile_base[g + 1]
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     }
     n = __reduce_add_sync(0xffffffffu, n) + (prefix + kKeys - 1) / kKeys;
     if (lane == 0) {
-      p.unit_base[i] = max(n, 1);  // rows without any key still have an output
+      base[i] = max(n, 1);  // rows without any key still have an output
       PrefixTile r{};
       r.row0 = first;
       r.rows = rows;
@@ -250,25 +256,35 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   long long units = 0;
   for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const long long n = i < ntiles ? p.unit_base[i] : 0, end = block_scan(n, warp_sums, total);
-    if (i < ntiles) p.unit_base[i] = units + end - n;
+    const long long n = i < ntiles ? base[i] : 0, end = block_scan(n, warp_sums, total);
+    if (i < ntiles) p.unit_base[i] = base[i] = units + end - n;
     units += total;
   }
-  if (tid == 0) p.unit_base[ntiles] = units;
+  if (tid == 0) p.unit_base[ntiles] = base[ntiles] = units;
   __syncthreads();
+  // Shares are equal in units and list starts: between two lists lie `gap` units
+  // of no work. A share holds more than `gap` units, so none is empty.
   const int n = (int)min((long long)p.shares, units);
+  const int gap = n ? (int)min((long long)kListCost, units / n - 1) : 0;
+  const long long all = units + (long long)gap * max(ntiles - 1, 0);
+  // where share k begins, and the tile that holds that unit
+  auto begin = [&](int k, int& tile) -> long long {
+    const long long v = all * k / n;
+    int lo = 0, hi = ntiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] + (long long)gap * (mid - 1) <= v) lo = mid;  // from the gap before it on
+      else hi = mid - 1;
+    }
+    tile = lo;
+    return base[lo] + max(0LL, v - base[lo] - (long long)gap * lo);
+  };
   for (int k = tid; k <= p.shares; k += kPlanThreads) {
     PrefixShare r{};
     if (k < n) {
-      r.begin = units * k / n;
-      r.end = units * (k + 1) / n;
-      int lo = 0, hi = ntiles - 1;  // the tile that holds unit `begin`
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.unit_base[mid] <= r.begin) lo = mid;
-        else hi = mid - 1;
-      }
-      r.tile = lo;
+      int after;
+      r.begin = begin(k, r.tile);
+      r.end = k + 1 < n ? begin(k + 1, after) : units;
     }
     p.share[k] = r;
   }
@@ -385,7 +401,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(br.full(s), 1), mbar_init(br.empty(s), 1);
-    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps);
+    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps + 1);
     mbar_init(br.sfull(), 1);
     mbar_init(br.pvdone(), 2);
     mbar_init(br.sempty(), 2 * kSoftWarps);
@@ -508,15 +524,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) give_up();
       }
     } else if (warp == 1) {
-      // ------------------------------------------- queries and keys
+      // ---------------------------------------------------- queries and keys
       if (lane == 0) {
         mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
 #pragma unroll 1
         for (int b = 0; b < 9; ++b)
           tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
       }
-      KeyCursor cur;
-      cur.init(prm, tile, k0);
       const bool two = prm.ps == 32;
       uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
       // a stage of two blocks of 64 keys, dims d0 .. and d1 .. (one: only the first)
@@ -537,14 +551,11 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; ok && i <= n; ++i) {
         if (i < n) {
-          t = cur.next();
           const int ds = tc % kDescs;
-          if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
-          if (lane == 0) {
-            descs[ds] = t;
-            mbar_arrive(br.dfull(ds));
-          }
+          if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
+          t = descs[ds];
           __syncwarp();
+          if (lane == 0) mbar_arrive(br.dempty(ds));
           ++tc;
           const int g = 4 * c + 2 * r;  // this CTA's 64 keys
           int r0 = t.row[0], r1 = t.row[1];
@@ -563,6 +574,23 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                             c ? before.row[(2 * s + 5) & 7] : before.row[2 * s + 1], false);
         }
         before = t;
+      }
+      if (!ok) give_up();
+    } else if (warp == 2) {
+      // ----------------------------------------------------------- key tiles
+      KeyCursor cur;
+      cur.init(prm, tile, k0);
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, ++tc) {
+        const KeyTile t = cur.next();
+        const int ds = tc % kDescs;
+        if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
+        if (lane == 0) {
+          descs[ds] = t;
+          mbar_arrive(br.dfull(ds));
+        }
+        __syncwarp();
       }
       if (!ok) give_up();
     } else if (warp == 3) {
@@ -869,6 +897,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   int k1 = x + 1;
   while (p.share[k1].end < end) ++k1;
   auto row_of = [&](int k) { return ((size_t)(p.share[k].begin >= begin ? 2 * k : 2 * k + 1)) * kTileRows + r; };
+  // parts four at a time, the first four's rows on their way while the weights
+  // are found
+  float4 y[4][2];
+  auto load = [&](int k) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + row_of(min(k + j, k1)) * kDv + half * 256);
+      y[j][0] = src[lane];
+      y[j][1] = src[32 + lane];
+    }
+  };
+  load(k0);
   float mx = -INFINITY, tot = 0.f;
   for (int k = k0 + lane; k <= k1; k += 32) mx = fmaxf(mx, p.part_lse[row_of(k)]);
   mx = warp_max_f32(mx);
@@ -881,18 +921,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   const bool some = tot != 0.f;
   const float inv = some ? 1.f / tot : 0.f;
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-  for (int k = k0; k <= k1; ++k) {
-    const size_t row = row_of(k);
-    const float v = p.part_lse[row], wt = v == -INFINITY ? 0.f : exp2f(v - mx) * inv;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + row * kDv + half * 256);
+#pragma unroll 1
+  for (int k = k0; k <= k1; k += 4) {
+    if (k > k0) load(k);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 y = src[32 * h + lane];
-      acc[h].x = fmaf(wt, y.x, acc[h].x);
-      acc[h].y = fmaf(wt, y.y, acc[h].y);
-      acc[h].z = fmaf(wt, y.z, acc[h].z);
-      acc[h].w = fmaf(wt, y.w, acc[h].w);
+    for (int j = 0; j < 4; ++j) {
+      if (k + j > k1) break;
+      const float v = p.part_lse[row_of(k + j)], wt = v == -INFINITY ? 0.f : exp2f(v - mx) * inv;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc[h].x = fmaf(wt, y[j][h].x, acc[h].x);
+        acc[h].y = fmaf(wt, y[j][h].y, acc[h].y);
+        acc[h].z = fmaf(wt, y[j][h].z, acc[h].z);
+        acc[h].w = fmaf(wt, y[j][h].w, acc[h].w);
+      }
     }
   }
   uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.row0 + r) * kDv + half * 256);
