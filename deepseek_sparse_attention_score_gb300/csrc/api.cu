@@ -509,6 +509,7 @@ int dsa_prefix_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, i
   if (G > kPrefixMaxGroups || max_kv > (1 << 30) || (long long)T * H >= kPrefixMaxRows) return DSA_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale * 1.4426950408889634f)) return DSA_ERR_INVALID_ARGUMENT;  // the kernel's logit factor
   if (T == 0 || H == 0) return DSA_OK;
+  if (!prefix_units_fit(T, H, G, max_kv)) return DSA_ERR_UNSUPPORTED;
   if (!prefix_lens) return DSA_ERR_INVALID_ARGUMENT;
   if (!ws || ws_bytes < prefix_workspace_bytes(T, H, G)) return DSA_ERR_WORKSPACE;
   if (!aligned16(ws)) return DSA_ERR_ALIGNMENT;

@@ -104,16 +104,6 @@ struct Bars {
 };
 
 // ------------------------------------------------------------- the work list
-__device__ __forceinline__ int request_kv(const PrefixParams& p, int s) {
-  return min(max(__ldg(p.seq_lens + s), 0), p.max_kv);
-}
-__device__ __forceinline__ int group_begin(const PrefixParams& p, int g) {
-  return p.group_offsets ? min(max(__ldg(p.group_offsets + g), 0), p.S) : g ? p.S : 0;
-}
-// Positions that group g (not empty) reads through its first request.
-__device__ __forceinline__ int group_prefix(const PrefixParams& p, int g) {
-  return min(max(__ldg(p.prefix_lens + g), 0), request_kv(p, min(group_begin(p, g), p.S - 1)));
-}
 // Request s's own keys for rows of tokens up to `last`: from position `start`
 // (a page's first) to `end`.
 struct Own {
@@ -129,54 +119,43 @@ __device__ __forceinline__ Own own_keys(const PrefixParams& p, int q0, int q1, i
   return w;
 }
 
-constexpr int kPlanThreads = 1024;
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& total) {
+constexpr int kPlanThreads = 512;
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   // inclusive, of one value per thread
   const int lane = lane_id(), w = warp_id();
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, v, d);
+    const int y = __shfl_up_sync(0xffffffffu, v, d);
     if (lane >= d) v += y;
   }
   if (lane == 31) warp_sums[w] = v;
   __syncthreads();
-  if (w == 0) {
-    long long x = warp_sums[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
-    }
-    warp_sums[lane] = x;
-  }
-  __syncthreads();
-  if (w) v += warp_sums[w - 1];
-  total = warp_sums[31];
+  int x = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, x);
+  v += __reduce_add_sync(0xffffffffu, lane < w ? x : 0);
   __syncthreads();
   return v;
 }
 
-// Tokens of group g: [x, y), none if it has no requests.
-__device__ __forceinline__ int2 group_tokens(const PrefixParams& p, int g) {
-  const int a = group_begin(p, g), b = group_begin(p, g + 1);
-  if (b <= a) return make_int2(0, 0);
-  return make_int2(__ldg(p.cu_q_lens + a), __ldg(p.cu_q_lens + b));
-}
-
 // One CTA lays out the row tiles, counts their key tiles, a warp per row tile and
-// a lane per request, and deals them out. The requests' offsets and lengths are
-// read many times: they wait in shared memory, if they fit.
-constexpr int kPlanRequests = 3584;
-constexpr int kPlanTiles = 1024;
+// a lane per request, and deals them out. What is read many times, or by other
+// threads than wrote it, waits in shared memory, if it fits.
+constexpr int kPlanRequests = 3072, kPlanGroups = 512, kPlanTiles = 1024;
 // A list that starts inside a share costs about as much as this many key tiles:
 // the pipeline runs empty, the outputs are written, the next queries fetched.
 constexpr int kListCost = 4;
+constexpr int kMaxShares = 128;
+struct PlanGroup {
+  int first_tile, token0, token1, prefix, page_base;
+};
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ long long warp_sums[32];
+  __shared__ int warp_sums[kPlanThreads / 32];
   __shared__ int32_t s_cu_q[kPlanRequests + 1], s_seq[kPlanRequests];
-  __shared__ long long s_base[kPlanTiles + 1];  // unit_base, if it fits
+  __shared__ PlanGroup s_group[kPlanGroups];
+  __shared__ int s_cost[kListCost + 1], s_begin[kListCost + 1][kMaxShares + 1], s_tile[kListCost + 1][kMaxShares + 1];
+  __shared__ int s_base[kPlanTiles + 1];  // unit_base
   const int tid = threadIdx.x, lane = lane_id();
   const int32_t *cu_q = p.cu_q_lens, *seq = p.seq_lens;
   if (p.S <= kPlanRequests) {
@@ -187,45 +166,72 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     cu_q = s_cu_q;
     seq = s_seq;
   }
-  long long total;
+  if (tid <= kListCost) s_cost[tid] = 0;
   int bad = 0;
-  long long tiles = 0;
+  // a group's requests [x, y) as they are given, and checked
+  auto requests = [&](int g, bool& ok) -> int2 {
+    const int a = p.group_offsets ? __ldg(p.group_offsets + g) : 0;
+    const int b = p.group_offsets ? __ldg(p.group_offsets + g + 1) : p.S;
+    ok = a >= 0 && b >= a && b <= p.S && (g > 0 || a == 0);
+    return ok ? make_int2(a, b) : make_int2(0, 0);
+  };
+  auto group_of = [&](int g, bool& ok) -> PlanGroup {
+    const int2 r = requests(g, ok);
+    PlanGroup x{0, 0, 0, 0, 0};
+    if (r.y > r.x) {
+      const int page_base = __ldg(p.cu_kv_lens + r.x) / p.ps, want = __ldg(p.prefix_lens + g);
+      x.page_base = page_base;
+      x.token0 = cu_q[r.x];
+      x.token1 = cu_q[r.y];
+      x.prefix = min(max(want, 0), min(max(seq[r.x], 0), p.max_kv));
+      ok = x.token0 >= 0 && x.token1 >= x.token0 && x.token1 <= p.T;
+      if (!ok) x.token1 = x.token0 = 0;
+      if (want != x.prefix) bad = 1;
+    }
+    return x;
+  };
+  __syncthreads();
+  int total, tiles = 0;
   for (int g0 = 0; g0 < p.G; g0 += kPlanThreads) {
     const int g = g0 + tid;
-    long long n = 0;
+    int n = 0;
+    PlanGroup x{};
     if (g < p.G) {
-      const int2 t = group_tokens(p, g);
-      const int raw0 = p.group_offsets ? __ldg(p.group_offsets + g) : 0;
-      const int raw1 = p.group_offsets ? __ldg(p.group_offsets + g + 1) : p.S;
-      bool ok = raw0 >= 0 && raw1 >= raw0 && raw1 <= p.S && t.x >= 0 && t.y >= t.x && t.y <= p.T;
-      if (g == 0 && raw0 != 0) ok = false;
-      if (g == p.G - 1 && raw1 != p.S) bad = 1;  // requests behind the last group: no rows of theirs are written
-      if (ok) n = ((long long)(t.y - t.x) * p.H + kTileRows - 1) / kTileRows;
-      else bad = 1;
-      if (ok && raw1 > raw0) {
-        const int want = __ldg(p.prefix_lens + g);
-        if (want < 0 || want != group_prefix(p, g)) bad = 1;
-      }
+      bool ok;
+      x = group_of(g, ok);
+      // requests behind the last group: no rows of theirs are written
+      if (!ok || (g == p.G - 1 && p.group_offsets && __ldg(p.group_offsets + p.G) != p.S)) bad = 1;
+      n = ((x.token1 - x.token0) * p.H + kTileRows - 1) / kTileRows;
     }
-    const long long end = block_scan(n, warp_sums, total);
-    if (g < p.G) p.tile_base[g] = (int)min(tiles + end - n, (long long)p.max_tiles);
+    const int end = block_scan(n, warp_sums, total);
+    if (g < p.G) {
+      x.first_tile = min(tiles + end - n, p.max_tiles);
+      if (p.G <= kPlanGroups) s_group[g] = x;
+      else p.tile_base[g] = x.first_tile;
+    }
     tiles += total;
   }
   if (tiles > p.max_tiles) bad = 1;
-  const int ntiles = (int)min(tiles, (long long)p.max_tiles);
-  if (tid == 0) p.tile_base[p.G] = ntiles;
-  long long* base = ntiles <= kPlanTiles ? s_base : p.unit_base;
+  const int ntiles = min(tiles, p.max_tiles);
+  int* base = ntiles <= kPlanTiles ? s_base : p.unit_base;
   __syncthreads();
   for (int i = warp_id(); i < ntiles; i += kPlanThreads / 32) {
-    int lo = 0, hi = p.G - 1;  // the group with tile_base[g] <= i < tile_base[g + 1]
+    int lo = 0, hi = p.G - 1;  // the group with first_tile <= i, the last such one: not empty
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (p.tile_base[mid] <= i) lo = mid;
+      if ((p.G <= kPlanGroups ? s_group[mid].first_tile : p.tile_base[mid]) <= i) lo = mid;
       else hi = mid - 1;
     }
-    const int2 t = group_tokens(p, lo);
-    const int first = t.x * p.H + (i - p.tile_base[lo]) * kTileRows, rows = min(kTileRows, t.y * p.H - first);
-    const int ta = first / p.H, tb = (first + rows - 1) / p.H, prefix = group_prefix(p, lo);
+    PlanGroup x;
+    if (p.G <= kPlanGroups) {
+      x = s_group[lo];
+    } else {
+      bool ok;
+      x = group_of(lo, ok);
+      x.first_tile = p.tile_base[lo];
+    }
+    const int first = x.token0 * p.H + (i - x.first_tile) * kTileRows, rows = min(kTileRows, x.token1 * p.H - first);
+    const int ta = first / p.H, tb = (first + rows - 1) / p.H;
     int s0 = 0, top = p.S;  // the request of token ta
     while (top - s0 > 1) {
       const int mid = (s0 + top) >> 1;
@@ -236,10 +242,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     for (int b = s0; b < p.S; b += 32) {
       const int s = b + lane;
       const bool in = s < p.S && cu_q[s] <= tb;
-      if (in) n += own_keys(p, cu_q[s], cu_q[s + 1], seq[s], tb, prefix).tiles();
+      if (in) n += own_keys(p, cu_q[s], cu_q[s + 1], seq[s], tb, x.prefix).tiles();
       if (!__all_sync(0xffffffffu, in)) break;
     }
-    n = __reduce_add_sync(0xffffffffu, n) + (prefix + kKeys - 1) / kKeys;
+    n = __reduce_add_sync(0xffffffffu, n) + (x.prefix + kKeys - 1) / kKeys;
     if (lane == 0) {
       base[i] = max(n, 1);  // rows without any key still have an output
       PrefixTile r{};
@@ -247,44 +253,61 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       r.rows = rows;
       r.s0 = s0;
       r.last = tb;
-      r.prefix = prefix;
-      r.page_base = __ldg(p.cu_kv_lens + group_begin(p, lo)) / p.ps;
+      r.prefix = x.prefix;
+      r.page_base = x.page_base;
       p.tiles[i] = r;
     }
   }
   __syncthreads();
-  long long units = 0;
+  int units = 0;
   for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    const long long n = i < ntiles ? base[i] : 0, end = block_scan(n, warp_sums, total);
+    const int n = i < ntiles ? base[i] : 0, end = block_scan(n, warp_sums, total);
     if (i < ntiles) p.unit_base[i] = base[i] = units + end - n;
     units += total;
   }
   if (tid == 0) p.unit_base[ntiles] = base[ntiles] = units;
   __syncthreads();
-  // Shares are equal in units and list starts: between two lists lie `gap` units
-  // of no work. A share holds more than `gap` units, so none is empty.
-  const int n = (int)min((long long)p.shares, units);
-  const int gap = n ? (int)min((long long)kListCost, units / n - 1) : 0;
-  const long long all = units + (long long)gap * max(ntiles - 1, 0);
-  // where share k begins, and the tile that holds that unit
-  auto begin = [&](int k, int& tile) -> long long {
-    const long long v = all * k / n;
-    int lo = 0, hi = ntiles - 1;
+  // The shares are equal runs of the lists with `gap` units of no work between
+  // two of them, so that a share in which a list starts has less work; of the
+  // gaps up to the cost of a start, the one with which the costliest share costs
+  // least. A share is longer than the gap, so none is empty.
+  const int n = min(p.shares, units), gaps = n ? min(kListCost, units / n - 1) + 1 : 0;
+  for (int j = tid; j < gaps * (n + 1); j += kPlanThreads) {
+    const int gap = j / (n + 1), k = j % (n + 1), all = units + gap * (ntiles - 1);
+    const int v = all / n * k + all % n * k / n;  // all * k / n
+    int lo = 0, hi = ntiles - 1;                  // the tile that holds v, from the gap before it on
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (base[mid] + (long long)gap * (mid - 1) <= v) lo = mid;  // from the gap before it on
+      if (base[mid] + gap * (mid - 1) <= v) lo = mid;
       else hi = mid - 1;
     }
-    tile = lo;
-    return base[lo] + max(0LL, v - base[lo] - (long long)gap * lo);
-  };
-  for (int k = tid; k <= p.shares; k += kPlanThreads) {
+    s_begin[gap][k] = k < n ? base[lo] + max(0, v - base[lo] - gap * lo) : units;
+    s_tile[gap][k] = k < n ? lo : ntiles;
+  }
+  __syncthreads();
+  for (int j = tid; j < gaps * n; j += kPlanThreads) {
+    const int gap = j / n, k = j % n, e = s_begin[gap][k + 1], t = s_tile[gap][k + 1];
+    const int starts = (e == base[t] ? t - 1 : t) - s_tile[gap][k];  // lists that start behind the share's begin
+    atomicMax(s_cost + gap, e - s_begin[gap][k] + kListCost * starts);
+  }
+  __syncthreads();
+  int gap = 0;
+  for (int j = 1; j < gaps; ++j) gap = s_cost[j] < s_cost[gap] ? j : gap;
+  for (int k = tid; k < p.shares; k += kPlanThreads) {
     PrefixShare r{};
+    r.cut = -1;
     if (k < n) {
-      int after;
-      r.begin = begin(k, r.tile);
-      r.end = k + 1 < n ? begin(k + 1, after) : units;
+      const int *sb = s_begin[gap], next = s_tile[gap][k + 1];
+      r.begin = sb[k];
+      r.end = sb[k + 1];
+      r.tile = s_tile[gap][k];
+      if (base[next] < r.end && r.begin <= base[next]) {
+        r.cut = next;
+        r.first_slot = r.begin == base[next] ? 2 * k : 2 * k + 1;
+        r.last = k + 1;  // the last share that begins inside the list
+        while (r.last + 1 < n && sb[r.last + 1] < base[next + 1]) ++r.last;
+      }
     }
     p.share[k] = r;
   }
@@ -441,10 +464,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t tc = 0, uc = 0, fc = 0;  // key tiles, lists, stages
   int ti = work.tile;
 #pragma unroll 1
-  for (long long u = work.begin; u < work.end; ++ti) {
+  for (int u = work.begin; u < work.end; ++ti) {
     const PrefixTile tile = prm.tiles[ti];
-    const long long list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
-    const int k0 = (int)(u - list0), n = (int)(min(work.end, list1) - u);
+    const int list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
+    const int k0 = u - list0, n = min(work.end, list1) - u;
     const bool whole = k0 == 0 && u + n == list1;
     const int slot_out = u == work.begin ? 2 * share : 2 * share + 1;
     const int row0 = tile.row0 + r * kRows;              // this CTA's first row of [T * H]
@@ -879,24 +902,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// Merges a list that was divided: block x looks at the end of share x and takes
-// the list that it cuts, if it is the first to; a warp takes half a row.
+// Merges a list that was divided: block x takes the one that the end of share x
+// is the first to cut; a warp takes half a row.
 constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int x = blockIdx.x, lane = lane_id();
-  const PrefixShare cut = p.share[x + 1];
-  if (cut.end == cut.begin) return;
-  const long long begin = p.unit_base[cut.tile], end = p.unit_base[cut.tile + 1];
-  if (begin == cut.begin || p.share[x].begin > begin) return;  // nothing is cut, or an earlier share's end cuts it first
-  const PrefixTile tile = p.tiles[cut.tile];
-  const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1;
+  const int k0 = blockIdx.x, lane = lane_id();
+  const PrefixShare share = p.share[k0];
+  if (share.cut < 0) return;
+  const PrefixTile tile = p.tiles[share.cut];
+  const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1, k1 = share.last;
   if (r >= tile.rows) return;
-  const int k0 = x;
-  int k1 = x + 1;
-  while (p.share[k1].end < end) ++k1;
-  auto row_of = [&](int k) { return ((size_t)(p.share[k].begin >= begin ? 2 * k : 2 * k + 1)) * kTileRows + r; };
+  auto row_of = [&](int k) { return (size_t)(k == k0 ? share.first_slot : 2 * k) * kTileRows + r; };
   // parts four at a time, the first four's rows on their way while the weights
   // are found
   float4 y[4][2];
@@ -948,7 +966,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
 }
 
 int max_tiles_of(int T, int H, int G) { return (int)(((long long)T * H + kTileRows - 1) / kTileRows) + G; }
-int max_shares() { return std::max(1, sm_count() / 4); }
+int max_shares() { return std::min(std::max(1, sm_count() / 4), kMaxShares); }
 // Clusters that the current device runs at once (a cluster lies in one GPC, so
 // there are fewer than SMs / 4), asked once per device.
 int clusters_at_once() {
@@ -989,14 +1007,20 @@ Layout layout_of(int T, int H, int G) {
   };
   l.tile_base = take(((size_t)G + 1) * 4);
   l.tiles = take(nt * sizeof(PrefixTile));
-  l.unit_base = take((nt + 1) * 8);
-  l.share = take((slots / 2 + 1) * sizeof(PrefixShare));
+  l.unit_base = take((nt + 1) * 4);
+  l.share = take(slots / 2 * sizeof(PrefixShare));
   l.part_lse = take(slots * kTileRows * 4);
   l.part_o = take(slots * kTileRows * kDv * 4);
   l.bytes = at;
   return l;
 }
 }  // namespace
+
+bool prefix_units_fit(int T, int H, int G, int max_kv) {
+  // a row tile has rows of at most ceil(256 / H) + 1 requests, and the prefix
+  const long long lists = 2 + (kTileRows + H - 1) / H, keys = ((long long)max_kv + kKeys - 1) / kKeys + 1;
+  return max_tiles_of(T, H, G) * lists * (keys + kListCost) < (1LL << 31);
+}
 
 size_t prefix_workspace_bytes(int T, int H, int G) { return layout_of(T, H, G).bytes; }
 
@@ -1005,7 +1029,7 @@ int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   prm.tile_base = reinterpret_cast<int32_t*>(w + l.tile_base);
   prm.tiles = reinterpret_cast<PrefixTile*>(w + l.tiles);
-  prm.unit_base = reinterpret_cast<long long*>(w + l.unit_base);
+  prm.unit_base = reinterpret_cast<int*>(w + l.unit_base);
   prm.share = reinterpret_cast<PrefixShare*>(w + l.share);
   prm.part_o = reinterpret_cast<float*>(w + l.part_o);
   prm.part_lse = reinterpret_cast<float*>(w + l.part_lse);

@@ -17,10 +17,15 @@ struct alignas(16) PrefixTile {
   int page_base;       // and where its page-table entries start
   int pad[2];
 };
-// What a cluster works on: units [begin, end), from row tile `tile` on.
+// What a cluster works on: units [begin, end), from row tile `tile` on; and the
+// list that its end is the first to cut.
 struct alignas(16) PrefixShare {
-  long long begin, end;
-  int tile, pad[3];
+  int begin, end;
+  int tile;
+  int cut;         // its row tile, -1: none
+  int last;        // last share that works on it
+  int first_slot;  // place of this share's part (share k's is 2k)
+  int pad[2];
 };
 
 struct PrefixParams {
@@ -41,13 +46,15 @@ struct PrefixParams {
   // workspace (set by run_prefix_mla)
   int32_t* tile_base;    // [G + 1] tiles of the groups before
   PrefixTile* tiles;
-  long long* unit_base;  // [tiles + 1] key tiles of the tiles before
-  PrefixShare* share;    // [shares + 1], those past the work empty
+  int* unit_base;        // [tiles + 1] key tiles of the tiles before
+  PrefixShare* share;    // [shares], those past the work empty
   float* part_o;    // [2 * shares][256][512]
   float* part_lse;  // [2 * shares][256], log2
   int max_tiles, shares;
 };
 
+// Whether all key tiles of a call, at most, can be counted in 31 bits.
+bool prefix_units_fit(int T, int H, int G, int max_kv);
 size_t prefix_workspace_bytes(int T, int H, int G);
 // ws: at least that many bytes.
 int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws);

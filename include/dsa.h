@@ -647,8 +647,10 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * are read; rows of a run past the visible length must hold finite values (see
  * dsa_sparse_mla_decode).
  * Outputs are the same on every run.
- * Supported: as dsa_dense_mla; 1 <= G <= 2^20, T * H < 2^31 - 2^16, max_kv <=
- * 2^30, |sm_scale| * 1.5 finite in fp32.
+ * Supported: as dsa_dense_mla; 1 <= G <= 2^20, T * H < 2^31 - 2^16, |sm_scale| *
+ * 1.5 finite in fp32, max_kv <= 2^30 and with (T * H / 256 + 1 + G) * (2 +
+ * ceil(256 / H)) * (max_kv / 256 + 6) below 2^31 (65535 tokens of 128 heads: two
+ * million keys).
  * ------------------------------------------------------------------------ */
 DSA_API size_t dsa_prefix_mla_workspace_size(int T, int H, int G);
 DSA_API int dsa_prefix_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
