@@ -317,7 +317,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
 // The key tiles of a list from tile k on, resolved by one whole warp.
 struct KeyCursor {
   const PrefixParams* p;
-  int prefix, last, s, seg;  // last token; next request; the segment (-1: prefix)
+  int prefix, last, seg;  // last token; the segment (-1: prefix)
+  int s, own_start, own_end, own_base;  // 32 requests from s on, one per lane: their own keys and page-table entries
+  uint32_t todo;                        // those with own keys still to visit
   int pos, end, left, page_base, lg;
   int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
 
@@ -334,7 +336,8 @@ struct KeyCursor {
     lg = 31 - __clz(prm.ps);
     prefix = tile.prefix;
     last = tile.last;
-    s = tile.s0;
+    s = tile.s0 - 32;
+    todo = 0;
     left = 0;
     const int np = (prefix + kKeys - 1) / kKeys;
     if (k < np) {
@@ -343,17 +346,41 @@ struct KeyCursor {
       next_request(k - np);
     }
   }
-  // the request that holds own tile k, counted from request s on
+  // the request that holds own tile k of those still to visit
   __device__ void next_request(int k) {
-    for (; s < p->S && __ldg(p->cu_q_lens + s) <= last; ++s) {
-      const Own w = own_keys(*p, __ldg(p->cu_q_lens + s), __ldg(p->cu_q_lens + s + 1), __ldg(p->seq_lens + s), last, prefix);
-      const int n = w.tiles();
-      if (k < n) {
-        open(s, w.start + k * kKeys, w.end, n - k, __ldg(p->cu_kv_lens + s) >> lg);
-        ++s;
-        return;
+    while (true) {
+      if (todo) {
+        const int n = todo >> lane_id() & 1 ? Own{own_start, own_end}.tiles() : 0;
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane_id() >= d) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, upto > k);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          k -= __shfl_sync(0xffffffffu, upto - n, l);
+          open(s + l, __shfl_sync(0xffffffffu, own_start, l) + k * kKeys, __shfl_sync(0xffffffffu, own_end, l),
+               __shfl_sync(0xffffffffu, n, l) - k, __shfl_sync(0xffffffffu, own_base, l));
+          todo &= 0xfffffffeu << l;
+          return;
+        }
+        k -= __shfl_sync(0xffffffffu, upto, 31);
       }
-      k -= n;
+      s += 32;
+      const int me = s + lane_id();
+      const int q0 = me < p->S ? __ldg(p->cu_q_lens + me) : last + 1;
+      todo = 0;
+      if (!__any_sync(0xffffffffu, q0 <= last)) break;
+      Own w{0, 0};
+      if (q0 <= last) {
+        w = own_keys(*p, q0, __ldg(p->cu_q_lens + me + 1), __ldg(p->seq_lens + me), last, prefix);
+        own_base = __ldg(p->cu_kv_lens + me) >> lg;
+      }
+      own_start = w.start;
+      own_end = w.end;
+      todo = __ballot_sync(0xffffffffu, w.tiles() > 0);
     }
     seg = p->S;  // no keys: the only tile of rows that see none
     pos = end = 0;
