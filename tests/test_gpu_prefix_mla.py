@@ -303,3 +303,77 @@ def test_cache_past_32_bit_offsets(dsa):
     b.meta[3].add_(P - n)
     b.table = [[x + P - n for x in t] for t in b.table]
     _check(dsa, b)
+
+
+@pytest.mark.parametrize("what", ["requests", "groups", "row tiles"])
+def test_more_than_the_plan_keeps_in_shared_memory(dsa, what):
+    """Thousands of requests (most of them paused), hundreds of groups, more
+    than a thousand row tiles."""
+    if what == "requests":
+        groups = [(70, [(1 if i % 97 == 5 else 0, 1 + i % 5) for i in range(3500)]), (33, [(0, 1)] * 200 + [(2, 40)])]
+        _check(dsa, Batch(groups, 16, 32))
+    elif what == "groups":
+        _check(dsa, Batch([(i % 70, [(i % 3, i % 3 + 1), (1, 1 + i % 40)][: 1 + i % 2]) for i in range(600)], 4, 32))
+    else:
+        _check(dsa, Batch([(40, [(700, 700), (1, 1), (1399, 1400)])], 128, 128))
+
+
+def test_appended_then_attended(dsa):
+    """A step as it is used: page tables from lengths, rows rotated on their way
+    into the cache together with the queries, then attention over the shared
+    prefix; eager, and captured and replayed while the requests grow."""
+    own = (61, 70, 62)  # two requests enter their fourth page
+    b = Batch([(130, [(1, own[0]), (1, own[1]), (3, own[2])])], 16)
+    S, H, T = 3, 16, b.T
+    freqs, scale = dsa.dsa_rope_freqs(64, scaling="yarn", factor=4.0, orig_max_pos=256, device="cuda")
+    width = max(len(t) for t in b.table) + 1
+    bt = torch.full((S, width), -1, dtype=torch.int32)
+    for s, t in enumerate(b.table):
+        bt[s, : len(t)] = torch.tensor(t)
+    used = {x for t in b.table for x in t}
+    free = _i32([x for x in range(b.kv.shape[0]) if x not in used])
+    b.kv = b.kv.nan_to_num()  # pages that the list hands out are written in part
+    PTW = sum(len(t) for t in b.table) + 4
+    seq, qn = b.meta[0], _i32(b.q_lens)
+    q_raw, rows = b.q.clone(), torch.randn(T, 576, device="cuda").to(BF)
+    q = torch.empty_like(q_raw)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    state = torch.zeros(3 + 2 * S, dtype=torch.int32, device="cuda")
+    bt, old = bt.cuda(), b.kv.clone()
+    tb = dsa.dsa_build_page_tables(qn, seq, bt, free, T=T, PTW=PTW, free_state=state, dev_status=st)
+    o, lse = torch.empty(T, H, 512, dtype=BF, device="cuda"), torch.empty(T, H, device="cuda")
+    ws = torch.empty(dsa.dsa_prefix_mla_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+
+    def step():
+        dsa.dsa_build_page_tables(qn, seq, bt, free, T=T, PTW=PTW, free_state=state, out=tb, dev_status=st)
+        dsa.dsa_rope_append(dsa.AppendTarget(rows, b.kv, rot_off=512, layout="interleaved", scale=scale), tb.positions,
+                            tb.slots, freqs, dev_status=st,
+                            rotate=dsa.RopeTarget(q_raw, q, rot_off=512, layout="interleaved", scale=scale))
+        dsa.dsa_prefix_mla(q, b.kv, seq, tb.cu_q_lens, tb.cu_kv_lens, tb.page_indices, b.prefix, max_kv=400,
+                           sm_scale=SCALE, o=o, lse=lse, ws=ws, dev_status=st)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for grow in (0, 1, 2):
+        b.kv.copy_(old)
+        b.seq = [130 + n + grow for n in own]
+        seq.copy_(_i32(b.seq))
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        pos = np.concatenate([np.arange(n - k, n) for n, k in zip(b.seq, b.q_lens)])
+        assert np.array_equal(tb.positions.cpu().numpy(), pos)
+        x, mag = R.rope(R.f64(rows)[:, None], pos, freqs.cpu().numpy(), 512, "interleaved", scale, False)
+        got = R.f64(b.kv.view(-1, 576)[tb.slots.long()])
+        assert (np.abs(got - x[:, 0]) <= R.rope_tol(x, mag, BF)[:, 0]).all()
+        y, mag = R.rope(R.f64(q_raw), pos, freqs.cpu().numpy(), 512, "interleaved", scale, False)
+        assert (np.abs(R.f64(q) - y) <= R.rope_tol(y, mag, BF)).all()
+        cu = tb.cu_kv_lens.cpu().numpy() // 64
+        pages = tb.page_indices.cpu().numpy()
+        b.table = [pages[a: c].tolist() for a, c in zip(cu, cu[1:])]
+        b.q = q
+        R.check_attend(o, lse, b.reference())
