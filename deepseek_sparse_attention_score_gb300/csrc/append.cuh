@@ -8,7 +8,7 @@
 namespace dsa {
 
 constexpr int kAppendMaxTargets = 4;
-constexpr int kAppendTokens = 8;  // of one warp, at most
+constexpr int kAppendRing = 12 * 1024, kAppendStages = 4;  // a warp's places in shared memory: bytes, and how many
 
 struct AppendTarget {
   const uint16_t* x;   // columns that pass, and with !split the rotated ones among them
@@ -16,17 +16,18 @@ struct AppendTarget {
   long long x_stride, xr_stride;  // elements
   uint8_t* cache;
   long long cache_stride;  // bytes of a cache row
-  int rot_at;              // byte of a cache row where the rotated columns start
-  int rot_off, pass;       // first rotated column; columns that pass (4 bits: none, they are quantised)
-  int first;               // units of the targets before
-  int half, split;
+  int D, rot_off;
+  int rot_at;    // byte of a cache row where the rotated columns start
+  int first;     // runs of 16 bytes that pass of the targets before (of 4-bit rows none: they are quantised)
+  int stage_at;  // byte of a token's place in shared memory
+  int half, split, q4;
   float scale;
 };
 struct AppendParams {
   AppendTarget tg[kAppendMaxTargets];
   int q4[kAppendMaxTargets], n_q4;  // targets that are quantised
-  int n, units, rot_dim, T;
-  int tokens;  // of a warp
+  int n, runs, rot_dim, T;
+  int stages, stage, row_bytes;  // a warp's places in shared memory; bytes of one, and of a token's source rows
   unsigned append_ctas;
   long long rows;  // of each cache: pages * page size
   const int32_t* positions;

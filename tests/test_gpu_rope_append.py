@@ -55,6 +55,9 @@ def _check_cache(cache, old, x, pos, slots, freqs, off, layout, scale):
     (37, 576, 512, 64, 640, 128, True), (130, 128, 0, 128, 128, 32, False), (3, 512, 0, 512, 512, 64, True),
     (9, 88, 40, 16, 104, 64, False), (9, 88, 40, 32, 104, 64, True), (2, 16, 0, 16, 16, 32, False),
     (700, 576, 0, 64, 576, 64, True), (4, 4096, 2048, 64, 4096, 32, False),
+    # through shared memory
+    (2501, 576, 512, 64, 640, 64, True), (2048, 128, 0, 64, 128, 32, False), (2100, 88, 40, 32, 104, 64, True),
+    (1900, 512, 0, 512, 512, 64, True), (3000, 16, 0, 16, 16, 128, False), (1850, 2048, 1024, 256, 2048, 64, False),
 ])
 def test_matches_64_bit(dsa, layout, T, D, off, rot, width, ps, split):
     P = -(-T // ps) + 2
@@ -65,6 +68,9 @@ def test_matches_64_bit(dsa, layout, T, D, off, rot, width, ps, split):
     if T > 4:
         slots[2] = -1
         pos[4] = -1  # either one makes a padding row
+    if T > 1000:  # and runs of them
+        slots[np.random.default_rng(1).random(T) < 0.3] = -1
+        slots[1000:1200] = -1
     freqs, scale = dsa.dsa_rope_freqs(rot, scaling="yarn", factor=40.0, device="cuda")
     if split:  # the rotated columns from a slice of a wider tensor
         wide = torch.cat([_rand((T, 8), 9), x[:, off: off + rot], _rand((T, 24), 10)], 1)
@@ -80,7 +86,7 @@ def test_matches_64_bit(dsa, layout, T, D, off, rot, width, ps, split):
     _check_cache(cache, old, x, pos, slots, freqs, off, layout, scale)
 
 
-@pytest.mark.parametrize("T", [1, 33, 1000])
+@pytest.mark.parametrize("T", [1, 33, 1000, 12999])
 def test_is_the_rotation_and_the_write_back(dsa, T):
     """The same values as dsa_rope followed by the write-backs, 16-bit and
     4-bit, queries and all."""
@@ -117,22 +123,28 @@ def test_is_the_rotation_and_the_write_back(dsa, T):
     assert torch.equal(kv4[:, :, :288], kv4_[:, :, :288])
 
 
-def test_quantised_rows_of_every_kind(dsa):
+@pytest.mark.parametrize("times", [1, 1040])
+def test_quantised_rows_of_every_kind(dsa, times):
     """4-bit groups with infinities, NaN, zeros, tiny and huge values, byte for
-    byte as the reference packs them; the rotary part in its place."""
+    byte as the reference packs them; the rotary part in its place; rows of
+    padding between them."""
     T = 12
     x = _rand((T, 576), 8)
     x[0, :16], x[1, 5], x[2, 17], x[3, :512] = 0, float("inf"), float("nan"), 0
     x[4, :512] *= 2.0 ** -12
     x[5, :512] *= 2.0 ** 14
-    pos, slots = np.zeros(T, np.int64), _slots(T, 64, 1)  # position 0: the rotation leaves the values
-    cache = torch.full((1, 64, 416), 77, dtype=torch.uint8, device="cuda")
+    rows = np.tile(R.q4_pack(x), (times, 1))
+    x, T = x.repeat(times, 1), T * times
+    P = -(-T // 64)
+    pos, slots = np.zeros(T, np.int64), _slots(T, P * 64, 1)  # position 0: the rotation leaves the values
+    slots[np.random.default_rng(2).random(T) < 0.2] = -1
+    cache = torch.full((P, 64, 416), 77, dtype=torch.uint8, device="cuda")
     freqs, _ = dsa.dsa_rope_freqs(64, device="cuda")
     dsa.dsa_rope_append(dsa.AppendTarget(x, cache, rot_off=512, layout="interleaved"), _i32(pos), _i32(slots), freqs)
     torch.cuda.synchronize()
-    want = np.full((64, 416), 77, np.uint8)
-    want[slots] = R.q4_pack(x)
-    got = cache.cpu().numpy()[0]
+    want = np.full((P * 64, 416), 77, np.uint8)
+    want[slots[slots >= 0]] = rows[slots >= 0]
+    got = cache.cpu().numpy().reshape(-1, 416)
     zero = (want[:, 288:].view(np.uint16) & 0x7FFF) == 0  # +0 and -0 are one value
     same = got == want
     same[:, 288:] |= np.repeat(zero & ((got[:, 288:].copy().view(np.uint16) & 0x7FFF) == 0), 2, 1)
