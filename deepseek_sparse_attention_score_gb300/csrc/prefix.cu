@@ -66,13 +66,11 @@ constexpr int OFF_LOCAL = OFF_RING + kStages * kStage;   // float [2][kRows]: ma
 constexpr int OFF_REMOTE = OFF_LOCAL + 2 * kRows * 4;    // float [2][kRows]: those of the other keys, two tiles
 constexpr int OFF_DESC = OFF_REMOTE + 2 * kRows * 4;
 constexpr int OFF_BAR = (OFF_DESC + kDescs * (int)sizeof(KeyTile) + 7) & ~7;
-constexpr int kNumBars = 2 * kStages + 2 * kDescs + 9 + 4 + 8;
+constexpr int kNumBars = 2 * kStages + 2 * kDescs + 10 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_DESC % 16 == 0, "alignment");
-constexpr int kStageLd = 256 + 16;  // bytes of a staged row: 128 bf16 or 64 fp32 columns
-static_assert(kSoftWarps * 32 * kStageLd <= kStages * kStage, "rows are staged in the ring");
 
 constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, 128, false, false);
 constexpr uint32_t kIdescPV = make_idesc_bf16(kTileRows, 256, false, true);
@@ -98,9 +96,10 @@ struct Bars {
   __device__ __forceinline__ uint64_t* ppeer() const { return rest(6); }   // each: P from the other half
   __device__ __forceinline__ uint64_t* lbar() const { return rest(7); }    // each: sums of weights from the other half
   __device__ __forceinline__ uint64_t* pother() const { return rest(8); }  // pair's: P of the other half, both CTAs
-  __device__ __forceinline__ uint64_t* local(int w) const { return rest(9 + w); }  // each: two warps of the same rows
+  __device__ __forceinline__ uint64_t* edone() const { return rest(9); }   // each: softmax warps, outputs are written
+  __device__ __forceinline__ uint64_t* local(int w) const { return rest(10 + w); }  // each: two warps of the same rows
   // each: those two and the maxima of the other half
-  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(13 + 4 * k + w); }
+  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(14 + 4 * k + w); }
 };
 
 // ------------------------------------------------------------- the work list
@@ -143,7 +142,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 constexpr int kPlanRequests = 3072, kPlanGroups = 512, kPlanTiles = 1024;
 // A list that starts inside a share costs about as much as this many key tiles:
 // the pipeline runs empty, the outputs are written, the next queries fetched.
-constexpr int kListCost = 4;
+constexpr int kListCost = 2;
 constexpr int kMaxShares = 128;
 struct PlanGroup {
   int first_tile, token0, token1, prefix, page_base;
@@ -461,6 +460,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(br.qbar(), 1);
     mbar_init(br.ppeer(), 1);
     mbar_init(br.lbar(), kSoftWarps);
+    mbar_init(br.edone(), kSoftWarps);
     for (int w = 0; w < 4; ++w) {
       mbar_init(br.local(w), 2);
       for (int k = 0; k < 2; ++k) mbar_init(br.remote(w, k), 2);
@@ -489,10 +489,35 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   // every role counts what it has passed since the kernel began: a barrier's
   // phase is that number's parity
   uint32_t tc = 0, uc = 0, fc = 0;  // key tiles, lists, stages
+  // a softmax thread's row of a tile: its request and visible positions
+  auto row_of = [&](const PrefixTile& tile) -> int2 {
+    const int row = (warp & 3) * 32 + lane;
+    if (row >= tile.rows - r * kRows) return make_int2(-2, 0);
+    const int t = (tile.row0 + r * kRows + row) / prm.H;
+    int s = tile.s0, top = prm.S;  // cu_q_lens[s] <= t < cu_q_lens[top]
+    for (int step = 1; s + step < top; step *= 2) {
+      if (__ldg(prm.cu_q_lens + s + step) > t) top = s + step;
+      else s += step;
+    }
+    while (top - s > 1) {
+      const int mid = (s + top) >> 1;
+      if (__ldg(prm.cu_q_lens + mid) > t) top = mid;
+      else s = mid;
+    }
+    const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, prm.max_kv, t,
+                                   prm.dev_status, s);
+    return make_int2(s, g.n_vis);
+  };
   int ti = work.tile;
+  PrefixTile tile{};
+  int2 mine{};  // my row of the tile
+  if (work.begin < work.end) {
+    tile = prm.tiles[ti];
+    if (warp >= 4) mine = row_of(tile);
+  }
+  bool ok = true;
 #pragma unroll 1
-  for (int u = work.begin; u < work.end; ++ti) {
-    const PrefixTile tile = prm.tiles[ti];
+  for (int u = work.begin; ok && u < work.end; ++ti) {
     const int list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
     const int k0 = u - list0, n = min(work.end, list1) - u;
     const bool whole = k0 == 0 && u + n == list1;
@@ -518,7 +543,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           commit(br.empty(slot), pair);
           if (++slot == kStages) slot = 0, phase ^= 1;
         };
-        bool ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
+        ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
         tc_fence_after();
 #pragma unroll 1
         for (int i = 0; ok && i <= n; ++i) {
@@ -575,11 +600,22 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------- queries and keys
-      if (lane == 0) {
-        mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
+      // Query blocks b0 .. b1 - 1: those for TMEM land in P's places, free once the
+      // last list's outputs are written, the others where they stay, free once its
+      // last QK^T has run.
+      auto load_queries = [&](int b0, int b1) {
+        if (lane == 0) {
 #pragma unroll 1
-        for (int b = 0; b < 9; ++b)
-          tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
+          for (int b = b0; b < b1; ++b)
+            tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
+        }
+        __syncwarp();
+      };
+      if (uc) ok = mbar_wait_warp(br.sfull(), (tc - 1) & 1, abort_flag);
+      if (ok) {
+        if (lane == 0) mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
+        __syncwarp();
+        load_queries(uc ? 4 : 0, 9);
       }
       const bool two = prm.ps == 32;
       uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
@@ -597,7 +633,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         return true;
       };
       KeyTile t{}, before{};
-      bool ok = true;
 #pragma unroll 1
       for (int i = 0; ok && i <= n; ++i) {
         if (i < n) {
@@ -616,6 +651,10 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; ok && j < kKStages; ++j)
             ok = j < 4 ? load(j * 64, 256 + j * 64, r0, r1, false) : load(512, 0, r0, r1, true);
           if (!ok) break;
+          if (uc && i == 0) {
+            if (!(ok = mbar_wait_warp(br.edone(), (uc - 1) & 1, abort_flag))) break;
+            load_queries(0, 4);
+          }
         }
         if (i > 0) {
 #pragma unroll
@@ -630,7 +669,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- key tiles
       KeyCursor cur;
       cur.init(prm, tile, k0);
-      bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++tc) {
         const KeyTile t = cur.next();
@@ -646,7 +684,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 3) {
       // --------------------------- P of the other half, for the MMA issuer
       const uint32_t a_pother = leader(br.pother());
-      bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++tc) {
         if (lane == 0) mbar_arrive_expect_tx(br.ppeer(), 2 * kQBlk);
@@ -663,27 +700,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
       // this warp's part of P, 32 rows x 64 keys, here and at the other half
       const uint32_t p_blk = smem0 + OFF_P + (2 * c + hh) * kQBlk, p_run = p_blk + q * 32 * 128;
-      // this row's request and visible positions
-      int my_s = -2, see = 0;
-      const int prefix = tile.prefix;
-      if (row < rows) {
-        const int t = (row0 + row) / prm.H;
-        int s = tile.s0, top = prm.S;  // cu_q_lens[s] <= t < cu_q_lens[top]
-        for (int step = 1; s + step < top; step *= 2) {
-          if (__ldg(prm.cu_q_lens + s + step) > t) top = s + step;
-          else s += step;
-        }
-        while (top - s > 1) {
-          const int mid = (s + top) >> 1;
-          if (__ldg(prm.cu_q_lens + mid) > t) top = mid;
-          else s = mid;
-        }
-        const TokenGeom g = token_geom(prm.seq_lens, prm.cu_q_lens, prm.cu_kv_lens, prm.S, prm.ps, prm.max_kv, t,
-                                       prm.dev_status, s);
-        my_s = s;
-        see = g.n_vis;
-      }
-      bool ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
+      const int my_s = mine.x, see = mine.y, prefix = tile.prefix;
+      ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
       if (ok) {
 #pragma unroll 1
         for (int b = 2 * hh; b < 2 * hh + 2; ++b) {
@@ -830,94 +848,99 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         m_run = m_use;
       }
       // ------------------------------------------------------------ epilogue
+      if (ok && u + n < work.end) {  // while the last PV runs: the next list's row
+        tile = prm.tiles[ti + 1];
+        mine = row_of(tile);
+      }
       ok = ok && mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
+      // P's places are idle now, on both sides. The sum of a row's weights comes in
+      // four parts, to the start of this CTA's own; the other half's, of the rows
+      // that the other CTA's warps of this number write, stage the outputs.
       if (ok) {
-        // the sum of a row's weights: four parts, in the idle P blocks
-        const uint32_t a_l = smem0 + OFF_P + ((2 * c + hh) * kRows + row) * 4;
-        st_async_f32(other(a_l), l_run, other(smem_u32(br.lbar())));
-        *reinterpret_cast<float*>(smem + (a_l - smem0)) = l_run;
+        const uint32_t a_l = OFF_P + 2 * c * kQBlk + ((2 * c + hh) * kRows + row) * 4;
+        const uint32_t a_there = OFF_P + 2 * (1 - c) * kQBlk + ((2 * c + hh) * kRows + row) * 4;
+        st_async_f32(other(smem0 + a_there), l_run, other(smem_u32(br.lbar())));
+        *reinterpret_cast<float*>(smem + a_l) = l_run;
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(br.lbar(), 32 * 4);
         ok = mbar_wait_warp(br.lbar(), uc & 1, abort_flag);
       }
       if (ok) {
         tc_fence_after();
-        const volatile float* lp = reinterpret_cast<const volatile float*>(smem + OFF_P) + row;
+        const volatile float* lp = reinterpret_cast<const volatile float*>(smem + OFF_P + 2 * c * kQBlk) + row;
         const float l = (lp[0] + lp[kRows]) + (lp[2 * kRows] + lp[3 * kRows]);
         const bool some = l != 0.f;  // a sum of weights is never negative; NaN counts
         const float inv_l = some ? 1.f / l : 0.f;
         const float lse2 = some ? m_run + log2f(l) : -INFINITY;
-        // the warp stages 32 rows of its 128 columns in the idle ring and writes
-        // them two rows at a time
+        // 128 bytes of 32 rows at a time, chunks of 16 bytes swizzled
         const int w0 = q * 32, nw = min(32, rows - w0);
-        uint8_t* stg = smem + OFF_RING + (warp - 4) * (32 * kStageLd);
+        const uint32_t stg = smem0 + OFF_P + (2 * (1 - c) + hh) * kQBlk + w0 * 128;
         const uint32_t col = tmem + lane_base + kColO + 128 * hh;
-        if (whole) {
+        const size_t part_row = (size_t)slot_out * kTileRows + r * kRows + w0;  // or, undivided, the output's
+        uint8_t* out = whole ? reinterpret_cast<uint8_t*>(prm.o + ((size_t)row0 + w0) * kDv + c * 256 + hh * 128)
+                             : reinterpret_cast<uint8_t*>(prm.part_o + part_row * kDv + c * 256 + hh * 128);
+        const size_t pitch = whole ? kDv * 2 : kDv * 4;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            uint32_t o[32];
-            tmem_ld32(col + c0, o);
-            tmem_ld_wait_regs(o);
+        for (int c0 = 0; c0 < 128; out += 128) {
+          uint32_t o[32], v[32];
+          tmem_ld32(col + c0, o);
+          tmem_ld_wait_regs(o);
+          if (whole) {
+            auto pack = [&](int at) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * e]) * inv_l,
-                                                          __uint_as_float(o[8 * j + 2 * e + 1]) * inv_l);
-                pk[e] = *reinterpret_cast<uint32_t*>(&b2);
+              for (int j = 0; j < 16; ++j) {
+                __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv_l,
+                                                          __uint_as_float(o[2 * j + 1]) * inv_l);
+                v[at + j] = *reinterpret_cast<uint32_t*>(&b2);
               }
-              *reinterpret_cast<uint4*>(stg + lane * kStageLd + c0 * 2 + j * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
+            };
+            pack(0);
+            tmem_ld32(col + c0 + 32, o);
+            tmem_ld_wait_regs(o);
+            pack(16);
+            c0 += 64;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(o[j]) * inv_l);
+            c0 += 32;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(stg + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int k = 4 * j + (lane >> 3);
+            if (k < nw)
+              *reinterpret_cast<uint4*>(out + k * pitch + (lane & 7) * 16) =
+                  *reinterpret_cast<const uint4*>(smem + (stg - smem0) + sw128_offset(k, lane & 7));
           }
           __syncwarp();
-          uint16_t* out = prm.o + ((size_t)row0 + w0) * kDv + c * 256 + hh * 128 + (lane & 15) * 8;
-#pragma unroll 4
-          for (int k = lane >> 4; k < nw; k += 2)
-            *reinterpret_cast<uint4*>(out + (size_t)k * kDv) =
-                *reinterpret_cast<const uint4*>(stg + k * kStageLd + (lane & 15) * 16);
-          if (c == 0 && hh == 0 && row < rows && prm.lse) prm.lse[(size_t)row0 + row] = lse2 * 0.69314718055994531f;
-        } else {
-          // normalised partial rows and their log-sums
-          const size_t out_row = (size_t)slot_out * kTileRows + r * kRows + w0;
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 64) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              uint32_t o[32];
-              tmem_ld32(col + c0 + 32 * h, o);
-              tmem_ld_wait_regs(o);
-#pragma unroll
-              for (int v = 0; v < 8; ++v)
-                *reinterpret_cast<float4*>(stg + lane * kStageLd + h * 128 + v * 16) =
-                    make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
-                                __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
-            }
-            __syncwarp();
-            float* out = prm.part_o + out_row * kDv + c * 256 + hh * 128 + c0 + (lane & 15) * 4;
-#pragma unroll 4
-            for (int k = lane >> 4; k < nw; k += 2)
-              *reinterpret_cast<float4*>(out + (size_t)k * kDv) =
-                  *reinterpret_cast<const float4*>(stg + k * kStageLd + (lane & 15) * 16);
-            __syncwarp();
-          }
-          if (c == 0 && hh == 0 && row < rows) prm.part_lse[out_row + lane] = lse2;
+        }
+        if (c == 0 && hh == 0 && row < rows) {
+          if (!whole) prm.part_lse[part_row + lane] = lse2;
+          else if (prm.lse) prm.lse[(size_t)row0 + row] = lse2 * 0.69314718055994531f;
         }
         tc_fence_before();
-        fence_proxy_async_smem();  // the staged rows' place is written by copies again
+        fence_proxy_async_smem();  // queries are copied to P's places next
+        __syncwarp();
+        if (lane == 0) mbar_arrive(br.edone());
+        __syncwarp();
       } else {
         give_up();
       }
     }
-    // all CTAs are done with the list: their MMAs have run and their copies landed
-    __syncwarp();
-    cluster_sync_all();
-    tc_fence_after();
-    if (*abort_flag) break;
+    // No barrier here: the next list's first keys are fetched, and its queries,
+    // while this one's outputs are written. Its first QK^T waits for the softmax
+    // warps of the pair (qready), so for their reads of O; its first P comes after
+    // an exchange of maxima with the warps whose places it writes.
     fc += (kKStages + kVStages) * n;
     u += n;
     ++uc;
+    if (warp < 4 && ok && u < work.end) tile = prm.tiles[ti + 1];
   }
+  __syncwarp();
+  cluster_sync_all();
   if (*abort_flag) {
     // unwinding: copies and MMAs in flight land within microseconds; wait longer
     const long long t0 = clock64();
