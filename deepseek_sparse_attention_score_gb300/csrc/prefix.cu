@@ -2,14 +2,14 @@
 // once for all of them. Per group of requests, and with rows (token, head):
 //   S = Q K^T over 576 dims, online softmax, O += P V, V = the first 512 dims.
 // The rows of a group are cut into tiles of 256, of any tokens and heads, since
-// [T, H] rows lie one behind another. A tile's keys are a list of key tiles of
-// 256: the prefix, read through the page table of the group's first request,
-// then the own positions of each request that has rows in the tile, which the
-// rows of others mask.
+// [T, H] rows lie one behind another. A tile's keys are a list of runs of up to
+// 128: of the prefix, read through the page table of the group's first request,
+// then of the own positions of each request that has rows in the tile, which the
+// rows of others mask. Two runs, of one request or of two, make a key tile.
 //
 // A cluster of four CTAs takes a row tile: CTA (c, r) = rank 2c + r has rows
 // 128r .. of it, value columns 256c .. (128 rows of all 512 columns in fp32 would
-// be the whole TMEM) and computes S for keys 128c .. of a key tile, so that no
+// be the whole TMEM) and computes S for run c of a key tile, so that no
 // product is computed twice; it gives its weights P to CTA (1 - c, r), which
 // needs them for the other value columns, and the two agree on the rows' maxima.
 // The MMAs are those of the pairs (c, 0), (c, 1): 256 rows, and either CTA
@@ -37,7 +37,7 @@ namespace dsa {
 namespace {
 constexpr int kDk = 576, kDv = 512;
 constexpr int kRows = 128, kTileRows = 2 * kRows;  // of a CTA, of a cluster
-constexpr int kKeys = 256, kRuns = kKeys / 32;     // of a key tile, and its runs of 32 keys
+constexpr int kRun = 128;                          // keys of a run, of which a key tile has two
 constexpr int kBlk = 64 * 128;                     // 64 keys x 64 dims
 constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (queries) or keys (P)
 // Stages of a key tile: five of two K blocks (64 keys of this CTA, dims 64j and
@@ -51,12 +51,16 @@ constexpr int kThreads = (4 + kSoftWarps) * 32;
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
 constexpr int kNoRow = -64;               // a box from here on lies outside the cache and lands as zeros
 
-// What the softmax and the copier know of a key tile.
+// What the softmax and the copier know of a key tile's runs.
+struct KeyRun {
+  int row[4];  // cache rows of keys 0, 32, 64 and 96, or kNoRow
+  int pos;     // of the first key
+  int seg;     // -1: prefix; else the request whose own keys they are
+  int valid;   // bit g: keys 32 g .. hold positions
+  int pad;
+};
 struct KeyTile {
-  int row[kRuns];  // cache row of each run of 32 keys, or kNoRow
-  int pos;         // of the first key
-  int seg;         // -1: prefix; else the request whose own keys they are
-  int valid;       // bit g: run g holds positions
+  KeyRun run[2];
 };
 
 constexpr int OFF_Q = 0;  // dims 256-575
@@ -107,7 +111,7 @@ struct Bars {
 // (a page's first) to `end`.
 struct Own {
   int start, end;
-  __device__ __forceinline__ int tiles() const { return end > start ? (end - start + kKeys - 1) / kKeys : 0; }
+  __device__ __forceinline__ int runs() const { return end > start ? (end - start + kRun - 1) / kRun : 0; }
 };
 __device__ __forceinline__ Own own_keys(const PrefixParams& p, int q0, int q1, int seq_len, int last, int prefix) {
   Own w{0, 0};
@@ -241,10 +245,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     for (int b = s0; b < p.S; b += 32) {
       const int s = b + lane;
       const bool in = s < p.S && cu_q[s] <= tb;
-      if (in) n += own_keys(p, cu_q[s], cu_q[s + 1], seq[s], tb, x.prefix).tiles();
+      if (in) n += own_keys(p, cu_q[s], cu_q[s + 1], seq[s], tb, x.prefix).runs();
       if (!__all_sync(0xffffffffu, in)) break;
     }
-    n = __reduce_add_sync(0xffffffffu, n) + (x.prefix + kKeys - 1) / kKeys;
+    n = (__reduce_add_sync(0xffffffffu, n) + (x.prefix + kRun - 1) / kRun + 1) / 2;
     if (lane == 0) {
       base[i] = max(n, 1);  // rows without any key still have an output
       PrefixTile r{};
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   if (bad) set_status(p.dev_status, DSA_STATUS_BAD_METADATA);
 }
 
-// The key tiles of a list from tile k on, resolved by one whole warp.
+// The runs of a list from run k on, resolved by one whole warp.
 struct KeyCursor {
   const PrefixParams* p;
   int prefix, last, seg;  // last token; the segment (-1: prefix)
@@ -322,11 +326,11 @@ struct KeyCursor {
   int pos, end, left, page_base, lg;
   int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
 
-  __device__ __forceinline__ void open(int sg, int first, int stop, int tiles, int base) {
+  __device__ __forceinline__ void open(int sg, int first, int stop, int runs, int base) {
     seg = sg;
     pos = first;
     end = stop;
-    left = tiles;
+    left = runs;
     page_base = base;
     win = -64;
   }
@@ -338,18 +342,18 @@ struct KeyCursor {
     s = tile.s0 - 32;
     todo = 0;
     left = 0;
-    const int np = (prefix + kKeys - 1) / kKeys;
+    const int np = (prefix + kRun - 1) / kRun;
     if (k < np) {
-      open(-1, k * kKeys, prefix, np - k, tile.page_base);
+      open(-1, k * kRun, prefix, np - k, tile.page_base);
     } else {
       next_request(k - np);
     }
   }
-  // the request that holds own tile k of those still to visit
+  // the request that holds own run k of those still to visit
   __device__ void next_request(int k) {
     while (true) {
       if (todo) {
-        const int n = todo >> lane_id() & 1 ? Own{own_start, own_end}.tiles() : 0;
+        const int n = todo >> lane_id() & 1 ? Own{own_start, own_end}.runs() : 0;
         int upto = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -360,7 +364,7 @@ struct KeyCursor {
         if (past) {
           const int l = __ffs(past) - 1;
           k -= __shfl_sync(0xffffffffu, upto - n, l);
-          open(s + l, __shfl_sync(0xffffffffu, own_start, l) + k * kKeys, __shfl_sync(0xffffffffu, own_end, l),
+          open(s + l, __shfl_sync(0xffffffffu, own_start, l) + k * kRun, __shfl_sync(0xffffffffu, own_end, l),
                __shfl_sync(0xffffffffu, n, l) - k, __shfl_sync(0xffffffffu, own_base, l));
           todo &= 0xfffffffeu << l;
           return;
@@ -379,24 +383,24 @@ struct KeyCursor {
       }
       own_start = w.start;
       own_end = w.end;
-      todo = __ballot_sync(0xffffffffu, w.tiles() > 0);
+      todo = __ballot_sync(0xffffffffu, w.runs() > 0);
     }
-    seg = p->S;  // no keys: the only tile of rows that see none
+    seg = p->S;  // no keys: behind the last run
     pos = end = 0;
     left = 1;
     win = 0;
     page = -1;
   }
-  // The next key tile, in every lane.
-  __device__ KeyTile next() {
+  // The next run, in every lane.
+  __device__ KeyRun next() {
     if (!left) next_request(0);
     --left;
-    KeyTile t;
+    KeyRun t;
     t.pos = pos;
     t.seg = seg;
-    t.valid = 0;
+    t.valid = t.pad = 0;
     const int e0 = pos >> lg;
-    if (pos < end && (e0 < win || ((pos + kKeys - 1) >> lg) >= win + 32)) {
+    if (pos < end && (e0 < win || ((pos + kRun - 1) >> lg) >= win + 32)) {
       win = e0;
       const int e = win + lane_id();
       page = -1;
@@ -414,13 +418,13 @@ struct KeyCursor {
       }
     }
 #pragma unroll
-    for (int g = 0; g < kRuns; ++g) {
+    for (int g = 0; g < 4; ++g) {
       const int at = pos + 32 * g, pg = __shfl_sync(0xffffffffu, page, ((at >> lg) - win) & 31);
       const bool ok = at < end && pg >= 0;
       t.row[g] = ok ? (pg << lg) + (at & (p->ps - 1)) : kNoRow;
       t.valid |= ok ? 1 << g : 0;
     }
-    pos += kKeys;
+    pos += kRun;
     return t;
   }
 };
@@ -632,21 +636,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         if (++slot == kStages) slot = 0, phase ^= 1;
         return true;
       };
-      KeyTile t{}, before{};
 #pragma unroll 1
       for (int i = 0; ok && i <= n; ++i) {
         if (i < n) {
           const int ds = tc % kDescs;
           if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-          t = descs[ds];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(br.dempty(ds));
+          const KeyRun& mine = descs[ds].run[c];  // of which this CTA has 64 keys
+          const int r0 = mine.row[2 * r], r1 = mine.row[2 * r + 1];
           ++tc;
-          const int g = 4 * c + 2 * r;  // this CTA's 64 keys
-          int r0 = t.row[0], r1 = t.row[1];
-#pragma unroll
-          for (int h = 2; h < kRuns; h += 2)
-            if (h == g) r0 = t.row[h], r1 = t.row[h + 1];
 #pragma unroll 1
           for (int j = 0; ok && j < kKStages; ++j)
             ok = j < 4 ? load(j * 64, 256 + j * 64, r0, r1, false) : load(512, 0, r0, r1, true);
@@ -656,22 +653,27 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             load_queries(0, 4);
           }
         }
-        if (i > 0) {
-#pragma unroll
-          for (int s = 0; s < kVStages; ++s)
-            ok = ok && load(c * 256 + r * 128, c * 256 + r * 128 + 64, c ? before.row[(2 * s + 4) & 7] : before.row[2 * s],
-                            c ? before.row[(2 * s + 5) & 7] : before.row[2 * s + 1], false);
+        if (i > 0) {  // V of the key tile before, first of run c
+          const int ds = (tc - (i < n ? 2 : 1)) % kDescs;
+#pragma unroll 1
+          for (int s = 0; ok && s < kVStages; ++s) {
+            const KeyRun& run = descs[ds].run[c ^ (s >> 1)];
+            ok = load(c * 256 + r * 128, c * 256 + r * 128 + 64, run.row[2 * (s & 1)], run.row[2 * (s & 1) + 1], false);
+          }
+          if (lane == 0) mbar_arrive(br.dempty(ds));
+          __syncwarp();
         }
-        before = t;
       }
       if (!ok) give_up();
     } else if (warp == 2) {
       // ----------------------------------------------------------- key tiles
       KeyCursor cur;
-      cur.init(prm, tile, k0);
+      cur.init(prm, tile, 2 * k0);
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++tc) {
-        const KeyTile t = cur.next();
+        KeyTile t;
+        t.run[0] = cur.next();
+        t.run[1] = cur.next();
         const int ds = tc % kDescs;
         if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
         if (lane == 0) {
@@ -733,8 +735,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && i < n; ++i, ++tc) {
         const int ds = tc % kDescs;
         if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-        const int p0 = descs[ds].pos + c * 128 + hh * 64, seg = descs[ds].seg;
-        const int valid = descs[ds].valid >> (4 * c + 2 * hh);
+        const KeyRun& run = descs[ds].run[c];
+        const int p0 = run.pos + hh * 64, seg = run.seg, valid = run.valid >> (2 * hh);
         __syncwarp();
         if (lane == 0) mbar_arrive(br.dempty(ds));
         const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
@@ -1068,7 +1070,7 @@ Layout layout_of(int T, int H, int G) {
 
 bool prefix_units_fit(int T, int H, int G, int max_kv) {
   // a row tile has rows of at most ceil(256 / H) + 1 requests, and the prefix
-  const long long lists = 2 + (kTileRows + H - 1) / H, keys = ((long long)max_kv + kKeys - 1) / kKeys + 1;
+  const long long lists = 2 + (kTileRows + H - 1) / H, keys = (long long)max_kv / (2 * kRun) + 4;
   return max_tiles_of(T, H, G) * lists * (keys + kListCost) < (1LL << 31);
 }
 
