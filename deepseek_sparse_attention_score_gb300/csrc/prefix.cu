@@ -20,14 +20,19 @@
 // workspace (at most two per cluster) and a second kernel merges them, in order,
 // so outputs are the same on every run.
 //
+// A request's own values are added to its own rows alone (the MMA leaves the others
+// of the tile as they are): their weights are zero, but 0 x NaN is not.
+//
 // Roles of a CTA: warp 0 issues the MMAs (r = 0), warp 1 copies queries and keys,
-// warp 2 resolves the keys a few tiles ahead, warp 3 passes on that the other half's P has arrived,
-// warps 4-11 run the softmax, a row and half of its columns of S per thread.
+// warp 2 resolves the keys a few tiles ahead, warp 3 passes on that the other half's
+// P has arrived, warps 4-11 run the softmax, a row and half of its columns of S per
+// thread.
 //
 // Per key tile i: QK^T(i), then PV(i - 1). S is read into registers at once and P
 // goes to shared memory, so that QK^T(i + 1) runs beside the softmax of tile i.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "prefix.cuh"
@@ -41,24 +46,33 @@ constexpr int kRun = 128;                          // keys of a run, of which a 
 constexpr int kBlk = 64 * 128;                     // 64 keys x 64 dims
 constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (queries) or keys (P)
 // Stages of a key tile: five of two K blocks (64 keys of this CTA, dims 64j and
-// 256 + 64j; the last has dims 512 alone), then four of V (64 keys, 128 dims of this CTA), first the
-// keys whose P this CTA computes
+// 256 + 64j; the last has dims 512 alone), then four of V (64 keys, 128 dims of this
+// CTA), first the keys whose P this CTA computes
 constexpr int kStages = 5, kStage = 2 * kBlk;
 constexpr int kKStages = 5, kVStages = 4;
 constexpr int kDescs = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = (4 + kSoftWarps) * 32;
+// Registers a thread: the softmax holds 64 logits. All together are what the CTA is
+// launched with; 104 and 200 took 1 % longer, 168 for all spills (2 %).
+constexpr int kHelperRegs = 136, kSoftRegs = 184;
+constexpr int kLaunchRegs = (kHelperRegs + kSoftWarps / 4 * kSoftRegs) / (1 + kSoftWarps / 4);
+static_assert(kLaunchRegs * (1 + kSoftWarps / 4) == kHelperRegs + kSoftWarps / 4 * kSoftRegs, "registers");
 constexpr float kRescaleThreshold = 8.f;  // log2 units: p stays <= 256
 constexpr int kNoRow = -64;               // a box from here on lies outside the cache and lands as zeros
 
-// What the softmax and the copier know of a key tile's runs.
+// the k lowest bits
+__device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; }
+
+// What the softmax, the copier and the MMA issuer know of a key tile's runs.
 struct KeyRun {
   int row[4];  // cache rows of keys 0, 32, 64 and 96, or kNoRow
   int pos;     // of the first key
   int seg;     // -1: prefix; else the request whose own keys they are
   int valid;   // bit g: keys 32 g .. hold positions
-  int pad;
+  int rows;    // the tile's rows a .. b - 1 that may see them: a | b << 16
 };
+constexpr int kAllRows = kTileRows << 16;
 struct KeyTile {
   KeyRun run[2];
 };
@@ -143,7 +157,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 // One CTA lays out the row tiles, counts their key tiles, a warp per row tile and
 // a lane per request, and deals them out. What is read many times, or by other
 // threads than wrote it, waits in shared memory, if it fits.
-constexpr int kPlanRequests = 3072, kPlanGroups = 512, kPlanTiles = 1024;
+constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024;
 // A list that starts inside a share costs about as much as this many key tiles:
 // the pipeline runs empty, the outputs are written, the next queries fetched.
 constexpr int kListCost = 2;
@@ -194,28 +208,31 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     return x;
   };
   __syncthreads();
-  int total, tiles = 0;
-  for (int g0 = 0; g0 < p.G; g0 += kPlanThreads) {
+  int total;
+  unsigned tiles = 0;
+  // 256 groups at a time: whatever the metadata hold, their sum fits 32 bits
+  for (int g0 = 0; g0 < p.G; g0 += 256) {
     const int g = g0 + tid;
-    int n = 0;
+    unsigned n = 0;
     PlanGroup x{};
-    if (g < p.G) {
+    const bool mine = tid < 256 && g < p.G;
+    if (mine) {
       bool ok;
       x = group_of(g, ok);
       // requests behind the last group: no rows of theirs are written
       if (!ok || (g == p.G - 1 && p.group_offsets && __ldg(p.group_offsets + p.G) != p.S)) bad = 1;
-      n = ((x.token1 - x.token0) * p.H + kTileRows - 1) / kTileRows;
+      n = ((unsigned)(x.token1 - x.token0) * p.H + kTileRows - 1) / kTileRows;
     }
-    const int end = block_scan(n, warp_sums, total);
-    if (g < p.G) {
-      x.first_tile = min(tiles + end - n, p.max_tiles);
+    const unsigned end = block_scan(n, warp_sums, total);
+    if (mine) {
+      x.first_tile = (int)min(tiles + end - n, (unsigned)p.max_tiles);
       if (p.G <= kPlanGroups) s_group[g] = x;
       else p.tile_base[g] = x.first_tile;
     }
-    tiles += total;
+    tiles = min(tiles + (unsigned)total, (unsigned)p.max_tiles + 1u);
   }
-  if (tiles > p.max_tiles) bad = 1;
-  const int ntiles = min(tiles, p.max_tiles);
+  if (tiles > (unsigned)p.max_tiles) bad = 1;
+  const int ntiles = (int)min(tiles, (unsigned)p.max_tiles);
   int* base = ntiles <= kPlanTiles ? s_base : p.unit_base;
   __syncthreads();
   for (int i = warp_id(); i < ntiles; i += kPlanThreads / 32) {
@@ -250,7 +267,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     }
     n = (__reduce_add_sync(0xffffffffu, n) + (x.prefix + kRun - 1) / kRun + 1) / 2;
     if (lane == 0) {
-      base[i] = max(n, 1);  // rows without any key still have an output
+      // rows without any key still have an output; no more than ordered metadata give
+      base[i] = n < 0 ? p.max_units : min(max(n, 1), p.max_units);
       PrefixTile r{};
       r.row0 = first;
       r.rows = rows;
@@ -325,13 +343,15 @@ struct KeyCursor {
   uint32_t todo;                        // those with own keys still to visit
   int pos, end, left, page_base, lg;
   int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
+  int row0, H, rows, own_rows;  // the tile's first row; heads; rows that see the segment, and each lane's request
 
-  __device__ __forceinline__ void open(int sg, int first, int stop, int runs, int base) {
+  __device__ __forceinline__ void open(int sg, int first, int stop, int runs, int base, int who) {
     seg = sg;
     pos = first;
     end = stop;
     left = runs;
     page_base = base;
+    rows = who;
     win = -64;
   }
   __device__ void init(const PrefixParams& prm, const PrefixTile& tile, int k) {
@@ -339,12 +359,14 @@ struct KeyCursor {
     lg = 31 - __clz(prm.ps);
     prefix = tile.prefix;
     last = tile.last;
+    row0 = tile.row0;
+    H = prm.H;
     s = tile.s0 - 32;
     todo = 0;
     left = 0;
     const int np = (prefix + kRun - 1) / kRun;
     if (k < np) {
-      open(-1, k * kRun, prefix, np - k, tile.page_base);
+      open(-1, k * kRun, prefix, np - k, tile.page_base, kAllRows);
     } else {
       next_request(k - np);
     }
@@ -365,7 +387,8 @@ struct KeyCursor {
           const int l = __ffs(past) - 1;
           k -= __shfl_sync(0xffffffffu, upto - n, l);
           open(s + l, __shfl_sync(0xffffffffu, own_start, l) + k * kRun, __shfl_sync(0xffffffffu, own_end, l),
-               __shfl_sync(0xffffffffu, n, l) - k, __shfl_sync(0xffffffffu, own_base, l));
+               __shfl_sync(0xffffffffu, n, l) - k, __shfl_sync(0xffffffffu, own_base, l),
+               __shfl_sync(0xffffffffu, own_rows, l));
           todo &= 0xfffffffeu << l;
           return;
         }
@@ -378,7 +401,10 @@ struct KeyCursor {
       if (!__any_sync(0xffffffffu, q0 <= last)) break;
       Own w{0, 0};
       if (q0 <= last) {
-        w = own_keys(*p, q0, __ldg(p->cu_q_lens + me + 1), __ldg(p->seq_lens + me), last, prefix);
+        const int q1 = __ldg(p->cu_q_lens + me + 1);
+        w = own_keys(*p, q0, q1, __ldg(p->seq_lens + me), last, prefix);
+        // rows of [T * H] fit 31 bits, those of other tiles lie outside 0 .. 256
+        own_rows = min(max(q0 * H - row0, 0), kTileRows) | min(max(q1 * H - row0, 0), kTileRows) << 16;
         own_base = __ldg(p->cu_kv_lens + me) >> lg;
       }
       own_start = w.start;
@@ -386,6 +412,7 @@ struct KeyCursor {
       todo = __ballot_sync(0xffffffffu, w.runs() > 0);
     }
     seg = p->S;  // no keys: behind the last run
+    rows = kAllRows;
     pos = end = 0;
     left = 1;
     win = 0;
@@ -398,7 +425,8 @@ struct KeyCursor {
     KeyRun t;
     t.pos = pos;
     t.seg = seg;
-    t.valid = t.pad = 0;
+    t.valid = 0;
+    t.rows = rows;
     const int e0 = pos >> lg;
     if (pos < end && (e0 < win || ((pos + kRun - 1) >> lg) >= win + 32)) {
       win = e0;
@@ -454,7 +482,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(br.full(s), 1), mbar_init(br.empty(s), 1);
-    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps + 1);
+    for (int s = 0; s < kDescs; ++s) mbar_init(br.dfull(s), 1), mbar_init(br.dempty(s), kSoftWarps + 1 + (r == 0));
     mbar_init(br.sfull(), 1);
     mbar_init(br.pvdone(), 2);
     mbar_init(br.sempty(), 2 * kSoftWarps);
@@ -512,434 +540,489 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
                                    prm.dev_status, s);
     return make_int2(s, g.n_vis);
   };
-  int ti = work.tile;
-  PrefixTile tile{};
-  int2 mine{};  // my row of the tile
-  if (work.begin < work.end) {
-    tile = prm.tiles[ti];
-    if (warp >= 4) mine = row_of(tile);
-  }
-  bool ok = true;
+  auto lists = [&](auto softmax) {
+    constexpr bool kSoft = decltype(softmax)::value;
+    int ti = work.tile;
+    PrefixTile tile{};
+    int2 mine{};  // my row of the tile
+    if (work.begin < work.end) {
+      tile = prm.tiles[ti];
+      if constexpr (kSoft) mine = row_of(tile);
+    }
+    bool ok = true;
 #pragma unroll 1
-  for (int u = work.begin; ok && u < work.end; ++ti) {
-    const int list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
-    const int k0 = u - list0, n = min(work.end, list1) - u;
-    const bool whole = k0 == 0 && u + n == list1;
-    const int slot_out = u == work.begin ? 2 * share : 2 * share + 1;
-    const int row0 = tile.row0 + r * kRows;              // this CTA's first row of [T * H]
-    const int rows = min(kRows, tile.rows - r * kRows);  // <= 0: none
-    if (warp == 0) {
-      // -------------------------------------------------------- MMA issuer
-      if (r == 0) {
-        const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
-        const uint64_t dq = make_sdesc(smem0 + OFF_Q, 16, 1024, kSwizzle128B);
-        const uint64_t dp = make_sdesc(smem0 + OFF_P, 16, 1024, kSwizzle128B);
-        const uint64_t dk = make_sdesc(smem0 + OFF_RING, 16, 1024, kSwizzle128B);
-        const uint64_t dv = make_sdesc(smem0 + OFF_RING, kBlk, 1024, kSwizzle128B);  // MN-major
-        const uint16_t pair = (uint16_t)(3 << rank);
-        auto commit = [&](uint64_t* bar, uint16_t to) {
-          if (lead) umma_commit_pair(bar, to);
-          __syncwarp();
-        };
-        uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
-        auto arrived = [&]() { return mbar_wait_warp(br.full(slot), phase, abort_flag); };
-        auto pass = [&]() {
-          commit(br.empty(slot), pair);
-          if (++slot == kStages) slot = 0, phase ^= 1;
-        };
-        ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
-        tc_fence_after();
-#pragma unroll 1
-        for (int i = 0; ok && i <= n; ++i) {
-          // small loops: the roles share the instruction cache
-          if (i < n) {
-            // S is free once the tile before has been read into registers
-            if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
+    for (int u = work.begin; ok && u < work.end; ++ti) {
+      const int list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
+      const int k0 = u - list0, n = min(work.end, list1) - u;
+      const bool whole = k0 == 0 && u + n == list1;
+      const int slot_out = u == work.begin ? 2 * share : 2 * share + 1;
+      const int row0 = tile.row0 + r * kRows;              // this CTA's first row of [T * H]
+      const int rows = min(kRows, tile.rows - r * kRows);  // <= 0: none
+      if constexpr (!kSoft) {
+        if (warp == 0) {
+          // -------------------------------------------------------- MMA issuer
+          if (r == 0) {
+            const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t dq = make_sdesc(smem0 + OFF_Q, 16, 1024, kSwizzle128B);
+            const uint64_t dp = make_sdesc(smem0 + OFF_P, 16, 1024, kSwizzle128B);
+            const uint64_t dk = make_sdesc(smem0 + OFF_RING, 16, 1024, kSwizzle128B);
+            const uint64_t dv = make_sdesc(smem0 + OFF_RING, kBlk, 1024, kSwizzle128B);  // MN-major
+            const uint16_t pair = (uint16_t)(3 << rank);
+            auto commit = [&](uint64_t* bar, uint16_t to) {
+              if (lead) umma_commit_pair(bar, to);
+              __syncwarp();
+            };
+            uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
+            auto arrived = [&]() { return mbar_wait_warp(br.full(slot), phase, abort_flag); };
+            auto pass = [&]() {
+              commit(br.empty(slot), pair);
+              if (++slot == kStages) slot = 0, phase ^= 1;
+            };
+            const int prefix_runs = (tile.prefix + kRun - 1) / kRun;
+            ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
             tc_fence_after();
-            // queries in TMEM and in shared memory by turns: the latter's reads and
-            // the copies into shared memory together are near its bandwidth
 #pragma unroll 1
-            for (int j = 0; j < kKStages; ++j) {
-              if (!(ok = arrived())) break;
-              const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4)), qb = dq + (uint64_t)(j * (kQBlk >> 4));
-              if (j < 4) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + j * 32 + k * 8, kb + k * 2, kIdescQK, j || k ? 1u : 0u);
-                  umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + (kBlk >> 4) + k * 2, kIdescQK, 1u);
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + k * 2, kIdescQK, 1u);
-              }
-              pass();
-            }
-            if (!ok) break;
-            commit(br.sfull(), pair);
-            ++tc;
-          }
-          if (i > 0) {
-            // the keys whose P was computed here, then those whose P comes from
-            // the other half, which takes longer
-            const uint32_t parity = (tc - (i < n ? 2 : 1)) & 1;
-#pragma unroll 1
-            for (int s = 0; s < kVStages; ++s) {
-              if (!(s & 1)) {
-                if (!(ok = mbar_wait_warp_cluster(s ? br.pother() : br.pfull(), parity, abort_flag))) break;
+            for (int i = 0; ok && i <= n; ++i) {
+              // small loops: the roles share the instruction cache
+              if (i < n) {
+                // S is free once the tile before has been read into registers
+                if (!(ok = mbar_wait_warp_cluster(br.sempty(), (tc & 1) ^ 1, abort_flag))) break;
                 tc_fence_after();
+                // queries in TMEM and in shared memory by turns: the latter's reads and
+                // the copies into shared memory together are near its bandwidth
+#pragma unroll 1
+                for (int j = 0; j < kKStages; ++j) {
+                  if (!(ok = arrived())) break;
+                  const uint64_t kb = dk + (uint64_t)(slot * (kStage >> 4)), qb = dq + (uint64_t)(j * (kQBlk >> 4));
+                  if (j < 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      umma_pair_ts_lead(lead, tm + kColS, tm + kColQ + j * 32 + k * 8, kb + k * 2, kIdescQK,
+                                        j || k ? 1u : 0u);
+                      umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + (kBlk >> 4) + k * 2, kIdescQK, 1u);
+                    }
+                  } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                      umma_pair_ss_lead(lead, tm + kColS, qb + k * 2, kb + k * 2, kIdescQK, 1u);
+                  }
+                  pass();
+                }
+                if (!ok) break;
+                commit(br.sfull(), pair);
+                ++tc;
               }
-              if (!(ok = arrived())) break;
-              const uint64_t vb = dv + (uint64_t)(slot * (kStage >> 4));
-              const uint64_t pb = dp + (uint64_t)(((rank + s) & 3) * (kQBlk >> 4));  // rank = 2c
+              if (i > 0) {
+                // the keys whose P was computed here, then those whose P comes from
+                // the other half, which takes longer
+                const uint32_t pv = tc - (i < n ? 2 : 1), parity = pv & 1;
+                auto weighted = [&](auto half, auto product) {
+#pragma unroll 1
+                  for (int s = 0; s < kVStages; ++s) {
+                    if (!(s & 1)) {
+                      if (!(ok = mbar_wait_warp_cluster(s ? br.pother() : br.pfull(), parity, abort_flag))) break;
+                      tc_fence_after();
+                      half(s >> 1);
+                    }
+                    if (!(ok = arrived())) break;
+                    const uint64_t vb = dv + (uint64_t)(slot * (kStage >> 4));
+                    const uint64_t pb = dp + (uint64_t)(((rank + s) & 3) * (kQBlk >> 4));  // rank = 2c
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_pair_ss_lead(lead, tm + kColO, pb + k * 2, vb + k * 128, kIdescPV, i > 1 || s || k ? 1u : 0u);
-              pass();
+                    for (int k = 0; k < 4; ++k) product(pb + k * 2, vb + k * 128);
+                    pass();
+                  }
+                };
+                if (2 * (k0 + i) <= prefix_runs) {
+                  weighted([](int) {},
+                           [&](uint64_t pb, uint64_t vb) {
+                             umma_pair_ss_lead(lead, tm + kColO, pb, vb, kIdescPV, 1u);
+                           });
+                } else {
+                  // Own keys: other requests' weights of them are zero, but zero times an
+                  // infinity or a NaN among the values would reach those rows.
+                  const KeyTile& keys = descs[pv % kDescs];
+                  if (!(ok = mbar_wait_warp(br.dfull(pv % kDescs), (pv / kDescs) & 1, abort_flag))) break;
+                  uint32_t off[2][8];
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const int who = keys.run[c ^ x].rows, a = who & 0xffff, b = who >> 16;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                      off[x][g] = __ballot_sync(0xffffffffu, (unsigned)(32 * g + lane - a) >= (unsigned)(b - a));
+                  }
+                  uint32_t now[8];
+                  weighted(
+                      [&](int x) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) now[g] = x ? off[1][g] : off[0][g];
+                      },
+                      [&](uint64_t pb, uint64_t vb) {
+                        umma_pair_ss_rows_lead(lead, tm + kColO, pb, vb, kIdescPV, now);
+                      });
+                }
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(br.dempty(pv % kDescs));
+                __syncwarp();
+                commit(br.pvdone(), 15);
+              }
             }
-            if (!ok) break;
-            commit(br.pvdone(), 15);
+            if (!ok) give_up();
           }
-        }
-        if (!ok) give_up();
-      }
-    } else if (warp == 1) {
-      // ---------------------------------------------------- queries and keys
-      // Query blocks b0 .. b1 - 1: those for TMEM land in P's places, free once the
-      // last list's outputs are written, the others where they stay, free once its
-      // last QK^T has run.
-      auto load_queries = [&](int b0, int b1) {
-        if (lane == 0) {
+        } else if (warp == 1) {
+          // ---------------------------------------------------- queries and keys
+          // Query blocks b0 .. b1 - 1: those for TMEM land in P's places, free once the
+          // last list's outputs are written, the others where they stay, free once its
+          // last QK^T has run.
+          auto load_queries = [&](int b0, int b1) {
+            if (lane == 0) {
 #pragma unroll 1
-          for (int b = b0; b < b1; ++b)
-            tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64, row0);
-        }
-        __syncwarp();
-      };
-      if (uc) ok = mbar_wait_warp(br.sfull(), (tc - 1) & 1, abort_flag);
-      if (ok) {
-        if (lane == 0) mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
-        __syncwarp();
-        load_queries(uc ? 4 : 0, 9);
-      }
-      const bool two = prm.ps == 32;
-      uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
-      // a stage of two blocks of 64 keys, dims d0 .. and d1 .. (one: only the first)
-      auto load = [&](int d0, int d1, int r0, int r1, bool one) -> bool {
-        if (!mbar_wait_warp(br.empty(slot), phase ^ 1, abort_flag)) return false;
-        if (lane == 0) {
-          const uint32_t bar = leader(br.full(slot)), dst = smem0 + OFF_RING + slot * kStage;
-          if (r == 0) mbar_arrive_expect_tx(br.full(slot), one ? kStage : 2 * kStage);
-          copy_block(dst, &kvmap, bar, d0, r0, r1, two);
-          if (!one) copy_block(dst + kBlk, &kvmap, bar, d1, r0, r1, two);
-        }
-        __syncwarp();
-        if (++slot == kStages) slot = 0, phase ^= 1;
-        return true;
-      };
-#pragma unroll 1
-      for (int i = 0; ok && i <= n; ++i) {
-        if (i < n) {
-          const int ds = tc % kDescs;
-          if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-          const KeyRun& mine = descs[ds].run[c];  // of which this CTA has 64 keys
-          const int r0 = mine.row[2 * r], r1 = mine.row[2 * r + 1];
-          ++tc;
-#pragma unroll 1
-          for (int j = 0; ok && j < kKStages; ++j)
-            ok = j < 4 ? load(j * 64, 256 + j * 64, r0, r1, false) : load(512, 0, r0, r1, true);
-          if (!ok) break;
-          if (uc && i == 0) {
-            if (!(ok = mbar_wait_warp(br.edone(), (uc - 1) & 1, abort_flag))) break;
-            load_queries(0, 4);
+              for (int b = b0; b < b1; ++b)
+                tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64,
+                            row0);
+            }
+            __syncwarp();
+          };
+          if (uc) ok = mbar_wait_warp(br.sfull(), (tc - 1) & 1, abort_flag);
+          if (ok) {
+            if (lane == 0) mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
+            __syncwarp();
+            load_queries(uc ? 4 : 0, 9);
           }
-        }
-        if (i > 0) {  // V of the key tile before, first of run c
-          const int ds = (tc - (i < n ? 2 : 1)) % kDescs;
+          const bool two = prm.ps == 32;
+          uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
+          // a stage of two blocks of 64 keys, dims d0 .. and d1 .. (one: only the first)
+          auto load = [&](int d0, int d1, int r0, int r1, bool one) -> bool {
+            if (!mbar_wait_warp(br.empty(slot), phase ^ 1, abort_flag)) return false;
+            if (lane == 0) {
+              const uint32_t bar = leader(br.full(slot)), dst = smem0 + OFF_RING + slot * kStage;
+              if (r == 0) mbar_arrive_expect_tx(br.full(slot), one ? kStage : 2 * kStage);
+              copy_block(dst, &kvmap, bar, d0, r0, r1, two);
+              if (!one) copy_block(dst + kBlk, &kvmap, bar, d1, r0, r1, two);
+            }
+            __syncwarp();
+            if (++slot == kStages) slot = 0, phase ^= 1;
+            return true;
+          };
 #pragma unroll 1
-          for (int s = 0; ok && s < kVStages; ++s) {
-            const KeyRun& run = descs[ds].run[c ^ (s >> 1)];
-            ok = load(c * 256 + r * 128, c * 256 + r * 128 + 64, run.row[2 * (s & 1)], run.row[2 * (s & 1) + 1], false);
+          for (int i = 0; ok && i <= n; ++i) {
+            if (i < n) {
+              const int ds = tc % kDescs;
+              if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
+              const KeyRun& mine = descs[ds].run[c];  // of which this CTA has 64 keys
+              const int r0 = mine.row[2 * r], r1 = mine.row[2 * r + 1];
+              ++tc;
+#pragma unroll 1
+              for (int j = 0; ok && j < kKStages; ++j)
+                ok = j < 4 ? load(j * 64, 256 + j * 64, r0, r1, false) : load(512, 0, r0, r1, true);
+              if (!ok) break;
+              if (uc && i == 0) {
+                if (!(ok = mbar_wait_warp(br.edone(), (uc - 1) & 1, abort_flag))) break;
+                load_queries(0, 4);
+              }
+            }
+            if (i > 0) {  // V of the key tile before, first of run c
+              const int ds = (tc - (i < n ? 2 : 1)) % kDescs;
+#pragma unroll 1
+              for (int s = 0; ok && s < kVStages; ++s) {
+                const KeyRun& run = descs[ds].run[c ^ (s >> 1)];
+                ok = load(c * 256 + r * 128, c * 256 + r * 128 + 64, run.row[2 * (s & 1)], run.row[2 * (s & 1) + 1],
+                          false);
+              }
+              if (lane == 0) mbar_arrive(br.dempty(ds));
+              __syncwarp();
+            }
           }
-          if (lane == 0) mbar_arrive(br.dempty(ds));
-          __syncwarp();
-        }
-      }
-      if (!ok) give_up();
-    } else if (warp == 2) {
-      // ----------------------------------------------------------- key tiles
-      KeyCursor cur;
-      cur.init(prm, tile, 2 * k0);
+          if (!ok) give_up();
+        } else if (warp == 2) {
+          // ----------------------------------------------------------- key tiles
+          KeyCursor cur;
+          cur.init(prm, tile, 2 * k0);
 #pragma unroll 1
-      for (int i = 0; i < n; ++i, ++tc) {
-        KeyTile t;
-        t.run[0] = cur.next();
-        t.run[1] = cur.next();
-        const int ds = tc % kDescs;
-        if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
-        if (lane == 0) {
-          descs[ds] = t;
-          mbar_arrive(br.dfull(ds));
-        }
-        __syncwarp();
-      }
-      if (!ok) give_up();
-    } else if (warp == 3) {
-      // --------------------------- P of the other half, for the MMA issuer
-      const uint32_t a_pother = leader(br.pother());
-#pragma unroll 1
-      for (int i = 0; i < n; ++i, ++tc) {
-        if (lane == 0) mbar_arrive_expect_tx(br.ppeer(), 2 * kQBlk);
-        if (!(ok = mbar_wait_warp(br.ppeer(), tc & 1, abort_flag))) break;
-        if (lane == 0) mbar_arrive_cluster(a_pother);
-        __syncwarp();
-      }
-      if (!ok) give_up();
-    } else if (warp >= 4) {
-      // ------------------------------------------------------------- softmax
-      const int q = warp & 3, hh = (warp - 4) >> 2;  // 32 TMEM lanes (rows); half of S's columns
-      const int row = q * 32 + lane;
-      const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-      const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
-      // this warp's part of P, 32 rows x 64 keys, here and at the other half
-      const uint32_t p_blk = smem0 + OFF_P + (2 * c + hh) * kQBlk, p_run = p_blk + q * 32 * 128;
-      const int my_s = mine.x, see = mine.y, prefix = tile.prefix;
-      ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
-      if (ok) {
-#pragma unroll 1
-        for (int b = 2 * hh; b < 2 * hh + 2; ++b) {
-          const uint8_t* src = smem + OFF_P + b * kQBlk + row * 128;
-          uint32_t v[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
-            v[4 * j] = x.x;
-            v[4 * j + 1] = x.y;
-            v[4 * j + 2] = x.z;
-            v[4 * j + 3] = x.w;
+          for (int i = 0; i < n; ++i, ++tc) {
+            const KeyRun run0 = cur.next(), run1 = cur.next();
+            const int ds = tc % kDescs;
+            if (!(ok = mbar_wait_warp(br.dempty(ds), ((tc / kDescs) & 1) ^ 1, abort_flag))) break;
+            if (lane == 0) {
+              descs[ds] = KeyTile{{run0, run1}};
+              mbar_arrive(br.dfull(ds));
+            }
+            __syncwarp();
           }
-          tmem_st32(tmem + lane_base + kColQ + b * 32, v);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        // The other half's copies of P write here next: of these 32 rows, after it
-        // has had this warp's maxima of the first tile.
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(leader(br.qready()));
-        __syncwarp();
-      }
-      const float sl2 = prm.scale_log2;
-      float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's columns
-      float* mx_local = reinterpret_cast<float*>(smem + OFF_LOCAL) + row;
-#pragma unroll 1
-      for (int i = 0; ok && i < n; ++i, ++tc) {
-        const int ds = tc % kDescs;
-        if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
-        const KeyRun& run = descs[ds].run[c];
-        const int p0 = run.pos + hh * 64, seg = run.seg, valid = run.valid >> (2 * hh);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(br.dempty(ds));
-        const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
-        const int lo = seg < 0 ? 0 : prefix - p0;
-        auto below = [](int k) -> uint32_t { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };
-        uint32_t mask[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) & ~below(lo - 32 * g) : 0u;
-        const bool full = __all_sync(0xffffffffu, (mask[0] & mask[1]) == 0xffffffffu);
-        if (!(ok = mbar_wait_warp(br.sfull(), tc & 1, abort_flag))) break;
-        tc_fence_after();
-        uint32_t s[2][32];
-        tmem_ld32(tmem + lane_base + kColS + 64 * hh, s[0]);
-        tmem_ld32(tmem + lane_base + kColS + 64 * hh + 32, s[1]);
-        tmem_ld_wait_regs(s[0]);
-        reg_fence(s[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(a_sempty);
-        // scaled logits, those of masked keys -inf: they are left out of maximum
-        // and weights, whatever they are
-        if (full) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[g][j] = __float_as_uint(__uint_as_float(s[g][j]) * sl2);
+          if (!ok) give_up();
         } else {
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              s[g][j] = (mask[g] >> j) & 1u ? __float_as_uint(__uint_as_float(s[g][j]) * sl2) : 0xff800000u;
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[g][j]), __uint_as_float(s[g][j + 1]));
-        // The row's maximum over the tile: first with the warp of the other
-        // columns, then one of the two tells the CTA of the other keys. The other
-        // CTA sends tile i + 2's when PV(i) has run, so after this one has read
-        // tile i's: two places are enough. One local place is: the second barrier
-        // is passed when both warps have read. All waits have limits, which named
-        // barriers' have not.
-        mx_local[hh * kRows] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(br.local(q));
-        if (!(ok = mbar_wait_warp(br.local(q), tc & 1, abort_flag))) break;
-        const float mine = fmaxf(mx_local[0], mx_local[kRows]);
-        const uint32_t a_mx = smem0 + OFF_REMOTE + ((tc & 1) * kRows + row) * 4;
-        uint64_t* rbar = br.remote(q, tc & 1);
-        if (hh == 0) st_async_f32(other(a_mx), mine, other(smem_u32(rbar)));
-        __syncwarp();
-        if (lane == 0) {
-          if (hh == 0) mbar_arrive_expect_tx(rbar, 32 * 4);
-          else mbar_arrive(rbar);
-        }
-        if (!(ok = mbar_wait_warp(rbar, (tc >> 1) & 1, abort_flag))) break;
-        const float m_new = max3(m_run, mine, *reinterpret_cast<volatile float*>(smem + (a_mx - smem0)));
-        const bool need = m_new > m_run + kRescaleThreshold;  // also true when m_run == -inf
-        const float m_use = need ? m_new : m_run;
-        const float alpha = need ? exp2f(m_run - m_new) : 1.f;
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;  // a row without keys so far: its weights are 2^-inf
-        const uint64_t nm2 = f32x2_pack(-m_sub, -m_sub);
-        uint64_t ps2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x0, x1;
-            f32x2_unpack(fadd2(f32x2_pack(__uint_as_float(s[g][2 * k]), __uint_as_float(s[g][2 * k + 1])), nm2), x0, x1);
-            x0 = ex2_approx(x0);
-            x1 = ex2_approx(x1);
-            ps2[k & 1] = fadd2(ps2[k & 1], f32x2_pack(x0, x1));
-            __nv_bfloat162 b2 = __floats2bfloat162_rn(x0, x1);  // P as a bf16 operand
-            s[g][k] = *reinterpret_cast<uint32_t*>(&b2);
-          }
-        // P's places, here and at the other half, and O are free once both
-        // pairs' PV of the tile before have run
-        if (i > 0 && !(ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag))) break;
-        if (i > 0 && __any_sync(0xffffffffu, need)) {
-          tc_fence_after();
+          // --------------------------- P of the other half, for the MMA issuer
+          const uint32_t a_pother = leader(br.pother());
 #pragma unroll 1
-          for (int k = 4 * hh; k < 4 * hh + 4; ++k) {
-            uint32_t ov[32];
-            tmem_ld32(tmem + lane_base + kColO + k * 32, ov);
-            tmem_ld_wait_regs(ov);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-            tmem_st32(tmem + lane_base + kColO + k * 32, ov);
+          for (int i = 0; i < n; ++i, ++tc) {
+            if (lane == 0) mbar_arrive_expect_tx(br.ppeer(), 2 * kQBlk);
+            if (!(ok = mbar_wait_warp(br.ppeer(), tc & 1, abort_flag))) break;
+            if (lane == 0) mbar_arrive_cluster(a_pother);
+            __syncwarp();
           }
+          if (!ok) give_up();
+        }
+      } else {
+        // ------------------------------------------------------------- softmax
+        const int q = warp & 3, hh = (warp - 4) >> 2;  // 32 TMEM lanes (rows); half of S's columns
+        const int row = q * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const uint32_t a_sempty = leader(br.sempty()), a_pfull = leader(br.pfull());
+        // this warp's part of P, 32 rows x 64 keys, here and at the other half
+        const uint32_t p_blk = smem0 + OFF_P + (2 * c + hh) * kQBlk, p_run = p_blk + q * 32 * 128;
+        const int my_s = mine.x, see = mine.y, prefix = tile.prefix;
+        ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
+        if (ok) {
+#pragma unroll 1
+          for (int b = 2 * hh; b < 2 * hh + 2; ++b) {
+            const uint8_t* src = smem + OFF_P + b * kQBlk + row * 128;
+            uint32_t v[32];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 x = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
+              v[4 * j] = x.x;
+              v[4 * j + 1] = x.y;
+              v[4 * j + 2] = x.z;
+              v[4 * j + 3] = x.w;
+            }
+            tmem_st32(tmem + lane_base + kColQ + b * 32, v);
+          }
+          // PV adds to O from the first tile on, as a request's own keys do not reach all rows
+          uint32_t zero[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) zero[j] = 0u;
+#pragma unroll 1
+          for (int k = 4 * hh; k < 4 * hh + 4; ++k) tmem_st32(tmem + lane_base + kColO + k * 32, zero);
           tmem_st_wait();
           tc_fence_before();
+          // The other half's copies of P write here next: of these 32 rows, after it
+          // has had this warp's maxima of the first tile.
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader(br.qready()));
+          __syncwarp();
         }
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            st_shared_v4(p_blk + sw128_offset(row, g * 4 + k), s[g][4 * k], s[g][4 * k + 1], s[g][4 * k + 2],
-                         s[g][4 * k + 3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          bulk_store_cluster(other(p_run), p_run, 32 * 128, other(smem_u32(br.ppeer())));
-          mbar_arrive_cluster(a_pfull);
-        }
-        float pa, pb;
-        f32x2_unpack(fadd2(ps2[0], ps2[1]), pa, pb);
-        l_run = l_run * alpha + (pa + pb);
-        m_run = m_use;
-      }
-      // ------------------------------------------------------------ epilogue
-      if (ok && u + n < work.end) {  // while the last PV runs: the next list's row
-        tile = prm.tiles[ti + 1];
-        mine = row_of(tile);
-      }
-      ok = ok && mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
-      // P's places are idle now, on both sides. The sum of a row's weights comes in
-      // four parts, to the start of this CTA's own; the other half's, of the rows
-      // that the other CTA's warps of this number write, stage the outputs.
-      if (ok) {
-        const uint32_t a_l = OFF_P + 2 * c * kQBlk + ((2 * c + hh) * kRows + row) * 4;
-        const uint32_t a_there = OFF_P + 2 * (1 - c) * kQBlk + ((2 * c + hh) * kRows + row) * 4;
-        st_async_f32(other(smem0 + a_there), l_run, other(smem_u32(br.lbar())));
-        *reinterpret_cast<float*>(smem + a_l) = l_run;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(br.lbar(), 32 * 4);
-        ok = mbar_wait_warp(br.lbar(), uc & 1, abort_flag);
-      }
-      if (ok) {
-        tc_fence_after();
-        const volatile float* lp = reinterpret_cast<const volatile float*>(smem + OFF_P + 2 * c * kQBlk) + row;
-        const float l = (lp[0] + lp[kRows]) + (lp[2 * kRows] + lp[3 * kRows]);
-        const bool some = l != 0.f;  // a sum of weights is never negative; NaN counts
-        const float inv_l = some ? 1.f / l : 0.f;
-        const float lse2 = some ? m_run + log2f(l) : -INFINITY;
-        // 128 bytes of 32 rows at a time, chunks of 16 bytes swizzled
-        const int w0 = q * 32, nw = min(32, rows - w0);
-        const uint32_t stg = smem0 + OFF_P + (2 * (1 - c) + hh) * kQBlk + w0 * 128;
-        const uint32_t col = tmem + lane_base + kColO + 128 * hh;
-        const size_t part_row = (size_t)slot_out * kTileRows + r * kRows + w0;  // or, undivided, the output's
-        uint8_t* out = whole ? reinterpret_cast<uint8_t*>(prm.o + ((size_t)row0 + w0) * kDv + c * 256 + hh * 128)
-                             : reinterpret_cast<uint8_t*>(prm.part_o + part_row * kDv + c * 256 + hh * 128);
-        const size_t pitch = whole ? kDv * 2 : kDv * 4;
+        const float sl2 = prm.scale_log2;
+        float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's columns
+        float* mx_local = reinterpret_cast<float*>(smem + OFF_LOCAL) + row;
 #pragma unroll 1
-        for (int c0 = 0; c0 < 128; out += 128) {
-          uint32_t o[32], v[32];
-          tmem_ld32(col + c0, o);
-          tmem_ld_wait_regs(o);
-          if (whole) {
-            auto pack = [&](int at) {
+        for (int i = 0; ok && i < n; ++i, ++tc) {
+          const int ds = tc % kDescs;
+          if (!(ok = mbar_wait_warp(br.dfull(ds), (tc / kDescs) & 1, abort_flag))) break;
+          const KeyRun& run = descs[ds].run[c];
+          const int p0 = run.pos + hh * 64, seg = run.seg, valid = run.valid >> (2 * hh);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(br.dempty(ds));
+          const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
+          const int lo = seg < 0 ? 0 : prefix - p0;
+          uint32_t mask[2];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv_l,
-                                                          __uint_as_float(o[2 * j + 1]) * inv_l);
-                v[at + j] = *reinterpret_cast<uint32_t*>(&b2);
-              }
-            };
-            pack(0);
-            tmem_ld32(col + c0 + 32, o);
-            tmem_ld_wait_regs(o);
-            pack(16);
-            c0 += 64;
+          for (int g = 0; g < 2; ++g) mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) & ~below(lo - 32 * g) : 0u;
+          const bool full = __all_sync(0xffffffffu, (mask[0] & mask[1]) == 0xffffffffu);
+          if (!(ok = mbar_wait_warp(br.sfull(), tc & 1, abort_flag))) break;
+          tc_fence_after();
+          uint32_t s[2][32];
+          tmem_ld32(tmem + lane_base + kColS + 64 * hh, s[0]);
+          tmem_ld32(tmem + lane_base + kColS + 64 * hh + 32, s[1]);
+          tmem_ld_wait_regs(s[0]);
+          reg_fence(s[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(a_sempty);
+          // scaled logits, those of masked keys -inf: they are left out of maximum
+          // and weights, whatever they are
+          if (full) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[g][j] = __float_as_uint(__uint_as_float(s[g][j]) * sl2);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(o[j]) * inv_l);
-            c0 += 32;
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                s[g][j] = (mask[g] >> j) & 1u ? __float_as_uint(__uint_as_float(s[g][j]) * sl2) : 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], __uint_as_float(s[g][j]), __uint_as_float(s[g][j + 1]));
+          // The row's maximum over the tile: first with the warp of the other
+          // columns, then one of the two tells the CTA of the other keys. The other
+          // CTA sends tile i + 2's when PV(i) has run, so after this one has read
+          // tile i's: two places are enough. One local place is: the second barrier
+          // is passed when both warps have read. All waits have limits, which named
+          // barriers' have not.
+          mx_local[hh * kRows] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(br.local(q));
+          if (!(ok = mbar_wait_warp(br.local(q), tc & 1, abort_flag))) break;
+          const float mine = fmaxf(mx_local[0], mx_local[kRows]);
+          const uint32_t a_mx = smem0 + OFF_REMOTE + ((tc & 1) * kRows + row) * 4;
+          uint64_t* rbar = br.remote(q, tc & 1);
+          if (hh == 0) st_async_f32(other(a_mx), mine, other(smem_u32(rbar)));
+          __syncwarp();
+          if (lane == 0) {
+            if (hh == 0) mbar_arrive_expect_tx(rbar, 32 * 4);
+            else mbar_arrive(rbar);
+          }
+          if (!(ok = mbar_wait_warp(rbar, (tc >> 1) & 1, abort_flag))) break;
+          const float m_new = max3(m_run, mine, *reinterpret_cast<volatile float*>(smem + (a_mx - smem0)));
+          const bool need = m_new > m_run + kRescaleThreshold;  // also true when m_run == -inf
+          const float m_use = need ? m_new : m_run;
+          const float alpha = need ? exp2f(m_run - m_new) : 1.f;
+          const float m_sub = m_use == -INFINITY ? 0.f : m_use;  // a row without keys so far: its weights are 2^-inf
+          const uint64_t nm2 = f32x2_pack(-m_sub, -m_sub);
+          uint64_t ps2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x0, x1;
+              f32x2_unpack(fadd2(f32x2_pack(__uint_as_float(s[g][2 * k]), __uint_as_float(s[g][2 * k + 1])), nm2), x0,
+                           x1);
+              x0 = ex2_approx(x0);
+              x1 = ex2_approx(x1);
+              ps2[k & 1] = fadd2(ps2[k & 1], f32x2_pack(x0, x1));
+              __nv_bfloat162 b2 = __floats2bfloat162_rn(x0, x1);  // P as a bf16 operand
+              s[g][k] = *reinterpret_cast<uint32_t*>(&b2);
+            }
+          // P's places, here and at the other half, and O are free once both
+          // pairs' PV of the tile before have run
+          if (i > 0 && !(ok = mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag))) break;
+          if (i > 0 && __any_sync(0xffffffffu, need)) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 4 * hh; k < 4 * hh + 4; ++k) {
+              uint32_t ov[32];
+              tmem_ld32(tmem + lane_base + kColO + k * 32, ov);
+              tmem_ld_wait_regs(ov);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+              tmem_st32(tmem + lane_base + kColO + k * 32, ov);
+            }
+            tmem_st_wait();
+            tc_fence_before();
           }
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared_v4(stg + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          __syncwarp();
+          for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int k = 4 * j + (lane >> 3);
-            if (k < nw)
-              *reinterpret_cast<uint4*>(out + k * pitch + (lane & 7) * 16) =
-                  *reinterpret_cast<const uint4*>(smem + (stg - smem0) + sw128_offset(k, lane & 7));
-          }
+            for (int k = 0; k < 4; ++k)
+              st_shared_v4(p_blk + sw128_offset(row, g * 4 + k), s[g][4 * k], s[g][4 * k + 1], s[g][4 * k + 2],
+                           s[g][4 * k + 3]);
+          fence_proxy_async_smem();
           __syncwarp();
+          if (lane == 0) {
+            bulk_store_cluster(other(p_run), p_run, 32 * 128, other(smem_u32(br.ppeer())));
+            mbar_arrive_cluster(a_pfull);
+          }
+          float pa, pb;
+          f32x2_unpack(fadd2(ps2[0], ps2[1]), pa, pb);
+          l_run = l_run * alpha + (pa + pb);
+          m_run = m_use;
         }
-        if (c == 0 && hh == 0 && row < rows) {
-          if (!whole) prm.part_lse[part_row + lane] = lse2;
-          else if (prm.lse) prm.lse[(size_t)row0 + row] = lse2 * 0.69314718055994531f;
+        // ------------------------------------------------------------ epilogue
+        if (ok && u + n < work.end) {  // while the last PV runs: the next list's row
+          tile = prm.tiles[ti + 1];
+          mine = row_of(tile);
         }
-        tc_fence_before();
-        fence_proxy_async_smem();  // queries are copied to P's places next
-        __syncwarp();
-        if (lane == 0) mbar_arrive(br.edone());
-        __syncwarp();
-      } else {
-        give_up();
+        ok = ok && mbar_wait_warp(br.pvdone(), (tc - 1) & 1, abort_flag);
+        // P's places are idle now, on both sides. The sum of a row's weights comes in
+        // four parts, to the start of this CTA's own; the other half's, of the rows
+        // that the other CTA's warps of this number write, stage the outputs.
+        if (ok) {
+          const uint32_t a_l = OFF_P + 2 * c * kQBlk + ((2 * c + hh) * kRows + row) * 4;
+          const uint32_t a_there = OFF_P + 2 * (1 - c) * kQBlk + ((2 * c + hh) * kRows + row) * 4;
+          st_async_f32(other(smem0 + a_there), l_run, other(smem_u32(br.lbar())));
+          *reinterpret_cast<float*>(smem + a_l) = l_run;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(br.lbar(), 32 * 4);
+          ok = mbar_wait_warp(br.lbar(), uc & 1, abort_flag);
+        }
+        if (ok) {
+          tc_fence_after();
+          const volatile float* lp = reinterpret_cast<const volatile float*>(smem + OFF_P + 2 * c * kQBlk) + row;
+          const float l = (lp[0] + lp[kRows]) + (lp[2 * kRows] + lp[3 * kRows]);
+          const bool some = l != 0.f;  // a sum of weights is never negative; NaN counts
+          const float inv_l = some ? 1.f / l : 0.f;
+          const float lse2 = some ? m_run + log2f(l) : -INFINITY;
+          // 128 bytes of 32 rows at a time, chunks of 16 bytes swizzled
+          const int w0 = q * 32, nw = min(32, rows - w0);
+          const uint32_t stg = smem0 + OFF_P + (2 * (1 - c) + hh) * kQBlk + w0 * 128;
+          const uint32_t col = tmem + lane_base + kColO + 128 * hh;
+          const size_t part_row = (size_t)slot_out * kTileRows + r * kRows + w0;  // or, undivided, the output's
+          uint8_t* out = whole ? reinterpret_cast<uint8_t*>(prm.o + ((size_t)row0 + w0) * kDv + c * 256 + hh * 128)
+                               : reinterpret_cast<uint8_t*>(prm.part_o + part_row * kDv + c * 256 + hh * 128);
+          const size_t pitch = whole ? kDv * 2 : kDv * 4;
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; out += 128) {
+            uint32_t o[32], v[32];
+            tmem_ld32(col + c0, o);
+            tmem_ld_wait_regs(o);
+            if (whole) {
+              auto pack = [&](int at) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv_l,
+                                                            __uint_as_float(o[2 * j + 1]) * inv_l);
+                  v[at + j] = *reinterpret_cast<uint32_t*>(&b2);
+                }
+              };
+              pack(0);
+              tmem_ld32(col + c0 + 32, o);
+              tmem_ld_wait_regs(o);
+              pack(16);
+              c0 += 64;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(o[j]) * inv_l);
+              c0 += 32;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(stg + sw128_offset(lane, j), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int k = 4 * j + (lane >> 3);
+              if (k < nw)
+                *reinterpret_cast<uint4*>(out + k * pitch + (lane & 7) * 16) =
+                    *reinterpret_cast<const uint4*>(smem + (stg - smem0) + sw128_offset(k, lane & 7));
+            }
+            __syncwarp();
+          }
+          if (c == 0 && hh == 0 && row < rows) {
+            if (!whole) prm.part_lse[part_row + lane] = lse2;
+            else if (prm.lse) prm.lse[(size_t)row0 + row] = lse2 * 0.69314718055994531f;
+          }
+          tc_fence_before();
+          fence_proxy_async_smem();  // queries are copied to P's places next
+          __syncwarp();
+          if (lane == 0) mbar_arrive(br.edone());
+          __syncwarp();
+        } else {
+          give_up();
+        }
+      }
+      // No barrier here: the next list's first keys are fetched, and its queries,
+      // while this one's outputs are written. Its first QK^T waits for the softmax
+      // warps of the pair (qready), so for their reads of O; its first P comes after
+      // an exchange of maxima with the warps whose places it writes.
+      fc += (kKStages + kVStages) * n;
+      u += n;
+      ++uc;
+      if constexpr (!kSoft) {
+        if (ok && u < work.end) tile = prm.tiles[ti + 1];
       }
     }
-    // No barrier here: the next list's first keys are fetched, and its queries,
-    // while this one's outputs are written. Its first QK^T waits for the softmax
-    // warps of the pair (qready), so for their reads of O; its first P comes after
-    // an exchange of maxima with the warps whose places it writes.
-    fc += (kKStages + kVStages) * n;
-    u += n;
-    ++uc;
-    if (warp < 4 && ok && u < work.end) tile = prm.tiles[ti + 1];
+  };
+  if (warp < 4) {
+    regs_dec<kHelperRegs>();
+    lists(std::false_type{});
+  } else {
+    regs_inc<kSoftRegs>();
+    lists(std::true_type{});
   }
   __syncwarp();
   cluster_sync_all();
@@ -1045,6 +1128,21 @@ int clusters_at_once() {
   cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+// The kernel's launch has the registers that its warps share out later: a CTA that
+// waits for more than there are would wait forever.
+bool registers_fit() {
+  static std::atomic<int> known{-1};
+  int fit = known.load(std::memory_order_relaxed);
+  if (fit >= 0) return fit;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, prefix_mla_kernel) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  fit = a.numRegs >= kLaunchRegs;
+  known.store(fit, std::memory_order_relaxed);
+  return fit;
+}
 struct Layout {
   size_t tile_base, tiles, unit_base, share, part_o, part_lse, bytes;
 };
@@ -1068,10 +1166,13 @@ Layout layout_of(int T, int H, int G) {
 }
 }  // namespace
 
+// Key tiles of a row tile, at most: it has rows of ceil(256 / H) + 1 requests or
+// fewer, and the prefix.
+static long long max_units_of(int H, int max_kv) {
+  return (2LL + (kTileRows + H - 1) / H) * ((long long)max_kv / (2 * kRun) + 4);
+}
 bool prefix_units_fit(int T, int H, int G, int max_kv) {
-  // a row tile has rows of at most ceil(256 / H) + 1 requests, and the prefix
-  const long long lists = 2 + (kTileRows + H - 1) / H, keys = (long long)max_kv / (2 * kRun) + 4;
-  return max_tiles_of(T, H, G) * lists * (keys + kListCost) < (1LL << 31);
+  return max_tiles_of(T, H, G) * (max_units_of(H, max_kv) + kListCost) < (1LL << 31);
 }
 
 size_t prefix_workspace_bytes(int T, int H, int G) { return layout_of(T, H, G).bytes; }
@@ -1086,10 +1187,11 @@ int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
   prm.part_o = reinterpret_cast<float*>(w + l.part_o);
   prm.part_lse = reinterpret_cast<float*>(w + l.part_lse);
   prm.max_tiles = max_tiles_of(prm.T, prm.H, prm.G);
+  prm.max_units = (int)max_units_of(prm.H, prm.max_kv);
   CUtensorMap kvmap, qmap;
   if (!encode_bf16_2d(&kvmap, prm.kv, (uint64_t)prm.P * prm.ps, (uint64_t)prm.row_stride, std::min(prm.ps, 64),
                       kDk) ||
-      !encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kRows, kDk))
+      !encode_bf16_2d(&qmap, prm.q, (uint64_t)prm.T * prm.H, kDk, kRows, kDk) || !registers_fit())
     return DSA_ERR_CUDA;
   set_smem_attr_once(reinterpret_cast<const void*>(prefix_mla_kernel), kSmem);
   prm.shares = clusters_at_once();

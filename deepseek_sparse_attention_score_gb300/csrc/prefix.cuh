@@ -50,7 +50,7 @@ struct PrefixParams {
   PrefixShare* share;    // [shares], those past the work empty
   float* part_o;    // [2 * shares][256][512]
   float* part_lse;  // [2 * shares][256], log2
-  int max_tiles, shares;
+  int max_tiles, max_units, shares;  // max_units: key tiles of one row tile
 };
 
 // Whether all key tiles of a call, at most, can be counted in 31 bits.

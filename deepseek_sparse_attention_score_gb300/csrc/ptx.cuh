@@ -99,6 +99,17 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) 
   return true;
 }
 
+// A warpgroup's registers a thread from here on: fewer, or more. What is taken has
+// to have been given back by others of the registers that the CTA was launched with.
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ------------------------------------------------- pairs of CTAs (clusters)
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -319,10 +330,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 __device__ __forceinline__ bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   bool ok = mbar_try_wait_cluster(bar, parity);
-  const long long t0 = clock64();
-  while (!ok && !*abort_flag) {
-    ok = mbar_try_wait_cluster(bar, parity);
-    if (!ok && clock64() - t0 > kWaitTimeoutClocks) *abort_flag = 1;
+  if (!ok) {
+    const long long t0 = clock64();
+    while (!ok && !*abort_flag) {
+      ok = mbar_try_wait_cluster(bar, parity);
+      if (!ok && clock64() - t0 > kWaitTimeoutClocks) *abort_flag = 1;
+    }
   }
   return __all_sync(0xffffffffu, ok);
 }
@@ -374,6 +387,19 @@ __device__ __forceinline__ void umma_pair_ts_lead(uint32_t lead, uint32_t d_tmem
       "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// D += A B^T in the rows whose bit in off is 0, word g for rows 32 g .. of the
+// 256; the other rows of D stay as they are.
+__device__ __forceinline__ void umma_pair_ss_rows_lead(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                       uint32_t idesc, const uint32_t (&off)[8]) {
+  asm volatile(
+      "{\n\t.reg .pred q, t;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, t;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(lead), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
+      "r"(off[5]), "r"(off[6]), "r"(off[7])
       : "memory");
 }
 // Arrive once on this barrier of each CTA in `mask` when every pair MMA issued

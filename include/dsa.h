@@ -647,11 +647,13 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * out of order or out of range, whose rows are not written.
  * Cache contents: of pages that hold a visible position runs of min(ps, 64) rows
  * are read; rows of a run past the visible length must hold finite values (see
- * dsa_sparse_mla_decode).
+ * dsa_sparse_mla_decode), and so must a group's prefix for each of its requests,
+ * though it end or have tokens inside it. A request's own rows, from the prefix
+ * on, reach its own outputs alone, whatever they hold.
  * Outputs are the same on every run.
  * Supported: as dsa_dense_mla; 1 <= G <= 2^20, T * H < 2^31 - 2^16, |sm_scale| *
  * 1.5 finite in fp32, max_kv <= 2^30 and with (T * H / 256 + 1 + G) * (2 +
- * ceil(256 / H)) * (max_kv / 256 + 6) below 2^31 (65535 tokens of 128 heads: two
+ * ceil(256 / H)) * (max_kv / 256 + 6) below 2^31 (65535 tokens of 128 heads: four
  * million keys).
  * ------------------------------------------------------------------------ */
 DSA_API size_t dsa_prefix_mla_workspace_size(int T, int H, int G);

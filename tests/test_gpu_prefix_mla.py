@@ -187,9 +187,7 @@ def test_as_the_window_call(dsa):
     assert (o.float() - o2.float()).abs().max() < 2e-2 and (lse - lse2).abs().max() < 1e-4
 
 
-def test_nan_and_infinities(dsa):
-    """NaN queries stay in their rows; a visible NaN key reaches the rows that
-    see it and no others."""
+def test_nan_queries_stay_in_their_rows(dsa):
     b = Batch([(130, [(1, 3), (3, 90)])], 16)
     o, lse = _check(dsa, b)
     b.q[1, 3, 5] = float("nan")
@@ -198,6 +196,34 @@ def test_nan_and_infinities(dsa):
     assert o2[1, 3].isnan().all() and lse2[1, 3].isnan()
     o2[1, 3], lse2[1, 3] = o[1, 3], lse[1, 3]
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("groups,H", [
+    ([(130, [(1, 3), (1, 90), (1, 600), (2, 40)])], 16), ([(0, [(1, 30), (1, 300), (1, 5)])], 40),
+    ([(64, [(1, 500)] * 7), (300, [(1, 9)] * 3)], 5), ([(256, [(1, 200), (1, 200)])], 128),
+    ([(10, [(1, 4000), (1, 3), (1, 4000)])], 16),  # lists that start with own keys
+    ([(20, [(1, 1)] * 100)], 1),
+], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_values_of_one_request_stay_with_it(dsa, groups, H, bad):
+    """An infinity or a NaN among a request's own keys reaches its own outputs
+    and none of the other requests', which share its row tile."""
+    b = Batch(groups, H)
+    o, lse = _check(dsa, b)
+    first = np.cumsum([0] + b.q_lens)
+    for s in {1, len(b.seq) - 1}:
+        last = b.seq[s] - 1
+        page = b.kv[b.table[s][last // 64]]
+        old = page[last % 64].clone()
+        page[last % 64, 3:512:7] = bad
+        o2, lse2 = b.call(dsa)
+        torch.cuda.synchronize()
+        own = slice(int(first[s + 1]) - 1, int(first[s + 1]))  # its last token sees the position
+        assert not o2[own].isfinite().all(-1).any()
+        others = torch.ones(b.T, dtype=torch.bool, device="cuda")
+        others[int(first[s]): int(first[s + 1])] = False
+        assert torch.equal(o[others], o2[others]) and torch.equal(lse[others], lse2[others])
+        page[last % 64] = old
 
 
 def test_empty_calls(dsa):
