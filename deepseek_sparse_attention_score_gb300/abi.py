@@ -994,7 +994,9 @@ def dsa_prefix_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, prefix_
         raise ValueError(f"without group_offsets there is one prefix, got {G}")
     o, lse = _attend_out(dev, T, H, Dv, o, lse, want_lse)
     if ws is None:
-        ws = torch.empty(dsa_prefix_mla_workspace_size(T, H, G), dtype=torch.uint8, device=dev)
+        with torch.cuda.device(dev):  # its size depends on the device
+            nb = dsa_prefix_mla_workspace_size(T, H, G)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     elif ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
     _launch(dev, "dsa_prefix_mla", _addr(q), _addr(kv), row_stride, *meta, a_prefix, a_groups, G, int(max_kv), T, S, P,

@@ -35,6 +35,9 @@ def _call(lib, **bad):
     (dict(groups=None), INVALID), (dict(G=0), INVALID), (dict(G=-1), INVALID), (dict(G=(1 << 20) + 1), UNSUPPORTED),
     (dict(max_kv=0), INVALID), (dict(max_kv=(1 << 30) + 1), UNSUPPORTED), (dict(T=-1), INVALID), (dict(S=0), INVALID),
     (dict(T=65536), UNSUPPORTED), (dict(T=65535, H=32768), UNSUPPORTED), (dict(ps=16), UNSUPPORTED),
+    # key tiles of all row tiles together: at most 2^31, which four million keys keep here
+    (dict(T=65535, H=128, max_kv=1 << 23), UNSUPPORTED), (dict(T=65535, H=128, max_kv=4000000, ws=None), WORKSPACE),
+    (dict(T=300, H=1, max_kv=1 << 30), UNSUPPORTED), (dict(T=1, H=1, max_kv=1 << 30, ws=None, G=1), UNSUPPORTED),
     (dict(P=1 << 26), UNSUPPORTED), (dict(H=-1), INVALID), (dict(Dk=512), UNSUPPORTED), (dict(Dv=576), UNSUPPORTED),
     (dict(row_stride=600), UNSUPPORTED), (dict(q=8), ALIGNMENT), (dict(kv=24), ALIGNMENT), (dict(o=4), ALIGNMENT),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=3e38), INVALID),
