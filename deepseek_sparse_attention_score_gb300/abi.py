@@ -994,8 +994,11 @@ def dsa_prefix_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, prefix_
         raise ValueError(f"without group_offsets there is one prefix, got {G}")
     o, lse = _attend_out(dev, T, H, Dv, o, lse, want_lse)
     if ws is None:
-        with torch.cuda.device(dev):  # its size depends on the device
+        if dev.type != "cuda" or torch.cuda.current_device() == dev.index:
             nb = dsa_prefix_mla_workspace_size(T, H, G)
+        else:
+            with torch.cuda.device(dev):  # the size depends on the device
+                nb = dsa_prefix_mla_workspace_size(T, H, G)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     elif ws.device != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")

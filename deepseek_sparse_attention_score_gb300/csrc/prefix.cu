@@ -830,17 +830,21 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_cluster(a_sempty);
           // scaled logits, those of masked keys -inf: they are left out of maximum
           // and weights, whatever they are
-          if (full) {
+          const uint64_t sl22 = f32x2_pack(sl2, sl2);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float x0, x1;
+              f32x2_unpack(fmul2(f32x2_pack(__uint_as_float(s[g][j]), __uint_as_float(s[g][j + 1])), sl22), x0, x1);
+              s[g][j] = __float_as_uint(x0);
+              s[g][j + 1] = __float_as_uint(x1);
+            }
+          if (!full) {
 #pragma unroll
             for (int g = 0; g < 2; ++g)
 #pragma unroll
-              for (int j = 0; j < 32; ++j) s[g][j] = __float_as_uint(__uint_as_float(s[g][j]) * sl2);
-          } else {
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                s[g][j] = (mask[g] >> j) & 1u ? __float_as_uint(__uint_as_float(s[g][j]) * sl2) : 0xff800000u;
+              for (int j = 0; j < 32; ++j) s[g][j] = (mask[g] >> j) & 1u ? s[g][j] : 0xff800000u;
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
