@@ -30,6 +30,18 @@
 //
 // Per key tile i: QK^T(i), then PV(i - 1). S is read into registers at once and P
 // goes to shared memory, so that QK^T(i + 1) runs beside the softmax of tile i.
+//
+// What bounds it: the tensor pipe, 4352 clocks per key tile of 256 rows x 256 keys,
+// with shared memory next to it (per CTA about 512 KB in and out, 4000 clocks). A key
+// tile takes 2.84 us, and 36 clusters run at once: 1.81 PFLOP/s, 94 % of the card's
+// measured rate. Another 20 us a call is not products: the plan 4-5, the first
+// queries and keys 5, the last outputs 5, the merge 6. Measured on 32 requests x 16384
+// shared keys, 128 heads (112 us in all, floor 77), step by step: pairs whose CTAs
+// compute S twice 161, clusters that share it 131, PV in order of arrival of P 127, the
+// plan's lengths in shared memory 121, keys resolved by a warp of their own 114.
+// Elsewhere: 64 requests x 32768 keys of 16 heads 84 us (39: the own keys of 16
+// requests in a row tile are each computed for all of its rows), 4 x 131072 keys of 128
+// heads 113 (77), ragged extends of 500 tokens 121 (78), two short requests 17 (latency).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -160,6 +172,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024;
 // A list that starts inside a share costs about as much as this many key tiles:
 // the pipeline runs empty, the outputs are written, the next queries fetched.
+// 4 / 3 / 2 / 1 took 113.5 / 112.3 / 112.1 / 115.1 us on the 32 x 16384 keys and 54.1 /
+// 54.1 / 52.6 / 55.0 on five groups of unlike size.
 constexpr int kListCost = 2;
 constexpr int kMaxShares = 128;
 struct PlanGroup {
@@ -1041,15 +1055,25 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// Merges a list that was divided: block x takes the one that the end of share x
-// is the first to cut; a warp takes half a row.
-constexpr int kMergeWarps = 8;
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
+// Merges the lists that were divided: block x takes the x-th of them, which the end of
+// some share is the first to cut; a warp takes half a row. About 8 us at 32 x 16384 keys:
+// 2304 blocks, some of them idle, took 1 us more, whole rows or loops over rows as much.
+constexpr int kMergeWarps = 8, kMergeCtas = 4;  // per SM
+__global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int k0 = blockIdx.x, lane = lane_id();
+  const int lane = lane_id();
+  int x = blockIdx.x, k0 = -1;
+#pragma unroll
+  for (int j = 0; j < kMaxShares / 32; ++j) {
+    const int k = 32 * j + lane;
+    const uint32_t cuts = __ballot_sync(0xffffffffu, k < p.shares && p.share[k].cut >= 0);
+    const uint32_t it = __ballot_sync(0xffffffffu, (cuts >> lane & 1) && __popc(cuts & below(lane)) == x);
+    if (it) k0 = 32 * j + __ffs(it) - 1;
+    x -= __popc(cuts);
+  }
+  if (k0 < 0) return;
   const PrefixShare share = p.share[k0];
-  if (share.cut < 0) return;
   const PrefixTile tile = p.tiles[share.cut];
   const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1, k1 = share.last;
   if (r >= tile.rows) return;
@@ -1060,7 +1084,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   auto load = [&](int k) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + row_of(min(k + j, k1)) * kDv + half * 256);
+      if (k + j > k1) break;
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + row_of(k + j) * kDv + half * 256);
       y[j][0] = src[lane];
       y[j][1] = src[32 + lane];
     }
@@ -1201,8 +1226,8 @@ int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
   prm.shares = clusters_at_once();
   DSA_LAUNCH_PDL(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, prm);
   DSA_LAUNCH_PDL(prefix_mla_kernel, dim3(4 * prm.shares), dim3(kThreads), kSmem, stream, prm, kvmap, qmap);
-  DSA_LAUNCH_PDL(prefix_merge_kernel, dim3(prm.shares, 2 * kTileRows / kMergeWarps), dim3(kMergeWarps * 32), 0, stream,
-                 prm);
+  DSA_LAUNCH_PDL(prefix_merge_kernel, dim3(std::min(prm.shares, prm.max_tiles), 2 * kTileRows / kMergeWarps),
+                 dim3(kMergeWarps * 32), 0, stream, prm);
   return DSA_OK;
 }
 
