@@ -35,13 +35,14 @@
 // with shared memory next to it (per CTA about 512 KB in and out, 4000 clocks). A key
 // tile takes 2.84 us, and 36 clusters run at once: 1.81 PFLOP/s, 94 % of the card's
 // measured rate. Another 20 us a call is not products: the plan 4-5, the first
-// queries and keys 5, the last outputs 5, the merge 6. Measured on 32 requests x 16384
-// shared keys, 128 heads (112 us in all, floor 77), step by step: pairs whose CTAs
+// queries and keys 5, the last outputs 5, the merge 7. Measured on 32 requests x 16384
+// shared keys, 128 heads (110 us in all, floor 77), step by step: pairs whose CTAs
 // compute S twice 161, clusters that share it 131, PV in order of arrival of P 127, the
-// plan's lengths in shared memory 121, keys resolved by a warp of their own 114.
-// Elsewhere: 64 requests x 32768 keys of 16 heads 84 us (39: the own keys of 16
-// requests in a row tile are each computed for all of its rows), 4 x 131072 keys of 128
-// heads 113 (77), ragged extends of 500 tokens 121 (78), two short requests 17 (latency).
+// plan's lengths in shared memory 121, keys resolved by a warp of their own 114,
+// runs of 128 keys 112. Elsewhere: 64 requests x 32768 keys of 16 heads 82 us (39: the
+// own keys of 16 requests in a row tile are each computed for all of its rows), 4 x
+// 131072 keys of 128 heads 112 (77), ragged extends of 500 tokens 120 (78), two short
+// requests 17 (latency).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
