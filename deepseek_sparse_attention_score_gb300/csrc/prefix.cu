@@ -170,7 +170,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 // One CTA lays out the row tiles, counts their key tiles, a warp per row tile and
 // a lane per request, and deals them out. What is read many times, or by other
 // threads than wrote it, waits in shared memory, if it fits.
-constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024;
+constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024, kPlanCopies = 128;
 // A list that starts inside a share costs about as much as this many key tiles:
 // the pipeline runs empty, the outputs are written, the next queries fetched.
 // 4 / 3 / 2 / 1 took 113.5 / 112.3 / 112.1 / 115.1 us on the 32 x 16384 keys and 54.1 /
@@ -188,8 +188,42 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   __shared__ PlanGroup s_group[kPlanGroups];
   __shared__ int s_cost[kListCost + 1], s_begin[kListCost + 1][kMaxShares + 1], s_tile[kListCost + 1][kMaxShares + 1];
   __shared__ int s_base[kPlanTiles + 1];  // unit_base
+  __shared__ PrefixTile s_tile_copy[kPlanCopies];
   const int tid = threadIdx.x, lane = lane_id();
   const int32_t *cu_q = p.cu_q_lens, *seq = p.seq_lens;
+  int bad = 0;
+  // A group's requests [a, b) as they are given, its prefix and the page-table place
+  // of its first request; whether its requests are in order.
+  struct Given {
+    int a, b, want, place;
+    bool ok;
+  };
+  auto given = [&](int g) -> Given {
+    Given x;
+    x.want = __ldg(p.prefix_lens + g);
+    x.a = p.group_offsets ? __ldg(p.group_offsets + g) : 0;
+    x.b = p.group_offsets ? __ldg(p.group_offsets + g + 1) : p.S;
+    x.ok = x.a >= 0 && x.b >= x.a && x.b <= p.S && (g > 0 || x.a == 0);
+    x.place = x.ok && x.b > x.a ? __ldg(p.cu_kv_lens + x.a) : 0;
+    return x;
+  };
+  auto group_of = [&](const Given& in, bool& ok) -> PlanGroup {
+    PlanGroup x{0, 0, 0, 0, 0};
+    ok = in.ok;
+    if (ok && in.b > in.a) {
+      x.page_base = in.place / p.ps;
+      x.token0 = cu_q[in.a];
+      x.token1 = cu_q[in.b];
+      x.prefix = min(max(in.want, 0), min(max(seq[in.a], 0), p.max_kv));
+      ok = x.token0 >= 0 && x.token1 >= x.token0 && x.token1 <= p.T;
+      if (!ok) x.token1 = x.token0 = 0;
+      if (in.want != x.prefix) bad = 1;
+    }
+    return x;
+  };
+  // the first groups' loads beside the requests'
+  Given early{};
+  if (tid < 256 && tid < p.G) early = given(tid);
   if (p.S <= kPlanRequests) {
     for (int i = tid; i <= p.S; i += kPlanThreads) {
       s_cu_q[i] = __ldg(p.cu_q_lens + i);
@@ -199,29 +233,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     seq = s_seq;
   }
   if (tid <= kListCost) s_cost[tid] = 0;
-  int bad = 0;
-  // a group's requests [x, y) as they are given, and checked
-  auto requests = [&](int g, bool& ok) -> int2 {
-    const int a = p.group_offsets ? __ldg(p.group_offsets + g) : 0;
-    const int b = p.group_offsets ? __ldg(p.group_offsets + g + 1) : p.S;
-    ok = a >= 0 && b >= a && b <= p.S && (g > 0 || a == 0);
-    return ok ? make_int2(a, b) : make_int2(0, 0);
-  };
-  auto group_of = [&](int g, bool& ok) -> PlanGroup {
-    const int2 r = requests(g, ok);
-    PlanGroup x{0, 0, 0, 0, 0};
-    if (r.y > r.x) {
-      const int page_base = __ldg(p.cu_kv_lens + r.x) / p.ps, want = __ldg(p.prefix_lens + g);
-      x.page_base = page_base;
-      x.token0 = cu_q[r.x];
-      x.token1 = cu_q[r.y];
-      x.prefix = min(max(want, 0), min(max(seq[r.x], 0), p.max_kv));
-      ok = x.token0 >= 0 && x.token1 >= x.token0 && x.token1 <= p.T;
-      if (!ok) x.token1 = x.token0 = 0;
-      if (want != x.prefix) bad = 1;
-    }
-    return x;
-  };
   __syncthreads();
   int total;
   unsigned tiles = 0;
@@ -233,9 +244,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     const bool mine = tid < 256 && g < p.G;
     if (mine) {
       bool ok;
-      x = group_of(g, ok);
+      const Given in = g0 ? given(g) : early;
+      x = group_of(in, ok);
       // requests behind the last group: no rows of theirs are written
-      if (!ok || (g == p.G - 1 && p.group_offsets && __ldg(p.group_offsets + p.G) != p.S)) bad = 1;
+      if (!ok || (g == p.G - 1 && in.b != p.S)) bad = 1;
       n = ((unsigned)(x.token1 - x.token0) * p.H + kTileRows - 1) / kTileRows;
     }
     const unsigned end = block_scan(n, warp_sums, total);
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       x = s_group[lo];
     } else {
       bool ok;
-      x = group_of(lo, ok);
+      x = group_of(given(lo), ok);
       x.first_tile = p.tile_base[lo];
     }
     const int first = x.token0 * p.H + (i - x.first_tile) * kTileRows, rows = min(kTileRows, x.token1 * p.H - first);
@@ -292,6 +304,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       r.prefix = x.prefix;
       r.page_base = x.page_base;
       p.tiles[i] = r;
+      if (i < kPlanCopies) s_tile_copy[i] = r;
     }
   }
   __syncthreads();
@@ -299,10 +312,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   for (int i0 = 0; i0 < ntiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
     const int n = i < ntiles ? base[i] : 0, end = block_scan(n, warp_sums, total);
-    if (i < ntiles) p.unit_base[i] = base[i] = units + end - n;
+    if (i < ntiles) {
+      base[i] = units + end - n;
+      p.tiles[i].begin = units + end - n;
+      p.tiles[i].end = units + end;
+    }
     units += total;
   }
-  if (tid == 0) p.unit_base[ntiles] = base[ntiles] = units;
+  if (tid == 0) base[ntiles] = units;
   __syncthreads();
   // The shares are equal runs of the lists with `gap` units of no work between
   // two of them, so that a share in which a list starts has less work; of the
@@ -332,14 +349,19 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   for (int j = 1; j < gaps; ++j) gap = s_cost[j] < s_cost[gap] ? j : gap;
   for (int k = tid; k < p.shares; k += kPlanThreads) {
     PrefixShare r{};
-    r.cut = -1;
     if (k < n) {
+      auto copy_of = [&](int i) { return i < kPlanCopies ? s_tile_copy[i] : p.tiles[i]; };
       const int *sb = s_begin[gap], next = s_tile[gap][k + 1];
       r.begin = sb[k];
       r.end = sb[k + 1];
       r.tile = s_tile[gap][k];
+      r.first = copy_of(r.tile);
+      r.first.begin = base[r.tile];
+      r.first.end = base[r.tile + 1];
       if (base[next] < r.end && r.begin <= base[next]) {
-        r.cut = next;
+        const PrefixTile cut = copy_of(next);
+        r.cut_row0 = cut.row0;
+        r.cut_rows = cut.rows;
         r.first_slot = r.begin == base[next] ? 2 * k : 2 * k + 1;
         r.last = k + 1;  // the last share that begins inside the list
         while (r.last + 1 < n && sb[r.last + 1] < base[next + 1]) ++r.last;
@@ -561,13 +583,13 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     PrefixTile tile{};
     int2 mine{};  // my row of the tile
     if (work.begin < work.end) {
-      tile = prm.tiles[ti];
+      tile = work.first;
       if constexpr (kSoft) mine = row_of(tile);
     }
     bool ok = true;
 #pragma unroll 1
     for (int u = work.begin; ok && u < work.end; ++ti) {
-      const int list0 = prm.unit_base[ti], list1 = prm.unit_base[ti + 1];  // the list's units
+      const int list0 = tile.begin, list1 = tile.end;  // the list's units
       const int k0 = u - list0, n = min(work.end, list1) - u;
       const bool whole = k0 == 0 && u + n == list1;
       const int slot_out = u == work.begin ? 2 * share : 2 * share + 1;
@@ -1068,16 +1090,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_ker
 #pragma unroll
   for (int j = 0; j < kMaxShares / 32; ++j) {
     const int k = 32 * j + lane;
-    const uint32_t cuts = __ballot_sync(0xffffffffu, k < p.shares && p.share[k].cut >= 0);
+    const uint32_t cuts = __ballot_sync(0xffffffffu, k < p.shares && p.share[k].cut_rows > 0);
     const uint32_t it = __ballot_sync(0xffffffffu, (cuts >> lane & 1) && __popc(cuts & below(lane)) == x);
     if (it) k0 = 32 * j + __ffs(it) - 1;
     x -= __popc(cuts);
   }
   if (k0 < 0) return;
   const PrefixShare share = p.share[k0];
-  const PrefixTile tile = p.tiles[share.cut];
   const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1, k1 = share.last;
-  if (r >= tile.rows) return;
+  if (r >= share.cut_rows) return;
   auto row_of = [&](int k) { return (size_t)(k == k0 ? share.first_slot : 2 * k) * kTileRows + r; };
   // parts four at a time, the first four's rows on their way while the weights
   // are found
@@ -1120,14 +1141,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_ker
       }
     }
   }
-  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)tile.row0 + r) * kDv + half * 256);
+  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)share.cut_row0 + r) * kDv + half * 256);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc[h].x, acc[h].y), hi = __floats2bfloat162_rn(acc[h].z, acc[h].w);
     dst[32 * h + lane] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
   }
   if (half == 0 && lane == 0 && p.lse)
-    p.lse[(size_t)tile.row0 + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
+    p.lse[(size_t)share.cut_row0 + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
 }
 
 int max_tiles_of(int T, int H, int G) { return (int)(((long long)T * H + kTileRows - 1) / kTileRows) + G; }

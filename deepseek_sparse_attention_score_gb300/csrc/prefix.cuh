@@ -15,17 +15,18 @@ struct alignas(16) PrefixTile {
   int s0, last;        // first request, last token
   int prefix;          // positions read through the group's first request
   int page_base;       // and where its page-table entries start
-  int pad[2];
+  int begin, end;      // its units, of all tiles' in a row
 };
-// What a cluster works on: units [begin, end), from row tile `tile` on; and the
-// list that its end is the first to cut.
+// What a cluster works on: units [begin, end), from row tile `tile` on, of which it
+// has a copy; and the list that its end is the first to cut.
 struct alignas(16) PrefixShare {
   int begin, end;
   int tile;
-  int cut;         // its row tile, -1: none
-  int last;        // last share that works on it
-  int first_slot;  // place of this share's part (share k's is 2k)
-  int pad[2];
+  int last;                // last share that works on the list that is cut
+  int first_slot;          // place of this share's part (share k's is 2k)
+  int cut_row0, cut_rows;  // the list's rows, 0: none is cut here first
+  int pad;
+  PrefixTile first;
 };
 
 struct PrefixParams {
@@ -46,7 +47,7 @@ struct PrefixParams {
   // workspace (set by run_prefix_mla)
   int32_t* tile_base;    // [G + 1] tiles of the groups before
   PrefixTile* tiles;
-  int* unit_base;        // [tiles + 1] key tiles of the tiles before
+  int* unit_base;        // [tiles + 1] key tiles of the tiles before, where shared memory is too small
   PrefixShare* share;    // [shares], those past the work empty
   float* part_o;    // [2 * shares][256][512]
   float* part_lse;  // [2 * shares][256], log2
