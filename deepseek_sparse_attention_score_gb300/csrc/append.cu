@@ -8,11 +8,11 @@
 // What bounds it is memory: each row is read once and written once. The rotated
 // columns go a pair per lane, which has formed that pair's cosine and sine
 // itself, once for all targets; a 4-bit row's latent dims one group of 16 per lane.
-//  - Few tokens: one per warp, whose rows go through registers; what counts is
-//    latency.
-//  - Many: a warp takes several in a row, whose rows bulk copies bring to shared
-//    memory, a few tokens ahead, and take from there to their slots, so that the
-//    bytes in flight cost no registers.
+//  - Rows by themselves: bulk copies bring them to shared memory, a few tokens ahead,
+//    and take them from there to their slots, so that the bytes in flight cost no
+//    registers, and few tokens no chain of loads.
+//  - With queries, or too wide for that: a token per warp, whose rows go through
+//    registers.
 //
 // A pair's frequency is held as the 64-bit fraction of a turn per position, so
 // that position times frequency, wrapped at 2^64, is the angle's fraction of a
@@ -62,11 +62,9 @@ __device__ __forceinline__ void put_group(const uint4& u, const uint4& v, uint8_
   row[kRow4Codes + lane_id()] = (uint8_t)sb;
 }
 
-// The slot of token t, -1 if nothing is written: a negative slot or position is a
-// padding row.
-__device__ __forceinline__ int slot_of(const AppendParams& p, long long t, int& pos) {
-  pos = __ldg(p.positions + t);
-  const int slot = __ldg(p.slots + t);
+// A token's slot, -1 if nothing is written: a negative slot or position is a padding
+// row.
+__device__ __forceinline__ int checked_slot(const AppendParams& p, int slot, int pos) {
   if (pos < 0 || slot < 0) return -1;
   if (slot >= p.rows) {
     set_status(p.dev_status, DSA_STATUS_BAD_INDEX);
@@ -104,8 +102,7 @@ __device__ __forceinline__ void append_token(const AppendParams& p, int t) {
     q1 = __ldg(x + 1);
   }
   const double freq = lane < pairs ? __ldg(p.freqs + lane) : 0.0;
-  int pos;
-  const int slot = slot_of(p, t, pos);
+  const int pos = __ldg(p.positions + t), slot = checked_slot(p, __ldg(p.slots + t), pos);
   if (slot < 0) return;
   auto row = [&](int k) { return p.tg[k].cache + slot * p.tg[k].cache_stride; };
 #pragma unroll
@@ -123,7 +120,8 @@ __device__ __forceinline__ void append_token(const AppendParams& p, int t) {
 #pragma unroll 1
     for (int k = 0; k < p.n; ++k) {
       const AppendTarget& g = p.tg[k];
-      turn_pair(g.xr + t * g.xr_stride, reinterpret_cast<uint16_t*>(row(k) + g.rot_at), i, p.rot_dim, g.half, cs, g.scale);
+      turn_pair(g.xr + t * g.xr_stride, reinterpret_cast<uint16_t*>(row(k) + g.rot_at), i, p.rot_dim, g.half, cs,
+                g.scale);
     }
   }
 #pragma unroll 1
@@ -169,9 +167,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) append_bulk_kernel(const __gr
     for (int s = 0; s < p.stages; ++s) mbar_init(&bars[warp][s], 1);
     fence_mbar_init();
   }
-  griddep_wait();
-  for (int i = threadIdx.x; i < pairs; i += kRopeWarps * 32) turns[i] = turn_of(__ldg(p.freqs + i));
-  __syncthreads();
+  __syncwarp();
   // tokens t0, t0 + step, ...: at any time the warps work on neighbouring rows
   const int t0 = blockIdx.x * kRopeWarps + warp, step = gridDim.x * kRopeWarps;
   const int n = t0 < p.T ? (p.T - 1 - t0) / step + 1 : 0;
@@ -202,6 +198,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) append_bulk_kernel(const __gr
     out_bytes = g.q4 ? kRow4Bytes : 2 * g.D;
     out_at = g.stage_at + (g.q4 ? 2 * g.D : 0);
   }
+  griddep_wait();
   int slots = -1, positions = 0;  // of 32 tokens, one per lane
   int fill = 0;                   // the place that is filled next, with the next token's rows
   auto load = [&]() {
@@ -216,13 +213,23 @@ __global__ void __launch_bounds__(kRopeWarps * 32) append_bulk_kernel(const __gr
   int loaded = min(n, p.stages - 2);
 #pragma unroll 1
   for (int j = 0; j < loaded; ++j) load();
+  // the first tokens' slots and the pairs' turns while the first rows are on their way
+  auto lookup = [&](int j) {
+    if (j + lane >= n) return;
+    const long long t = t0 + (long long)(j + lane) * step;
+    slots = __ldg(p.slots + t);
+    positions = __ldg(p.positions + t);
+  };
+  lookup(0);
+  for (int i = threadIdx.x; i < pairs; i += kRopeWarps * 32) turns[i] = turn_of(__ldg(p.freqs + i));
+  __syncthreads();
   bool ok = true;
   int j = 0, place = 0, phase = 0;
 #pragma unroll 1
   for (; j < n; ++j) {
     if (j % 32 == 0) {
-      slots = -1;
-      if (j + lane < n) slots = slot_of(p, t0 + (long long)(j + lane) * step, positions);
+      if (j) lookup(j);
+      slots = checked_slot(p, slots, positions);
     }
     const int slot = __shfl_sync(0xffffffffu, slots, j % 32), pos = __shfl_sync(0xffffffffu, positions, j % 32);
     if (loaded < n) {
@@ -308,30 +315,31 @@ int run_rope_append(cudaStream_t stream, const dsa_rope_target* rot, int n_rot, 
   p.slots = slots;
   p.freqs = freqs;
   p.dev_status = dev_status;
-  // Through shared memory from 12 tokens per SM on, with 4-bit rows, whose
-  // quantising counts there, from 80. Measured, registers / shared memory, latent
-  // rows and indexer keys: 16 bits, 1024 tokens 3.4 / 3.6 us, 2048 4.4 / 3.9, 8192
-  // 9.9 / 8.0, 65537 50 / 33 (a plain copy of as many bytes 29.3); 4 bits, 4096
-  // tokens 5.4 / 5.6, 16384 14.6 / 14.3, 65537 48 / 37. CTAs per SM: 16 bits, 65537
-  // tokens, 3 / 4 / 5 / 6 CTAs 39.7 / 33.5 / 41.0 / 39.7 us (fewer leave the memory
-  // idle, more spread over more rows at a time); 4 bits 50.9 / 40.6 / 45.0 / 37.4.
-  p.stages = std::min(kAppendStages, kAppendRing / p.stage);
-  if (p.stages >= 3 && T >= (p.n_q4 ? 80 : 12) * sm_count()) {
-    const long long ctas = std::min<long long>((p.n_q4 ? 6 : 4) * sm_count(), (T + kRopeWarps - 1) / kRopeWarps);
-    set_smem_attr_once(reinterpret_cast<const void*>(append_bulk_kernel), kRopeWarps * kAppendRing);
-    DSA_LAUNCH_PDL(append_bulk_kernel, dim3((unsigned)ctas), dim3(kRopeWarps * 32), kRopeWarps * p.stages * p.stage,
-                   stream, p);
-    return n_rot ? run_rope(stream, rot, n_rot, T, rot_dim, positions, freqs, false) : DSA_OK;
-  }
   RopeParams group[2] = {};
   unsigned grid[2] = {};
   if (n_rot) {
     const int rc = plan_rope(rot, n_rot, T, rot_dim, positions, freqs, false, group, grid);
     if (rc != DSA_OK) return rc;
   }
-  p.append_ctas = (unsigned)((T + (long long)kRopeWarps - 1) / kRopeWarps);
-  if ((long long)p.append_ctas + grid[0] >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
-  DSA_LAUNCH_PDL(append_kernel, dim3(p.append_ctas + grid[0]), dim3(kRopeWarps * 32), kRopeSmem, stream, p, group[0]);
+  // Rows by themselves go through shared memory, with targets of dsa_rope beside them
+  // through registers, in one launch with those. Measured, latent rows and indexer
+  // keys by themselves, registers / shared memory: 16 bits, 8 tokens 2.9 / 2.4 us, 512
+  // 3.1 / 2.6, 8192 9.9 / 6.9, 65537 50 / 33 (a plain copy of as many bytes 29.3); 4 bits,
+  // 8 tokens 2.8 / 2.5, 4096 5.4 / 4.6, 65537 48 / 36. With 128 heads' queries, one launch
+  // / two: 64 tokens 3.9 / 6.0, 1024 14.7 / 20.7, 4096 42 / 57. CTAs per SM: 65537 tokens,
+  // 3 / 4 / 5 / 6 CTAs 38.2 / 32.7 / 40.0 / 38.7 us (fewer leave the memory idle, more
+  // spread over more rows at a time); 4 bits 49.8 / 39.5 / 41.1 / 36.3.
+  p.stages = std::min(kAppendStages, kAppendRing / p.stage);
+  if (p.stages >= 3 && !group[0].n) {
+    const long long ctas = std::min<long long>((p.n_q4 ? 6 : 4) * sm_count(), (T + kRopeWarps - 1LL) / kRopeWarps);
+    set_smem_attr_once(reinterpret_cast<const void*>(append_bulk_kernel), kRopeWarps * kAppendRing);
+    DSA_LAUNCH_PDL(append_bulk_kernel, dim3((unsigned)ctas), dim3(kRopeWarps * 32), kRopeWarps * p.stages * p.stage,
+                   stream, p);
+  } else {
+    p.append_ctas = (unsigned)((T + (long long)kRopeWarps - 1) / kRopeWarps);
+    if ((long long)p.append_ctas + grid[0] >= (1LL << 31)) return DSA_ERR_UNSUPPORTED;
+    DSA_LAUNCH_PDL(append_kernel, dim3(p.append_ctas + grid[0]), dim3(kRopeWarps * 32), kRopeSmem, stream, p, group[0]);
+  }
   return group[1].n ? run_rope_elements(stream, group[1], grid[1]) : DSA_OK;
 }
 

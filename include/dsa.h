@@ -531,9 +531,8 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
 /* ------------------------------------------------------------------------
  * Appending rows to the paged caches with the rotary positions applied on the
  * way (no counterpart on the pages, whose rows arrive rotated): dsa_rope of a
- * step's new rows and their write-back in one pass, and with it (in the same
- * launch, when tokens are few) dsa_rope of other targets, such as the layer's
- * queries. Row t of an append
+ * step's new rows and their write-back in one pass, and with it, in the same
+ * launch, dsa_rope of other targets, such as the layer's queries. Row t of an append
  * target goes to cache row slots[t] (page * ps + row, as dsa_build_page_tables
  * numbers them); every other row of the cache, and the columns of a row from D
  * on, are left untouched.
@@ -560,8 +559,7 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
  * those of dsa_rope.
  * Supported: rot_dim a multiple of 16 up to 512, D <= 4096, D, rot_off and the
  * strides multiples of 8, 16-byte aligned rows and caches, P * ps < 2^31.
- * Targets of `rotate` take a launch of their own if they do not lie on 16 bytes,
- * and with many tokens.
+ * Targets of `rotate` that do not lie on 16 bytes take a launch of their own.
  * Needs no workspace.
  * ------------------------------------------------------------------------ */
 enum dsa_cache_format { DSA_CACHE_BF16 = 0, DSA_CACHE_Q4 = 1 };

@@ -123,6 +123,41 @@ def test_is_the_rotation_and_the_write_back(dsa, T):
     assert torch.equal(kv4[:, :, :288], kv4_[:, :, :288])
 
 
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("T,D,off,rot,width,split", [
+    (1, 576, 512, 64, 640, True), (37, 576, 512, 64, 576, False), (130, 128, 0, 128, 128, False),
+    (9, 88, 40, 32, 104, True), (3, 512, 0, 512, 512, True), (2501, 576, 512, 64, 576, True),
+    (1850, 1024, 512, 256, 1024, False), (2, 4096, 2048, 64, 4096, False), (700, 576, 512, 64, 416, False),
+    (13, 576, 512, 64, 416, True),
+])
+def test_beside_other_targets(dsa, layout, T, D, off, rot, width, split):
+    """Rows by themselves and with another tensor that turns in the same launch
+    take different ways to the cache, with the same arithmetic: the same bytes."""
+    ps, P = 32, -(-T // 32) + 1
+    x = _rand((T, D), T)
+    x[T // 2, 3] = float("inf")
+    cache = _rand((P, ps, width), 2)
+    if width == 416:
+        cache = torch.full((P, ps, 416), 5, dtype=torch.uint8, device="cuda")
+    slots = _slots(T, P * ps, 4)
+    slots[np.random.default_rng(6).random(T) < 0.1] = -1
+    pos, slots = _i32(np.random.default_rng(5).integers(0, 1 << 20, T)), _i32(slots)
+    freqs, scale = dsa.dsa_rope_freqs(rot, device="cuda")
+    q = _rand((T, 2, rot), 7)
+    old, got = cache.clone(), []
+    for rotate in ([], [dsa.RopeTarget(q, torch.empty_like(q))]):
+        to = cache.clone()
+        if split:
+            g = dsa.AppendTarget(torch.cat([x[:, :off], x[:, off + rot:]], 1), to, x_rot=x[:, off: off + rot],
+                                 rot_off=off, layout=layout, scale=scale)
+        else:
+            g = dsa.AppendTarget(x, to, rot_off=off, rot_dim=rot, layout=layout, scale=scale)
+        dsa.dsa_rope_append(g, pos, slots, freqs, rotate=rotate)
+        got.append(to.view(torch.uint8))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], got[1]) and (T < 9 or not torch.equal(got[0], old.view(torch.uint8)))
+
+
 @pytest.mark.parametrize("times", [1, 1040])
 def test_quantised_rows_of_every_kind(dsa, times):
     """4-bit groups with infinities, NaN, zeros, tiny and huge values, byte for
