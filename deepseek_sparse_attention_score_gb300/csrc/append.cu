@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
 // p.stage bytes for a token's rows: of each target the source row, laid out as
 // the cache row, and behind a 4-bit target's the row of codes.
 __global__ void __launch_bounds__(kRopeWarps * 32) append_bulk_kernel(const __grid_constant__ AppendParams p) {
-  griddep_launch_dependents();
+  if (p.next_early) griddep_launch_dependents();
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kRopeWarps][kAppendStages];
   __shared__ unsigned long long turns[kRopeMaxDim / 2];
@@ -326,12 +326,18 @@ int run_rope_append(cudaStream_t stream, const dsa_rope_target* rot, int n_rot, 
   // keys by themselves, registers / shared memory: 16 bits, 8 tokens 2.9 / 2.4 us, 512
   // 3.1 / 2.6, 8192 9.9 / 6.9, 65537 50 / 33 (a plain copy of as many bytes 29.3); 4 bits,
   // 8 tokens 2.8 / 2.5, 4096 5.4 / 4.6, 65537 48 / 36. With 128 heads' queries, one launch
-  // / two: 64 tokens 3.9 / 6.0, 1024 14.7 / 20.7, 4096 42 / 57. CTAs per SM: 65537 tokens,
+  // / two: 64 tokens 4.1 / 6.1, 1024 15.3 / 18.0, 4096 42 / 46. CTAs per SM: 65537 tokens,
   // 3 / 4 / 5 / 6 CTAs 38.2 / 32.7 / 40.0 / 38.7 us (fewer leave the memory idle, more
   // spread over more rows at a time); 4 bits 49.8 / 39.5 / 41.1 / 36.3.
   p.stages = std::min(kAppendStages, kAppendRing / p.stage);
   if (p.stages >= 3 && !group[0].n) {
     const long long ctas = std::min<long long>((p.n_q4 ? 6 : 4) * sm_count(), (T + kRopeWarps - 1LL) / kRopeWarps);
+    // The next kernel's CTAs may come early where they find most of the GPU idle. CTAs
+    // that come to SMs whose shared memory these hold keep the little L1 that is left
+    // for as long as that kernel runs: dsa_rope of 128 heads behind 1024, 4096, 8192 rows
+    // 21, 56, 99 us the two, 18, 46, 86 if it starts when these have ended; behind 64
+    // rows 6.1, and 6.7.
+    p.next_early = ctas <= sm_count();
     set_smem_attr_once(reinterpret_cast<const void*>(append_bulk_kernel), kRopeWarps * kAppendRing);
     DSA_LAUNCH_PDL(append_bulk_kernel, dim3((unsigned)ctas), dim3(kRopeWarps * 32), kRopeWarps * p.stages * p.stage,
                    stream, p);

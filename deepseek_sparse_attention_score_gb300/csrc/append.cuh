@@ -29,6 +29,7 @@ struct AppendParams {
   int n, runs, rot_dim, T;
   int stages, stage, row_bytes;  // a warp's places in shared memory; bytes of one, and of a token's source rows
   unsigned append_ctas;
+  bool next_early;  // append_bulk_kernel lets the stream's next kernel launch at once
   long long rows;  // of each cache: pages * page size
   const int32_t* positions;
   const int32_t* slots;
