@@ -100,7 +100,7 @@ constexpr int OFF_BAR = (OFF_DESC + kDescs * (int)sizeof(KeyTile) + 7) & ~7;
 constexpr int kNumBars = 2 * kStages + 2 * kDescs + 10 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+static_assert(kSmem <= 227 * 1024, "shared memory");
 static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_DESC % 16 == 0, "alignment");
 
 constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, 128, false, false);
@@ -173,8 +173,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024, kPlanCopies = 128;
 // A list that starts inside a share costs about as much as this many key tiles:
 // the pipeline runs empty, the outputs are written, the next queries fetched.
-// 4 / 3 / 2 / 1 took 113.5 / 112.3 / 112.1 / 115.1 us on the 32 x 16384 keys and 54.1 /
-// 54.1 / 52.6 / 55.0 on five groups of unlike size.
+// 4 / 3 / 2 / 1 take 109.2 / 109.2 / 109.4 / 112.0 us on the 32 x 16384 keys and 50.3 /
+// 49.3 / 48.8 / 48.8 on five groups of unlike size.
 constexpr int kListCost = 2;
 constexpr int kMaxShares = 128;
 struct PlanGroup {
