@@ -62,7 +62,7 @@ constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (querie
 // 256 + 64j; the last has dims 512 alone), then four of V (64 keys, 128 dims of this
 // CTA), first the keys whose P this CTA computes
 constexpr int kStages = 5, kStage = 2 * kBlk;
-constexpr int kKStages = 5, kVStages = 4;
+constexpr int kKStages = 5, kVStages = 4, kQStages = 4;
 constexpr int kDescs = 4;
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = (4 + kSoftWarps) * 32;
@@ -97,7 +97,7 @@ constexpr int OFF_LOCAL = OFF_RING + kStages * kStage;   // float [2][kRows]: ma
 constexpr int OFF_REMOTE = OFF_LOCAL + 2 * kRows * 4;    // float [2][kRows]: those of the other keys, two tiles
 constexpr int OFF_DESC = OFF_REMOTE + 2 * kRows * 4;
 constexpr int OFF_BAR = (OFF_DESC + kDescs * (int)sizeof(KeyTile) + 7) & ~7;
-constexpr int kNumBars = 2 * kStages + 2 * kDescs + 10 + 4 + 8;
+constexpr int kNumBars = 2 * kStages + 2 * kDescs + 9 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -127,10 +127,9 @@ struct Bars {
   __device__ __forceinline__ uint64_t* ppeer() const { return rest(6); }   // each: P from the other half
   __device__ __forceinline__ uint64_t* lbar() const { return rest(7); }    // each: sums of weights from the other half
   __device__ __forceinline__ uint64_t* pother() const { return rest(8); }  // pair's: P of the other half, both CTAs
-  __device__ __forceinline__ uint64_t* edone() const { return rest(9); }   // each: softmax warps, outputs are written
-  __device__ __forceinline__ uint64_t* local(int w) const { return rest(10 + w); }  // each: two warps of the same rows
+  __device__ __forceinline__ uint64_t* local(int w) const { return rest(9 + w); }  // each: two warps of the same rows
   // each: those two and the maxima of the other half
-  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(14 + 4 * k + w); }
+  __device__ __forceinline__ uint64_t* remote(int w, int k) const { return rest(13 + 4 * k + w); }
 };
 
 // ------------------------------------------------------------- the work list
@@ -529,7 +528,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(br.qbar(), 1);
     mbar_init(br.ppeer(), 1);
     mbar_init(br.lbar(), kSoftWarps);
-    mbar_init(br.edone(), kSoftWarps);
     for (int w = 0; w < 4; ++w) {
       mbar_init(br.local(w), 2);
       for (int k = 0; k < 2; ++k) mbar_init(br.remote(w, k), 2);
@@ -593,6 +591,8 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
       const int k0 = u - list0, n = min(work.end, list1) - u;
       const bool whole = k0 == 0 && u + n == list1;
       const int slot_out = u == work.begin ? 2 * share : 2 * share + 1;
+      const uint32_t from = fc;  // the first stage; from the second list on those of the queries for TMEM
+      if (uc) fc += kQStages;
       const int row0 = tile.row0 + r * kRows;              // this CTA's first row of [T * H]
       const int rows = min(kRows, tile.rows - r * kRows);  // <= 0: none
       if constexpr (!kSoft) {
@@ -609,7 +609,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
               if (lead) umma_commit_pair(bar, to);
               __syncwarp();
             };
-            uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
+            uint32_t slot = from % kStages, phase = (from / kStages) & 1;
             auto arrived = [&]() { return mbar_wait_warp(br.full(slot), phase, abort_flag); };
             auto pass = [&]() {
               commit(br.empty(slot), pair);
@@ -618,6 +618,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             const int prefix_runs = (tile.prefix + kRun - 1) / kRun;
             ok = mbar_wait_warp_cluster(br.qready(), uc & 1, abort_flag);
             tc_fence_after();
+            for (uint32_t j = from; j != fc; ++j) pass();  // the queries' stages have been read
 #pragma unroll 1
             for (int i = 0; ok && i <= n; ++i) {
               // small loops: the roles share the instruction cache
@@ -707,26 +708,29 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           }
         } else if (warp == 1) {
           // ---------------------------------------------------- queries and keys
-          // Query blocks b0 .. b1 - 1: those for TMEM land in P's places, free once the
-          // last list's outputs are written, the others where they stay, free once its
-          // last QK^T has run.
-          auto load_queries = [&](int b0, int b1) {
-            if (lane == 0) {
+          // Query blocks: those for TMEM land in P's places, of later lists in stages
+          // of the ring, the others where they stay, free once the last QK^T has run.
+          uint32_t slot = from % kStages, phase = (from / kStages) & 1;
+          if (uc) ok = mbar_wait_warp(br.sfull(), (tc - 1) & 1, abort_flag);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
 #pragma unroll 1
-              for (int b = b0; b < b1; ++b)
-                tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64,
-                            row0);
+            for (int b = uc ? kQStages : 0; b < 9; ++b)
+              tma_load_2d(smem + (b < 4 ? OFF_P + b * kQBlk : OFF_Q + (b - 4) * kQBlk), &qmap, br.qbar(), b * 64,
+                          row0);
+          }
+          __syncwarp();
+#pragma unroll 1
+          for (int b = 0; ok && uc && b < kQStages; ++b) {
+            if (!(ok = mbar_wait_warp(br.empty(slot), phase ^ 1, abort_flag))) break;
+            if (lane == 0) {
+              if (r == 0) mbar_arrive(br.full(slot));  // keeps its phases; nobody waits for this one
+              tma_load_2d(smem + OFF_RING + slot * kStage, &qmap, br.qbar(), b * 64, row0);
             }
             __syncwarp();
-          };
-          if (uc) ok = mbar_wait_warp(br.sfull(), (tc - 1) & 1, abort_flag);
-          if (ok) {
-            if (lane == 0) mbar_arrive_expect_tx(br.qbar(), 9 * kQBlk);
-            __syncwarp();
-            load_queries(uc ? 4 : 0, 9);
+            if (++slot == kStages) slot = 0, phase ^= 1;
           }
           const bool two = prm.ps == 32;
-          uint32_t slot = fc % kStages, phase = (fc / kStages) & 1;
           // a stage of two blocks of 64 keys, dims d0 .. and d1 .. (one: only the first)
           auto load = [&](int d0, int d1, int r0, int r1, bool one) -> bool {
             if (!mbar_wait_warp(br.empty(slot), phase ^ 1, abort_flag)) return false;
@@ -752,10 +756,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
               for (int j = 0; ok && j < kKStages; ++j)
                 ok = j < 4 ? load(j * 64, 256 + j * 64, r0, r1, false) : load(512, 0, r0, r1, true);
               if (!ok) break;
-              if (uc && i == 0) {
-                if (!(ok = mbar_wait_warp(br.edone(), (uc - 1) & 1, abort_flag))) break;
-                load_queries(0, 4);
-              }
             }
             if (i > 0) {  // V of the key tile before, first of run c
               const int ds = (tc - (i < n ? 2 : 1)) % kDescs;
@@ -807,11 +807,14 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
         // this warp's part of P, 32 rows x 64 keys, here and at the other half
         const uint32_t p_blk = smem0 + OFF_P + (2 * c + hh) * kQBlk, p_run = p_blk + q * 32 * 128;
         const int my_s = mine.x, see = mine.y, prefix = tile.prefix;
-        ok = mbar_wait_warp(br.qbar(), uc & 1, abort_flag);
-        if (ok) {
+        // The queries of list k for TMEM, from P's places or from the ring's stages from
+        // `stage` on.
+        auto take_queries = [&](uint32_t k, bool ring, uint32_t stage) {
+          if (!(ok = mbar_wait_warp(br.qbar(), k & 1, abort_flag))) return;
 #pragma unroll 1
           for (int b = 2 * hh; b < 2 * hh + 2; ++b) {
-            const uint8_t* src = smem + OFF_P + b * kQBlk + row * 128;
+            const int at = ring ? OFF_RING + (int)((stage + b) % kStages) * kStage : OFF_P + b * kQBlk;
+            const uint8_t* src = smem + at + row * 128;
             uint32_t v[32];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -823,6 +826,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tmem_st32(tmem + lane_base + kColQ + b * 32, v);
           }
+          tmem_st_wait();
+          tc_fence_before();
+          // Bulk copies write here next: the other half's of P, of these 32 rows after it
+          // has had this warp's maxima of the first tile, or keys.
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader(br.qready()));
+          __syncwarp();
+        };
+        if (!uc) take_queries(0, false, 0);
+        if (ok) {
           // PV adds to O from the first tile on, as a request's own keys do not reach all rows
           uint32_t zero[32];
 #pragma unroll
@@ -831,12 +845,6 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           for (int k = 4 * hh; k < 4 * hh + 4; ++k) tmem_st32(tmem + lane_base + kColO + k * 32, zero);
           tmem_st_wait();
           tc_fence_before();
-          // The other half's copies of P write here next: of these 32 rows, after it
-          // has had this warp's maxima of the first tile.
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(leader(br.qready()));
-          __syncwarp();
         }
         const float sl2 = prm.scale_log2;
         float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's columns
@@ -979,12 +987,19 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float*>(smem + a_l) = l_run;
           __syncwarp();
           if (lane == 0) mbar_arrive_expect_tx(br.lbar(), 32 * 4);
+          __syncwarp();
           ok = mbar_wait_warp(br.lbar(), uc & 1, abort_flag);
         }
+        float l = 0.f;
         if (ok) {
           tc_fence_after();
           const volatile float* lp = reinterpret_cast<const volatile float*>(smem + OFF_P + 2 * c * kQBlk) + row;
-          const float l = (lp[0] + lp[kRows]) + (lp[2 * kRows] + lp[3 * kRows]);
+          l = (lp[0] + lp[kRows]) + (lp[2 * kRows] + lp[3 * kRows]);
+          // The next list's first QK^T runs while this one's outputs are written. The sums
+          // have been read by then: its first P lands there.
+          if (u + n < work.end) take_queries(uc + 1, true, fc + (kKStages + kVStages) * n);
+        }
+        if (ok) {
           const bool some = l != 0.f;  // a sum of weights is never negative; NaN counts
           const float inv_l = some ? 1.f / l : 0.f;
           const float lse2 = some ? m_run + log2f(l) : -INFINITY;
@@ -1038,18 +1053,17 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
             else if (prm.lse) prm.lse[(size_t)row0 + row] = lse2 * 0.69314718055994531f;
           }
           tc_fence_before();
-          fence_proxy_async_smem();  // queries are copied to P's places next
-          __syncwarp();
-          if (lane == 0) mbar_arrive(br.edone());
+          fence_proxy_async_smem();  // the other half's P is copied to its places next
           __syncwarp();
         } else {
           give_up();
         }
       }
-      // No barrier here: the next list's first keys are fetched, and its queries,
-      // while this one's outputs are written. Its first QK^T waits for the softmax
-      // warps of the pair (qready), so for their reads of O; its first P comes after
-      // an exchange of maxima with the warps whose places it writes.
+      // No barrier here: the next list's queries and first keys are fetched while this
+      // one's last PV runs, and its first QK^T runs while its outputs are written. Its
+      // first PV waits for the softmax warps (pfull), so for their reads of O and the
+      // zeros; its first P comes after an exchange of maxima with the warps whose
+      // places it writes.
       fc += (kKStages + kVStages) * n;
       u += n;
       ++uc;
