@@ -36,12 +36,12 @@
 // tile takes 2.84 us, and 36 clusters run at once: 1.81 PFLOP/s, 94 % of the card's
 // measured rate. Another 20 us a call is not products: the plan 4-5, the first
 // queries and keys 5, the last outputs 5, the merge 7. Measured on 32 requests x 16384
-// shared keys, 128 heads (110 us in all, floor 77), step by step: pairs whose CTAs
+// shared keys, 128 heads (109 us in all, floor 77), step by step: pairs whose CTAs
 // compute S twice 161, clusters that share it 131, PV in order of arrival of P 127, the
 // plan's lengths in shared memory 121, keys resolved by a warp of their own 114,
 // runs of 128 keys 112. Elsewhere: 64 requests x 32768 keys of 16 heads 82 us (39: the
 // own keys of 16 requests in a row tile are each computed for all of its rows), 4 x
-// 131072 keys of 128 heads 112 (77), ragged extends of 500 tokens 120 (78), two short
+// 131072 keys of 128 heads 112 (77), ragged extends of 500 tokens 118 (78), two short
 // requests 17 (latency).
 #include <algorithm>
 #include <atomic>
@@ -170,10 +170,10 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 // a lane per request, and deals them out. What is read many times, or by other
 // threads than wrote it, waits in shared memory, if it fits.
 constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024, kPlanCopies = 128;
-// A list that starts inside a share costs about as much as this many key tiles:
-// the pipeline runs empty, the outputs are written, the next queries fetched.
-// 4 / 3 / 2 / 1 take 109.2 / 109.2 / 109.4 / 112.0 us on the 32 x 16384 keys and 50.3 /
-// 49.3 / 48.8 / 48.8 on five groups of unlike size.
+// A list that starts inside a share costs about as much as this many key tiles: the
+// pipeline runs empty, the next queries are fetched, the outputs written.
+// 3 / 2 / 1 take 109.2 / 108.9 / 111.1 us on the 32 x 16384 keys and 49.1 / 47.4 / 47.2
+// on five groups of unlike size.
 constexpr int kListCost = 2;
 constexpr int kMaxShares = 128;
 struct PlanGroup {
