@@ -630,7 +630,9 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * rows: the same pages, or copies of them. Those positions are read through the
  * page table of the group's first request, the positions from prefix_lens[g] on
  * through each request's own. Visible are, as ever, j <= pos(t), j < seq_len: a
- * request may be shorter than the prefix or have new tokens inside it.
+ * request may be shorter than the prefix or have new tokens inside it. Pays from
+ * about 2000 shared positions on; below, dsa_window_mla without a window, each
+ * request by itself, is the faster.
  *   prefix_lens    int32 [G], 0 (nothing shared) .. the first request's length
  *   group_offsets  int32 [G + 1], 0 .. S in order; NULL with G == 1: one group
  *   max_kv         upper bound of seq_lens (a longer one is clamped and flagged)
