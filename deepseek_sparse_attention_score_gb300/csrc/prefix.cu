@@ -60,7 +60,8 @@ constexpr int kBlk = 64 * 128;                     // 64 keys x 64 dims
 constexpr int kQBlk = kRows * 128;                 // 128 rows x 64 dims (queries) or keys (P)
 // Stages of a key tile: five of two K blocks (64 keys of this CTA, dims 64j and
 // 256 + 64j; the last has dims 512 alone), then four of V (64 keys, 128 dims of this
-// CTA), first the keys whose P this CTA computes
+// CTA), first the keys whose P this CTA computes. Before a list that is not a
+// cluster's first, four of queries for TMEM (128 rows x 64 dims).
 constexpr int kStages = 5, kStage = 2 * kBlk;
 constexpr int kKStages = 5, kVStages = 4, kQStages = 4;
 constexpr int kDescs = 4;
@@ -91,7 +92,8 @@ struct KeyTile {
 };
 
 constexpr int OFF_Q = 0;  // dims 256-575
-constexpr int OFF_P = OFF_Q + 5 * kQBlk;  // four blocks of 64 keys; before, the queries for TMEM: dims 0-255
+// four blocks of 64 keys; before, the first list's queries for TMEM: dims 0-255
+constexpr int OFF_P = OFF_Q + 5 * kQBlk;
 constexpr int OFF_RING = OFF_P + 4 * kQBlk;
 constexpr int OFF_LOCAL = OFF_RING + kStages * kStage;   // float [2][kRows]: maxima of the two halves of S's columns
 constexpr int OFF_REMOTE = OFF_LOCAL + 2 * kRows * 4;    // float [2][kRows]: those of the other keys, two tiles
@@ -101,6 +103,7 @@ constexpr int kNumBars = 2 * kStages + 2 * kDescs + 9 + 4 + 8;
 constexpr int OFF_MISC = OFF_BAR + kNumBars * 8;
 constexpr int kSmem = OFF_MISC + 16;  // TMEM address, abort flag
 static_assert(kSmem <= 227 * 1024, "shared memory");
+static_assert(kQBlk <= kStage, "queries in a stage");
 static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_DESC % 16 == 0, "alignment");
 
 constexpr uint32_t kIdescQK = make_idesc_bf16(kTileRows, 128, false, false);
