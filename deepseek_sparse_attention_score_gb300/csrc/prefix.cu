@@ -39,9 +39,9 @@
 // shared keys, 128 heads (109 us in all, floor 77), step by step: pairs whose CTAs
 // compute S twice 161, clusters that share it 131, PV in order of arrival of P 127, the
 // plan's lengths in shared memory 121, keys resolved by a warp of their own 114,
-// runs of 128 keys 112. Elsewhere: 64 requests x 32768 keys of 16 heads 82 us (39: the
+// runs of 128 keys 112. Elsewhere: 64 requests x 32768 keys of 16 heads 81 us (39: the
 // own keys of 16 requests in a row tile are each computed for all of its rows), 4 x
-// 131072 keys of 128 heads 112 (77), ragged extends of 500 tokens 118 (78), two short
+// 131072 keys of 128 heads 110 (77), ragged extends of 500 tokens 118 (78), two short
 // requests 17 (latency).
 #include <algorithm>
 #include <atomic>
@@ -1096,9 +1096,12 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Merges the lists that were divided: block x takes the x-th of them, which the end of
-// some share is the first to cut; a warp takes half a row. About 8 us at 32 x 16384 keys:
-// 2304 blocks, some of them idle, took 1 us more, whole rows or loops over rows as much.
+// some share is the first to cut; a warp takes half a row or a quarter. About 8 us at
+// 32 x 16384 keys: 2304 blocks, some of them idle, took 1 us more, whole rows or loops
+// over rows as much.
 constexpr int kMergeWarps = 8, kMergeCtas = 4;  // per SM
+constexpr unsigned kFewLists = 8;
+template <int kPieces>  // of 128 columns, 8 / kPieces parts of them in flight
 __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_kernel(const PrefixParams p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -1114,19 +1117,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_ker
   }
   if (k0 < 0) return;
   const PrefixShare share = p.share[k0];
-  const int w = blockIdx.y * kMergeWarps + warp_id(), r = w >> 1, half = w & 1, k1 = share.last;
+  constexpr int kUnits = 4 / kPieces, kAhead = 8 / kPieces;  // units of a row
+  const int w = blockIdx.y * kMergeWarps + warp_id(), r = w / kUnits, unit = w % kUnits, k1 = share.last;
   if (r >= share.cut_rows) return;
   auto row_of = [&](int k) { return (size_t)(k == k0 ? share.first_slot : 2 * k) * kTileRows + r; };
-  // parts four at a time, the first four's rows on their way while the weights
-  // are found
-  float4 y[4][2];
+  // the first parts' rows are on their way while the weights are found
+  float4 y[kAhead][kPieces];
   auto load = [&](int k) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       if (k + j > k1) break;
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + row_of(k + j) * kDv + half * 256);
-      y[j][0] = src[lane];
-      y[j][1] = src[32 + lane];
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + row_of(k + j) * kDv + unit * kPieces * 128);
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) y[j][h] = src[32 * h + lane];
     }
   };
   load(k0);
@@ -1141,16 +1144,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_ker
   for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, d);
   const bool some = tot != 0.f;
   const float inv = some ? 1.f / tot : 0.f;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  float4 acc[kPieces];
+#pragma unroll
+  for (int h = 0; h < kPieces; ++h) acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int k = k0; k <= k1; k += 4) {
+  for (int k = k0; k <= k1; k += kAhead) {
     if (k > k0) load(k);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kAhead; ++j) {
       if (k + j > k1) break;
       const float v = p.part_lse[row_of(k + j)], wt = v == -INFINITY ? 0.f : exp2f(v - mx) * inv;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kPieces; ++h) {
         acc[h].x = fmaf(wt, y[j][h].x, acc[h].x);
         acc[h].y = fmaf(wt, y[j][h].y, acc[h].y);
         acc[h].z = fmaf(wt, y[j][h].z, acc[h].z);
@@ -1158,13 +1163,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeCtas) prefix_merge_ker
       }
     }
   }
-  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)share.cut_row0 + r) * kDv + half * 256);
+  uint2* dst = reinterpret_cast<uint2*>(p.o + ((size_t)share.cut_row0 + r) * kDv + unit * kPieces * 128);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kPieces; ++h) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc[h].x, acc[h].y), hi = __floats2bfloat162_rn(acc[h].z, acc[h].w);
     dst[32 * h + lane] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
   }
-  if (half == 0 && lane == 0 && p.lse)
+  if (unit == 0 && lane == 0 && p.lse)
     p.lse[(size_t)share.cut_row0 + r] = some ? (mx + log2f(tot)) * 0.69314718055994531f : -INFINITY;
 }
 
@@ -1265,8 +1270,16 @@ int run_prefix_mla(cudaStream_t stream, PrefixParams prm, void* ws) {
   prm.shares = clusters_at_once();
   DSA_LAUNCH_PDL(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, prm);
   DSA_LAUNCH_PDL(prefix_mla_kernel, dim3(4 * prm.shares), dim3(kThreads), kSmem, stream, prm, kvmap, qmap);
-  DSA_LAUNCH_PDL(prefix_merge_kernel, dim3(std::min(prm.shares, prm.max_tiles), 2 * kTileRows / kMergeWarps),
-                 dim3(kMergeWarps * 32), 0, stream, prm);
+  // Quarters of rows where few lists have many parts each: 4 row tiles 81.9 us, by halves
+  // 83.0, 2 tiles 111.2 and 112.5; but 12 tiles 50.2 and 48.2, 16 tiles 113.2 and 109.8, and
+  // 32 rows in all 17.5 and 17.2.
+  const unsigned lists = (unsigned)std::min(prm.shares, prm.max_tiles);
+  if (lists <= kFewLists && (long long)prm.T * prm.H > kTileRows)
+    DSA_LAUNCH_PDL(prefix_merge_kernel<1>, dim3(lists, 4 * kTileRows / kMergeWarps), dim3(kMergeWarps * 32), 0, stream,
+                   prm);
+  else
+    DSA_LAUNCH_PDL(prefix_merge_kernel<2>, dim3(lists, 2 * kTileRows / kMergeWarps), dim3(kMergeWarps * 32), 0, stream,
+                   prm);
   return DSA_OK;
 }
 
