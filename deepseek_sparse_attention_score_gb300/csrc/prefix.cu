@@ -7,6 +7,10 @@
 // then of the own positions of each request that has rows in the tile, which the
 // rows of others mask. Two runs, of one request or of two, make a key tile.
 //
+// Keys are fetched in boxes of min(page size, 64) rows. The shared part ends with the
+// prefix's last whole box: the box of its end holds the first request's own rows as
+// well, so every request reads that one from a page of its own.
+//
 // A cluster of four CTAs takes a row tile: CTA (c, r) = rank 2c + r has rows
 // 128r .. of it, value columns 256c .. (128 rows of all 512 columns in fp32 would
 // be the whole TMEM) and computes S for run c of a key tile, so that no
@@ -136,8 +140,8 @@ struct Bars {
 };
 
 // ------------------------------------------------------------- the work list
-// Request s's own keys for rows of tokens up to `last`: from position `start`
-// (a page's first) to `end`.
+// Request s's own keys for rows of tokens up to `last`: from position `start` (the
+// end of what is shared) to `end`.
 struct Own {
   int start, end;
   __device__ __forceinline__ int runs() const { return end > start ? (end - start + kRun - 1) / kRun : 0; }
@@ -147,7 +151,7 @@ __device__ __forceinline__ Own own_keys(const PrefixParams& p, int q0, int q1, i
   if (q1 <= q0 || last < q0) return w;
   const int kv = min(max(seq_len, 0), p.max_kv);
   const int end = min(kv, kv - (q1 - q0) + min(last, q1 - 1) - q0 + 1);
-  if (end > prefix) w.start = prefix & -p.ps, w.end = end;
+  if (end > prefix) w.start = prefix, w.end = end;
   return w;
 }
 
@@ -220,6 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       ok = x.token0 >= 0 && x.token1 >= x.token0 && x.token1 <= p.T;
       if (!ok) x.token1 = x.token0 = 0;
       if (in.want != x.prefix) bad = 1;
+      x.prefix &= -min(p.ps, 64);  // whole boxes
     }
     return x;
   };
@@ -861,10 +866,9 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(br.dempty(ds));
           const int hi = (seg < 0 ? min(see, prefix) : seg == my_s ? see : 0) - p0;
-          const int lo = seg < 0 ? 0 : prefix - p0;
           uint32_t mask[2];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) & ~below(lo - 32 * g) : 0u;
+          for (int g = 0; g < 2; ++g) mask[g] = (valid >> g) & 1 ? below(hi - 32 * g) : 0u;
           const bool full = __all_sync(0xffffffffu, (mask[0] & mask[1]) == 0xffffffffu);
           if (!(ok = mbar_wait_warp(br.sfull(), tc & 1, abort_flag))) break;
           tc_fence_after();

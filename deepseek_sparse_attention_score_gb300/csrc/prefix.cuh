@@ -13,7 +13,7 @@ constexpr int kPrefixMaxGroups = 1 << 20;
 struct alignas(16) PrefixTile {
   int row0, rows;      // of [T * H]
   int s0, last;        // first request, last token
-  int prefix;          // positions read through the group's first request
+  int prefix;          // positions read through the group's first request, whole boxes of keys
   int page_base;       // and where its page-table entries start
   int begin, end;      // its units, of all tiles' in a row
 };

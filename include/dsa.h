@@ -627,9 +627,10 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * of requests has in common are read once for all of its queries.
  * Groups are runs of requests: group g has the requests group_offsets[g] ..
  * group_offsets[g + 1] - 1, whose first prefix_lens[g] positions hold the same
- * rows: the same pages, or copies of them. Those positions are read through the
- * page table of the group's first request, the positions from prefix_lens[g] on
- * through each request's own. Visible are, as ever, j <= pos(t), j < seq_len: a
+ * rows: the same pages, or copies of them. The prefix's whole runs of min(ps, 64)
+ * positions are read through the page table of the group's first request, the
+ * positions behind them, the rest of the prefix among them, through each
+ * request's own. Visible are, as ever, j <= pos(t), j < seq_len: a
  * request may be shorter than the prefix or have new tokens inside it. Pays from
  * about 2000 shared positions on; below, dsa_window_mla without a window, each
  * request by itself, is the faster.
@@ -648,8 +649,8 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * Cache contents: of pages that hold a visible position runs of min(ps, 64) rows
  * are read; rows of a run past the visible length must hold finite values (see
  * dsa_sparse_mla_decode), and so must a group's prefix for each of its requests,
- * though it end or have tokens inside it. A request's own rows, from the prefix
- * on, reach its own outputs alone, whatever they hold.
+ * though it end or have tokens inside it. What a request holds from the prefix
+ * on, the group's first one too, reaches its own outputs alone, whatever it is.
  * Outputs are the same on every run.
  * Supported: as dsa_dense_mla; 1 <= G <= 2^20, T * H < 2^31 - 2^16, |sm_scale| *
  * 1.5 finite in fp32, max_kv <= 2^30 and with (T * H / 256 + 1 + G) * (2 +
