@@ -184,7 +184,7 @@ constexpr int kPlanRequests = 3000, kPlanGroups = 512, kPlanTiles = 1024, kPlanC
 constexpr int kListCost = 2;
 constexpr int kMaxShares = 128;
 struct PlanGroup {
-  int first_tile, token0, token1, prefix, page_base;
+  int first_tile, a, b, prefix, page_base;  // requests [a, b), none if it is refused
 };
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixParams p) {
   griddep_launch_dependents();
@@ -218,11 +218,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
     ok = in.ok;
     if (ok && in.b > in.a) {
       x.page_base = in.place / p.ps;
-      x.token0 = cu_q[in.a];
-      x.token1 = cu_q[in.b];
       x.prefix = min(max(in.want, 0), min(max(seq[in.a], 0), p.max_kv));
-      ok = x.token0 >= 0 && x.token1 >= x.token0 && x.token1 <= p.T;
-      if (!ok) x.token1 = x.token0 = 0;
+      ok = cu_q[in.a] >= 0 && cu_q[in.b] >= cu_q[in.a] && cu_q[in.b] <= p.T;
+      if (ok) x.a = in.a, x.b = in.b;
       if (in.want != x.prefix) bad = 1;
       x.prefix &= -min(p.ps, 64);  // whole boxes
     }
@@ -231,16 +229,23 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
   // the first groups' loads beside the requests'
   Given early{};
   if (tid < 256 && tid < p.G) early = given(tid);
+  bool down = false;
   if (p.S <= kPlanRequests) {
-    for (int i = tid; i <= p.S; i += kPlanThreads) {
-      s_cu_q[i] = __ldg(p.cu_q_lens + i);
-      if (i < p.S) s_seq[i] = __ldg(p.seq_lens + i);
+    for (int i = tid; i < p.S; i += kPlanThreads) {
+      const int q0 = __ldg(p.cu_q_lens + i), q1 = __ldg(p.cu_q_lens + i + 1), n = __ldg(p.seq_lens + i);
+      s_cu_q[i] = q0;
+      if (i == p.S - 1) s_cu_q[p.S] = q1;
+      s_seq[i] = n;
+      down |= q1 < q0;
     }
     cu_q = s_cu_q;
     seq = s_seq;
+  } else {
+#pragma unroll 1
+    for (int i = tid; i < p.S; i += kPlanThreads) down |= __ldg(p.cu_q_lens + i + 1) < __ldg(p.cu_q_lens + i);
   }
   if (tid <= kListCost) s_cost[tid] = 0;
-  __syncthreads();
+  const bool descents = __syncthreads_or(down);
   int total;
   unsigned tiles = 0;
   // 256 groups at a time: whatever the metadata hold, their sum fits 32 bits
@@ -253,9 +258,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       bool ok;
       const Given in = g0 ? given(g) : early;
       x = group_of(in, ok);
+#pragma unroll 1
+      for (int s = x.a; descents && s < x.b; ++s)
+        if (cu_q[s] > cu_q[s + 1]) ok = false, x.b = x.a;
       // requests behind the last group: no rows of theirs are written
       if (!ok || (g == p.G - 1 && in.b != p.S)) bad = 1;
-      n = ((unsigned)(x.token1 - x.token0) * p.H + kTileRows - 1) / kTileRows;
+      n = ((unsigned)(cu_q[x.b] - cu_q[x.a]) * p.H + kTileRows - 1) / kTileRows;
     }
     const unsigned end = block_scan(n, warp_sums, total);
     if (mine) {
@@ -281,21 +289,21 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       x = s_group[lo];
     } else {
       bool ok;
-      x = group_of(given(lo), ok);
+      x = group_of(given(lo), ok);  // in order, as it has tiles
       x.first_tile = p.tile_base[lo];
     }
-    const int first = x.token0 * p.H + (i - x.first_tile) * kTileRows, rows = min(kTileRows, x.token1 * p.H - first);
+    const int first = cu_q[x.a] * p.H + (i - x.first_tile) * kTileRows, rows = min(kTileRows, cu_q[x.b] * p.H - first);
     const int ta = first / p.H, tb = (first + rows - 1) / p.H;
-    int s0 = 0, top = p.S;  // the request of token ta
+    int s0 = x.a, top = x.b;  // the request of token ta: offsets of other groups may be in any order
     while (top - s0 > 1) {
       const int mid = (s0 + top) >> 1;
       if (cu_q[mid] <= ta) s0 = mid;
       else top = mid;
     }
     int n = 0;
-    for (int b = s0; b < p.S; b += 32) {
+    for (int b = s0; b < x.b; b += 32) {
       const int s = b + lane;
-      const bool in = s < p.S && cu_q[s] <= tb;
+      const bool in = s < x.b && cu_q[s] <= tb;
       if (in) n += own_keys(p, cu_q[s], cu_q[s + 1], seq[s], tb, x.prefix).runs();
       if (!__all_sync(0xffffffffu, in)) break;
     }
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       r.row0 = first;
       r.rows = rows;
       r.s0 = s0;
-      r.last = tb;
+      r.s1 = x.b;
       r.prefix = x.prefix;
       r.page_base = x.page_base;
       p.tiles[i] = r;
@@ -382,12 +390,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
 // The runs of a list from run k on, resolved by one whole warp.
 struct KeyCursor {
   const PrefixParams* p;
-  int prefix, last, seg;  // last token; the segment (-1: prefix)
+  int prefix, s1, seg;  // the group's end; the segment (-1: prefix)
   int s, own_start, own_end, own_base;  // 32 requests from s on, one per lane: their own keys and page-table entries
   uint32_t todo;                        // those with own keys still to visit
   int pos, end, left, page_base, lg;
   int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
-  int row0, H, rows, own_rows;  // the tile's first row; heads; rows that see the segment, and each lane's request
+  int row0, row1, H;   // the tile's rows; heads
+  int rows, own_rows;  // rows that see the segment, and each lane's request
 
   __device__ __forceinline__ void open(int sg, int first, int stop, int runs, int base, int who) {
     seg = sg;
@@ -402,9 +411,10 @@ struct KeyCursor {
     p = &prm;
     lg = 31 - __clz(prm.ps);
     prefix = tile.prefix;
-    last = tile.last;
     row0 = tile.row0;
     H = prm.H;
+    row1 = row0 + tile.rows;
+    s1 = tile.s1;
     s = tile.s0 - 32;
     todo = 0;
     left = 0;
@@ -440,7 +450,8 @@ struct KeyCursor {
       }
       s += 32;
       const int me = s + lane_id();
-      const int q0 = me < p->S ? __ldg(p->cu_q_lens + me) : last + 1;
+      const int last = (row1 - 1) / H;  // token
+      const int q0 = me < s1 ? __ldg(p->cu_q_lens + me) : last + 1;
       todo = 0;
       if (!__any_sync(0xffffffffu, q0 <= last)) break;
       Own w{0, 0};
@@ -569,7 +580,7 @@ __global__ void __cluster_dims__(4, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     if (row >= tile.rows - r * kRows) return make_int2(-2, 0);
     const int t = (tile.row0 + r * kRows + row) / prm.H;
-    int s = tile.s0, top = prm.S;  // cu_q_lens[s] <= t < cu_q_lens[top]
+    int s = tile.s0, top = tile.s1;  // cu_q_lens[s] <= t < cu_q_lens[top]
     for (int step = 1; s + step < top; step *= 2) {
       if (__ldg(prm.cu_q_lens + s + step) > t) top = s + step;
       else s += step;
