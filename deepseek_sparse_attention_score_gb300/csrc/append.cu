@@ -14,11 +14,13 @@
 //  - With queries, or too wide for that: a token per warp, whose rows go through
 //    registers.
 //
-// A pair's frequency is held as the 64-bit fraction of a turn per position, so
-// that position times frequency, wrapped at 2^64, is the angle's fraction of a
-// turn, exact to the frequency's 53 bits: integer products in the place of the
+// A pair's frequency is held as the 64-bit fraction of a turn per position, off
+// by 2^-65 of a turn at most, so that position times frequency, wrapped at 2^64, is
+// the angle's fraction of a turn: integer products in the place of the
 // five fp64 operations per token and pair of rope.cu, which are shared by all
-// heads there but by two rows here.
+// heads there but by two rows here. The whole product goes to fp32, signed, so that
+// small angles keep fp32's relative precision as they do there (its upper half alone
+// leaves steps of 2^-32 turns, which at 10^-9 radians is all of the angle).
 #include "append.cuh"
 #include "q4.cuh"
 #include "rope.cuh"
@@ -31,12 +33,13 @@ constexpr int kRunsPerLane = 3;  // a latent row and an indexer key: 72 runs
 // Cosine and sine of a pair that turns by `turn` 2^-64 turns per position.
 __device__ __forceinline__ float2 cos_sin(unsigned long long turn, int pos) {
   float s, c;  // of the nearer way round: -1/2 .. 1/2 of a turn
-  sincospif((float)(int)((turn * (unsigned)pos) >> 32) * 0x1p-31f, &s, &c);
+  sincospif((float)(long long)(turn * (unsigned)pos) * 0x1p-63f, &s, &c);
   return make_float2(c, s);
 }
 __device__ __forceinline__ unsigned long long turn_of(double radians) {
-  const double f = radians * 0.15915494309189533577;  // 1 / (2 pi)
-  return __double2ull_rn((f - floor(f)) * 0x1p64);
+  const double f = fabs(radians) * 0.15915494309189533577;  // 1 / (2 pi)
+  const unsigned long long turn = __double2ull_rn((f - floor(f)) * 0x1p64);
+  return radians < 0.0 ? 0ull - turn : turn;  // 1 - f would round a small f
 }
 // Pair i of bf16 columns x, turned into columns y; R columns in all. x and y may
 // be global or shared memory, and the same.

@@ -552,11 +552,12 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
  *   positions  int32 [T], slots int32 [T]: a row where either is negative
  *              (padding) is appended nowhere; the targets of `rotate` follow
  *              the position alone
- *   freqs      fp64 [rot_dim / 2]
+ *   freqs      fp64 [rot_dim / 2], finite
  * A slot >= P * ps sets DSA_STATUS_BAD_INDEX and its row is skipped. Slots of
  * a call are distinct: of rows with one slot any may win, 16 bytes at a time.
- * No source may overlap a cache or an output. Angles, products and rounding are
- * those of dsa_rope.
+ * No source may overlap a cache or an output. Products and rounding are those of
+ * dsa_rope; angles are formed another way, to fp32's relative precision too (and
+ * 2^-65 of a turn per position), so that a result may lie one rounding step apart.
  * Supported: rot_dim a multiple of 16 up to 512, D <= 4096, D, rot_off and the
  * strides multiples of 8, 16-byte aligned rows and caches, P * ps < 2^31.
  * Targets of `rotate` that do not lie on 16 bytes take a launch of their own.
