@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "indexer.cuh"
 #include "prefix.cuh"
+#include "rows.h"
 #include "steps.cuh"
 
 namespace dsa {
@@ -646,6 +647,44 @@ int dsa_rope(dsa_stream_t stream, const dsa_rope_target* targets, int n_targets,
   return run_rope(static_cast<cudaStream_t>(stream), targets, n_targets, T, rot_dim, positions, freqs, inverse != 0);
 }
 
+// Whether a part of the call writes what another reads or writes, in rows that its
+// strides step over: the columns between a tensor's rows may be others'.
+static bool append_parts_meet(const dsa_append_target* append, int n_append, const dsa_rope_target* rotate,
+                              int n_rotate, int T, int rot_dim, long long cache_rows) {
+  auto address = [](const void* p) { return (long long)reinterpret_cast<uintptr_t>(p); };
+  auto cache_of = [&](const dsa_append_target& g) -> Rows {
+    const bool q4 = g.format == DSA_CACHE_Q4;
+    return {address(g.cache), cache_rows, q4 ? DSA_Q4_ROW_BYTES : 2 * g.cache_stride, q4 ? DSA_Q4_ROW_BYTES : 2 * g.D};
+  };
+  auto meets_target = [&](const Rows& r, const void* base, long long st, long long sh, const dsa_rope_target& g) {
+    const long long es = g.dtype == DSA_DTYPE_F32 ? 4 : 2;
+    const bool place = g.x == g.y;  // touches the rotated columns only
+    return rows_meet(r, {address(base) + (place ? g.rot_off * es : 0), T, st * es, (place ? rot_dim : g.D) * es}, g.H,
+                     sh * es);
+  };
+  for (int i = 0; i < n_append; ++i) {
+    const dsa_append_target& g = append[i];
+    const Rows cache = cache_of(g);
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(cache, cache_of(append[j]))) return true;
+    const bool split = g.x_rot != nullptr;
+    const Rows source[2] = {{address(g.x), T, 2 * g.x_stride, 2 * (split ? g.D - rot_dim : g.D)},
+                            {address(g.x_rot), split ? T : 0, 2 * g.x_rot_stride, 2 * rot_dim}};
+    for (const Rows& x : source) {
+      for (int j = 0; j < n_append; ++j)
+        if (rows_meet(x, cache_of(append[j]))) return true;
+      for (int j = 0; j < n_rotate; ++j)
+        if (meets_target(x, rotate[j].y, rotate[j].y_stride_t, rotate[j].y_stride_h, rotate[j])) return true;
+    }
+    for (int j = 0; j < n_rotate; ++j) {
+      const dsa_rope_target& r = rotate[j];
+      if (meets_target(cache, r.x, r.x_stride_t, r.x_stride_h, r) || meets_target(cache, r.y, r.y_stride_t, r.y_stride_h, r))
+        return true;
+    }
+  }
+  return false;
+}
+
 int dsa_rope_append(dsa_stream_t stream, const dsa_append_target* append, int n_append, const dsa_rope_target* rotate,
                     int n_rotate, int T, int rot_dim, const int32_t* positions, const int32_t* slots,
                     const double* freqs, int P, int ps, int32_t* dev_status) {
@@ -676,11 +715,11 @@ int dsa_rope_append(dsa_stream_t stream, const dsa_append_target* append, int n_
     if ((reads_x && g.x_stride % 8) || (split && g.x_rot_stride % 8) || (!q4 && g.cache_stride % 8))
       return DSA_ERR_UNSUPPORTED;
     if ((reads_x && !aligned16(g.x)) || !aligned16(g.x_rot) || !aligned16(g.cache)) return DSA_ERR_ALIGNMENT;
-    for (int j = 0; j < i; ++j)
-      if (P > 0 && append[j].cache == g.cache) return DSA_ERR_INVALID_ARGUMENT;
   }
   if (T == 0) return DSA_OK;
   if (!positions || !slots || !freqs) return DSA_ERR_INVALID_ARGUMENT;
+  if (append_parts_meet(append, n_append, rotate, n_rotate, T, rot_dim, (long long)P * ps))
+    return DSA_ERR_INVALID_ARGUMENT;
   return run_rope_append(static_cast<cudaStream_t>(stream), rotate, n_rotate, append, n_append, T, rot_dim, positions,
                          slots, freqs, (long long)P * ps, dev_status);
 }

@@ -555,7 +555,9 @@ DSA_API int dsa_q4_read_rows(dsa_stream_t stream, const uint8_t* cache, int P, i
  *   freqs      fp64 [rot_dim / 2], finite
  * A slot >= P * ps sets DSA_STATUS_BAD_INDEX and its row is skipped. Slots of
  * a call are distinct: of rows with one slot any may win, 16 bytes at a time.
- * No source may overlap a cache or an output. Products and rounding are those of
+ * No source may overlap a cache or an output of `rotate`, no cache another or
+ * what `rotate` reads or writes: such a call is refused (rows that lie between
+ * another tensor's, as in a fused projection, are not an overlap). Products and rounding are those of
  * dsa_rope; angles are formed another way, to fp32's relative precision too (and
  * 2^-65 of a turn per position), so that a result may lie one rounding step apart.
  * Supported: rot_dim a multiple of 16 up to 512, D <= 4096, D, rot_off and the
