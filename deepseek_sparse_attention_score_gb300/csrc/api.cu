@@ -150,7 +150,7 @@ static int attend_check(const uint16_t* q, const uint16_t* kv, int row_stride, i
   if (row_stride != 576 && row_stride != 640) return DSA_ERR_UNSUPPORTED;
   if (T > 0 && H > 0 && (!q || !kv || !o)) return DSA_ERR_INVALID_ARGUMENT;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(o)) return DSA_ERR_ALIGNMENT;
-  if (T > 65535) return DSA_ERR_UNSUPPORTED;  // grid.y
+  if (T > 65535) return DSA_ERR_UNSUPPORTED;  // grid.y of the sparse, dense and window kernels; one bound for all
   return DSA_OK;
 }
 

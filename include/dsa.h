@@ -173,7 +173,8 @@ DSA_API int dsa_build_block_union(dsa_stream_t stream, const int32_t* topk_units
  *   ws     workspace of dsa_sparse_mla_decode_workspace_size(T, H, Dv) bytes
  *          (split-key partials; 0 bytes needed when T*H is large)
  * Supported: Dk == 576, Dv == 512, row_stride in {576, 640}, ps in
- * {32, 64, 128}, H >= 1 (heads are processed 128 at a time).
+ * {32, 64, 128}, H >= 1 (heads are processed 128 at a time), T <= 65535 (this
+ * and every attention entry below).
  * Cache contents: with page units (and in the query-block and dense forms)
  * whole runs of 32 rows of each selected page are read and the rows past
  * the visible length are masked with a probability of exactly 0, so those
@@ -655,10 +656,10 @@ DSA_API int dsa_window_mla(dsa_stream_t stream, const uint16_t* q, const uint16_
  * though it end or have tokens inside it. What a request holds from the prefix
  * on, the group's first one too, reaches its own outputs alone, whatever it is.
  * Outputs are the same on every run.
- * Supported: as dsa_dense_mla; 1 <= G <= 2^20, T * H < 2^31 - 2^16, |sm_scale| *
- * 1.5 finite in fp32, max_kv <= 2^30 and with (T * H / 256 + 1 + G) * (2 +
- * ceil(256 / H)) * (max_kv / 256 + 6) below 2^31 (65535 tokens of 128 heads: four
- * million keys).
+ * Supported: as dsa_dense_mla, T <= 65535 among it; 1 <= G <= 2^20, T * H <
+ * 2^31 - 2^16, |sm_scale| * 1.5 finite in fp32, max_kv <= 2^30 and with
+ * (T * H / 256 + 1 + G) * (2 + ceil(256 / H)) * (max_kv / 256 + 6) below 2^31
+ * (65535 tokens of 128 heads: four million keys).
  * ------------------------------------------------------------------------ */
 DSA_API size_t dsa_prefix_mla_workspace_size(int T, int H, int G);
 DSA_API int dsa_prefix_mla(dsa_stream_t stream, const uint16_t* q, const uint16_t* kv, int row_stride,
