@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const PrefixP
       r.rows = rows;
       r.s0 = s0;
       r.s1 = x.b;
+      r.last = tb;
       r.prefix = x.prefix;
       r.page_base = x.page_base;
       p.tiles[i] = r;
@@ -395,7 +396,7 @@ struct KeyCursor {
   uint32_t todo;                        // those with own keys still to visit
   int pos, end, left, page_base, lg;
   int win, page;  // first entry of the window of pages, this lane's page in it (-1: none)
-  int row0, row1, H;   // the tile's rows; heads
+  int row0, last, H;   // the tile's first row and last token; heads
   int rows, own_rows;  // rows that see the segment, and each lane's request
 
   __device__ __forceinline__ void open(int sg, int first, int stop, int runs, int base, int who) {
@@ -413,7 +414,7 @@ struct KeyCursor {
     prefix = tile.prefix;
     row0 = tile.row0;
     H = prm.H;
-    row1 = row0 + tile.rows;
+    last = tile.last;
     s1 = tile.s1;
     s = tile.s0 - 32;
     todo = 0;
@@ -450,7 +451,6 @@ struct KeyCursor {
       }
       s += 32;
       const int me = s + lane_id();
-      const int last = (row1 - 1) / H;  // token
       const int q0 = me < s1 ? __ldg(p->cu_q_lens + me) : last + 1;
       todo = 0;
       if (!__any_sync(0xffffffffu, q0 <= last)) break;

@@ -12,7 +12,7 @@ constexpr int kPrefixMaxGroups = 1 << 20;
 // A row tile: 256 rows or fewer of one group.
 struct alignas(16) PrefixTile {
   int row0, rows;      // of [T * H]
-  int s0, s1;          // first request, end of the group's
+  int s0, s1, last;    // first request, end of the group's, last token
   int prefix;          // positions read through the group's first request, whole boxes of keys
   int page_base;       // and where its page-table entries start
   int begin, end;      // its units, of all tiles' in a row
