@@ -974,9 +974,9 @@ def dsa_prefix_mla(q, kv, seq_lens, cu_q_lens, cu_kv_lens, page_indices, prefix_
     requests that share a prefix: the requests ``group_offsets[g]`` ..
     ``group_offsets[g + 1] - 1`` (int32 [G + 1]; None: all are one group) hold
     the same rows in their first ``prefix_lens[g]`` positions (int32 [G]), which
-    are read once for all of them, through the first one's pages. Pays from
-    about 2000 shared positions on (below, :func:`dsa_window_mla` without a
-    window is faster). ``ws``: at least ``dsa_prefix_mla_workspace_size(T, H, G)``
+    are read together for all of them, through the first one's pages. Pays from
+    about 4000 shared positions on, with 128 heads or 64 requests from 2000 on
+    (below, :func:`dsa_window_mla` without a window is as fast or faster). ``ws``: at least ``dsa_prefix_mla_workspace_size(T, H, G)``
     bytes, one for each call that may run at once; allocated if None. ``q`` may
     have padding rows behind the last token, whose outputs are left as they are."""
     dev = q.device

@@ -327,7 +327,7 @@ int run_rope_append(cudaStream_t stream, const dsa_rope_target* rot, int n_rot, 
   // Rows by themselves go through shared memory, with targets of dsa_rope beside them
   // through registers, in one launch with those. Measured, latent rows and indexer
   // keys by themselves, registers / shared memory: 16 bits, 8 tokens 2.9 / 2.4 us, 512
-  // 3.1 / 2.6, 8192 9.9 / 6.9, 65537 50 / 33 (a plain copy of as many bytes 29.3); 4 bits,
+  // 3.1 / 2.6, 8192 9.9 / 7.7, 65537 50 / 33 (a plain copy of as many bytes 29.3); 4 bits,
   // 8 tokens 2.8 / 2.5, 4096 5.4 / 4.6, 65537 48 / 36. With 128 heads' queries, one launch
   // / two: 64 tokens 4.1 / 6.1, 1024 15.3 / 18.0, 4096 42 / 46. CTAs per SM: 65537 tokens,
   // 3 / 4 / 5 / 6 CTAs 38.2 / 32.7 / 40.0 / 38.7 us (fewer leave the memory idle, more

@@ -1,5 +1,5 @@
 // Absorbed-MLA attention of requests that share a prefix, whose keys are read
-// once for all of them. Per group of requests, and with rows (token, head):
+// together for all of them. Per group of requests, and with rows (token, head):
 //   S = Q K^T over 576 dims, online softmax, O += P V, V = the first 512 dims.
 // The rows of a group are cut into tiles of 256, of any tokens and heads, since
 // [T, H] rows lie one behind another. A tile's keys are a list of runs of up to
