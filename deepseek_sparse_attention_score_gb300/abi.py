@@ -803,7 +803,8 @@ def dsa_rope_append(targets, positions, slots, freqs, *, rotate=(), dev_status=N
     row ``slots[t]`` (both int32 [T], as :func:`dsa_build_page_tables` makes
     them; a row where either is negative is written nowhere). The
     :class:`RopeTarget` in ``rotate``, such as the layer's queries, turn in the
-    same launch, as :func:`dsa_rope` turns them. ``freqs``: fp64 [rot_dim / 2].
+    same launch, as :func:`dsa_rope` turns them. A call of which one part writes
+    what another reads or writes is refused. ``freqs``: fp64 [rot_dim / 2].
     Returns the caches, one or a list as ``targets`` came."""
     one = isinstance(targets, AppendTarget)
     ts = [targets] if one else list(targets)
